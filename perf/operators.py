@@ -1,0 +1,529 @@
+"""The attention operators beside the scaled GEMMs: cases, plain forms, 64-bit values.
+
+Three operators of a decoder's attention, between its QKV projection and its
+output projection:
+
+append   rotate the new queries and keys by their positions and append keys and
+         values to a paged cache held in e4m3 with one e8m0 scale for each block
+         of 16 tokens and head.
+decode   attention of the newest tokens of many sequences over that cache.
+prompt   attention over whole prompts, packed, causal, grouped heads.
+
+Heads come as [tokens, heads, D] views of the projection's output rows
+[tokens, (Hq + 2 Hk) D].  The cache is [pages][Hk][page][D] codes and
+[pages][Hk][page / 16] scales; a sequence's pages are listed in its row of the
+block table.
+
+``own`` False: elementary torch operations in fp32.  ``own`` True: the calls of
+``fp8_scaled_gemm_sm_gb300``.
+"""
+import math
+import random
+
+import numpy as np
+import torch
+
+own = False
+
+BLOCK = 16      # tokens that share a scale
+NAN_CODE = 0x7F
+
+
+# --------------------------------------------------------------------------- cases
+
+
+def listed():
+    return [
+        # one decode step of a small batch: a launch and little else
+        dict(name="append_step_8", op="append", B=8, new_lo=1, new_hi=1, ctx_lo=5, ctx_hi=900, hq=32, hk=8, d=128, page=64,
+             rot=128, inter=False, k_out=False, lens=1),
+        # one decode step of a large batch, small pages, half of the head rotated, interleaved pairs
+        dict(name="append_step_512", op="append", B=512, new_lo=1, new_hi=1, ctx_lo=1, ctx_hi=2000, hq=32, hk=8, d=128, page=16,
+             rot=64, inter=True, k_out=False, lens=2),
+        # ragged chunks of prompts behind contexts that end inside a block, 64-wide heads
+        dict(name="append_chunks_41", op="append", B=41, new_lo=3, new_hi=1500, ctx_lo=1, ctx_hi=700, hq=24, hk=24, d=64, page=32,
+             rot=64, inter=False, k_out=True, lens=3),
+        # a long prompt and its neighbours, from empty caches
+        dict(name="append_prompt_48k", op="append", B=3, new_lo=9000, new_hi=24000, ctx_lo=0, ctx_hi=0, hq=32, hk=8, d=128, page=64,
+             rot=128, inter=False, k_out=True, lens=4),
+        # one user
+        dict(name="decode_1", op="decode", B=1, qn=1, len_lo=777, len_hi=777, idle=0, hq=32, hk=8, d=128, page=64, lens=5),
+        # a serving batch of ragged lengths, two slots idle
+        dict(name="decode_64_ragged", op="decode", B=64, qn=1, len_lo=64, len_hi=16000, idle=2, hq=32, hk=8, d=128, page=64, lens=6),
+        # few rows over a very long cache: the work has to be split along the tokens
+        dict(name="decode_2_long", op="decode", B=2, qn=1, len_lo=120001, len_hi=131072, idle=0, hq=64, hk=8, d=128, page=128, lens=7),
+        # four drafted tokens checked at once, ungrouped 64-wide heads, small pages
+        dict(name="decode_200_draft4", op="decode", B=200, qn=4, len_lo=7, len_hi=4000, idle=0, hq=16, hk=16, d=64, page=16, lens=8),
+        # one short question
+        dict(name="prompt_1_short", op="prompt", B=1, q_lo=77, q_hi=77, ctx_lo=0, ctx_hi=0, hq=32, hk=8, d=128, causal=True, lens=9),
+        # ragged prompts in one pack, ungrouped 64-wide heads
+        dict(name="prompt_29_ragged", op="prompt", B=29, q_lo=1, q_hi=2500, ctx_lo=0, ctx_hi=0, hq=16, hk=16, d=64, causal=True, lens=10),
+        # chunks of prompts after the keys that came before, five heads a group
+        dict(name="prompt_6_chunks", op="prompt", B=6, q_lo=300, q_hi=2048, ctx_lo=100, ctx_hi=6000, hq=40, hk=8, d=128, causal=True, lens=11),
+        # one long document
+        dict(name="prompt_1_16k", op="prompt", B=1, q_lo=16384, q_hi=16384, ctx_lo=0, ctx_hi=0, hq=32, hk=8, d=128, causal=True, lens=12),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["append", "decode", "prompt"])
+    hk = rng.choice([1, 2, 4, 8, 16])
+    hq = hk * rng.choice([1, 2, 3, 4, 5, 7, 8, 16] if hk <= 4 else [1, 2, 4, 5, 7])
+    d = rng.choice([64, 64, 96, 128, 128, 128])
+    c = dict(op=op, hq=hq, hk=hk, d=d, lens=rng.randrange(1 << 20))
+    if op == "append":
+        B = _log(rng, 1, 700)
+        step = rng.random() < 0.5
+        hi = 1 if step else max(2, min(_log(rng, 2, 20000), 40000 * 48 // ((hq + 2 * hk) * B)))
+        ctx_hi = max(2, min(_log(rng, 2, 4000), 400_000_000 // (B * hk * d)))
+        c.update(B=B, new_lo=1, new_hi=hi, ctx_lo=0 if rng.random() < 0.3 else 1, ctx_hi=ctx_hi, page=rng.choice([16, 32, 64, 128]),
+                 rot=rng.choice([d, d, d // 2]), inter=rng.random() < 0.4, k_out=not step)
+    elif op == "decode":
+        B = _log(rng, 1, 400)
+        qn = rng.choice([1, 1, 1, 2, 3, 5])
+        hi = max(2, min(_log(rng, 16, 131072), 500_000_000 // (B * hk * d), 400_000_000 // (B * hq * qn)))
+        c.update(B=B, qn=qn, len_lo=max(1, hi // rng.choice([1, 2, 30])), len_hi=hi, idle=rng.choice([0, 0, 1]) if B > 1 else 0,
+                 page=rng.choice([16, 32, 64, 128]))
+    else:
+        B = _log(rng, 1, 40)
+        q_hi = max(2, min(_log(rng, 2, 12000), int((2.5e9 / (B * hq)) ** 0.5)))
+        ctx_hi = rng.choice([0, 0, _log(rng, 1, 4000)])
+        ctx_hi = int(min(ctx_hi, max(0, 2.5e9 / (B * hq * q_hi) - q_hi)))
+        c.update(B=B, q_lo=max(1, q_hi // rng.choice([1, 3, 40])), q_hi=q_hi, ctx_lo=min(1, ctx_hi), ctx_hi=ctx_hi, causal=rng.random() < 0.85)
+    return c
+
+
+def _lens(case, lo, hi, salt):
+    """Lengths of the case's sequences, spread over their logarithm; the first is the longest."""
+    rng = random.Random(case["lens"] * 8 + salt)
+    return [hi] + [lo if lo == hi else (_log(rng, max(lo, 1), hi) if lo else rng.randint(lo, hi)) for _ in range(case["B"] - 1)]
+
+
+def _append_lens(case):
+    return _lens(case, case["new_lo"], case["new_hi"], 1), _lens(case, case["ctx_lo"], case["ctx_hi"], 2)
+
+
+def _decode_lens(case):
+    n = _lens(case, case["len_lo"], case["len_hi"], 3)
+    return n[:1] + [0] * case["idle"] + n[1 + case["idle"]:]
+
+
+def _prompt_lens(case):
+    q = _lens(case, case["q_lo"], case["q_hi"], 4)
+    return q, [a + b for a, b in zip(q, _lens(case, case["ctx_lo"], case["ctx_hi"], 5))]
+
+
+# --------------------------------------------------------------------------- inputs
+
+
+def _cum(lens, dev):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=dev)
+
+
+def _table(lens, page, gen, dev):
+    """A block table over shuffled pages, unused entries -1, and the number of pages in the cache."""
+    need = [-(-n // page) for n in lens]
+    total = sum(need) + 3
+    ids = torch.randperm(total, generator=gen, device=dev)[: sum(need)].to(torch.int32)
+    width = max(max(need), 1)
+    at = torch.arange(width, device=dev)[None, :] < torch.tensor(need, device=dev)[:, None]
+    table = torch.full((len(lens), width), -1, dtype=torch.int32, device=dev)
+    table[at] = ids
+    return table, total
+
+
+def _rotary(max_pos, rot, dev):
+    """cos and sin of the position angles, [max_pos][2][rot / 2] fp32, positions stretched twofold for a long context."""
+    inv = 10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=dev) / rot)
+    ang = (torch.arange(max_pos, dtype=torch.float64, device=dev) / 2.0)[:, None] * inv
+    return torch.stack([ang.cos(), ang.sin()], 1).float().contiguous()
+
+
+def _rows(tokens, case, gen, dev):
+    """The projection's output rows, q / k / v views of them; some channels of k and v are far larger than others, as trained models have them."""
+    hq, hk, d = case["hq"], case["hk"], case["d"]
+    x = torch.randn(tokens, hq + 2 * hk, d, generator=gen, device=dev)
+    w = torch.exp(0.7 * torch.randn(1, 2 * hk, d, generator=gen, device=dev))
+    x[:, hq:] *= w
+    x = x.to(torch.bfloat16)
+    return x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+
+
+def _stale(pages, case, gen, dev):
+    """A cache that has been used before: codes and scales of all kinds, NaN codes among them."""
+    hk, page, d = case["hk"], case["page"], case["d"]
+    codes = [torch.randint(0, 256, (pages, hk, page, d), generator=gen, device=dev, dtype=torch.uint8) for _ in range(2)]
+    scales = [torch.randint(115, 123, (pages, hk, page // BLOCK), generator=gen, device=dev, dtype=torch.uint8) for _ in range(2)]
+    return codes[0], codes[1], scales[0], scales[1]
+
+
+def _plan(case, rotary=None, inter=False):
+    from fp8_scaled_gemm_sm_gb300 import PagedAttention
+
+    return PagedAttention(case["hq"], case["hk"], case["d"], page_size=case.get("page", 64), rotary=rotary, interleaved=inter)
+
+
+def prepare(case, seed):
+    dev = torch.device("cuda")
+    gen = torch.Generator(dev)
+    gen.manual_seed(seed * 1000003 + case["lens"])
+    s = dict(case=case)
+    if case["op"] == "append":
+        new, ctx = _append_lens(case)
+        s["table"], pages = _table([a + b for a, b in zip(new, ctx)], case["page"], gen, dev)
+        s["q"], s["k"], s["v"] = _rows(sum(new), case, gen, dev)
+        s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"] = _stale(pages, case, gen, dev)
+        s["cu"] = _cum(new, dev)
+        s["ctx"] = torch.tensor(ctx, dtype=torch.int32, device=dev)
+        s["rotary"] = _rotary(max(a + b for a, b in zip(new, ctx)), case["rot"], dev)
+        if own:
+            s["plan"] = _plan(case, s["rotary"], case["inter"])
+    elif case["op"] == "decode":
+        lens = _decode_lens(case)
+        s["table"], pages = _table(lens, case["page"], gen, dev)
+        kc, vc, ks, vs = _stale(pages, case, gen, dev)
+        # the codes of the sequences' tokens: normal values quantised at their block's scale (|code| up to 448)
+        for c in (kc, vc):
+            for i in range(0, pages, 4096):
+                x = torch.randn(c[i:i + 4096].shape, generator=gen, device=dev) * 110
+                fresh = x.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+                used = torch.zeros(pages, dtype=torch.bool, device=dev)
+                used[s["table"][s["table"] >= 0].long()] = True
+                c[i:i + 4096] = torch.where(used[i:i + 4096, None, None, None], fresh, c[i:i + 4096])
+        # slots past a sequence's end keep what was there
+        last = torch.tensor([max(n - 1, 0) for n in lens], device=dev)
+        rows = torch.arange(case["B"], device=dev)
+        lp = s["table"][rows, last // case["page"]].long()
+        live = torch.tensor([n > 0 for n in lens], device=dev)
+        dead = torch.arange(case["page"], device=dev)[None, :] > (last % case["page"])[:, None]
+        for c in (kc, vc):
+            part = c[lp[live]]
+            part.masked_fill_(dead[live][:, None, :, None], NAN_CODE)
+            c[lp[live]] = part
+        s.update(k_cache=kc, v_cache=vc, k_scale=ks, v_scale=vs)
+        x = torch.randn(case["B"] * case["qn"], case["hq"], case["d"], generator=gen, device=dev) * 2
+        s["q"] = x.to(torch.bfloat16)
+        s["lens"] = torch.tensor(lens, dtype=torch.int32, device=dev)
+        if own:
+            s["plan"] = _plan(case)
+    else:
+        ql, kl = _prompt_lens(case)
+        if ql == kl:
+            s["q"], s["k"], s["v"] = _rows(sum(ql), case, gen, dev)
+        else:
+            s["q"], _, _ = _rows(sum(ql), case, gen, dev)
+            _, s["k"], s["v"] = _rows(sum(kl), dict(case, hq=0), gen, dev)
+        s["cu_q"], s["cu_k"] = _cum(ql, dev), _cum(kl, dev)
+        s["max_q"], s["max_k"] = max(ql), max(kl)
+        if own:
+            s["plan"] = _plan(case)
+    return s
+
+
+# --------------------------------------------------------------------------- one pass
+
+
+def run(s):
+    op = s["case"]["op"]
+    if not own:
+        return {"append": _plain_append, "decode": _plain_decode, "prompt": _plain_prompt}[op](s)
+    if op == "append":
+        q, k = s["plan"].append(s["q"], s["k"], s["v"], (s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"]), s["table"],
+                                s["ctx"], s["cu"], k_out=s["case"]["k_out"])
+        return _append_out(s, q, k)
+    if op == "decode":
+        out, lse = s["plan"].decode(s["q"], (s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"]), s["table"], s["lens"],
+                                    q_tokens=s["case"]["qn"])
+        return dict(out=out, lse=lse)
+    out, lse = s["plan"].prompt(s["q"], s["k"], s["v"], s["cu_q"], s["cu_k"], causal=s["case"]["causal"])
+    return dict(out=out, lse=lse)
+
+
+def _append_out(s, q, k):
+    e4m3 = torch.float8_e4m3fn
+    out = dict(q=q, k_cache=s["k_cache"].view(e4m3), v_cache=s["v_cache"].view(e4m3), k_scale=s["k_scale"], v_scale=s["v_scale"])
+    if k is not None:
+        out["k"] = k
+    return out
+
+
+def _pow2(code):
+    """2^(code - 127) of e8m0 codes below 255."""
+    code = code.to(torch.int32)
+    return torch.where(code > 0, code << 23, 0x00400000).view(torch.float32)
+
+
+def _scale_code(amax):
+    """The e8m0 code of the least power of two s with amax <= 448 s; 0 for amax = 0."""
+    m, x = torch.frexp(amax)
+    e = torch.where(m <= 0.875, x - 9, x - 8)
+    return torch.where(amax > 0, (e + 127).clamp(0, 254), 0)
+
+
+def _e4m3(x):
+    return x.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def _rotate(x, cos, sin, inter):
+    rot = 2 * cos.shape[-1]
+    x = x.float()
+    if inter:
+        a, b = x[..., 0:rot:2], x[..., 1:rot:2]
+    else:
+        a, b = x[..., : rot // 2], x[..., rot // 2:rot]
+    a, b = a * cos - b * sin, a * sin + b * cos
+    y = torch.stack([a, b], -1).flatten(-2) if inter else torch.cat([a, b], -1)
+    return torch.cat([y, x[..., rot:]], -1)
+
+
+def _plain_append(s):
+    case = s["case"]
+    page, B, T = case["page"], case["B"], s["q"].shape[0]
+    cu, ctx, table = s["cu"].long(), s["ctx"].long(), s["table"].long()
+    t = torch.arange(T, device=cu.device)
+    b = torch.searchsorted(cu, t, right=True) - 1
+    pos = ctx[b] + t - cu[b]
+    cs = s["rotary"][pos]
+    cos, sin = cs[:, 0][:, None, :], cs[:, 1][:, None, :]
+    q = _rotate(s["q"], cos, sin, case["inter"])
+    k = _rotate(s["k"], cos, sin, case["inter"])
+    pg, slot = table[b, pos // page], pos % page
+    blk = slot // BLOCK
+    # the first block of a sequence's new tokens may hold older ones
+    old = (ctx % BLOCK > 0) & (cu[1:] > cu[:-1])
+    first = ctx.clamp(max=table.shape[1] * page - 1)
+    opg, oslot = table[torch.arange(B, device=cu.device), first // page].clamp(min=0), first % page
+    before = torch.arange(BLOCK, device=cu.device)[None, :] < (ctx % BLOCK)[:, None]
+    for x, cache, scale in ((k, s["k_cache"], s["k_scale"]), (s["v"].float(), s["v_cache"], s["v_scale"])):
+        hk, nb = scale.shape[1], scale.shape[2]
+        amax = x.abs().amax(-1)                                    # [T, Hk]
+        code = _scale_code(amax)
+        flat = (pg * nb + blk)[:, None].expand(T, hk)
+        new = torch.zeros(scale.shape[0] * nb, hk, dtype=code.dtype, device=code.device)
+        new.scatter_reduce_(0, flat, code, "amax")
+        new = new.view(-1, nb, hk)
+        was = scale[opg, :, oslot // BLOCK].to(code.dtype)         # [B, Hk]
+        grown = torch.where(old[:, None], torch.maximum(was, new[opg, oslot // BLOCK]), 0)
+        new.index_put_((opg[old], (oslot // BLOCK)[old]), grown[old])
+        # older codes at the grown scale
+        at = ((oslot // BLOCK) * BLOCK)[:, None] + torch.arange(BLOCK, device=cu.device)
+        held = cache[opg[:, None], :, at]                          # [B, 16, Hk, D]
+        val = held.view(torch.float8_e4m3fn).float() * _pow2(was - grown + 127)[:, None, :, None]
+        sel = before & old[:, None]
+        cache[opg[:, None].expand_as(at)[sel], :, at[sel]] = _e4m3(val)[sel]
+        now = new[pg, blk]                                         # [T, Hk]
+        cache[pg, :, slot] = _e4m3(x * _pow2(254 - now)[..., None])
+        scale[pg, :, blk] = now.to(torch.uint8)
+    return _append_out(s, q.to(torch.bfloat16), k.to(torch.bfloat16) if case["k_out"] else None)
+
+
+def _softmax_v(sc, hide, v):
+    """softmax over the last axis of sc, where not hidden, times v; rows with nothing to see give 0 and -inf."""
+    sc.masked_fill_(hide, -math.inf)
+    m = sc.amax(-1, keepdim=True)
+    base = torch.where(torch.isinf(m), 0.0, m)
+    p = sc.sub_(base).exp_()
+    n = p.sum(-1, keepdim=True)
+    o = torch.matmul(p, v) / torch.where(n == 0, 1.0, n)
+    return o, (base + n.log()).squeeze(-1)
+
+
+def _plain_decode(s):
+    case = s["case"]
+    B, qn, hq, hk, d, page = (case[x] for x in ("B", "qn", "hq", "hk", "d", "page"))
+    g, L = hq // hk, s["table"].shape[1] * page
+    pg = s["table"].long().clamp(min=0)
+    at = torch.arange(L, device=pg.device)
+    lens = s["lens"].long()
+    there = (at[None, :] < lens[:, None])[:, None, :, None]
+
+    def values(codes, scale):
+        x = codes[pg].view(torch.float8_e4m3fn).float()            # [B, P, Hk, page, D]
+        x *= _pow2(scale[pg]).repeat_interleave(BLOCK, -1)[..., None]
+        return x.transpose(1, 2).reshape(B, hk, L, d).masked_fill_(~there, 0.0)
+
+    q = s["q"].float().view(B, qn, hk, g, d).permute(0, 2, 1, 3, 4).reshape(B, hk, qn * g, d)
+    sc = torch.matmul(q * d ** -0.5, values(s["k_cache"], s["k_scale"]).transpose(2, 3))
+    i = torch.arange(qn, device=pg.device).repeat_interleave(g)
+    hide = at[None, None, :] >= (lens[:, None] - (qn - 1 - i)[None, :])[..., None]
+    o, lse = _softmax_v(sc, hide[:, None], values(s["v_cache"], s["v_scale"]))
+    o = o.view(B, hk, qn, g, d).permute(0, 2, 1, 3, 4).reshape(B * qn, hq, d)
+    lse = lse.view(B, hk, qn, g).permute(0, 2, 1, 3).reshape(B * qn, hq)
+    return dict(out=o.to(torch.bfloat16), lse=lse)
+
+
+def _plain_prompt(s):
+    case = s["case"]
+    B, hq, hk, d = case["B"], case["hq"], case["hk"], case["d"]
+    g = hq // hk
+    cq, ck = s["cu_q"].long(), s["cu_k"].long()
+    lq, lk = cq.diff(), ck.diff()
+    i, j = torch.arange(s["max_q"], device=cq.device), torch.arange(s["max_k"], device=cq.device)
+    iq = (cq[:-1, None] + i).clamp(max=max(s["q"].shape[0] - 1, 0))
+    ik = (ck[:-1, None] + j).clamp(max=max(s["k"].shape[0] - 1, 0))
+    q = s["q"][iq].float().transpose(1, 2)                         # [B, Hq, Lq, D]
+    k = s["k"][ik].float().transpose(1, 2)
+    v = s["v"][ik].float().transpose(1, 2)
+    sc = torch.matmul(q.reshape(B, hk, g * len(i), d) * d ** -0.5, k.transpose(2, 3)).view(B, hq, len(i), len(j))
+    hide = (j[None, None, :] >= lk[:, None, None])
+    if case["causal"]:
+        hide = hide | (j[None, None, :] > (i[None, :] + (lk - lq)[:, None])[..., None])
+    sc = sc.view(B, hk, g, len(i), len(j))
+    o, lse = _softmax_v(sc, hide[:, None, None], v[:, :, None])
+    rows = i[None, :] < lq[:, None]
+    o = o.view(B, hq, len(i), d).transpose(1, 2)[rows]
+    lse = lse.view(B, hq, len(i)).transpose(1, 2)[rows]
+    return dict(out=o.to(torch.bfloat16), lse=lse)
+
+
+# --------------------------------------------------------------------------- work
+
+
+def work(case):
+    hq, hk, d = case["hq"], case["hk"], case["d"]
+    if case["op"] == "append":
+        new, _ = _append_lens(case)
+        T = sum(new)
+        read = T * (hq + 2 * hk) * d * 2 + T * case["rot"] * 4
+        write = T * hq * d * 2 + T * 2 * hk * (d + 1 / BLOCK) + (T * hk * d * 2 if case["k_out"] else 0)
+        return dict(bytes=read + write, flops=T * (hq + hk) * case["rot"] * 3 + 2 * T * hk * d)
+    if case["op"] == "decode":
+        n = sum(_decode_lens(case))
+        rows = case["B"] * case["qn"] * hq
+        return dict(bytes=n * hk * 2 * (d + 1 / BLOCK) + rows * (4 * d + 4), flops=4 * n * case["qn"] * hq * d)
+    ql, kl = _prompt_lens(case)
+    if case["causal"]:
+        seen = sum(b * a - a * (a - 1) // 2 for a, b in zip(ql, kl))
+    else:
+        seen = sum(b * a for a, b in zip(ql, kl))
+    return dict(bytes=sum(ql) * hq * (4 * d + 4) + sum(kl) * hk * d * 4, flops=4 * seen * hq * d)
+
+
+# --------------------------------------------------------------------------- 64 bits
+
+
+def _decode_e4m3(dev):
+    """The 256 values of e4m3 by its definition."""
+    v = []
+    for c in range(256):
+        e, m = (c >> 3) & 15, c & 7
+        x = math.nan if (c & 127) == 127 else (m / 8 * 2.0 ** -6 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7))
+        v.append(-x if c & 128 else x)
+    return torch.tensor(v, dtype=torch.float64, device=dev)
+
+
+def _round_e4m3(x):
+    """The nearest e4m3 value (ties to even), saturated, of a float64 tensor."""
+    _, e = torch.frexp(x)
+    step = torch.pow(torch.tensor(2.0, dtype=torch.float64, device=x.device), (e - 1).clamp(min=-6).double() - 3)
+    return (torch.round(x / step) * step).clamp(-448, 448)
+
+
+def exact(case, seed):
+    global own
+    mine, own = own, False
+    try:
+        s = prepare(case, seed)
+    finally:
+        own = mine
+    return {"append": _exact_append, "decode": _exact_decode, "prompt": _exact_prompt}[case["op"]](case, s)
+
+
+def _exact_append(case, s):
+    dev, hk, d, page, rot = s["q"].device, case["hk"], case["d"], case["page"], case["rot"]
+    lut = _decode_e4m3(dev)
+    val = [lut[s[n].long()] for n in ("k_cache", "v_cache")]
+    exps = [s[n].cpu().numpy().astype(int) for n in ("k_scale", "v_scale")]
+    new, ctx = _append_lens(case)
+    if sum(new) // BLOCK + 2 * case["B"] > 12000:
+        return None  # it goes block by block: too slow for so many
+    cs = s["rotary"].double()
+    qs, ks = [], []
+    t0 = 0
+    table = s["table"].cpu().numpy()
+    for b in range(case["B"]):
+        x = [s[n][t0:t0 + new[b]].double() for n in ("q", "k", "v")]
+        c = cs[ctx[b]:ctx[b] + new[b]]
+        for n in (0, 1):
+            y = x[n].clone()
+            i = torch.arange(rot // 2, device=dev)
+            lo, hi = (2 * i, 2 * i + 1) if case["inter"] else (i, i + rot // 2)
+            y[..., lo] = x[n][..., lo] * c[:, None, 0] - x[n][..., hi] * c[:, None, 1]
+            y[..., hi] = x[n][..., lo] * c[:, None, 1] + x[n][..., hi] * c[:, None, 0]
+            x[n] = y
+        qs.append(x[0])
+        ks.append(x[1])
+        t0 += new[b]
+        end = ctx[b] + new[b]
+        for p0 in range(ctx[b] // BLOCK * BLOCK, end, BLOCK):
+            lo, hi = max(p0, ctx[b]), min(p0 + BLOCK, end)
+            pg, s0 = int(table[b, p0 // page]), p0 % page
+            for n in (0, 1):
+                part = x[1 + n][lo - ctx[b]:hi - ctx[b]].transpose(0, 1)      # [Hk, tokens, D]
+                m, e = torch.frexp(part.abs().amax((1, 2)))
+                code = torch.where(m > 0, torch.where(m <= 0.875, e - 9, e - 8) + 127, 0)
+                if lo > p0:
+                    was = torch.tensor(exps[n][pg, :, s0 // BLOCK], device=dev)
+                    code = torch.maximum(code, was)
+                    held = val[n][pg, :, s0:s0 + lo - p0]
+                    val[n][pg, :, s0:s0 + lo - p0] = _round_e4m3(held * torch.exp2((was - code).double())[:, None, None])
+                val[n][pg, :, s0 + lo - p0:s0 + hi - p0] = _round_e4m3(part / torch.exp2((code - 127).double())[:, None, None])
+    out = dict(q=torch.cat(qs), k_cache=val[0], v_cache=val[1], k_scale=None, v_scale=None)
+    if case["k_out"]:
+        out["k"] = torch.cat(ks)
+    return out
+
+
+def _exact_rows(q, k, v, first, group):
+    """q [n, Hq, D] over k, v [m, Hk, D]; query i sees the keys below first + i (all 64 bits)."""
+    n, hq, d = q.shape
+    o = torch.zeros(n, hq, d, dtype=torch.float64, device=q.device)
+    lse = torch.full((n, hq), -math.inf, dtype=torch.float64, device=q.device)
+    m = k.shape[0]
+    if m == 0:
+        return o, lse
+    step = max(1, 60_000_000 // m)
+    see = (first + torch.arange(n, device=q.device)).clamp(0, m)
+    for h in range(hq):
+        kh, vh = k[:, h // group].double(), v[:, h // group].double()
+        for i in range(0, n, step):
+            sc = q[i:i + step, h].double() @ kh.T / math.sqrt(d)
+            gone = torch.arange(m, device=q.device)[None, :] >= see[i:i + step, None]
+            sc[gone] = -math.inf
+            some = see[i:i + step] > 0
+            lse[i:i + step, h] = torch.logsumexp(sc, -1)
+            o[i:i + step, h] = torch.where(some[:, None], torch.softmax(sc, -1).nan_to_num(0.0) @ vh, 0.0)
+    return o, lse
+
+
+def _exact_decode(case, s):
+    hk, d, page, qn = case["hk"], case["d"], case["page"], case["qn"]
+    if case["B"] * case["hq"] > 5000:
+        return None
+    lut = _decode_e4m3(s["q"].device)
+    outs = []
+    for b, n in enumerate(_decode_lens(case)):
+        pg = s["table"][b, : -(-n // page)].long()
+
+        def tokens(codes, scale):
+            x = lut[codes[pg].long()] * torch.exp2(scale[pg].double() - 127).repeat_interleave(BLOCK, -1)[..., None]
+            return x.transpose(1, 2).reshape(-1, hk, d)[:n]
+
+        q = s["q"][b * qn:(b + 1) * qn]
+        outs.append(_exact_rows(q, tokens(s["k_cache"], s["k_scale"]), tokens(s["v_cache"], s["v_scale"]), n - qn + 1, case["hq"] // hk))
+    return dict(out=torch.cat([o for o, _ in outs]), lse=torch.cat([x for _, x in outs]))
+
+
+def _exact_prompt(case, s):
+    ql, kl = _prompt_lens(case)
+    outs, iq, ik = [], 0, 0
+    for a, b in zip(ql, kl):
+        first = b - a + 1 if case["causal"] else b
+        q, k, v = s["q"][iq:iq + a], s["k"][ik:ik + b], s["v"][ik:ik + b]
+        outs.append(_exact_rows(q, k, v, first, case["hq"] // case["hk"]))
+        iq, ik = iq + a, ik + b
+    return dict(out=torch.cat([o for o, _ in outs]), lse=torch.cat([x for _, x in outs]))
