@@ -161,10 +161,13 @@ def _stale(pages, case, gen, dev):
     return codes[0], codes[1], scales[0], scales[1]
 
 
-def _plan(case, rotary=None, inter=False):
-    from fp8_scaled_gemm_sm_gb300 import PagedAttention
+def _plan(s, rotary=None, inter=False):
+    from fp8_scaled_gemm_sm_gb300 import KVCache, PagedAttention
 
-    return PagedAttention(case["hq"], case["hk"], case["d"], page_size=case.get("page", 64), rotary=rotary, interleaved=inter)
+    case = s["case"]
+    s["plan"] = PagedAttention(case["hq"], case["hk"], case["d"], page_size=case.get("page", 64), rotary=rotary, interleaved=inter)
+    if "k_cache" in s:
+        s["cache"] = KVCache(s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"])
 
 
 def prepare(case, seed):
@@ -181,7 +184,7 @@ def prepare(case, seed):
         s["ctx"] = torch.tensor(ctx, dtype=torch.int32, device=dev)
         s["rotary"] = _rotary(max(a + b for a, b in zip(new, ctx)), case["rot"], dev)
         if own:
-            s["plan"] = _plan(case, s["rotary"], case["inter"])
+            _plan(s, s["rotary"], case["inter"])
     elif case["op"] == "decode":
         lens = _decode_lens(case)
         s["table"], pages = _table(lens, case["page"], gen, dev)
@@ -209,7 +212,7 @@ def prepare(case, seed):
         s["q"] = x.to(torch.bfloat16)
         s["lens"] = torch.tensor(lens, dtype=torch.int32, device=dev)
         if own:
-            s["plan"] = _plan(case)
+            _plan(s)
     else:
         ql, kl = _prompt_lens(case)
         if ql == kl:
@@ -220,7 +223,7 @@ def prepare(case, seed):
         s["cu_q"], s["cu_k"] = _cum(ql, dev), _cum(kl, dev)
         s["max_q"], s["max_k"] = max(ql), max(kl)
         if own:
-            s["plan"] = _plan(case)
+            _plan(s)
     return s
 
 
@@ -232,12 +235,10 @@ def run(s):
     if not own:
         return {"append": _plain_append, "decode": _plain_decode, "prompt": _plain_prompt}[op](s)
     if op == "append":
-        q, k = s["plan"].append(s["q"], s["k"], s["v"], (s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"]), s["table"],
-                                s["ctx"], s["cu"], k_out=s["case"]["k_out"])
+        q, k = s["plan"].append(s["q"], s["k"], s["v"], s["cache"], s["table"], s["ctx"], s["cu"], k_out=s["case"]["k_out"])
         return _append_out(s, q, k)
     if op == "decode":
-        out, lse = s["plan"].decode(s["q"], (s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"]), s["table"], s["lens"],
-                                    q_tokens=s["case"]["qn"])
+        out, lse = s["plan"].decode(s["q"], s["cache"], s["table"], s["lens"], q_tokens=s["case"]["qn"])
         return dict(out=out, lse=lse)
     out, lse = s["plan"].prompt(s["q"], s["k"], s["v"], s["cu_q"], s["cu_k"], causal=s["case"]["causal"])
     return dict(out=out, lse=lse)
