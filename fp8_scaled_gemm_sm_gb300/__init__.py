@@ -8,5 +8,18 @@ kernels in ``libscaledgemm.so`` (C ABI: ``include/scaled_gemm.h``).
 it for torch CUDA tensors.  There is no fallback: if the library is missing or
 the device is not sm_103, calls raise.  Importing the package loads nothing;
 the library is loaded by the first call.
+
+``PagedAttention`` is the attention between two such GEMMs: rotary positions and
+append to a paged 8-bit key/value cache, attention of the newest tokens over it,
+and attention over whole prompts (``include/scaled_attention.h``).
 """
 from .binding import MODES, ScaledGemm, ScaledGemmError  # noqa: F401
+
+
+def __getattr__(name):
+    # the attention layer imports torch, so it is loaded when first asked for
+    if name in ("KVCache", "PagedAttention", "rotary_table"):
+        from . import attention
+
+        return getattr(attention, name)
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -22,10 +22,29 @@ STATUS = {
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libscaledgemm.so")
 
-# Exported symbols and their signatures (the declarations of include/scaled_gemm.h).
+# Exported symbols and their signatures (the declarations of include/scaled_gemm.h
+# and include/scaled_attention.h).
 _i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
 _int = ctypes.c_int
+_f32 = ctypes.c_float
+
+
+class KvCacheArgs(ctypes.Structure):
+    """sg_kv_cache_t"""
+
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("num_pages", _i64), ("k_page_stride", _i64),
+                ("v_page_stride", _i64)]
+
+
+class RotaryArgs(ctypes.Structure):
+    """sg_rotary_t"""
+
+    _fields_ = [("table", _vp), ("max_pos", _i64), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+_cache_p = ctypes.POINTER(KvCacheArgs)
+_rotary_p = ctypes.POINTER(RotaryArgs)
 SIGNATURES = {
     "scaled_gemm_create": (_int, [ctypes.POINTER(_vp), _int, _i64, _i64, _i64, _int]),
     "scaled_gemm_launch": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
@@ -38,6 +57,13 @@ SIGNATURES = {
     "scaled_gemm_set_debug": (_int, [_vp, _i64, _i64]),
     "scaled_gemm_launch_noalloc": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp]),
     "scaled_gemm_quantize": (_int, [_int, _int, _vp, _i64, _i64, _vp, _vp, _vp]),
+    "scaled_attn_create": (_int, [ctypes.POINTER(_vp), _i64, _i64, _i64, _i64, _int]),
+    "scaled_attn_destroy": (_int, [_vp]),
+    "scaled_attn_append": (_int, [_vp, _cache_p, _rotary_p, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64,
+                                  _vp, _vp, _vp]),
+    "scaled_attn_decode": (_int, [_vp, _cache_p, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _f32, _vp, _vp, _vp]),
+    "scaled_attn_prompt": (_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _int, _f32, _vp, _vp, _vp]),
+    "scaled_attn_debug_status": (_int, [_vp, _vp, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]),
 }
 DTYPES = {"bf16": 0, "f32": 1}
 
@@ -162,6 +188,40 @@ def scaled_gemm_set_tile(h, bn=0):
 
 def scaled_gemm_set_debug(h, timeout_ns=0, skip_kstep=-1):
     _check(lib().scaled_gemm_set_debug(h, int(timeout_ns), int(skip_kstep)), "scaled_gemm_set_debug")
+
+
+def scaled_attn_create(Hq, Hk, D, page, device=-1):
+    h = _vp()
+    _check(lib().scaled_attn_create(ctypes.byref(h), int(Hq), int(Hk), int(D), int(page), int(device)), "scaled_attn_create")
+    return h.value
+
+
+def scaled_attn_destroy(h):
+    _check(lib().scaled_attn_destroy(h), "scaled_attn_destroy")
+
+
+def scaled_attn_append(h, cache, rotary, q, q_stride, k, k_stride, v, v_stride, table, table_stride, ctx_lens, cu_seqlens,
+                       T, B, q_out, k_out, stream=0):
+    """Rotate q and k, append k and v to the cache (see include/scaled_attention.h); cache is a
+    KvCacheArgs, rotary a RotaryArgs."""
+    _check(lib().scaled_attn_append(h, cache, rotary, q, q_stride, k, k_stride, v, v_stride, table, table_stride, ctx_lens,
+                                    cu_seqlens, T, B, q_out, k_out, stream), "scaled_attn_append")
+
+
+def scaled_attn_decode(h, cache, q, q_stride, qn, table, table_stride, kv_lens, B, scale, out, lse, stream=0):
+    _check(lib().scaled_attn_decode(h, cache, q, q_stride, qn, table, table_stride, kv_lens, B, scale, out, lse, stream),
+           "scaled_attn_decode")
+
+
+def scaled_attn_prompt(h, q, q_stride, k, k_stride, v, v_stride, cu_q, cu_k, Tq, Tk, B, causal, scale, out, lse, stream=0):
+    _check(lib().scaled_attn_prompt(h, q, q_stride, k, k_stride, v, v_stride, cu_q, cu_k, Tq, Tk, B, causal, scale, out, lse,
+                                    stream), "scaled_attn_prompt")
+
+
+def scaled_attn_debug_status(h, stream=0):
+    code, where = ctypes.c_int32(), ctypes.c_int32()
+    _check(lib().scaled_attn_debug_status(h, stream or None, ctypes.byref(code), ctypes.byref(where)), "scaled_attn_debug_status")
+    return code.value, where.value
 
 
 class ScaledGemm:

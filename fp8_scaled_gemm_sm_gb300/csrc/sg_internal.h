@@ -72,6 +72,14 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, ui
                uint64_t outer, uint64_t row_pitch_bytes, uint32_t box_inner, uint32_t box_outer,
                CUtensorMapSwizzle swizzle);
 
+// Same for a 3D tensor (dims and strides innermost first; strides in bytes of
+// dims 1 and 2).
+bool encode_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t dims[3],
+               const uint64_t strides[2], const uint32_t box[3], CUtensorMapSwizzle swizzle);
+
+// Log a refused call under SG_DEBUG and hand its status back.
+sg_status_t refuse(sg_status_t s, const char* what);
+
 // Remember a CUDA error from a kernel launch for SG_DEBUG reporting (per thread).
 void note_cuda_error(cudaError_t e);
 const char* last_cuda_error();
