@@ -1,5 +1,6 @@
 // scaled_attention.cu -- the C ABI of the attention operators: plans, argument
 // checks and dispatch (include/scaled_attention.h).
+#include <cmath>
 #include <new>
 
 #include <cuda.h>
@@ -229,6 +230,7 @@ sg_status_t scaled_attn_decode(sg_attn_t h, const sg_kv_cache_t* cache, const vo
   const sg::AttnShape& s = h->shape;
   if (B < 0 || qn < 0) return refuse(SG_ERR_INVALID_ARG, "decode: negative size");
   if (B > (1 << 24) || qn > 4096 || B * qn > kMaxDim) return refuse(SG_ERR_UNSUPPORTED_SHAPE, "decode: B > 2^24 or qn > 4096");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return refuse(SG_ERR_INVALID_ARG, "decode: scale");
   if (B == 0 || qn == 0) return SG_OK;
   SG_TRY(check_cache(h, cache));
   SG_TRY(check_rows(q, q_stride, s.Hq, s.D, "decode: q"));
@@ -266,6 +268,7 @@ sg_status_t scaled_attn_prompt(sg_attn_t h, const void* q, int64_t q_stride, con
   const sg::AttnShape& s = h->shape;
   if (Tq < 0 || Tk < 0 || B < 0) return refuse(SG_ERR_INVALID_ARG, "prompt: negative size");
   if (Tq > kMaxDim || Tk > kMaxDim || B > (1 << 24)) return refuse(SG_ERR_UNSUPPORTED_SHAPE, "prompt: T >= 2^31 or B > 2^24");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return refuse(SG_ERR_INVALID_ARG, "prompt: scale");
   if (Tq == 0 || B == 0) return SG_OK;
   SG_TRY(check_rows(q, q_stride, s.Hq, s.D, "prompt: q"));
   if (Tk > 0) {

@@ -607,6 +607,9 @@ def test_refusals():
         (1, lambda: plan.decode(q, cache, table, n3, out=q)),                  # overlap
         (1, lambda: plan.prompt(q, kv, kv, n4, out=q)),
         (1, lambda: plan.append(q, kv, kv, cache, table, n3, n4, k_out=kv)),   # k_out is v too
+        (1, lambda: plan.decode(q, cache, table, n3, scale=0.0)),
+        (1, lambda: plan.prompt(q, kv, kv, n4, scale=-1.0)),
+        (1, lambda: plan.prompt(q, kv, kv, n4, scale=float("inf"))),
         (2, lambda: pkg.PagedAttention(4, 2, 64, 48)),
         (2, lambda: pkg.PagedAttention(4, 3, 64, 32)),
         (2, lambda: pkg.PagedAttention(4, 2, 144, 32)),
