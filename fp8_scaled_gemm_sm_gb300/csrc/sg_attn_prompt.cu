@@ -2,108 +2,437 @@
 //
 // For query row i of a sequence with n queries and m keys, over the keys
 // j <= i + m - n (causal) or all m,
-//     s_j = scale q_i . k_j,   o_i = sum_j e^(s_j - mx) v_j / sum_j e^(s_j - mx),
-// in one pass with a running maximum and sum.  One warp per row and head; a lane
-// owns 4 dimensions.
+//     s_j = scale q_i . k_j,   o_i = sum_j 2^(c s_j - r) v_j / sum_j 2^(c s_j - r),   c = log2 e,
+// in one pass over tiles of 128 keys.  r is a reference that follows the running
+// maximum: any r gives the same quotient, so it is moved only when the maximum has
+// passed it by more than 2^8 (weights up to 2^8 lose nothing in fp32 or bf16), which
+// makes rescaling the output rare.
+//
+// Rows are packed: a tile's 128 rows are 128 / G tokens times G query heads of one
+// key/value head (G the largest power of two in the group), so grouped heads share
+// each K and V tile, the causal edge wastes less, and short prompts fill rows.
+// A CTA owns two such row tiles and runs them in opposition: while the tensor
+// cores work for one, the other's softmax runs.  Per CTA:
+//   warps 0-3, 4-7  softmax of tile 0 / 1, one thread a row: S from tensor memory to
+//                   registers, maximum, 2^x, row sum, P = bf16 back over S's columns; at the end
+//                   the output row, divided by the sum, straight to memory.
+//   warp 8          TMA producer: both Q tiles once, then K_0, V_0, K_1, V_1, ... through a ring.
+//   warp 9          MMA issuer: S_t = Q_t K_j^T (operands in shared memory), O_t += P_t V_j (P in
+//                   tensor memory, V as it lies in memory: N-major).
+// The tensor cores take the MMAs in order, so S_t of block j + 1, issued after
+// O_t += P_t V_j, cannot overwrite P_t early, and a softmax thread that sees it
+// complete may also touch O_t.
+// P is rounded to bf16 (V is bf16, and an MMA has one operand type): an error of at most 2^-9 of each weight,
+// against the 2^-9 of the rounded output; the row sums take the unrounded weights.
+//
+// V rows past a sequence's end belong to the next one: those that share a 16-key
+// MMA step with valid ones are zeroed in shared memory, the rest are not multiplied.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "sg_attn.h"
-#include "sg_ptx.cuh"
+#include "sg_attn_ptx.cuh"
 
 namespace sg {
 
 namespace {
 
+constexpr int kRows = 128;   // rows of a tile, keys of a block
+constexpr int kThreads = 384;
+// Registers a thread of the softmax warpgroups and of the third (producer, MMA issuer, two
+// idle warps): 2 x 216 + 72 = 3 x 168, what the block is launched with.
+constexpr int kSoftmaxRegs = 216, kIssueRegs = 72;
+constexpr float kSlack = 8.f;  // log2 of the largest weight
+
 struct PromptParams {
-  const uint16_t *q, *k, *v;
-  int64_t q_stride, k_stride, v_stride;
   const int32_t *cu_q, *cu_k;
-  int Tq, Tk, B, Hq, Hk, D, causal;
+  int Tq, Tk, B, Hq, D, causal;
+  int group;            // query heads of a key/value head
+  int gshift;           // log2 of the query heads packed into a tile
+  int head_groups;      // Hq >> gshift
+  int units;
   float scale_log2;
   uint16_t* out;
   float* lse;
+  int* status;
+  uint64_t timeout_ns;
 };
 
-__device__ __forceinline__ void load4(const uint16_t* x, float (&f)[4]) {
-  const uint2 w = *reinterpret_cast<const uint2*>(x);
-  f[0] = __uint_as_float(w.x << 16);
-  f[1] = __uint_as_float(w.x & 0xFFFF0000u);
-  f[2] = __uint_as_float(w.y << 16);
-  f[3] = __uint_as_float(w.y & 0xFFFF0000u);
-}
+template <int HD>
+struct PromptLayout {
+  static constexpr int kBoxes = HD / 64;                  // 64-column (128-byte) boxes of a row
+  static constexpr int kBox = kRows * 128;                // bytes of a box
+  static constexpr int kTile = kBoxes * kBox;             // a Q, K or V tile
+  static constexpr int kStages = HD == 128 ? 5 : 8;
+  static constexpr int kOffKv = 2 * kTile;
+  static constexpr int kOffBar = kOffKv + kStages * kTile;
+  static constexpr int kNumBars = 2 * kStages + 8;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kBytes = kOffMisc + 64;
+  static constexpr int kDynSmem = kBytes + 1024;
+  static_assert(kDynSmem <= 232448, "shared memory");
+};
 
-__global__ void __launch_bounds__(128) prompt_rows_kernel(const PromptParams p) {
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const PromptParams p) {
+  using L = PromptLayout<HD>;
+  constexpr int S = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sQ = smem_addr(smem), sKv = smem_addr(smem + L::kOffKv), bar0 = smem_addr(smem + L::kOffBar);
+  auto kv_full = [&](int s) { return bar0 + 8 * s; };
+  auto kv_empty = [&](int s) { return bar0 + 8 * (S + s); };
+  auto s_full = [&](int t) { return bar0 + 8 * (2 * S + t); };
+  auto p_full = [&](int t) { return bar0 + 8 * (2 * S + 2 + t); };
+  auto o_full = [&](int t) { return bar0 + 8 * (2 * S + 4 + t); };
+  const uint32_t q_full = bar0 + 8 * (2 * S + 6), drain_bar = bar0 + 8 * (2 * S + 7);
+  int* misc = reinterpret_cast<int*>(smem + L::kOffMisc);  // [0] TMEM base, [1] abort, [2..13] counts
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
   grid_dep_launch();
   grid_dep_wait();
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (item >= static_cast<int64_t>(p.Tq) * p.Hq) return;
-  const int row = static_cast<int>(item / p.Hq), h = static_cast<int>(item % p.Hq), hk = h / (p.Hq / p.Hk);
-  int b = 0;
-  for (int i = lane; i < p.B; i += 32) b += p.cu_q[i + 1] <= row;
-  b = __reduce_add_sync(0xffffffffu, b);
-  const bool live = 4 * lane < p.D;
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  if (b < p.B) {
-    const int q0 = min(max(p.cu_q[b], 0), p.Tq), q1 = min(max(p.cu_q[b + 1], 0), p.Tq);
-    const int k0 = min(max(p.cu_k[b], 0), p.Tk), k1 = min(max(p.cu_k[b + 1], k0), p.Tk);
-    const int see = p.causal ? min(k1 - k0, row - q0 + 1 + (k1 - k0) - (q1 - q0)) : k1 - k0;
-    float q[4] = {0.f, 0.f, 0.f, 0.f};
-    if (live) load4(p.q + row * p.q_stride + h * p.D + 4 * lane, q);
-    for (int j = 0; j < see; ++j) {
-      float k[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (live) {
-        load4(p.k + (k0 + j) * p.k_stride + hk * p.D + 4 * lane, k);
-        load4(p.v + (k0 + j) * p.v_stride + hk * p.D + 4 * lane, v);
+  // Units of 2 row tiles are numbered from cu_q[b] / tokens + b for sequence b (at most
+  // n / tokens + 1 of them), heads fastest, the last (for causal prompts: the
+  // longest) rows first.
+  const int tile_tokens = kRows >> p.gshift;
+  const int unit = p.units - 1 - static_cast<int>(blockIdx.x) / p.head_groups;
+  const int head0 = static_cast<int>(blockIdx.x) % p.head_groups << p.gshift;
+  auto clampq = [&](int i) { return min(max(__ldg(p.cu_q + i), 0), p.Tq); };
+  int below = 0;
+  for (int i = tid; i < p.B; i += kThreads) below += clampq(i) / (2 * tile_tokens) + i <= unit;
+  below = __reduce_add_sync(0xffffffffu, below);
+  if (lane == 0) misc[2 + warp] = below;
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(kv_full(s), 1);
+      mbar_init(kv_empty(s), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(s_full(t), 1);
+      mbar_init(p_full(t), kRows);
+      mbar_init(o_full(t), 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(drain_bar, 1);
+    misc[1] = 0;
+    fence_mbarrier_init();
+  }
+  __syncthreads();
+  int b = -1;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) b += misc[2 + w];
+  if (b < 0) return;
+  const int q0 = clampq(b), lq = clampq(b + 1) - q0;
+  const int k0 = min(max(__ldg(p.cu_k + b), 0), p.Tk), lk = min(max(__ldg(p.cu_k + b + 1), k0), p.Tk) - k0;
+  const int tok0 = (unit - (q0 / (2 * tile_tokens) + b)) * 2 * tile_tokens;
+  if (tok0 >= lq) return;
+  auto visible = [&](int tok) { return p.causal ? min(lk, tok + 1 + lk - lq) : lk; };
+  int blocks[2], kmax[2];  // key blocks of a tile, keys that its last row sees
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int first = tok0 + t * tile_tokens;
+    kmax[t] = first < lq ? max(visible(min(first + tile_tokens, lq) - 1), 0) : 0;
+    blocks[t] = (kmax[t] + kRows - 1) / kRows;
+  }
+  const int num_blocks = max(blocks[0], blocks[1]);
+  if (warp == 9) {
+    tmem_alloc(smem_addr(&misc[0]), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+  const Watchdog wd{p.status, p.timeout_ns, reinterpret_cast<volatile int*>(&misc[1])};
+
+  if (warp >= 8) {
+    reg_dec<kIssueRegs>();
+    if (warp == 8) {
+      // ---------------- TMA producer ----------------
+      if (lane == 0 && num_blocks > 0) {
+        const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
+        const int tiles = tok0 + tile_tokens < lq ? 2 : 1;
+        mbar_arrive_expect_tx(q_full, tiles * L::kTile);
+        for (int t = 0; t < tiles; ++t)
+          for (int x = 0; x < L::kBoxes; ++x)
+            tma_load_3d_hint(sQ + t * L::kTile + x * L::kBox, &tmQ, x * 64, head0, q0 + tok0 + t * tile_tokens, q_full, once);
+        const int kv_head = head0 / p.group;
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, last_par = 0;
+        bool ok = true;
+        for (int i = 0; i < 2 * num_blocks; ++i) {
+          if (!mbar_wait(kv_empty(stage), phase ^ 1, wd, kWhereProducerEmpty)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(kv_full(stage), L::kTile);
+          for (int x = 0; x < L::kBoxes; ++x)
+            tma_load_3d_hint(sKv + stage * L::kTile + x * L::kBox, (i & 1) ? &tmV : &tmK, x * 64, kv_head,
+                             k0 + (i >> 1) * kRows, kv_full(stage), keep);
+          issued |= 1u << stage;
+          last_par = (last_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) {  // loads in flight must land before the CTA can exit
+          mbar_wait_drain(q_full, 0, 200000000ull);
+          for (int s = 0; s < S; ++s)
+            if ((issued >> s) & 1) mbar_wait_drain(kv_full(s), (last_par >> s) & 1, 200000000ull);
+        }
       }
-      float s = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
+    } else if (warp == 9) {
+      // ---------------- MMA issuer (one lane issues) ----------------
+      if (num_blocks > 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        auto advance = [&]() {
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
+        };
+        auto scores = [&](int t, int j, int st) {  // S_t = Q_t K_j^T
+          const int n = (min(kRows, kmax[t] - j * kRows) + 15) & ~15;
+          const uint32_t idesc = instr_desc(1, 1, kRows, n);
+          const uint64_t a = kmajor_sw128_desc(sQ + t * L::kTile), k = kmajor_sw128_desc(sKv + st * L::kTile);
+  #pragma unroll
+          for (int i = 0; i < HD / 16; ++i) {
+            const uint32_t at = (i / 4) * L::kBox + (i % 4) * 32;
+            mma_f16_ss(tmem + t * 128, desc_advance(a, at), desc_advance(k, at), idesc, i != 0);
+          }
+          mma_commit(s_full(t));
+        };
+        bool ok = mbar_wait(q_full, 0, wd, kWhereMmaFull) && mbar_wait(kv_full(0), 0, wd, kWhereMmaFull);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          tc_fence_after();
+          if (lane == 0) {
+            if (blocks[0] > 0) scores(0, 0, 0);
+            if (blocks[1] > 0) scores(1, 0, 0);
+            mma_commit(kv_empty(0));
+          }
+          advance();
+        }
+        for (int j = 0; j < num_blocks && ok; ++j) {
+          ok = __all_sync(0xffffffffu, mbar_wait(kv_full(stage), phase, wd, kWhereMmaFull));
+          if (!ok) break;
+          const int vs = stage;
+          advance();
+          const int left = lk - j * kRows;  // V rows of this sequence
+          if (left < kRows && (left & 15)) {
+            const int rows = 16 - (left & 15);
+            for (int i = lane; i < rows * 8 * L::kBoxes; i += 32)
+              st_shared_v4(sKv + vs * L::kTile + (i / (rows * 8)) * L::kBox + left * 128 + (i % (rows * 8)) * 16, 0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          bool k_ready = false;
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (j >= blocks[t]) continue;
+            ok = __all_sync(0xffffffffu, mbar_wait(p_full(t), j & 1, wd, kWhereMmaTmemEmpty));
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t idesc = instr_desc(1, 1, kRows, HD) | kIdescBMajorN;
+              const uint64_t v = smem_desc(sKv + vs * L::kTile, L::kBox, 1024, 2);
+              const int steps = (min(kRows, kmax[t] - j * kRows) + 15) / 16;
+              for (int i = 0; i < steps; ++i)
+                mma_f16_ts(tmem + 256 + t * HD, tmem + t * 128 + i * 8, desc_advance(v, i * 2048), idesc, (j | i) != 0);
+              if (j + 1 == blocks[t]) mma_commit(o_full(t));
+            }
+            if (j + 1 < blocks[t]) {
+              if (!k_ready) {
+                ok = __all_sync(0xffffffffu, mbar_wait(kv_full(stage), phase, wd, kWhereMmaFull));
+                if (!ok) break;
+                tc_fence_after();
+                k_ready = true;
+              }
+              if (lane == 0) scores(t, j + 1, stage);
+            }
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            mma_commit(kv_empty(vs));
+            if (k_ready) mma_commit(kv_empty(stage));
+          }
+          if (k_ready) advance();
+        }
+        // every MMA has finished and every commit has landed before the CTA exits
+        if (lane == 0) {
+          mma_commit(drain_bar);
+          mbar_wait_drain(drain_bar, 0, 200000000ull);
+        }
+      }
+    }
+  } else {
+    reg_inc<kSoftmaxRegs>();
+    // ---------------- softmax and output ----------------
+    const int t = warp >> 2, quarter = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_addr = tmem + lanes + t * 128, o_addr = tmem + lanes + 256 + t * HD;
+    const int row = quarter * 32 + lane;
+    const int tok = tok0 + t * tile_tokens + (row >> p.gshift);
+    const int head = head0 + (row & ((1 << p.gshift) - 1));
+    const int lim = visible(tok);
+    const int lim_warp = visible(tok0 + t * tile_tokens + (quarter * 32 >> p.gshift));  // least of the warp's
+    const int n = blocks[t];
+    const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
+    float ref = -INFINITY;     // r, in log2 units
+    uint64_t sum2 = 0;         // two partial row sums
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      ok = __all_sync(0xffffffffu, mbar_wait(s_full(t), j & 1, wd, kWhereEpiTmemFull));
+      if (!ok) break;
+      tc_fence_after();
+      const int chunks = (min(kRows, kmax[t] - j * kRows) + 31) / 32;
+      uint32_t s[4][32];
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      s *= p.scale_log2;
-      const float mn = fmaxf(m, s);
-      const float keep = mn == -INFINITY ? 1.f : exp2f(m - mn), w = mn == -INFINITY ? 0.f : exp2f(s - mn);
-      l = l * keep + w;
+      for (int c = 0; c < 4; ++c)
+        if (c < chunks) tmem_ld_32x32b_x32(s_addr + 32 * c, s[c]);
+      tmem_wait_ld();
+      const int room = lim - j * kRows;
+      if (lim_warp - j * kRows < kRows) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = o[e] * keep + w * v[e];
-      m = mn;
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * c + i >= room) s[c][i] = 0xFF800000u;
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[c][i]));
+      mx *= p.scale_log2;
+      if (j == 0) {
+        ref = mx;
+      } else {
+        const bool move = mx > ref + kSlack;
+        if (__any_sync(0xffffffffu, move)) {
+          const float by = move ? ex2(ref - mx) : 1.f;
+          if (move) ref = mx;
+          const uint64_t by2 = pack_f32x2(by, by);
+          sum2 = mul_f32x2(sum2, by2);
+#pragma unroll
+          for (int c = 0; c < HD / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(o_addr + 32 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+            tmem_st_32x32b_x32(o_addr + 32 * c, o);
+          }
+        }
+      }
+      const float neg = ref == -INFINITY ? 0.f : -ref;
+      const uint64_t neg2 = pack_f32x2(neg, neg);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c < chunks) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float x, y;
+            unpack_f32x2(fma_f32x2(pack_f32x2(s[c][2 * i], s[c][2 * i + 1]), scale2, neg2), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            sum2 = add_f32x2(sum2, pack_f32x2(x, y));
+            w[i] = pack_bf16x2(x, y);
+          }
+          tmem_st_32x32b_x16(s_addr + 16 * c, w);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(p_full(t));
+    }
+    if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), 0, wd, kWhereEpiTmemFull));
+    if (ok) {
+      tc_fence_after();
+      float lo, hi;
+      unpack_f32x2(sum2, lo, hi);
+      const float sum = lo + hi;
+      const bool none = sum == 0.f;
+      const float inv = none ? 0.f : 1.f / sum;
+      const int64_t at = static_cast<int64_t>(q0 + tok) * p.Hq + head;
+#pragma unroll
+      for (int c = 0; c < HD / 32; ++c) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld_32x32b_x32(o_addr + 32 * c, o);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+        if (tok < lq) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (32 * c + 8 * i < p.D) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(o[8 * i + 2 * e + 1]));
+              *reinterpret_cast<uint4*>(p.out + at * p.D + 32 * c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+      }
+      if (tok < lq && p.lse) p.lse[at] = none ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
     }
   }
-  if (live) {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint2*>(p.out + item * p.D + 4 * lane) =
-        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
-  if (lane == 0 && p.lse) p.lse[item] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-}  // namespace
-
-cudaError_t prompt_prepare() { return cudaSuccess; }
-
-sg_status_t prompt_launch(const AttnShape& s, const AttnArgs& a) {
+template <int HD>
+sg_status_t launch(const AttnShape& s, const AttnArgs& a) {
   PromptParams p{};
-  p.q = static_cast<const uint16_t*>(a.q);
-  p.k = static_cast<const uint16_t*>(a.k);
-  p.v = static_cast<const uint16_t*>(a.v);
-  p.q_stride = a.q_stride;
-  p.k_stride = a.k_stride;
-  p.v_stride = a.v_stride;
   p.cu_q = a.cu_q;
   p.cu_k = a.cu_k;
   p.Tq = static_cast<int>(a.Tq);
   p.Tk = static_cast<int>(a.Tk);
   p.B = static_cast<int>(a.B);
   p.Hq = s.Hq;
-  p.Hk = s.Hk;
   p.D = s.D;
   p.causal = a.causal;
+  p.group = s.Hq / s.Hk;
+  while (p.gshift < 7 && p.group % (2 << p.gshift) == 0) ++p.gshift;
+  p.head_groups = s.Hq >> p.gshift;
+  const int64_t units = a.Tq / (2 * (kRows >> p.gshift)) + a.B;
+  if (units * p.head_groups >= (int64_t(1) << 31)) return SG_ERR_UNSUPPORTED_SHAPE;
+  p.units = static_cast<int>(units);
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.out = static_cast<uint16_t*>(a.out);
   p.lse = a.lse;
-  const int64_t rows = a.Tq * s.Hq;
-  GemmLaunch l(dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, a.stream, 1);
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, prompt_rows_kernel, p);
+  p.status = s.status;
+  p.timeout_ns = s.timeout_ns;
+  // q as [tokens][heads][D]; without keys nothing reads the other two maps
+  const bool keys = a.Tk > 0;
+  const uint64_t el = 2, D = s.D;
+  const uint64_t dq[3] = {D, static_cast<uint64_t>(s.Hq), static_cast<uint64_t>(a.Tq)};
+  const uint64_t dk[3] = {D, static_cast<uint64_t>(s.Hk), static_cast<uint64_t>(keys ? a.Tk : a.Tq)};
+  const uint64_t sq[2] = {D * el, static_cast<uint64_t>(a.q_stride) * el};
+  const uint64_t sk[2] = {D * el, static_cast<uint64_t>(keys ? a.k_stride : a.q_stride) * el};
+  const uint64_t sv[2] = {D * el, static_cast<uint64_t>(keys ? a.v_stride : a.q_stride) * el};
+  const uint32_t bq[3] = {64, 1u << p.gshift, static_cast<uint32_t>(kRows >> p.gshift)};
+  const uint32_t bk[3] = {64, 1, kRows};
+  CUtensorMap tmQ, tmK, tmV;
+  if (!encode_3d(&tmQ, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, dq, sq, bq, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_3d(&tmK, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, keys ? a.k : a.q, dk, sk, bk, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_3d(&tmV, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, keys ? a.v : a.q, dk, sv, bk, CU_TENSOR_MAP_SWIZZLE_128B))
+    return SG_ERR_CUDA;
+  GemmLaunch l(dim3(static_cast<unsigned>(units * p.head_groups)), dim3(kThreads), PromptLayout<HD>::kDynSmem, a.stream, 1);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, prompt_kernel<HD>, tmQ, tmK, tmV, p);
   if (e != cudaSuccess) {
     note_cuda_error(e);
     cudaGetLastError();
@@ -111,5 +440,16 @@ sg_status_t prompt_launch(const AttnShape& s, const AttnArgs& a) {
   }
   return SG_OK;
 }
+
+}  // namespace
+
+cudaError_t prompt_prepare() {
+  const cudaError_t e = cudaFuncSetAttribute(prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptLayout<64>::kDynSmem);
+  return e == cudaSuccess
+             ? cudaFuncSetAttribute(prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptLayout<128>::kDynSmem)
+             : e;
+}
+
+sg_status_t prompt_launch(const AttnShape& s, const AttnArgs& a) { return s.D > 64 ? launch<128>(s, a) : launch<64>(s, a); }
 
 }  // namespace sg
