@@ -9,26 +9,29 @@
 // output's weights 2^(s_j + b_j - n), the value scale inside, so that the
 // tensor cores multiply codes): o = 2^(n - m) sum_j 2^(s_j + b_j - n) V_j / sum_j 2^(s_j - m).
 //
-// The bound is memory: every code is read once, 2 D bytes a token and head, and a
-// code takes 4 G multiply-adds for G query rows of its head.  Codes become fp16
-// exactly (two a instruction), queries are scaled per row by a power of two and
-// are then exact in fp16, weights are rounded to fp16 (2^-11 of each), products
-// add up in fp32 in mma.sync m16n8k16 with up to 16 query rows of a key/value head as M: bf16
-// has no room for them to be the bound.  A warp keeps everything in registers:
-//   * the contraction order over dimensions is free, so a lane takes K as it
-//     lies: lane (n, c) holds 16-byte runs c (and c + 4) of key n's row, four dimensions a k-step;
-//   * the order of keys is free too: the keys whose weights the score tile leaves in a
-//     lane are the ones whose V rows it reads, 16 bytes each; interleaving pairs of rows by
-//     bytes gives the operand of one output tile per dimension.
+// The bound is memory: every code is read once, 2 D bytes a token and head.  What
+// competes with it is the arithmetic on codes, so a warp does as little of it as it can, in registers:
+//   * Products add up in fp32 in mma.sync with keys (or dimensions) as its M and the query rows of
+//     a key/value head, 8 a tile, as its N: groups of up to 8 rows leave nothing idle but unused columns.
+//     Codes become fp16 exactly (two a conversion); queries are scaled per row by a power of two and are then exact in
+//     fp16; weights are rounded to fp16 (2^-11 of each).  (mma.sync on e4m3 operands measured slower: it
+//     converts them too, and a query takes two terms.)
+//   * The contraction order over dimensions is free, so a lane takes K as it
+//     lies: lane (g, c) holds 16-byte runs c (and c + 4) of keys g and g + 8, four dimensions a k-step.
+//   * The order of keys is free too: an 8 x 8 transpose (movmatrix) leaves lane (g, c) the weights
+//     of row g and keys 2 c, 2 c + 1; it reads those keys' V rows, 16 bytes each, and
+//     interleaving pairs of rows by bytes gives the operand of two dimensions.
+//   * References move only when a maximum has passed them by 2^8, found by one vote a tile.
 // Rows lie in shared memory with the TMA swizzle; which key and run a lane takes
 // is chosen so that these reads have no bank conflicts.
 //
-// Work: all tiles of all (sequence, head) segments are numbered, every warp takes
-// the same number of consecutive ones (lengths are on the device; each CTA sums them up),
-// loaded into its own ring by TMA ahead of use, across segments.  A segment inside a warp's range is
-// finished there; a segment cut by ranges leaves partial sums, which a second kernel
-// joins in the order of the ranges, so results do not depend on timing.
+// Work: all tiles of all (sequence, head) segments are numbered, with an allowance for each
+// segment's own cost, and every warp takes an equal range of the numbers (lengths are on
+// the device; each CTA sums them up), loaded into its own ring by TMA ahead of use, across
+// segments.  Segments that are short beside a range are not cut; the parts of a cut one are joined
+// by a second kernel in the order of its ranges, so results do not depend on timing.
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "sg_attn.h"
@@ -39,17 +42,18 @@ namespace sg {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kKeys = 32;       // keys of a tile
-constexpr int kRowTile = 16;    // query rows of an MMA
 constexpr int kMinTiles = 2;    // least tiles of a warp's range
-constexpr float kSlack = 8.f;   // log2 of the largest output weight
+constexpr int kSegCost = 3;     // what a segment costs beside its tiles, in tiles
+constexpr int kUncut = 4;       // segments of up to 1 / kUncut of a range are not cut
+constexpr int kMaxWarps = 16;
+constexpr int kJoinWarps = 8;
+constexpr float kSlack = 8.f;   // log2 of the largest weight
 
-struct Segment {  // a segment cut by ranges: the range that starts it joins it
-  int32_t b, hr;        // sequence; head * row tiles + row tile; b < 0: none
-  int32_t last;         // the last range with a part of it
-  int32_t pad;
+// What the join kernel does for a segment (or range): ranges first .. last have parts of
+// segment (b, hr); last < 0: nothing.
+struct Cut {
+  int b, hr, first, last;
 };
 
 struct DecodeParams {
@@ -59,21 +63,25 @@ struct DecodeParams {
   int64_t table_stride;
   const uint8_t *k_scale, *v_scale;
   int64_t num_pages;
-  int B, qn, Hq, Hk, D, page, group, row_tiles;
+  int B, qn, Hq, Hk, D, page, page_shift, group, row_tiles;
   float scale_log2;
   uint16_t* out;
   float* lse;
-  float* part_o;      // [2 ranges][16][HD]
-  float4* part_ml;    // [2 ranges][16]: m, n, sum
-  Segment* cut;       // [ranges]
+  float* part_o;      // [2 ranges][rows][HD]: the part that begins a segment (odd), one that does not
+  float4* part_ml;    // [2 ranges][rows]: m, n, sum
+  Cut* cuts;          // by segment, or by range where there are fewer of those
+  int by_segment;
   int* status;
   uint64_t timeout_ns;
 };
 
-template <int HD>
+// NR: tiles of 8 query rows.
+template <int HD, int NR>
 struct DecodeLayout {
+  static constexpr int kWarps = HD == 128 ? (NR == 1 ? 12 : 8) : (NR == 1 ? 16 : 12);
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kTile = kKeys * HD;               // bytes of a K or V tile
-  static constexpr int kStages = HD == 128 ? 3 : 6;
+  static constexpr int kStages = 196608 / (2 * kTile * kWarps);
   static constexpr int kRing = 2 * kTile * kStages;      // a warp's ring
   static constexpr int kOffInfo = kWarps * kRing;        // uint2 per warp and stage
   static constexpr int kOffBar = kOffInfo + kWarps * kStages * 8;
@@ -81,7 +89,7 @@ struct DecodeLayout {
   static constexpr int kOffMisc = kOffSum + (kThreads + 1) * 8;
   static constexpr int kBytes = kOffMisc + 16 + 8 * kWarps;
   static constexpr int kDynSmem = kBytes + 1024;
-  static_assert(kDynSmem <= 232448, "shared memory");
+  static_assert(kDynSmem <= 232448 && kWarps <= kMaxWarps, "shared memory");
 };
 
 // Key row (of 8) that lane group n takes in a score tile.
@@ -108,11 +116,21 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
   return v;
 }
 
-// Two e4m3 codes (low 16 bits) as fp16.
-__device__ __forceinline__ uint32_t codes_f16x2(uint32_t two) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(two)));
-  return d;
+// Four e4m3 codes as two pairs of fp16.
+__device__ __forceinline__ void codes_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit elements, two a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -121,51 +139,78 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A position in the numbered tiles: tile t of the segment (b, hr), which has `tiles`.
-struct Cursor {
-  int b, hr, t, tiles, len;
+// a / b for a >= 0, b > 0, in 32 bits where they fit.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// Tiles [t, t1) of segment (b, hr), whose numbers start at `start`.
+struct Part {
+  int b, hr, t, t1, tiles, len;
+  int64_t start;
 };
 
+// The parts of a range [begin, end) of numbers: segment after segment, kSegCost
+// numbers and then one a tile; uncut segments belong to the range of their start.
 struct Walk {
   const DecodeParams& p;
   int segs;  // segments of a sequence
+  int64_t begin, end;
+  int uncut;
   __device__ __forceinline__ int len(int b) const {
     const int64_t cap = p.table_stride * p.page;  // below 2^31
     return static_cast<int>(min(static_cast<int64_t>(max(__ldg(p.lens + b), 0)), cap));
   }
-  __device__ __forceinline__ int tiles(int len) const { return (len + kKeys - 1) / kKeys; }
-  __device__ __forceinline__ void load(Cursor& c) const {  // skips empty sequences
-    while (c.b < p.B) {
-      c.len = len(c.b);
-      c.tiles = tiles(c.len);
-      if (c.tiles > 0) return;
-      ++c.b;
+  __device__ __forceinline__ static int tiles(int len) { return (len + kKeys - 1) / kKeys; }
+  __device__ __forceinline__ static int64_t numbers(int len) { return len > 0 ? tiles(len) + kSegCost : 0; }
+  // The first part at or after segment c; false: none.
+  __device__ __forceinline__ bool find(Part& c) const {
+    while (c.start < end) {
+      if (c.hr == segs) {
+        c.hr = 0;
+        do {
+          if (++c.b >= p.B) return false;
+          c.len = len(c.b);
+        } while (c.len == 0);
+        c.tiles = tiles(c.len);
+      }
+      if (c.tiles <= uncut) {
+        c.t = 0;
+        c.t1 = c.start >= begin ? c.tiles : 0;
+      } else {
+        const int64_t first = c.start + kSegCost;
+        c.t = static_cast<int>(max(begin - first, static_cast<int64_t>(0)));
+        c.t1 = static_cast<int>(min(end - first, static_cast<int64_t>(c.tiles)));
+      }
+      if (c.t < c.t1) return true;
+      c.start += c.tiles + kSegCost;
+      ++c.hr;
     }
+    return false;
   }
-  __device__ __forceinline__ void next(Cursor& c) const {
-    if (++c.t < c.tiles) return;
-    c.t = 0;
-    if (++c.hr < segs) return;
-    c.hr = 0;
-    ++c.b;
-    load(c);
+  __device__ __forceinline__ bool next(Part& c) const {
+    c.start += c.tiles + kSegCost;
+    ++c.hr;
+    return find(c);
   }
 };
 
-template <int HD>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int HD, int NR>
+__global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const DecodeParams p) {
-  using L = DecodeLayout<HD>;
-  constexpr int S = L::kStages;
+  using L = DecodeLayout<HD, NR>;
+  constexpr int S = L::kStages, kWarps = L::kWarps, kThreads = L::kThreads;
   constexpr int kRuns = HD / 64;        // 16-byte runs of a key row in a lane
-  constexpr int kOut = HD / 8;          // output tiles
+  constexpr int kOut = HD / 16;         // output tiles of 16 dimensions
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -174,20 +219,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t info = smem_addr(smem + L::kOffInfo) + warp * S * 8;
   const uint32_t bars = smem_addr(smem + L::kOffBar) + warp * S * 8;
   int64_t* sums = reinterpret_cast<int64_t*>(smem + L::kOffSum);
-  int* misc = reinterpret_cast<int*>(smem + L::kOffMisc);
+  int* misc = reinterpret_cast<int*>(smem + L::kOffMisc);  // [0] abort
   int64_t* warp_sums = reinterpret_cast<int64_t*>(smem + L::kOffMisc + 16);
   if (tid == 0) misc[0] = 0;
-  if (lane == 0)
+  if (lane == 0) {
     for (int s = 0; s < S; ++s) mbar_init(bars + 8 * s, 1);
-  if (tid == 0) fence_mbarrier_init();
+    fence_mbarrier_init();
+  }
   grid_dep_launch();
   grid_dep_wait();
 
-  // Tiles before each run of `per` sequences, and in all.
-  const Walk walk{p, p.Hk * p.row_tiles};
+  // Numbers before each run of `per` sequences, and in all.
+  Walk walk{p, p.Hk * p.row_tiles, 0, 0, 0};
   const int per = (p.B + kThreads - 1) / kThreads;
   int64_t mine = 0;
-  for (int i = tid * per; i < min((tid + 1) * per, p.B); ++i) mine += walk.tiles(walk.len(i));
+  for (int i = tid * per; i < min((tid + 1) * per, p.B); ++i) mine += walk.numbers(walk.len(i));
   int64_t scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -211,57 +257,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         reinterpret_cast<uint4*>(p.out + b * n * p.D)[i] = make_uint4(0, 0, 0, 0);
       if (p.lse)
         for (int64_t i = tid; i < n; i += kThreads) p.lse[b * n + i] = -INFINITY;
+      if (p.by_segment)
+        for (int i = tid; i < walk.segs; i += kThreads) p.cuts[b * walk.segs + i].last = -1;
     }
 
-  // this warp's range of tiles; neighbouring ranges on different SMs
-  const int ranges = gridDim.x * kWarps;
-  const int range = warp * gridDim.x + blockIdx.x;
-  const int64_t quota = max((total + ranges - 1) / ranges, static_cast<int64_t>(kMinTiles));
-  const int64_t begin = min(range * quota, total), end = min(begin + quota, total);
-  if (lane == 0) p.cut[range].b = -1;
-  if (begin >= end) return;
+  // As many ranges as there are warps, or as few as the least range allows; those few on as many SMs as there are.
+  const int64_t quota = max(quotient(total + gridDim.x * kWarps - 1, gridDim.x * kWarps), static_cast<int64_t>(kMinTiles + kSegCost));
+  const int warps = static_cast<int>(quotient(quotient(total + quota - 1, quota) + gridDim.x - 1, gridDim.x));
+  const int range = blockIdx.x * warps + warp;
+  walk.begin = warp < warps ? min(range * quota, total) : total;
+  walk.end = min(walk.begin + quota, total);
+  walk.uncut = static_cast<int>(min(quota / kUncut, static_cast<int64_t>(1 << 20)));
+  if (!p.by_segment && lane == 0 && warp < kWarps) p.cuts[blockIdx.x + gridDim.x * warp].last = -1;
+  if (walk.begin >= walk.end) return;
 
-  Cursor c{};  // the tile to compute
-  int64_t seg_begin;  // number of its segment's first tile
+  Part c{};  // the part to compute
   {
-    int lo = 0, hi = kThreads;  // the run of sequences: sums[lo] <= begin < sums[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (sums[mid] <= begin) lo = mid; else hi = mid;
-    }
-    int64_t at = sums[lo];
+    int lo = 0;  // the run of sequences: sums[lo] <= begin < sums[lo + 1]
+#pragma unroll 1
+    for (int i = lane; i < kThreads; i += 32) lo += sums[i + 1] <= walk.begin;
+    lo = __reduce_add_sync(0xffffffffu, lo);
+    c.start = sums[lo];
     c.b = lo * per;
     for (;;) {
       c.len = walk.len(c.b);
-      c.tiles = walk.tiles(c.len);
-      const int64_t n = static_cast<int64_t>(c.tiles) * walk.segs;
-      if (begin < at + n) break;
-      at += n;
+      const int64_t n = walk.numbers(c.len);
+      if (walk.begin < c.start + n * walk.segs) {
+        c.hr = static_cast<int>(quotient(walk.begin - c.start, n));
+        c.start += c.hr * n;
+        break;
+      }
+      c.start += n * walk.segs;
       ++c.b;
     }
-    const int64_t in = begin - at;
-    c.hr = static_cast<int>(in / c.tiles);
-    c.t = static_cast<int>(in % c.tiles);
-    seg_begin = begin - c.t;
+    c.tiles = walk.tiles(c.len);
   }
-  Cursor ahead = c;  // the tile to load
-  int64_t loaded = begin;
+  bool some = walk.find(c);
+  Part ahead = c;  // the part to load, its tile `ahead.t`
+  bool more = some;
   const Watchdog wd{p.status, p.timeout_ns, reinterpret_cast<volatile int*>(&misc[0])};
   const uint64_t policy = l2_policy_evict_first();
-  const int blocks_page = p.page / kKvBlock;
+  const int in_page = p.page - 1, block_shift = p.page_shift - 4;
+  int ahead_head = 0;  // key/value head of the part being loaded
 
-  // Pages and scales of 32 tiles of the segment being loaded, a tile a lane.
+  // Pages and scales of 32 tiles of the part being loaded, a tile a lane.
   int batch = -1;                    // its first tile; -1: none
   int page0 = -1, page1 = -1;
   uint32_t scales = 0;               // k block 0, k block 1, v block 0, v block 1
   auto refresh = [&]() {
     batch = ahead.t;
-    const int h = ahead.hr / p.row_tiles;
+    ahead_head = ahead.hr / p.row_tiles;
     const int key = (ahead.t + lane) * kKeys;
     const int32_t* row = p.table + ahead.b * p.table_stride;
     auto page_of = [&](int k) {
       if (k >= ahead.len) return -1;
-      const int pg = __ldg(row + k / p.page);
+      const int pg = __ldg(row + (k >> p.page_shift));
       return pg >= 0 && pg < p.num_pages ? pg : -1;
     };
     page0 = page_of(key);
@@ -271,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       const int pg = i ? page1 : page0;
       if (pg >= 0) {
-        const int64_t at = (static_cast<int64_t>(pg) * p.Hk + h) * blocks_page + (key + 16 * i) % p.page / kKvBlock;
+        const int64_t at = ((static_cast<int64_t>(pg) * p.Hk + ahead_head) << block_shift) + (((key + 16 * i) & in_page) >> 4);
         scales |= static_cast<uint32_t>(__ldg(p.k_scale + at)) << (8 * i) | static_cast<uint32_t>(__ldg(p.v_scale + at)) << (16 + 8 * i);
       }
     }
@@ -280,12 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (batch < 0 || ahead.t >= batch + 32) refresh();
     const int from = ahead.t - batch;
     const int pg0 = __shfl_sync(0xffffffffu, page0, from), pg1 = __shfl_sync(0xffffffffu, page1, from);
-    const uint32_t sc = __shfl_sync(0xffffffffu, scales, from);
     if (lane == 0) {
-      const uint32_t gone = (pg0 < 0 ? 1u : 0u) | (pg1 < 0 ? 2u : 0u);
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(info + 8 * stage), "r"(sc), "r"(gone) : "memory");
       const uint32_t bar = bars + 8 * stage, k = ring + 2 * stage * L::kTile, v = k + L::kTile;
-      const int row = ahead.hr / p.row_tiles * p.page + ahead.t * kKeys % p.page;
+      const int row = (ahead_head << p.page_shift) + (ahead.t * kKeys & in_page);
       mbar_arrive_expect_tx(bar, 2 * L::kTile);
       tma_load_3d_hint(k, &tmK, 0, row, pg0, bar, policy);
       tma_load_3d_hint(v, &tmV, 0, row, pg0, bar, policy);
@@ -294,48 +341,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_3d_hint(v + L::kTile / 2, &tmV, 0, row, pg1, bar, policy);
       }
     }
-    const int b = ahead.b, hr = ahead.hr;
-    walk.next(ahead);
-    if (ahead.b != b || ahead.hr != hr) batch = -1;
-    ++loaded;
+    const uint32_t sc = __shfl_sync(0xffffffffu, scales, from);
+    if (lane == 0) {
+      const uint32_t gone = (pg0 < 0 ? 1u : 0u) | (pg1 < 0 ? 2u : 0u);
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(info + 8 * stage), "r"(sc), "r"(gone) : "memory");
+    }
+    __syncwarp();
+    if (++ahead.t == ahead.t1) {
+      batch = -1;
+      more = walk.next(ahead);
+    }
   };
   int in_flight = 0;  // stages loaded and not yet consumed
-  for (int s = 0; s < S && loaded < end; ++s, ++in_flight) load(s);
+  for (int s = 0; s < S && more; ++s, ++in_flight) load(s);
 
-  const int n8 = lane >> 2, c4 = lane & 3;
-  const int kr = key_row<HD>(n8), kv0 = key_row<HD>(2 * c4), kv1 = key_row<HD>(2 * c4 + 1);
+  const int g8 = lane >> 2, c4 = lane & 3;
+  const int kr = key_row<HD>(g8), kv0 = key_row<HD>(2 * c4), kv1 = key_row<HD>(2 * c4 + 1);
+  const int run_d = HD == 128 ? 16 * kr : 8 * g8;  // first dimension of this lane's outputs
   int stage = 0;
   uint32_t phase = 0;
   bool ok = true;
-  int64_t tile = begin;
-  while (tile < end && ok) {
-    // ---- a segment, or the part of it in this range
+  while (some && ok) {
+    // ---- a segment, or the part of it in this range.  Row r of N is column r:
+    // operands take row g8, results rows 2 c4 and 2 c4 + 1.
     const int h = c.hr / p.row_tiles, rt = c.hr % p.row_tiles;
-    const int part_first = c.t;
-    const int part_tiles = static_cast<int>(min(static_cast<int64_t>(c.tiles - c.t), end - tile));
-    uint32_t qf[4 * kRuns][4];
-    float q_scale[2];
-    int lim[2];      // keys that rows n8 and n8 + 8 see
-    int64_t row_at[2];
+    uint32_t qf[NR][4 * kRuns][2];
+    float q_scale[NR][2];
+    int lim[NR][2];      // keys that rows 2 c4, 2 c4 + 1 see
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = rt * kRowTile + n8 + 8 * r;
+    for (int r = 0; r < NR; ++r) {
+      const int row = (rt * NR + r) * 8 + g8;
       const bool live = row < p.qn * p.group;
-      const int qi = live ? row / p.group : 0;
-      row_at[r] = live ? (static_cast<int64_t>(c.b) * p.qn + qi) * p.Hq + h * p.group + row % p.group : -1;
-      lim[r] = live ? c.len - (p.qn - 1 - qi) : 0;
+      const uint16_t* src = p.q + (static_cast<int64_t>(c.b) * p.qn + (live ? row / p.group : 0)) * p.q_stride +
+                            (h * p.group + row % p.group) * p.D;
       uint4 w[2 * kRuns];
       float top = 0.f;
 #pragma unroll
-      for (int u = 0; u < kRuns; ++u)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int d = 64 * u + 16 * c4 + 8 * i;
-          w[2 * u + i] = make_uint4(0, 0, 0, 0);
-          if (live && d < p.D)
-            w[2 * u + i] = *reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(c.b) * p.qn + qi) * p.q_stride +
-                                                           (h * p.group + row % p.group) * p.D + d);
-        }
+      for (int i = 0; i < 2 * kRuns; ++i) {
+        const int d = 64 * (i / 2) + 16 * c4 + 8 * (i % 2);
+        w[i] = live && d < p.D ? *reinterpret_cast<const uint4*>(src + d) : make_uint4(0, 0, 0, 0);
+      }
       auto lo = [](uint32_t x) { return __uint_as_float(x << 16); };
       auto hi = [](uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); };
 #pragma unroll
@@ -350,125 +395,160 @@ __global__ void __launch_bounds__(kThreads, 1)
       // fp16 down to 2^-38 of it
       const int field = min(268 - static_cast<int>(__float_as_uint(top) >> 23), 253);
       const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
-      q_scale[r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
+      const float down = top == INFINITY ? __uint_as_float(0x7FC00000u)  // such a row is NaN
+                                         : p.scale_log2 * __uint_as_float(static_cast<uint32_t>(254 - field) << 23);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        q_scale[r][e] = __shfl_sync(0xffffffffu, down, (2 * c4 + e) * 4);
+        const int mine_row = (rt * NR + r) * 8 + 2 * c4 + e;
+        lim[r][e] = mine_row < p.qn * p.group ? c.len - (p.qn - 1 - mine_row / p.group) : 0;
+      }
       // k-step 4 u + i: this lane's dimensions 64 u + 16 c + 4 i ..+3
 #pragma unroll
-      for (int u = 0; u < kRuns; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4& q4 = w[2 * u + i / 2];
-          const uint32_t x = (i & 1) ? q4.z : q4.x, y = (i & 1) ? q4.w : q4.y;
-          qf[4 * u + i][r] = pack_f16x2(lo(x) * up, hi(x) * up);
-          qf[4 * u + i][2 + r] = pack_f16x2(lo(y) * up, hi(y) * up);
-        }
+      for (int i = 0; i < 4 * kRuns; ++i) {
+        const uint4& q4 = w[i / 2];
+        const uint32_t x = (i & 1) ? q4.z : q4.x, y = (i & 1) ? q4.w : q4.y;
+        qf[r][i][0] = pack_f16x2(lo(x) * up, hi(x) * up);
+        qf[r][i][1] = pack_f16x2(lo(y) * up, hi(y) * up);
+      }
     }
-    float o[kOut][4];
+    float o[NR][kOut][4];
+    float m[NR][2], n[NR][2], sum[NR][2];
 #pragma unroll
-    for (int i = 0; i < kOut; ++i)
+    for (int r = 0; r < NR; ++r) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, n[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+      for (int i = 0; i < kOut; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[r][i][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[r][e] = n[r][e] = -INFINITY;
+        sum[r][e] = 0.f;
+      }
+    }
 
-    for (int pt = 0; pt < part_tiles; ++pt) {
+    for (int t = c.t; t < c.t1; ++t) {
       ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, phase, wd, kWhereMmaFull));
       if (!ok) break;
       const uint32_t sk = ring + 2 * stage * L::kTile, sv = sk + L::kTile;
       const uint2 about = ld_shared_v2(info + 8 * stage);
-      const int key0 = (part_first + pt) * kKeys;
-      // scores
-      float s[4][4];
+      const int key0 = t * kKeys;
+      // scores: s[r][j][2 i + e] of key 16 j + 8 i + kr, row 2 c4 + e
+      float s[NR][2][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[r][j][e] = 0.f;
 #pragma unroll
         for (int u = 0; u < kRuns; ++u) {
-          const uint4 k = ld_shared_v4(run_addr<HD>(sk, 8 * i + kr, c4 + 4 * u));
-          const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+          const uint4 x = ld_shared_v4(run_addr<HD>(sk, 16 * j + kr, c4 + 4 * u));
+          const uint4 y = ld_shared_v4(run_addr<HD>(sk, 16 * j + 8 + kr, c4 + 4 * u));
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int x = 0; x < 4; ++x) mma_16x8x16(s[i], qf[4 * u + x], codes_f16x2(w[x]), codes_f16x2(w[x] >> 16));
+          for (int i = 0; i < 4; ++i) {
+            uint32_t a0, a1, a2, a3;
+            codes_f16(xw[i], a0, a2);
+            codes_f16(yw[i], a1, a3);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) mma_16x8x16(s[r][j], a0, a1, a2, a3, qf[r][4 * u + i][0], qf[r][4 * u + i][1]);
+          }
         }
       }
       float kx[2], vx[2];  // key scales, value exponents of the two blocks
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int kc = (about.x >> (8 * i)) & 255, vc = (about.x >> (16 + 8 * i)) & 255;
-        kx[i] = kc == 255 ? __uint_as_float(0x7FC00000u) : exp2_code(kc);
-        vx[i] = vc == 255 ? __uint_as_float(0x7FC00000u) : static_cast<float>(vc - 127);
+      for (int j = 0; j < 2; ++j) {
+        const int kc = (about.x >> (8 * j)) & 255, vc = (about.x >> (16 + 8 * j)) & 255;
+        kx[j] = kc == 255 ? __uint_as_float(0x7FC00000u) : exp2_code(kc);
+        vx[j] = vc == 255 ? __uint_as_float(0x7FC00000u) : static_cast<float>(vc - 127);
       }
       const bool edge = key0 + kKeys > c.len - (p.qn - 1) || about.y != 0;
-      float ms[2] = {-INFINITY, -INFINITY}, mn[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = e >> 1;
-          float x = s[i][e] * (kx[i >> 1] * q_scale[r]);
-          if (edge) {
-            const int key = key0 + 8 * i + ((e & 1) ? kv1 : kv0);
-            if (key >= lim[r] || ((about.y >> (i >> 1)) & 1)) x = -INFINITY;
-          }
-          s[i][e] = x;
-          ms[r] = fmaxf(ms[r], x);
-          mn[r] = fmaxf(mn[r], x + vx[i >> 1]);
-        }
-      }
       bool move = false;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        ms[r] = fmaxf(ms[r], __shfl_xor_sync(0xffffffffu, ms[r], 1));
-        mn[r] = fmaxf(mn[r], __shfl_xor_sync(0xffffffffu, mn[r], 1));
-        ms[r] = fmaxf(ms[r], __shfl_xor_sync(0xffffffffu, ms[r], 2));
-        mn[r] = fmaxf(mn[r], __shfl_xor_sync(0xffffffffu, mn[r], 2));
-        if (ms[r] > m[r]) {
-          sum[r] *= ex2(m[r] - ms[r]);
-          m[r] = ms[r];
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = -INFINITY, vtop = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float by = kx[j] * q_scale[r][e];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float x = s[r][j][2 * i + e] * by;
+              if (edge && (key0 + 16 * j + 8 * i + kr >= lim[r][e] || ((about.y >> j) & 1))) x = -INFINITY;
+              s[r][j][2 * i + e] = x;
+            }
+            const float two = fmaxf(s[r][j][e], s[r][j][2 + e]);
+            top = fmaxf(top, two);
+            vtop = fmaxf(vtop, two + vx[j]);
+          }
+          move |= top > m[r][e] + kSlack || vtop > n[r][e] + kSlack;
         }
-        move |= mn[r] > n[r] + kSlack;
-      }
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          if (mn[r] > n[r] + kSlack) {
-            const float by = ex2(n[r] - mn[r]);
-            n[r] = mn[r];
+        for (int r = 0; r < NR; ++r)
 #pragma unroll
-            for (int i = 0; i < kOut; ++i) {
-              o[i][2 * r] *= by;
-              o[i][2 * r + 1] *= by;
+          for (int e = 0; e < 2; ++e) {
+            float top = -INFINITY, vtop = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float two = fmaxf(s[r][j][e], s[r][j][2 + e]);
+              top = fmaxf(top, two);
+              vtop = fmaxf(vtop, two + vx[j]);
+            }
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) {
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+              vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, x));
+            }
+            if (top > m[r][e]) {
+              sum[r][e] *= ex2(m[r][e] - top);
+              m[r][e] = top;
+            }
+            if (vtop > n[r][e]) {
+              const float by = ex2(n[r][e] - vtop);
+              n[r][e] = vtop;
+#pragma unroll
+              for (int i = 0; i < kOut; ++i) {
+                o[r][i][e] *= by;
+                o[r][i][2 + e] *= by;
+              }
             }
           }
       }
-      // weights
-      float neg_m[2], neg_n[2];
+      // weights; then of row g8 and keys 2 c4, 2 c4 + 1
+      uint32_t w[NR][2][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        neg_m[r] = m[r] == -INFINITY ? 0.f : -m[r];
-        neg_n[r] = n[r] == -INFINITY ? 0.f : -n[r];
-      }
-      uint32_t w[4][2];
+      for (int r = 0; r < NR; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 2; ++j) {
+          float neg_m[2], by[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float x = s[i][2 * r], y = s[i][2 * r + 1];
-          sum[r] += ex2(x + neg_m[r]) + ex2(y + neg_m[r]);
-          const float by = vx[i >> 1] + neg_n[r];
-          w[i][r] = pack_f16x2(ex2(x + by), ex2(y + by));
+          for (int e = 0; e < 2; ++e) {
+            neg_m[e] = m[r][e] == -INFINITY ? 0.f : -m[r][e];
+            by[e] = n[r][e] == -INFINITY ? 0.f : vx[j] - n[r][e];
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float x = s[r][j][2 * i], y = s[r][j][2 * i + 1];
+            sum[r][0] += ex2(x + neg_m[0]);
+            sum[r][1] += ex2(y + neg_m[1]);
+            w[r][j][i] = transpose8(pack_f16x2(ex2(x + by[0]), ex2(y + by[1])));
+          }
         }
-      // output += weights times codes, 16 keys at a time
+      // output += codes times weights, 16 keys at a time
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const uint32_t a[4] = {w[2 * g][0], w[2 * g][1], w[2 * g + 1][0], w[2 * g + 1][1]};
+      for (int j = 0; j < 2; ++j) {
         uint32_t v[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int row = 16 * g + 8 * (i >> 1) + ((i & 1) ? kv1 : kv0);
+          const int row = 16 * j + 8 * (i >> 1) + ((i & 1) ? kv1 : kv0);
           if constexpr (HD == 128) {
-            const uint4 x = ld_shared_v4(run_addr<HD>(sv, row, key_row<HD>(n8)));
+            const uint4 x = ld_shared_v4(run_addr<HD>(sv, row, kr));
             v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
           } else {
-            const uint2 x = ld_shared_v2(run_addr<HD>(sv, row, n8 >> 1) + 8 * (n8 & 1));
+            const uint2 x = ld_shared_v2(run_addr<HD>(sv, row, g8 >> 1) + 8 * (g8 & 1));
             v[i][0] = x.x, v[i][1] = x.y;
           }
           if (edge && key0 + row >= c.len) {  // stale codes may be NaN
@@ -477,18 +557,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
 #pragma unroll
-        for (int e = 0; e < HD / 32; ++e) {
-          const uint32_t x0 = __byte_perm(v[0][e], v[1][e], 0x5140), x1 = __byte_perm(v[0][e], v[1][e], 0x7362);
-          const uint32_t y0 = __byte_perm(v[2][e], v[3][e], 0x5140), y1 = __byte_perm(v[2][e], v[3][e], 0x7362);
-          mma_16x8x16(o[4 * e], a, codes_f16x2(x0), codes_f16x2(y0));
-          mma_16x8x16(o[4 * e + 1], a, codes_f16x2(x0 >> 16), codes_f16x2(y0 >> 16));
-          mma_16x8x16(o[4 * e + 2], a, codes_f16x2(x1), codes_f16x2(y1));
-          mma_16x8x16(o[4 * e + 3], a, codes_f16x2(x1 >> 16), codes_f16x2(y1 >> 16));
-        }
+        for (int e = 0; e < HD / 32; ++e)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            // dimensions 4 e + 2 half and the next of this lane's run
+            uint32_t a0, a1, a2, a3;
+            codes_f16(__byte_perm(v[0][e], v[1][e], half ? 0x7362 : 0x5140), a0, a1);
+            codes_f16(__byte_perm(v[2][e], v[3][e], half ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) mma_16x8x16(o[r][2 * e + half], a0, a1, a2, a3, w[r][j][0], w[r][j][1]);
+          }
       }
       __syncwarp();  // every lane has read the stage
       --in_flight;
-      if (loaded < end) {
+      if (more) {
         load(stage);
         ++in_flight;
       }
@@ -500,57 +582,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) break;
 
     // ---- the segment's end, or the range's
+    const bool whole = c.t == 0 && c.t1 == c.tiles;
+    const int64_t slot = 2 * static_cast<int64_t>(range) + (c.t == 0);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-    }
-    const bool whole = part_tiles == c.tiles;
-    const int slot = 2 * range + (part_first == 0);
+    for (int r = 0; r < NR; ++r)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      if (row_at[r] < 0) continue;
-      if (whole) {
-        const bool none = sum[r] == 0.f;
-        const float by = none ? 0.f : ex2(n[r] - m[r]) / sum[r];
-        uint16_t* dst = p.out + row_at[r] * p.D;
-        // this lane's dimensions: two runs of kOut from output columns 2 c and 2 c + 1
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int d0 = HD == 128 ? 64 * half + 16 * c4 : 16 * c4 + 8 * half;
-          if (d0 < p.D) {
+        for (int x = 4; x < 32; x <<= 1) sum[r][e] += __shfl_xor_sync(0xffffffffu, sum[r][e], x);
+        const int in_tile = 8 * r + 2 * c4 + e, row = rt * NR * 8 + in_tile;
+        if (row >= p.qn * p.group) continue;
+        if (whole) {
+          const int64_t at = (static_cast<int64_t>(c.b) * p.qn + row / p.group) * p.Hq + h * p.group + row % p.group;
+          const bool none = sum[r][e] == 0.f;
+          const float by = none ? 0.f : ex2(n[r][e] - m[r][e]) / sum[r][e];
+          if (run_d < p.D) {
 #pragma unroll
-            for (int i = 0; i < kOut; i += 8) {
+            for (int i = 0; i < kOut; i += 4) {
               uint32_t u[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float x = o[i + 2 * e][2 * r + half], y = o[i + 2 * e + 1][2 * r + half];
-                u[e] = none ? 0u : pack_bf16x2(x * by, y * by);
-              }
-              *reinterpret_cast<uint4*>(dst + d0 + i) = make_uint4(u[0], u[1], u[2], u[3]);
+              for (int x = 0; x < 4; ++x)
+                u[x] = none ? 0u : pack_bf16x2(o[r][i + x][e] * by, o[r][i + x][2 + e] * by);
+              *reinterpret_cast<uint4*>(p.out + at * p.D + run_d + 2 * i) = make_uint4(u[0], u[1], u[2], u[3]);
             }
           }
-        }
-        if (c4 == 0 && p.lse) p.lse[row_at[r]] = none ? -INFINITY : (m[r] + log2f(sum[r])) * 0.6931471805599453f;
-      } else {
-        const int64_t at = static_cast<int64_t>(slot) * kRowTile + n8 + 8 * r;
+          if (g8 == 0 && p.lse) p.lse[at] = none ? -INFINITY : (m[r][e] + log2f(sum[r][e])) * 0.6931471805599453f;
+        } else {
+          const int64_t at = slot * (8 * NR) + in_tile;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int d0 = HD == 128 ? 64 * half + 16 * c4 : 16 * c4 + 8 * half;
-#pragma unroll
-          for (int i = 0; i < kOut; i += 4)
-            *reinterpret_cast<float4*>(p.part_o + at * HD + d0 + i) =
-                make_float4(o[i][2 * r + half], o[i + 1][2 * r + half], o[i + 2][2 * r + half], o[i + 3][2 * r + half]);
+          for (int i = 0; i < kOut; i += 2)
+            *reinterpret_cast<float4*>(p.part_o + at * HD + run_d + 2 * i) =
+                make_float4(o[r][i][e], o[r][i][2 + e], o[r][i + 1][e], o[r][i + 1][2 + e]);
+          if (g8 == 0) p.part_ml[at] = make_float4(m[r][e], n[r][e], sum[r][e], 0.f);
         }
-        if (c4 == 0) p.part_ml[at] = make_float4(m[r], n[r], sum[r], 0.f);
       }
+    if (c.t == 0 && lane == 0 && (p.by_segment || !whole)) {
+      const int64_t first = c.start + kSegCost;
+      p.cuts[p.by_segment ? c.b * walk.segs + c.hr : blockIdx.x + gridDim.x * warp] =
+          whole ? Cut{0, 0, 0, -1} : Cut{c.b, c.hr, range, static_cast<int>(quotient(first + c.tiles - 1, quota))};
     }
-    if (!whole && part_first == 0 && lane == 0)
-      p.cut[range] = Segment{c.b, c.hr, static_cast<int32_t>((seg_begin + c.tiles - 1) / quota), 0};
-    tile += part_tiles;
-    seg_begin = tile;
-    c.t += part_tiles - 1;
-    walk.next(c);
+    some = walk.next(c);
   }
   if (!ok) {  // loads in flight must land before the CTA can exit
     for (int i = 0; i < in_flight; ++i) {
@@ -564,48 +635,73 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of the segment that range blockIdx.x starts and later ones continue.
-template <int HD>
-__global__ void __launch_bounds__(256) decode_join_kernel(const DecodeParams p) {
+// Joins the parts of a cut segment; a lane owns 4 dimensions.  Few parts: a warp a row, in the first
+// block of the segment.  Many: a block a row, whose warps share out the parts.
+template <int HD, int NR>
+__global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const DecodeParams p) {
+  __shared__ float4 shared_o[kJoinWarps][32];
+  __shared__ float shared_sum[kJoinWarps];
   grid_dep_launch();
   grid_dep_wait();
-  const int first = blockIdx.x;
-  const Segment s = p.cut[first];
-  if (s.b < 0) return;
-  const int h = s.hr / p.row_tiles, rt = s.hr % p.row_tiles;
-  const int rows = min(kRowTile, p.qn * p.group - rt * kRowTile);
-  constexpr int kQuads = HD / 4;
-  auto slot = [&](int i) { return static_cast<int64_t>(2 * i + (i == first)) * kRowTile; };
-  for (int i = threadIdx.x; i < rows * kQuads; i += 256) {
-    const int row = i / kQuads, d = i % kQuads * 4;
-    float m = -INFINITY, n = -INFINITY;
-#pragma unroll 4
-    for (int k = first; k <= s.last; ++k) {
-      const float4 ml = p.part_ml[slot(k) + row];
+  const Cut cut = p.cuts[blockIdx.x];
+  if (cut.last < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row0 = cut.hr % p.row_tiles * NR * 8, head = cut.hr / p.row_tiles * p.group;
+  const int rows = min(8 * NR, p.qn * p.group - row0);
+  const int count = cut.last - cut.first + 1;
+  const bool many = count > 2 * kJoinWarps;
+  if (!many && blockIdx.y > 0) return;
+  auto at = [&](int k, int row) { return (2 * (cut.first + k) + (k == 0)) * (8 * NR) + row; };
+  const int d = 4 * lane < HD ? 4 * lane : 0;
+  for (int row = many ? blockIdx.y : warp; row < rows; row += many ? gridDim.y : kJoinWarps) {
+    float m = -INFINITY, n = -INFINITY, sum = 0.f;
+    for (int k = lane; k < count; k += 32) {
+      const float4 ml = p.part_ml[at(k, row)];
       m = fmaxf(m, ml.x);
       n = fmaxf(n, ml.y);
     }
-    const float neg_m = m == -INFINITY ? 0.f : -m, neg_n = n == -INFINITY ? 0.f : -n;
-    float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int k = first; k <= s.last; ++k) {
-      const float4 ml = p.part_ml[slot(k) + row];
-      const float4 x = *reinterpret_cast<const float4*>(p.part_o + (slot(k) + row) * HD + d);
-      sum += ml.z * ex2(ml.x + neg_m);
-      const float by = ex2(ml.y + neg_n);
-      o[0] += x.x * by;
-      o[1] += x.y * by;
-      o[2] += x.z * by;
-      o[3] += x.w * by;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+      n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, x));
     }
+    const float m0 = m == -INFINITY ? 0.f : m, n0 = n == -INFINITY ? 0.f : n;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = many ? warp : 0; k < count; k += many ? kJoinWarps : 1) {
+      const float4 ml = p.part_ml[at(k, row)];
+      const float4 x = *reinterpret_cast<const float4*>(p.part_o + static_cast<int64_t>(at(k, row)) * HD + d);
+      sum += ml.z * ex2(ml.x - m0);
+      const float by = ex2(ml.y - n0);
+      o.x += x.x * by;
+      o.y += x.y * by;
+      o.z += x.z * by;
+      o.w += x.w * by;
+    }
+    if (many) {
+      __syncthreads();  // the last row's have been read
+      shared_o[warp][lane] = o;
+      shared_sum[warp] = sum;
+      __syncthreads();
+      if (warp != 0) continue;
+#pragma unroll
+      for (int i = 1; i < kJoinWarps; ++i) {
+        const float4 x = shared_o[i][lane];
+        o.x += x.x;
+        o.y += x.y;
+        o.z += x.z;
+        o.w += x.w;
+        sum += shared_sum[i];
+      }
+    }
+    const int r = row0 + row;
+    const int64_t to = (static_cast<int64_t>(cut.b) * p.qn + r / p.group) * p.Hq + head + r % p.group;
     const bool none = sum == 0.f;
-    const float by = none ? 0.f : ex2(-neg_n + neg_m) / sum;
-    const int r = rt * kRowTile + row;
-    const int64_t at = (static_cast<int64_t>(s.b) * p.qn + r / p.group) * p.Hq + h * p.group + r % p.group;
-    if (d < p.D)
-      *reinterpret_cast<uint2*>(p.out + at * p.D + d) =
-          none ? make_uint2(0, 0) : make_uint2(pack_bf16x2(o[0] * by, o[1] * by), pack_bf16x2(o[2] * by, o[3] * by));
-    if (d == 0 && p.lse) p.lse[at] = none ? -INFINITY : (-neg_m + log2f(sum)) * 0.6931471805599453f;
+    const float by = none ? 0.f : ex2(n - m) / sum;
+    if (4 * lane < p.D)
+      *reinterpret_cast<uint2*>(p.out + to * p.D + d) =
+          none ? make_uint2(0, 0) : make_uint2(pack_bf16x2(o.x * by, o.y * by), pack_bf16x2(o.z * by, o.w * by));
+    if (lane == 0 && p.lse) p.lse[to] = none ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
   }
 }
 
@@ -616,10 +712,11 @@ sg_status_t launch_error(cudaError_t e) {
   return SG_ERR_CUDA;
 }
 
-int num_ranges(const AttnShape& s) { return s.num_sms * kWarps; }
+int64_t max_ranges(const AttnShape& s) { return static_cast<int64_t>(s.num_sms) * kMaxWarps; }
 
-template <int HD>
+template <int HD, int NR>
 sg_status_t launch(const AttnShape& s, const AttnArgs& a, DecodeParams& p) {
+  using L = DecodeLayout<HD, NR>;
   const uint64_t D = s.D, rows = static_cast<uint64_t>(s.Hk) * s.page;
   const uint64_t dims[3] = {D, rows, static_cast<uint64_t>(a.cache.num_pages)};
   const uint64_t sk[2] = {D, static_cast<uint64_t>(a.cache.k_page_stride)}, sv[2] = {D, static_cast<uint64_t>(a.cache.v_page_stride)};
@@ -629,27 +726,35 @@ sg_status_t launch(const AttnShape& s, const AttnArgs& a, DecodeParams& p) {
   if (!encode_3d(&tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.cache.k, dims, sk, box, sw) ||
       !encode_3d(&tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.cache.v, dims, sv, box, sw))
     return SG_ERR_CUDA;
-  p.part_o = static_cast<float*>(s.workspace);
-  p.part_ml = reinterpret_cast<float4*>(p.part_o + static_cast<size_t>(2) * num_ranges(s) * kRowTile * 128);
-  p.cut = reinterpret_cast<Segment*>(p.part_ml + static_cast<size_t>(2) * num_ranges(s) * kRowTile);
-  GemmLaunch l(dim3(s.num_sms), dim3(kThreads), DecodeLayout<HD>::kDynSmem, a.stream, 1);
-  const sg_status_t r = launch_error(cudaLaunchKernelEx(&l.cfg, decode_kernel<HD>, tmK, tmV, p));
+  p.row_tiles = (p.qn * p.group + 8 * NR - 1) / (8 * NR);
+  const int64_t segments = a.B * s.Hk * p.row_tiles, ranges = static_cast<int64_t>(s.num_sms) * L::kWarps;
+  p.by_segment = segments <= ranges;
+  GemmLaunch l(dim3(s.num_sms), dim3(L::kThreads), L::kDynSmem, a.stream, 1);
+  const sg_status_t r = launch_error(cudaLaunchKernelEx(&l.cfg, decode_kernel<HD, NR>, tmK, tmV, p));
   if (r != SG_OK) return r;
-  GemmLaunch j(dim3(num_ranges(s)), dim3(256), 0, a.stream, 1);
-  return launch_error(cudaLaunchKernelEx(&j.cfg, decode_join_kernel<HD>, p));
+  // blocks for a row each where that many fit the GPU at once
+  const int64_t joins = p.by_segment ? segments : ranges, fit = 8 * s.num_sms / joins;
+  const unsigned per_row = static_cast<unsigned>(fit < 1 ? 1 : fit < 8 * NR ? fit : 8 * NR);
+  GemmLaunch j(dim3(static_cast<unsigned>(joins), per_row), dim3(32 * kJoinWarps), 0, a.stream, 1);
+  return launch_error(cudaLaunchKernelEx(&j.cfg, decode_join_kernel<HD, NR>, p));
+}
+
+template <int HD, int NR>
+cudaError_t prepare() {
+  return cudaFuncSetAttribute(decode_kernel<HD, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeLayout<HD, NR>::kDynSmem);
 }
 
 }  // namespace
 
 size_t decode_workspace_bytes(const AttnShape& s) {
-  return static_cast<size_t>(2) * num_ranges(s) * kRowTile * (128 * 4 + 16) + static_cast<size_t>(num_ranges(s)) * sizeof(Segment);
+  return static_cast<size_t>(max_ranges(s)) * (2 * 16 * (128 * 4 + 16) + sizeof(Cut));
 }
 
 cudaError_t decode_prepare() {
-  const cudaError_t e = cudaFuncSetAttribute(decode_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeLayout<64>::kDynSmem);
-  return e == cudaSuccess
-             ? cudaFuncSetAttribute(decode_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeLayout<128>::kDynSmem)
-             : e;
+  cudaError_t e = prepare<64, 1>();
+  if (e == cudaSuccess) e = prepare<64, 2>();
+  if (e == cudaSuccess) e = prepare<128, 1>();
+  return e == cudaSuccess ? prepare<128, 2>() : e;
 }
 
 sg_status_t decode_launch(const AttnShape& s, const AttnArgs& a) {
@@ -668,16 +773,22 @@ sg_status_t decode_launch(const AttnShape& s, const AttnArgs& a) {
   p.Hk = s.Hk;
   p.D = s.D;
   p.page = s.page;
+  while ((1 << p.page_shift) < s.page) ++p.page_shift;
   p.group = s.Hq / s.Hk;
-  p.row_tiles = (p.qn * p.group + kRowTile - 1) / kRowTile;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.out = static_cast<uint16_t*>(a.out);
   p.lse = a.lse;
+  p.part_o = static_cast<float*>(s.workspace);
+  p.part_ml = reinterpret_cast<float4*>(p.part_o + max_ranges(s) * 2 * 16 * 128);
+  p.cuts = reinterpret_cast<Cut*>(p.part_ml + max_ranges(s) * 2 * 16);
   p.status = s.status;
   p.timeout_ns = s.timeout_ns;
   AttnArgs args = a;
   if (args.cache.num_pages == 0) args.cache.num_pages = 1;  // a tensor map has no empty dimension; nothing reads it
-  return s.D > 64 ? launch<128>(s, args, p) : launch<64>(s, args, p);
+  // Up to 8 query rows of a key/value head take half the registers, which
+  // more warps use; more rows go 16 at a time, so that the cache is read half as often.
+  if (p.qn * p.group <= 8) return s.D > 64 ? launch<128, 1>(s, args, p) : launch<64, 1>(s, args, p);
+  return s.D > 64 ? launch<128, 2>(s, args, p) : launch<64, 2>(s, args, p);
 }
 
 }  // namespace sg

@@ -271,7 +271,7 @@ def _check_decode(lens, hq, hk, d, page, qn, host, q, out, lse, scale=None):
         assert (err <= tol).all(), (b, n, float((err / tol).max()))
         assert np.array_equal(np.isinf(gl[r]), np.isinf(ls)), (b, n)
         fin = np.isfinite(ls)
-        assert (np.abs(gl[r] - ls)[fin] <= ref.lse_tolerance(ls, big)[fin]).all(), (b, n)
+        assert (np.abs(gl[r][fin] - ls[fin]) <= ref.lse_tolerance(ls, big)[fin]).all(), (b, n)
 
 
 DECODE = [
@@ -367,6 +367,20 @@ def test_decode_rows_of_very_different_size():
     _check_decode(lens, 6, 1, 128, 32, 1, (table, codes, scales), q, out, lse)
 
 
+def test_decode_rows_that_are_not_finite_stay_alone():
+    lens = [70, 40]
+    plan, args, host, _, _ = _decode(lens, 6, 2, 64, 16, 1, 36)
+    q = args[0].clone()
+    q[0, 1, 3] = float("nan")
+    q[1, 5, 0] = float("inf")
+    out, lse = plan.decode(q, *args[1:])
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(out[0, 1].float()).all()) and bool(torch.isnan(out[1, 5].float()).all())
+    q[0, 1], q[1, 5] = args[0][0, 1], args[0][1, 5]
+    out[0, 1], lse[0, 1], out[1, 5], lse[1, 5] = (t for o in [plan.decode(q, *args[1:])] for t in (o[0][0, 1], o[1][0, 1], o[0][1, 5], o[1][1, 5]))
+    _check_decode(lens, 6, 2, 64, 16, 1, host, q, out, lse)
+
+
 def test_decode_cache_offsets_past_32_bits():
     # pages far apart: the last ones start beyond 4 GiB of codes
     pkg = _pkg()
@@ -432,7 +446,7 @@ def _check_prompt(ql, kl, hq, hk, d, causal, q, k, v, out, lse, scale=None):
         assert (err <= tol).all(), (b, n, m, float((err / tol).max()), np.argwhere(~(err <= tol))[:4])
         assert np.array_equal(np.isinf(gl[r]), np.isinf(ls)), (b, n, m)
         fin = np.isfinite(ls)
-        assert (np.abs(gl[r] - ls)[fin] <= ref.lse_tolerance(ls, big)[fin]).all(), (b, n, m)
+        assert (np.abs(gl[r][fin] - ls[fin]) <= ref.lse_tolerance(ls, big)[fin]).all(), (b, n, m)
 
 
 def _prompt_inputs(ql, kl, hq, hk, d, seed):
