@@ -13,9 +13,11 @@
 // The bound is memory: 2 (Hq + 2 Hk) D bytes read and 2 Hq D + 2 Hk D (+ 2 Hk D)
 // written per token, each once.  One CTA takes the new tokens of one block of
 // positions of one sequence (so a block's scale has one owner: no atomics, no
-// order), and its warps share out the heads: a warp takes all tokens of a K or V
-// head, or a few tokens of a run of query heads, whose cosines stay in registers.
-// Lanes own 16 elements of a row (a run of 8 pairs, two 16-byte loads).
+// order).  Lanes own 16 elements of a row (a run of 8 pairs, two 16-byte loads); the
+// rows that a warp holds at once are tokens times heads, as many tokens as there are, so
+// that one new token a sequence fills lanes as well as sixteen.  K and V rows are kept
+// as bf16 in shared memory and rotated twice, for the maximum and for the codes: their fp32 values would
+// take the registers of half the warps, and with those the loads in flight.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -34,12 +36,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kHeadPasses = 8;  // passes over query heads that reuse one set of cosines
+constexpr int kCtas = 3;        // resident CTAs an SM
 
 struct AppendParams {
   sg_kv_cache_t cache;
   const float* rot_table;
   int64_t max_pos;
-  int rot, interleaved;
+  int rot, by_token;
   const uint16_t *q, *k, *v;
   int64_t q_stride, k_stride, v_stride;
   const int32_t *table, *ctx, *cu;
@@ -54,11 +57,12 @@ struct Run {
   bool live, rotated;
 };
 
+template <bool INTER>
 __device__ __forceinline__ Run make_run(int j, const AppendParams& p) {
   Run r;
   r.live = j < p.D / 16;
   r.rotated = j < p.rot / 16;
-  if (r.rotated && !p.interleaved) {
+  if (r.rotated && !INTER) {
     r.off_a = 8 * j;
     r.off_b = p.rot / 2 + 8 * j;
   } else {
@@ -100,21 +104,26 @@ __device__ __forceinline__ void load_angles(const AppendParams& p, int64_t pos, 
   const int64_t row = pos < p.max_pos ? pos : p.max_pos - 1;
   const float4* c = reinterpret_cast<const float4*>(p.rot_table + row * p.rot + 8 * j);
   const float4* s = reinterpret_cast<const float4*>(p.rot_table + row * p.rot + p.rot / 2 + 8 * j);
-  *reinterpret_cast<float4*>(g.c) = __ldg(c);
-  *reinterpret_cast<float4*>(g.c + 4) = __ldg(c + 1);
-  *reinterpret_cast<float4*>(g.s) = __ldg(s);
-  *reinterpret_cast<float4*>(g.s + 4) = __ldg(s + 1);
+  // volatile: loaded where they are used, not for all of a warp's tokens ahead of time
+  auto load = [](float* f, const float4* a) {
+    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "l"(a));
+  };
+  load(g.c, c);
+  load(g.c + 4, c + 1);
+  load(g.s, s);
+  load(g.s + 4, s + 1);
 }
 
 // f[0..7] and f[8..15]: the run's halves; rotated in place.
-__device__ __forceinline__ void rotate(float (&f)[16], const Angles& g, bool interleaved) {
+template <bool INTER>
+__device__ __forceinline__ void rotate(float (&f)[16], const Angles& g) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float x = interleaved ? f[2 * i] : f[i];
-    const float y = interleaved ? f[2 * i + 1] : f[8 + i];
+    const float x = INTER ? f[2 * i] : f[i];
+    const float y = INTER ? f[2 * i + 1] : f[8 + i];
     const float xr = __fsub_rn(__fmul_rn(x, g.c[i]), __fmul_rn(y, g.s[i]));
     const float yr = __fadd_rn(__fmul_rn(x, g.s[i]), __fmul_rn(y, g.c[i]));
-    if (interleaved) {
+    if (INTER) {
       f[2 * i] = xr;
       f[2 * i + 1] = yr;
     } else {
@@ -163,105 +172,128 @@ struct Unit {
   int slot0;    // the block's first slot in the page
 };
 
-// All tokens of one K or V head of the unit.
-template <int LPR>
-__device__ __forceinline__ void append_head(const AppendParams& p, const Unit& u, int head, bool is_k, int lane) {
-  constexpr int kRows = 32 / LPR;               // tokens a pass
+// How a warp's rows are split into tokens and heads: row r is token r % tokens of
+// head r / tokens.
+struct Split {
+  int tokens, heads, shift;  // tokens = 1 << shift
+};
+
+// The unit's tokens of `split.heads` K (or V) heads from `head0`; `keep`: this lane's shared memory.
+template <int LPR, bool INTER, bool IS_K>
+__device__ __forceinline__ void append_heads(const AppendParams& p, const Unit& u, const Split& split, int head0, int lane,
+                                             uint32_t keep) {
+  constexpr int kRows = 32 / LPR;               // rows a pass
   constexpr int kPasses = kKvBlock / kRows;
   const int j = lane % LPR, row = lane / LPR;
-  const Run run = make_run(j, p);
-  const uint16_t* src = is_k ? p.k + static_cast<int64_t>(head) * p.D : p.v + static_cast<int64_t>(head) * p.D;
-  const int64_t stride = is_k ? p.k_stride : p.v_stride;
-  Run vr = run;
-  if (!is_k) {
-    vr.off_a = 16 * j;
-    vr.off_b = 16 * j + 8;
+  const int t0 = row & (split.tokens - 1), head = head0 + (row >> split.shift);
+  Run run = make_run<INTER>(j, p);
+  if (!IS_K) {
+    run.rotated = false;
+    run.off_a = 16 * j;
+    run.off_b = 16 * j + 8;
   }
+  run.live = run.live && head < p.Hk;
+  const uint16_t* src = (IS_K ? p.k : p.v) + static_cast<int64_t>(u.t0) * (IS_K ? p.k_stride : p.v_stride) + head * p.D;
+  const int64_t stride = IS_K ? p.k_stride : p.v_stride;
   uint8_t* scale = nullptr;
   uint8_t* codes = nullptr;
   int was = 0;
-  if (u.page_id >= 0) {
-    const int64_t nb = p.page / kKvBlock;
-    scale = (is_k ? p.cache.k_scale : p.cache.v_scale) +
-            (static_cast<int64_t>(u.page_id) * p.Hk + head) * nb + u.slot0 / kKvBlock;
-    codes = static_cast<uint8_t*>(is_k ? p.cache.k : p.cache.v) +
-            static_cast<int64_t>(u.page_id) * (is_k ? p.cache.k_page_stride : p.cache.v_page_stride) +
+  if (u.page_id >= 0 && head < p.Hk) {
+    scale = (IS_K ? p.cache.k_scale : p.cache.v_scale) +
+            (static_cast<int64_t>(u.page_id) * p.Hk + head) * (p.page / kKvBlock) + u.slot0 / kKvBlock;
+    codes = static_cast<uint8_t*>(IS_K ? p.cache.k : p.cache.v) +
+            static_cast<int64_t>(u.page_id) * (IS_K ? p.cache.k_page_stride : p.cache.v_page_stride) +
             (static_cast<int64_t>(head) * p.page + u.slot0) * p.D;
     if (u.held > 0) was = min(static_cast<int>(*scale), 254);
   }
-  Raw raw[kPasses];
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
-    const int t = i * kRows + row;
-    if (t < u.n && run.live) raw[i] = load_raw(src + (u.t0 + t) * stride, vr);
-  }
-  float f[kPasses][16];
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int t = i * kRows + row;
+    const int t = i * split.tokens + t0;
     if (t < u.n && run.live) {
-      widen(raw[i].a, f[i]);
-      widen(raw[i].b, f[i] + 8);
-      if (is_k && run.rotated) {
-        Angles g;
-        load_angles(p, u.pos + t, j, g);
-        if (p.interleaved)
-          rotate(f[i], g, true);
-        else
-          rotate(f[i], g, false);
-      }
-      if (is_k && p.k_out) {
-        uint16_t* o = p.k_out + (static_cast<int64_t>(u.t0 + t) * p.Hk + head) * p.D;
-        *reinterpret_cast<uint4*>(o + vr.off_a) = narrow(f[i]);
-        *reinterpret_cast<uint4*>(o + vr.off_b) = narrow(f[i] + 8);
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(f[i][e]));
+      cp_async_16(keep + i * 1024, src + t * stride + run.off_a, 16);
+      cp_async_16(keep + i * 1024 + 512, src + t * stride + run.off_b, 16);
     }
   }
-  if (u.page_id < 0) return;
-  // non-negative floats order as their bits
-  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+  auto value = [&](int i, float (&f)[16]) {
+    Raw x;
+    const uint32_t at = keep + i * 1024;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.a.x), "=r"(x.a.y), "=r"(x.a.z), "=r"(x.a.w) : "r"(at) : "memory");
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.b.x), "=r"(x.b.y), "=r"(x.b.z), "=r"(x.b.w) : "r"(at + 512) : "memory");
+    widen(x.a, f);
+    widen(x.b, f + 8);
+    if (IS_K && run.rotated) {
+      Angles g;
+      load_angles(p, u.pos + i * split.tokens + t0, j, g);
+      rotate<INTER>(f, g);
+    }
+  };
+  cp_async_wait_all();  // this lane's own: no other reads them
+  float amax = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < kPasses; ++i) {
+    const int t = i * split.tokens + t0;
+    if (t < u.n && run.live) {
+      float f[16];
+      value(i, f);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(f[e]));
+    }
+  }
+  // over the lanes of a head
+  const int span = LPR << split.shift;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1)
+    if (x < span) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, x));
   amax = fminf(amax, FLT_MAX);
   int code = amax > 0.f ? min(max(mx_exponent(amax) + 127, 0), 254) : 0;
-  if (u.held > 0) {
+  if (u.held > 0 && codes) {
     code = max(code, was);
     if (code > was) {
       const float by = exp2_code(max(127 + was - code, 0));
       const int vecs = u.held * p.D / 16;  // a block's rows are contiguous
-      for (int i = lane; i < vecs; i += 32) {
+      for (int i = lane & (span - 1); i < vecs; i += span) {
         uint4* c = reinterpret_cast<uint4*>(codes) + i;
         *c = rescale16(*c, by);
       }
     }
   }
   const float inv = exp2_code(254 - code);
-  if (lane == 0) *scale = static_cast<uint8_t>(code);
-#pragma unroll
+  if (scale && (lane & (span - 1)) == 0) *scale = static_cast<uint8_t>(code);
+#pragma unroll 1
   for (int i = 0; i < kPasses; ++i) {
-    const int t = i * kRows + row;
+    const int t = i * split.tokens + t0;
     if (t < u.n && run.live) {
-      uint8_t* o = codes + static_cast<int64_t>(u.held + t) * p.D;
-      *reinterpret_cast<uint2*>(o + vr.off_a) = codes8(f[i], inv);
-      *reinterpret_cast<uint2*>(o + vr.off_b) = codes8(f[i] + 8, inv);
+      float f[16];
+      value(i, f);
+      if (IS_K && p.k_out) {
+        uint16_t* o = p.k_out + (static_cast<int64_t>(u.t0 + t) * p.Hk + head) * p.D;
+        *reinterpret_cast<uint4*>(o + run.off_a) = narrow(f);
+        *reinterpret_cast<uint4*>(o + run.off_b) = narrow(f + 8);
+      }
+      if (codes) {
+        uint8_t* o = codes + (u.held + t) * p.D;
+        *reinterpret_cast<uint2*>(o + run.off_a) = codes8(f, inv);
+        *reinterpret_cast<uint2*>(o + run.off_b) = codes8(f + 8, inv);
+      }
     }
   }
 }
 
-template <int LPR>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams p) {
+template <int LPR, bool INTER>
+__global__ void __launch_bounds__(kThreads, kCtas) kv_append_kernel(const AppendParams p) {
   __shared__ int found[kWarps];
+  __shared__ __align__(16) uint8_t kept[kWarps][kKvBlock / (32 / LPR) * 1024];
   grid_dep_launch();
   grid_dep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // Blocks of positions are numbered from cu[b] / 16 + 2 b for sequence b: n new
-  // tokens touch at most n / 16 + 2 blocks, so the ranges do not overlap and the
-  // number of starts at or below a block's number gives its sequence.
+  // The blocks of positions that new tokens touch, by number: by token, a block belongs to its
+  // first one; otherwise sequence b's begin at cu[b] / 16 + 2 b (n tokens touch at
+  // most n / 16 + 2 blocks).  Either way the number of starts at or below gives the sequence.
   const int unit = blockIdx.x;
   auto cu = [&](int i) { return min(max(__ldg(p.cu + i), 0), p.T); };
+  auto start = [&](int i) { return p.by_token ? cu(i) : cu(i) / kKvBlock + 2 * i; };
   int below = 0;
-  for (int i = tid; i < p.B; i += kThreads) below += (cu(i) / kKvBlock + 2 * i <= unit);
+  for (int i = tid; i < p.B; i += kThreads) below += start(i) <= unit;
   below = __reduce_add_sync(0xffffffffu, below);
   if (lane == 0) found[warp] = below;
   __syncthreads();
@@ -271,7 +303,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
   if (b < 0) return;
   const int first = cu(b), last = cu(b + 1);
   const int64_t ctx = max(__ldg(p.ctx + b), 0);
-  const int64_t block = ctx / kKvBlock + (unit - (first / kKvBlock + 2 * b));
+  int64_t block;
+  if (p.by_token) {
+    if (unit >= last || (unit > first && (ctx + (unit - first)) % kKvBlock != 0)) return;
+    block = (ctx + (unit - first)) / kKvBlock;
+  } else {
+    block = ctx / kKvBlock + (unit - (first / kKvBlock + 2 * b));
+  }
   Unit u;
   u.pos = max(ctx, block * kKvBlock);
   const int64_t end = min(ctx + (last - first), (block + 1) * kKvBlock);
@@ -284,46 +322,63 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
   if (u.page_id >= p.cache.num_pages) u.page_id = -1;
   u.slot0 = static_cast<int>(block * kKvBlock % p.page);
 
-  constexpr int kGroups = 32 / LPR;  // rows a warp takes at once
-  const int tq = u.n >= kGroups ? kGroups : (u.n > 1 ? min(kGroups, u.n > 2 ? 4 : 2) : 1);  // tokens among them
-  const int hp = kGroups / tq;                                                                // heads among them
-  const int head_runs = (p.Hq + hp * kHeadPasses - 1) / (hp * kHeadPasses);
-  const int q_items = (u.n + tq - 1) / tq * head_runs;
-  const int items = 2 * p.Hk + q_items;
+  constexpr int kRows = 32 / LPR;  // rows a warp takes at once
+  Split split{kRows, 1, LPR == 8 ? 2 : 3};
+  while (split.tokens > 1 && split.tokens / 2 >= u.n) {
+    split.tokens /= 2;
+    split.heads *= 2;
+    --split.shift;
+  }
+  const int kv_runs = (p.Hk + split.heads - 1) / split.heads;
+  const int head_runs = (p.Hq + split.heads * kHeadPasses - 1) / (split.heads * kHeadPasses);
+  const int items = 2 * kv_runs + (u.n + split.tokens - 1) / split.tokens * head_runs;
   const int j = lane % LPR, row = lane / LPR;
-  const Run run = make_run(j, p);
+  const Run run = make_run<INTER>(j, p);
+  const uint32_t keep = smem_addr(kept[warp]) + lane * 16;
   for (int it = blockIdx.y * kWarps + warp; it < items; it += gridDim.y * kWarps) {
-    if (it < 2 * p.Hk) {
-      append_head<LPR>(p, u, it >> 1, (it & 1) == 0, lane);
+    if (it < kv_runs) {
+      append_heads<LPR, INTER, true>(p, u, split, it * split.heads, lane, keep);
       continue;
     }
-    const int qi = it - 2 * p.Hk;
-    const int t = qi / head_runs * tq + row % tq;
-    const int h0 = (qi % head_runs) * hp * kHeadPasses + row / tq;
+    if (it < 2 * kv_runs) {
+      append_heads<LPR, INTER, false>(p, u, split, (it - kv_runs) * split.heads, lane, keep);
+      continue;
+    }
+    const int qi = it - 2 * kv_runs;
+    const int t = (qi / head_runs << split.shift) + (row & (split.tokens - 1));
+    const int h0 = (qi % head_runs) * split.heads * kHeadPasses + (row >> split.shift);
     if (t >= u.n || !run.live) continue;
     Angles g;
     if (run.rotated) load_angles(p, u.pos + t, j, g);
     const uint16_t* src = p.q + (u.t0 + t) * p.q_stride;
     uint16_t* dst = p.q_out + static_cast<int64_t>(u.t0 + t) * p.Hq * p.D;
-#pragma unroll 4
-    for (int i = 0; i < kHeadPasses; ++i) {
-      const int h = h0 + i * hp;
-      if (h < p.Hq) {
-        const Raw raw = load_raw(src + h * p.D, run);
-        float f[16];
-        widen(raw.a, f);
-        widen(raw.b, f + 8);
-        if (run.rotated) {
-          if (p.interleaved)
-            rotate(f, g, true);
-          else
-            rotate(f, g, false);
+#pragma unroll 1
+    for (int i0 = 0; i0 < kHeadPasses; i0 += 2) {
+      Raw raw[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int h = h0 + (i0 + i) * split.heads;
+        if (h < p.Hq) raw[i] = load_raw(src + h * p.D, run);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int h = h0 + (i0 + i) * split.heads;
+        if (h < p.Hq) {
+          float f[16];
+          widen(raw[i].a, f);
+          widen(raw[i].b, f + 8);
+          if (run.rotated) rotate<INTER>(f, g);
+          *reinterpret_cast<uint4*>(dst + h * p.D + run.off_a) = narrow(f);
+          *reinterpret_cast<uint4*>(dst + h * p.D + run.off_b) = narrow(f + 8);
         }
-        *reinterpret_cast<uint4*>(dst + h * p.D + run.off_a) = narrow(f);
-        *reinterpret_cast<uint4*>(dst + h * p.D + run.off_b) = narrow(f + 8);
       }
     }
   }
+}
+
+template <int LPR>
+cudaError_t launch(const cudaLaunchConfig_t* cfg, bool inter, const AppendParams& p) {
+  return inter ? cudaLaunchKernelEx(cfg, kv_append_kernel<LPR, true>, p) : cudaLaunchKernelEx(cfg, kv_append_kernel<LPR, false>, p);
 }
 
 }  // namespace
@@ -334,7 +389,6 @@ sg_status_t append_launch(const AttnShape& s, const AttnArgs& a) {
   p.rot_table = a.rotary.table;
   p.max_pos = a.rotary.max_pos;
   p.rot = a.rotary.rot;
-  p.interleaved = a.rotary.interleaved != 0;
   p.q = static_cast<const uint16_t*>(a.q);
   p.k = static_cast<const uint16_t*>(a.k);
   p.v = static_cast<const uint16_t*>(a.v);
@@ -353,10 +407,13 @@ sg_status_t append_launch(const AttnShape& s, const AttnArgs& a) {
   p.page = s.page;
   p.q_out = static_cast<uint16_t*>(a.out);
   p.k_out = static_cast<uint16_t*>(a.k_out);
-  const unsigned units = static_cast<unsigned>(a.Tq / kKvBlock + 2 * a.B);
+  // Numbering by token launches a CTA a token, which is less where most sequences get one or two.
+  const int64_t by_block = a.Tq / kKvBlock + 2 * a.B;
+  p.by_token = a.Tq <= by_block;
+  const unsigned units = static_cast<unsigned>(p.by_token ? a.Tq : by_block);
   GemmLaunch l(dim3(units, 1), dim3(kThreads), 0, a.stream, 1);
-  const cudaError_t e = s.D > 64 ? cudaLaunchKernelEx(&l.cfg, kv_append_kernel<8>, p)
-                                 : cudaLaunchKernelEx(&l.cfg, kv_append_kernel<4>, p);
+  const bool inter = a.rotary.interleaved != 0;
+  const cudaError_t e = s.D > 64 ? launch<8>(&l.cfg, inter, p) : launch<4>(&l.cfg, inter, p);
   if (e != cudaSuccess) {
     note_cuda_error(e);
     cudaGetLastError();
