@@ -15,9 +15,10 @@
 // positions of one sequence (so a block's scale has one owner: no atomics, no
 // order).  Lanes own 16 elements of a row (a run of 8 pairs, two 16-byte loads); the
 // rows that a warp holds at once are tokens times heads, as many tokens as there are, so
-// that one new token a sequence fills lanes as well as sixteen.  K and V rows are kept
-// as bf16 in shared memory and rotated twice, for the maximum and for the codes: their fp32 values would
-// take the registers of half the warps, and with those the loads in flight.
+// that one new token a sequence fills lanes as well as sixteen.  K and V rows
+// wait in shared memory, loaded there asynchronously, and are rotated twice, for the block's maximum and
+// for its codes: in registers their fp32 values would take the room of half the warps, and with those the
+// loads in flight; in shared memory, that of the cosines in L1 (48k-token prompt 251 us, 281 with fp32 kept).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -26,23 +27,26 @@
 #include <cfloat>
 
 #include "sg_attn.h"
+#include "sg_attn_ptx.cuh"
 #include "sg_mx.cuh"
-#include "sg_ptx.cuh"
 
 namespace sg {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+constexpr int kPassBytes = 1024;  // shared memory of a warp's pass: 32 bytes a lane
 constexpr int kHeadPasses = 8;  // passes over query heads that reuse one set of cosines
-constexpr int kCtas = 3;        // resident CTAs an SM
+constexpr int kCtas = 6;        // resident CTAs an SM
+constexpr int kWaves = 5;       // CTAs wanted, in times what the GPU holds
 
 struct AppendParams {
   sg_kv_cache_t cache;
   const float* rot_table;
   int64_t max_pos;
   int rot, by_token;
+  float one;  // 1
   const uint16_t *q, *k, *v;
   int64_t q_stride, k_stride, v_stride;
   const int32_t *table, *ctx, *cu;
@@ -96,6 +100,12 @@ __device__ __forceinline__ uint4 narrow(const float* f) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
+__device__ __forceinline__ uint4 ld_shared_16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
 struct Angles {
   float c[8], s[8];
 };
@@ -114,31 +124,31 @@ __device__ __forceinline__ void load_angles(const AppendParams& p, int64_t pos, 
   load(g.s + 4, s + 1);
 }
 
-// f[0..7] and f[8..15]: the run's halves; rotated in place.
+// f[0..7] and f[8..15]: the run's halves; rotated in place, two pairs an instruction.  The sum of two
+// rounded products is formed as fma(product, one, product) with a `one` that the
+// compiler does not know: it contracts a packed multiplication and addition otherwise.
 template <bool INTER>
-__device__ __forceinline__ void rotate(float (&f)[16], const Angles& g) {
+__device__ __forceinline__ void rotate(float (&f)[16], const Angles& g, float one) {
+  const uint64_t one2 = pack_f32x2(one, one);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float x = INTER ? f[2 * i] : f[i];
-    const float y = INTER ? f[2 * i + 1] : f[8 + i];
-    const float xr = __fsub_rn(__fmul_rn(x, g.c[i]), __fmul_rn(y, g.s[i]));
-    const float yr = __fadd_rn(__fmul_rn(x, g.s[i]), __fmul_rn(y, g.c[i]));
-    if (INTER) {
-      f[2 * i] = xr;
-      f[2 * i + 1] = yr;
-    } else {
-      f[i] = xr;
-      f[8 + i] = yr;
-    }
+  for (int i = 0; i < 8; i += 2) {
+    const int x0 = INTER ? 2 * i : i, x1 = INTER ? 2 * i + 2 : i + 1, y = INTER ? 1 : 8;
+    const uint64_t x = pack_f32x2(f[x0], f[x1]), z = pack_f32x2(f[x0 + y], f[x1 + y]);
+    const uint64_t c = pack_f32x2(g.c[i], g.c[i + 1]), s = pack_f32x2(g.s[i], g.s[i + 1]);
+    const uint64_t ns = pack_f32x2(-g.s[i], -g.s[i + 1]);  // x c - y s = x c + y (-s), rounded alike
+    unpack_f32x2(fma_f32x2(mul_f32x2(x, c), one2, mul_f32x2(z, ns)), f[x0], f[x1]);
+    unpack_f32x2(fma_f32x2(mul_f32x2(x, s), one2, mul_f32x2(z, c)), f[x0 + y], f[x1 + y]);
   }
 }
 
 __device__ __forceinline__ uint2 codes8(const float* f, float inv) {
   uint32_t w[2] = {0, 0};
+  const uint64_t inv2 = pack_f32x2(inv, inv);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t pair =
-        __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * inv, f[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    float2 y;
+    unpack_f32x2(mul_f32x2(pack_f32x2(f[2 * i], f[2 * i + 1]), inv2), y.x, y.y);
+    const uint32_t pair = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
     w[i >> 1] |= (pair & 0xFFFFu) << (16 * (i & 1));
   }
   return make_uint2(w[0], w[1]);
@@ -168,7 +178,7 @@ __device__ __forceinline__ uint4 rescale16(uint4 c, float by) {
 struct Unit {
   int t0, n, held;
   int64_t pos;
-  int page_id;  // -1: no page, nothing is written
+  int page_id;  // outside [0, num_pages): no page, nothing is written
   int slot0;    // the block's first slot in the page
 };
 
@@ -195,10 +205,18 @@ __device__ __forceinline__ void append_heads(const AppendParams& p, const Unit& 
   run.live = run.live && head < p.Hk;
   const uint16_t* src = (IS_K ? p.k : p.v) + static_cast<int64_t>(u.t0) * (IS_K ? p.k_stride : p.v_stride) + head * p.D;
   const int64_t stride = IS_K ? p.k_stride : p.v_stride;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int t = i * split.tokens + t0;
+    if (t < u.n && run.live) {
+      cp_async_16(keep + i * kPassBytes, src + t * stride + run.off_a, 16);
+      cp_async_16(keep + i * kPassBytes + 512, src + t * stride + run.off_b, 16);
+    }
+  }
   uint8_t* scale = nullptr;
   uint8_t* codes = nullptr;
   int was = 0;
-  if (u.page_id >= 0 && head < p.Hk) {
+  if (u.page_id >= 0 && u.page_id < p.cache.num_pages && head < p.Hk) {
     scale = (IS_K ? p.cache.k_scale : p.cache.v_scale) +
             (static_cast<int64_t>(u.page_id) * p.Hk + head) * (p.page / kKvBlock) + u.slot0 / kKvBlock;
     codes = static_cast<uint8_t*>(IS_K ? p.cache.k : p.cache.v) +
@@ -206,25 +224,13 @@ __device__ __forceinline__ void append_heads(const AppendParams& p, const Unit& 
             (static_cast<int64_t>(head) * p.page + u.slot0) * p.D;
     if (u.held > 0) was = min(static_cast<int>(*scale), 254);
   }
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int t = i * split.tokens + t0;
-    if (t < u.n && run.live) {
-      cp_async_16(keep + i * 1024, src + t * stride + run.off_a, 16);
-      cp_async_16(keep + i * 1024 + 512, src + t * stride + run.off_b, 16);
-    }
-  }
   auto value = [&](int i, float (&f)[16]) {
-    Raw x;
-    const uint32_t at = keep + i * 1024;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.a.x), "=r"(x.a.y), "=r"(x.a.z), "=r"(x.a.w) : "r"(at) : "memory");
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.b.x), "=r"(x.b.y), "=r"(x.b.z), "=r"(x.b.w) : "r"(at + 512) : "memory");
-    widen(x.a, f);
-    widen(x.b, f + 8);
+    widen(ld_shared_16(keep + i * kPassBytes), f);
+    widen(ld_shared_16(keep + i * kPassBytes + 512), f + 8);
     if (IS_K && run.rotated) {
       Angles g;
       load_angles(p, u.pos + i * split.tokens + t0, j, g);
-      rotate<INTER>(f, g);
+      rotate<INTER>(f, g, p.one);
     }
   };
   cp_async_wait_all();  // this lane's own: no other reads them
@@ -236,7 +242,7 @@ __device__ __forceinline__ void append_heads(const AppendParams& p, const Unit& 
       float f[16];
       value(i, f);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(f[e]));
+      for (int e = 0; e < 16; e += 2) amax = fmaxf(amax, fmaxf(fabsf(f[e]), fabsf(f[e + 1])));
     }
   }
   // over the lanes of a head
@@ -281,28 +287,29 @@ __device__ __forceinline__ void append_heads(const AppendParams& p, const Unit& 
 
 template <int LPR, bool INTER>
 __global__ void __launch_bounds__(kThreads, kCtas) kv_append_kernel(const AppendParams p) {
-  __shared__ int found[kWarps];
-  __shared__ __align__(16) uint8_t kept[kWarps][kKvBlock / (32 / LPR) * 1024];
+  __shared__ int4 found;  // sequence, its first row, the row past its last, its tokens in the cache
+  __shared__ __align__(16) uint8_t kept[kWarps][kKvBlock / (32 / LPR) * kPassBytes];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) found.x = -1;
+  __syncthreads();
   grid_dep_launch();
   grid_dep_wait();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // The blocks of positions that new tokens touch, by number: by token, a block belongs to its
   // first one; otherwise sequence b's begin at cu[b] / 16 + 2 b (n tokens touch at
-  // most n / 16 + 2 blocks).  Either way the number of starts at or below gives the sequence.
+  // most n / 16 + 2 blocks).  Either way the last start at or below gives the sequence; the thread that
+  // finds it has read all there is to know of it (one round of loads, not two).
   const int unit = blockIdx.x;
-  auto cu = [&](int i) { return min(max(__ldg(p.cu + i), 0), p.T); };
-  auto start = [&](int i) { return p.by_token ? cu(i) : cu(i) / kKvBlock + 2 * i; };
-  int below = 0;
-  for (int i = tid; i < p.B; i += kThreads) below += start(i) <= unit;
-  below = __reduce_add_sync(0xffffffffu, below);
-  if (lane == 0) found[warp] = below;
+  auto clamp = [&](int c) { return min(max(c, 0), p.T); };
+  auto start = [&](int c, int i) { return p.by_token ? c : c / kKvBlock + 2 * i; };
+  for (int i = tid; i < p.B; i += kThreads) {
+    const int c0 = clamp(__ldg(p.cu + i)), c1 = clamp(__ldg(p.cu + i + 1)), ctx = __ldg(p.ctx + i);
+    if (start(c0, i) <= unit && (i + 1 == p.B || unit < start(c1, i + 1))) found = make_int4(i, c0, c1, max(ctx, 0));
+  }
   __syncthreads();
-  int b = -1;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) b += found[w];
+  const int b = found.x;
   if (b < 0) return;
-  const int first = cu(b), last = cu(b + 1);
-  const int64_t ctx = max(__ldg(p.ctx + b), 0);
+  const int first = found.y, last = found.z;
+  const int64_t ctx = found.w;
   int64_t block;
   if (p.by_token) {
     if (unit >= last || (unit > first && (ctx + (unit - first)) % kKvBlock != 0)) return;
@@ -319,7 +326,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv_append_kernel(const Append
   u.held = static_cast<int>(u.pos - block * kKvBlock);
   const int64_t at = block * kKvBlock / p.page;
   u.page_id = at < p.table_stride ? __ldg(p.table + b * p.table_stride + at) : -1;
-  if (u.page_id >= p.cache.num_pages) u.page_id = -1;
   u.slot0 = static_cast<int>(block * kKvBlock % p.page);
 
   constexpr int kRows = 32 / LPR;  // rows a warp takes at once
@@ -367,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv_append_kernel(const Append
           float f[16];
           widen(raw[i].a, f);
           widen(raw[i].b, f + 8);
-          if (run.rotated) rotate<INTER>(f, g);
+          if (run.rotated) rotate<INTER>(f, g, p.one);
           *reinterpret_cast<uint4*>(dst + h * p.D + run.off_a) = narrow(f);
           *reinterpret_cast<uint4*>(dst + h * p.D + run.off_b) = narrow(f + 8);
         }
@@ -389,6 +395,7 @@ sg_status_t append_launch(const AttnShape& s, const AttnArgs& a) {
   p.rot_table = a.rotary.table;
   p.max_pos = a.rotary.max_pos;
   p.rot = a.rotary.rot;
+  p.one = 1.f;
   p.q = static_cast<const uint16_t*>(a.q);
   p.k = static_cast<const uint16_t*>(a.k);
   p.v = static_cast<const uint16_t*>(a.v);
@@ -411,7 +418,15 @@ sg_status_t append_launch(const AttnShape& s, const AttnArgs& a) {
   const int64_t by_block = a.Tq / kKvBlock + 2 * a.B;
   p.by_token = a.Tq <= by_block;
   const unsigned units = static_cast<unsigned>(p.by_token ? a.Tq : by_block);
-  GemmLaunch l(dim3(units, 1), dim3(kThreads), 0, a.stream, 1);
+  // A CTA's warps take one or more items each: of 16 tokens, 2 Hk heads of K and V, and the
+  // query heads 8 at a time for as many tokens as a warp holds.  Fewer units than some waves of
+  // CTAs are split along the items, down to one a warp.
+  const int64_t rows = s.D > 64 ? 4 : 8;
+  const int64_t items = p.by_token ? 2 * ((s.Hk + rows - 1) / rows) + (s.Hq + rows * kHeadPasses - 1) / (rows * kHeadPasses)
+                                   : 2 * s.Hk + kKvBlock / rows * ((s.Hq + kHeadPasses - 1) / kHeadPasses);
+  const int64_t want = (p.by_token ? 1 : kWaves) * kCtas * s.num_sms / units, most = (items + kWarps - 1) / kWarps;
+  const unsigned split = static_cast<unsigned>(want < 1 ? 1 : want < most ? want : most);
+  GemmLaunch l(dim3(units, split), dim3(kThreads), 0, a.stream, 1);
   const bool inter = a.rotary.interleaved != 0;
   const cudaError_t e = s.D > 64 ? launch<8>(&l.cfg, inter, p) : launch<4>(&l.cfg, inter, p);
   if (e != cudaSuccess) {
