@@ -15,6 +15,10 @@ from . import binding
 
 BLOCK = 16  # tokens that share a scale
 
+# torch's current stream as a number; without the Stream object, building which takes longer than a launch
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 class KVCache:
     """Keys and values of ``num_pages`` pages: e4m3 codes uint8 [num_pages, Hk, page, D]
@@ -139,7 +143,7 @@ class PagedAttention:
         return t
 
     def _stream(self, stream):
-        return torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
+        return _current_stream(self.device.index) if stream is None else stream
 
     # -- operators ----------------------------------------------------------------
 
