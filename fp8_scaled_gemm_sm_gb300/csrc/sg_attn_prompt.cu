@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             if (blocks[0] > 0) scores(0, 0, 0);
             if (blocks[1] > 0) scores(1, 0, 0);
             mma_commit(kv_empty(0));
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, mbar_wait(p_full(t), j & 1, wd, kWhereMmaTmemEmpty));
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
+            if (elect_one()) {
               const uint32_t idesc = instr_desc(1, 1, kRows, HD) | kIdescBMajorN;
               const uint64_t v = smem_desc(sKv + vs * L::kTile, L::kBox, 1024, 2);
               const int steps = (min(kRows, kmax[t] - j * kRows) + 15) / 16;
@@ -252,18 +252,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 k_ready = true;
               }
-              if (lane == 0) scores(t, j + 1, stage);
+              if (elect_one()) scores(t, j + 1, stage);
             }
           }
           if (!ok) break;
-          if (lane == 0) {
+          if (elect_one()) {
             mma_commit(kv_empty(vs));
             if (k_ready) mma_commit(kv_empty(stage));
           }
           if (k_ready) advance();
         }
         // every MMA has finished and every commit has landed before the CTA exits
-        if (lane == 0) {
+        if (elect_one()) {
           mma_commit(drain_bar);
           mbar_wait_drain(drain_bar, 0, 200000000ull);
         }
