@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = blocks[t];
     const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
     float ref = -INFINITY;     // r, in log2 units
-    uint64_t sum2 = 0;         // two partial row sums
+    uint64_t sum2[2] = {0, 0};  // four partial row sums
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       ok = __all_sync(0xffffffffu, mbar_wait(s_full(t), j & 1, wd, kWhereEpiTmemFull));
@@ -303,11 +303,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i)
             if (32 * c + i >= room) s[c][i] = 0xFF800000u;
       }
-      float mx = -INFINITY;
+      float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains: one would wait for itself
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[c][i]));
+        for (int i = 0; i < 32; i += 2)
+          tops[(i >> 1) & 3] = max3(tops[(i >> 1) & 3], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+      float mx = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
       mx *= p.scale_log2;
       if (j == 0) {
         ref = mx;
@@ -317,7 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float by = move ? ex2(ref - mx) : 1.f;
           if (move) ref = mx;
           const uint64_t by2 = pack_f32x2(by, by);
-          sum2 = mul_f32x2(sum2, by2);
+          sum2[0] = mul_f32x2(sum2[0], by2);
+          sum2[1] = mul_f32x2(sum2[1], by2);
 #pragma unroll
           for (int c = 0; c < HD / 32; ++c) {
             uint32_t o[32];
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             unpack_f32x2(fma_f32x2(pack_f32x2(s[c][2 * i], s[c][2 * i + 1]), scale2, neg2), x, y);
             x = ex2(x);
             y = ex2(y);
-            sum2 = add_f32x2(sum2, pack_f32x2(x, y));
+            sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(x, y));
             w[i] = pack_bf16x2(x, y);
           }
           tmem_st_32x32b_x16(s_addr + 16 * c, w);
@@ -355,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       tc_fence_after();
       float lo, hi;
-      unpack_f32x2(sum2, lo, hi);
+      unpack_f32x2(add_f32x2(sum2[0], sum2[1]), lo, hi);
       const float sum = lo + hi;
       const bool none = sum == 0.f;
       const float inv = none ? 0.f : 1.f / sum;
