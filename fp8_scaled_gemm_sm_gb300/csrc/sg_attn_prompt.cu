@@ -40,8 +40,9 @@ namespace {
 constexpr int kRows = 128;   // rows of a tile, keys of a block
 constexpr int kThreads = 384;
 // Registers a thread of the softmax warpgroups and of the third (producer, MMA issuer, two
-// idle warps): 2 x 216 + 72 = 3 x 168, what the block is launched with.
-constexpr int kSoftmaxRegs = 216, kIssueRegs = 72;
+// idle warps): 2 x 200 + 104 = 3 x 168, what the block is launched with.
+constexpr int kSoftmaxRegs = 200, kIssueRegs = 104;
+constexpr int kEarly = 4;  // 16-key steps of a block whose weights are handed over first
 constexpr float kSlack = 8.f;  // log2 of the largest weight
 
 struct PromptParams {
@@ -66,7 +67,7 @@ struct PromptLayout {
   static constexpr int kStages = HD == 128 ? 5 : 8;
   static constexpr int kOffKv = 2 * kTile;
   static constexpr int kOffBar = kOffKv + kStages * kTile;
-  static constexpr int kNumBars = 2 * kStages + 8;
+  static constexpr int kNumBars = 2 * kStages + 10;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffMisc + 64;
   static constexpr int kDynSmem = kBytes + 1024;
@@ -87,8 +88,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto kv_empty = [&](int s) { return bar0 + 8 * (S + s); };
   auto s_full = [&](int t) { return bar0 + 8 * (2 * S + t); };
   auto p_full = [&](int t) { return bar0 + 8 * (2 * S + 2 + t); };
-  auto o_full = [&](int t) { return bar0 + 8 * (2 * S + 4 + t); };
-  const uint32_t q_full = bar0 + 8 * (2 * S + 6), drain_bar = bar0 + 8 * (2 * S + 7);
+  auto p_half = [&](int t) { return bar0 + 8 * (2 * S + 4 + t); };
+  auto o_full = [&](int t) { return bar0 + 8 * (2 * S + 6 + t); };
+  const uint32_t q_full = bar0 + 8 * (2 * S + 8), drain_bar = bar0 + 8 * (2 * S + 9);
   int* misc = reinterpret_cast<int*>(smem + L::kOffMisc);  // [0] TMEM base, [1] abort, [2..13] counts
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -112,6 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full(t), 1);
+      mbar_init(p_half(t), kRows);
       mbar_init(p_full(t), kRows);
       mbar_init(o_full(t), 1);
     }
@@ -234,18 +237,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool k_ready = false;
           for (int t = 0; t < 2 && ok; ++t) {
             if (j >= blocks[t]) continue;
-            ok = __all_sync(0xffffffffu, mbar_wait(p_full(t), j & 1, wd, kWhereMmaTmemEmpty));
+            const int steps = (min(kRows, kmax[t] - j * kRows) + 15) / 16;
+          const uint64_t v = smem_desc(sKv + vs * L::kTile, L::kBox, 1024, 2);
+          const uint32_t idesc = instr_desc(1, 1, kRows, HD) | kIdescBMajorN;
+          // O_t += P_t V_j: what is stored first, then the rest
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(h ? p_full(t) : p_half(t), j & 1, wd, kWhereMmaTmemEmpty));
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-              const uint32_t idesc = instr_desc(1, 1, kRows, HD) | kIdescBMajorN;
-              const uint64_t v = smem_desc(sKv + vs * L::kTile, L::kBox, 1024, 2);
-              const int steps = (min(kRows, kmax[t] - j * kRows) + 15) / 16;
-              for (int i = 0; i < steps; ++i)
-                mma_f16_ts(tmem + 256 + t * HD, tmem + t * 128 + i * 8, desc_advance(v, i * 2048), idesc, (j | i) != 0);
-              if (j + 1 == blocks[t]) mma_commit(o_full(t));
+#pragma unroll
+              for (int i = h ? kEarly : 0; i < (h ? 8 : kEarly); ++i)
+                if (i < steps)
+                  mma_f16_ts(tmem + 256 + t * HD, tmem + t * 128 + i * 8, desc_advance(v, i * 2048), idesc, (j | i) != 0);
+              if (h && j + 1 == blocks[t]) mma_commit(o_full(t));
             }
-            if (j + 1 < blocks[t]) {
+          }
+          if (!ok) break;
+          if (j + 1 < blocks[t]) {
               if (!k_ready) {
                 ok = __all_sync(0xffffffffu, mbar_wait(kv_full(stage), phase, wd, kWhereMmaFull));
                 if (!ok) break;
@@ -321,14 +331,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t by2 = pack_f32x2(by, by);
           sum2[0] = mul_f32x2(sum2[0], by2);
           sum2[1] = mul_f32x2(sum2[1], by2);
-#pragma unroll
-          for (int c = 0; c < HD / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(o_addr + 32 * c, o);
+#pragma unroll 1
+          for (int c = 0; c < HD / 16; ++c) {  // S fills the registers: a little of O at a time
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(o_addr + 16 * c, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
-            tmem_st_32x32b_x32(o_addr + 32 * c, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+            tmem_st_32x32b_x16(o_addr + 16 * c, o);
           }
         }
       }
@@ -348,6 +358,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[i] = pack_bf16x2(x, y);
           }
           tmem_st_32x32b_x16(s_addr + 16 * c, w);
+        }
+        if (c == kEarly / 2 - 1) {
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(p_half(t));
         }
       }
       tmem_wait_st();
