@@ -17,8 +17,9 @@
 //                   registers, maximum, 2^x, row sum, P = bf16 back over S's columns; at the end
 //                   the output row, divided by the sum, straight to memory.
 //   warp 8          TMA producer: both Q tiles once, then K_0, V_0, K_1, V_1, ... through a ring.
-//   warp 9          MMA issuer: S_t = Q_t K_j^T (operands in shared memory), O_t += P_t V_j (P in
-//                   tensor memory, V as it lies in memory: N-major).
+//   warp 9          MMA issuer, one elected thread: S_t = Q_t K_j^T (operands in shared memory), O_t +=
+//                   P_t V_j (P in tensor memory, V as it lies in memory: N-major).
+//   warp 10         V rows past a sequence's end (below).
 // The tensor cores take the MMAs in order, so S_t of block j + 1, issued after
 // O_t += P_t V_j, cannot overwrite P_t early, and a softmax thread that sees it
 // complete may also touch O_t.
@@ -67,7 +68,7 @@ struct PromptLayout {
   static constexpr int kStages = HD == 128 ? 5 : 8;
   static constexpr int kOffKv = 2 * kTile;
   static constexpr int kOffBar = kOffKv + kStages * kTile;
-  static constexpr int kNumBars = 2 * kStages + 10;
+  static constexpr int kNumBars = 2 * kStages + 12;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffMisc + 64;
   static constexpr int kDynSmem = kBytes + 1024;
@@ -91,6 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto p_half = [&](int t) { return bar0 + 8 * (2 * S + 4 + t); };
   auto o_full = [&](int t) { return bar0 + 8 * (2 * S + 6 + t); };
   const uint32_t q_full = bar0 + 8 * (2 * S + 8), drain_bar = bar0 + 8 * (2 * S + 9);
+  const uint32_t v_last = bar0 + 8 * (2 * S + 10), v_clean = bar0 + 8 * (2 * S + 11);
   int* misc = reinterpret_cast<int*>(smem + L::kOffMisc);  // [0] TMEM base, [1] abort, [2..13] counts
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -119,6 +121,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(o_full(t), 1);
     }
     mbar_init(q_full, 1);
+    mbar_init(v_last, 1);
+    mbar_init(v_clean, 1);
     mbar_init(drain_bar, 1);
     misc[1] = 0;
     fence_mbarrier_init();
@@ -141,6 +145,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     blocks[t] = (kmax[t] + kRows - 1) / kRows;
   }
   const int num_blocks = max(blocks[0], blocks[1]);
+  // rows of the last V block that are not this sequence's but share a 16-key step with some that are
+  const int past = lk - (num_blocks - 1) * kRows;
+  const int tail_rows = num_blocks > 0 && past < kRows ? (16 - past) & 15 : 0;
   if (warp == 9) {
     tmem_alloc(smem_addr(&misc[0]), 512);
     tmem_relinquish();
@@ -188,9 +195,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((issued >> s) & 1) mbar_wait_drain(kv_full(s), (last_par >> s) & 1, 200000000ull);
         }
       }
+    } else if (warp == 10) {
+      // ---------------- V rows past the sequence's end ----------------
+      if (tail_rows > 0) {
+        const int st = (2 * num_blocks - 1) % S;  // the last V block's: all other loads come before it
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(v_last, 0, wd, kWhereMmaFull));
+        if (ok) {
+          for (int i = lane; i < tail_rows * 8 * L::kBoxes; i += 32)
+            st_shared_v4(sKv + st * L::kTile + (i / (tail_rows * 8)) * L::kBox + past * 128 + (i % (tail_rows * 8)) * 16, 0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_clean);
+        }
+      }
     } else if (warp == 9) {
-      // ---------------- MMA issuer (one lane issues) ----------------
-      if (num_blocks > 0) {
+      // ---------------- MMA issuer ----------------
+      if (num_blocks > 0 && elect_one()) {
         int stage = 0;
         uint32_t phase = 0;
         auto advance = [&]() {
@@ -199,84 +219,72 @@ __global__ void __launch_bounds__(kThreads, 1)
             phase ^= 1;
           }
         };
-        auto scores = [&](int t, int j, int st) {  // S_t = Q_t K_j^T
+        auto wait = [&](uint32_t bar, uint32_t parity, int where) {
+          const bool got = mbar_wait<true>(bar, parity, wd, where);
+          tc_fence_after();
+          return got;
+        };
+        auto scores = [&](int t, int j) {  // S_t = Q_t K_j^T
           const int n = (min(kRows, kmax[t] - j * kRows) + 15) & ~15;
           const uint32_t idesc = instr_desc(1, 1, kRows, n);
-          const uint64_t a = kmajor_sw128_desc(sQ + t * L::kTile), k = kmajor_sw128_desc(sKv + st * L::kTile);
-  #pragma unroll
+          const uint64_t a = kmajor_sw128_desc(sQ + t * L::kTile), k = kmajor_sw128_desc(sKv + stage * L::kTile);
+#pragma unroll
           for (int i = 0; i < HD / 16; ++i) {
             const uint32_t at = (i / 4) * L::kBox + (i % 4) * 32;
             mma_f16_ss(tmem + t * 128, desc_advance(a, at), desc_advance(k, at), idesc, i != 0);
           }
           mma_commit(s_full(t));
         };
-        bool ok = mbar_wait(q_full, 0, wd, kWhereMmaFull) && mbar_wait(kv_full(0), 0, wd, kWhereMmaFull);
-        ok = __all_sync(0xffffffffu, ok);
+        bool ok = wait(q_full, 0, kWhereMmaFull) && wait(kv_full(0), 0, kWhereMmaFull);
         if (ok) {
-          tc_fence_after();
-          if (elect_one()) {
-            if (blocks[0] > 0) scores(0, 0, 0);
-            if (blocks[1] > 0) scores(1, 0, 0);
-            mma_commit(kv_empty(0));
-          }
-          advance();
+          if (blocks[0] > 0) scores(0, 0);
+          if (blocks[1] > 0) scores(1, 0);
+          mma_commit(kv_empty(0));
         }
+        advance();
         for (int j = 0; j < num_blocks && ok; ++j) {
-          ok = __all_sync(0xffffffffu, mbar_wait(kv_full(stage), phase, wd, kWhereMmaFull));
-          if (!ok) break;
+          ok = wait(kv_full(stage), phase, kWhereMmaFull);  // V_j
           const int vs = stage;
           advance();
-          const int left = lk - j * kRows;  // V rows of this sequence
-          if (left < kRows && (left & 15)) {
-            const int rows = 16 - (left & 15);
-            for (int i = lane; i < rows * 8 * L::kBoxes; i += 32)
-              st_shared_v4(sKv + vs * L::kTile + (i / (rows * 8)) * L::kBox + left * 128 + (i % (rows * 8)) * 16, 0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
+          if (ok && j + 1 == num_blocks && tail_rows > 0) {
+            mbar_arrive(v_last);
+            ok = wait(v_clean, 0, kWhereMmaFull);
           }
           bool k_ready = false;
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (j >= blocks[t]) continue;
-            const int steps = (min(kRows, kmax[t] - j * kRows) + 15) / 16;
           const uint64_t v = smem_desc(sKv + vs * L::kTile, L::kBox, 1024, 2);
-          const uint32_t idesc = instr_desc(1, 1, kRows, HD) | kIdescBMajorN;
-          // O_t += P_t V_j: what is stored first, then the rest
+          constexpr uint32_t idesc = instr_desc(1, 1, kRows, HD) | kIdescBMajorN;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(h ? p_full(t) : p_half(t), j & 1, wd, kWhereMmaTmemEmpty));
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
+          for (int t = 0; t < 2; ++t) {
+            if (ok && j < blocks[t]) {
+              const int steps = (min(kRows, kmax[t] - j * kRows) + 15) / 16;
+              // O_t += P_t V_j: what is stored first, then the rest
 #pragma unroll
-              for (int i = h ? kEarly : 0; i < (h ? 8 : kEarly); ++i)
-                if (i < steps)
-                  mma_f16_ts(tmem + 256 + t * HD, tmem + t * 128 + i * 8, desc_advance(v, i * 2048), idesc, (j | i) != 0);
-              if (h && j + 1 == blocks[t]) mma_commit(o_full(t));
-            }
-          }
-          if (!ok) break;
-          if (j + 1 < blocks[t]) {
-              if (!k_ready) {
-                ok = __all_sync(0xffffffffu, mbar_wait(kv_full(stage), phase, wd, kWhereMmaFull));
-                if (!ok) break;
-                tc_fence_after();
-                k_ready = true;
+              for (int h = 0; h < 2; ++h) {
+                ok = ok && wait(h ? p_full(t) : p_half(t), j & 1, kWhereMmaTmemEmpty);
+                if (ok) {
+#pragma unroll
+                  for (int i = h ? kEarly : 0; i < (h ? 8 : kEarly); ++i)
+                    if (i < steps)
+                      mma_f16_ts(tmem + 256 + t * HD, tmem + t * 128 + i * 8, desc_advance(v, i * 2048), idesc, (j | i) != 0);
+                  if (h && j + 1 == blocks[t]) mma_commit(o_full(t));
+                }
               }
-              if (elect_one()) scores(t, j + 1, stage);
+              if (ok && j + 1 < blocks[t]) {
+                if (!k_ready) ok = wait(kv_full(stage), phase, kWhereMmaFull);
+                k_ready = true;
+                if (ok) scores(t, j + 1);
+              }
             }
           }
-          if (!ok) break;
-          if (elect_one()) {
-            mma_commit(kv_empty(vs));
-            if (k_ready) mma_commit(kv_empty(stage));
+          mma_commit(kv_empty(vs));
+          if (k_ready) {
+            mma_commit(kv_empty(stage));
+            advance();
           }
-          if (k_ready) advance();
         }
         // every MMA has finished and every commit has landed before the CTA exits
-        if (elect_one()) {
-          mma_commit(drain_bar);
-          mbar_wait_drain(drain_bar, 0, 200000000ull);
-        }
+        mma_commit(drain_bar);
+        mbar_wait_drain(drain_bar, 0, 200000000ull);
       }
     }
   } else {
