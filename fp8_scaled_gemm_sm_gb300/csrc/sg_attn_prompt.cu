@@ -365,9 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(x, y));
             w[i] = pack_bf16x2(x, y);
           }
+          if (c == kEarly / 2) {  // by now what was stored before is there
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(p_half(t));
+          }
           tmem_st_32x32b_x16(s_addr + 16 * c, w);
-        }
-        if (c == kEarly / 2 - 1) {
+        } else if (c == kEarly / 2) {
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(p_half(t));
