@@ -42,8 +42,9 @@ constexpr int kRows = 128;   // rows of a tile, keys of a block
 constexpr int kThreads = 384;
 // Registers a thread of the softmax warpgroups and of the third (producer, MMA issuer, two
 // idle warps): 2 x 200 + 104 = 3 x 168, what the block is launched with.
-constexpr int kSoftmaxRegs = 200, kIssueRegs = 104;
+constexpr int kSoftmaxRegs = 192, kIssueRegs = 120;
 constexpr int kEarly = 4;  // 16-key steps of a block whose weights are handed over first
+constexpr int kTileKeys = 64, kTileThreads = 192;  // of the kernel with one row tile a CTA, for D <= 64
 constexpr float kSlack = 8.f;  // log2 of the largest weight
 
 struct PromptParams {
@@ -59,6 +60,140 @@ struct PromptParams {
   int* status;
   uint64_t timeout_ns;
 };
+
+// What a CTA works on: `tokens` consecutive query tokens of a sequence.
+struct Unit {
+  int b;            // sequence; -1: nothing
+  int q0, lq;       // its first query and their number
+  int k0, lk;       // its keys
+  int first;        // the unit's first token in the sequence
+};
+
+__device__ __forceinline__ Unit sequence(const PromptParams& p, int b) {
+  Unit u;
+  u.b = b;
+  u.q0 = min(max(__ldg(p.cu_q + b), 0), p.Tq);
+  u.lq = max(min(max(__ldg(p.cu_q + b + 1), 0), p.Tq) - u.q0, 0);
+  u.k0 = min(max(__ldg(p.cu_k + b), 0), p.Tk);
+  u.lk = min(max(__ldg(p.cu_k + b + 1), u.k0), p.Tk) - u.k0;
+  u.first = 0;
+  return u;
+}
+
+// Unit `x` of all sequences' units of `tokens` tokens, those that see most keys first, so
+// that the GPU does not end on a few long ones.  A unit's level is the number of
+// its keys in units of tokens; the number of units at or above a level is a sum over sequences, one a
+// lane and round, so a search for x's level takes a dozen warp sums.
+// More than kPickRounds * 32 sequences are numbered from cu_q[b] / tokens + b
+// (at most n / tokens + 1 units each), the last rows first.
+constexpr int kPickRounds = 4;
+
+__device__ __forceinline__ Unit pick_unit(const PromptParams& p, int x, int tokens, int lane) {
+  if (p.B > kPickRounds * 32) {
+    const int unit = p.units - 1 - x;
+    int b = -1;
+    for (int i = lane; i < p.B; i += 32) b += min(max(__ldg(p.cu_q + i), 0), p.Tq) / tokens + i <= unit;
+    b = __reduce_add_sync(0xffffffffu, b) + 31;  // every lane began at -1
+    Unit u{};
+    u.b = -1;
+    if (b < 0) return u;
+    u = sequence(p, b);
+    u.first = (unit - (u.q0 / tokens + b)) * tokens;
+    if (u.first < 0 || u.first >= u.lq) u.b = -1;
+    return u;
+  }
+  if (p.B == 1) {
+    Unit u = sequence(p, 0);
+    u.first = ((u.lq + tokens - 1) / tokens - 1 - x) * tokens;
+    if (u.first < 0) u.b = -1;
+    return u;
+  }
+  int n[kPickRounds], off[kPickRounds];  // a sequence's units, and the level below its first
+  int top = 0;
+#pragma unroll
+  for (int r = 0; r < kPickRounds; ++r) {
+    n[r] = off[r] = 0;
+    if (32 * r + lane < p.B) {
+      const Unit u = sequence(p, 32 * r + lane);
+      n[r] = (u.lq + tokens - 1) / tokens;
+      off[r] = (p.causal ? max(u.lk - u.lq, 0) : u.lk) / tokens;
+      top = max(top, off[r] + (p.causal ? n[r] : 1));
+    }
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  // units of a sequence at levels from `level` on: unit i is at off + i, or all at off
+  auto above = [&](int r, int level) {
+    return p.causal ? min(n[r], max(off[r] + n[r] - level, 0)) : (off[r] >= level ? n[r] : 0);
+  };
+  auto count = [&](int level) {
+    int c = 0;
+#pragma unroll
+    for (int r = 0; r < kPickRounds; ++r)
+      if (32 * r < p.B) c += above(r, level);
+    return __reduce_add_sync(0xffffffffu, c);
+  };
+  int lo = 0, hi = top + 1;  // count(lo) > x >= count(hi)
+  Unit u{};
+  u.b = -1;
+  if (count(0) <= x) return u;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (count(mid) > x) lo = mid; else hi = mid;
+  }
+  int rest = x - count(lo + 1);
+#pragma unroll
+  for (int r = 0; r < kPickRounds; ++r) {
+    if (32 * r >= p.B) break;
+    const int here = above(r, lo) - above(r, lo + 1);
+    int scan = here;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += up;
+    }
+    const int all = __shfl_sync(0xffffffffu, scan, 31);
+    if (rest < all) {
+      const int owner = __ffs(__ballot_sync(0xffffffffu, rest < scan)) - 1;
+      const int before = __shfl_sync(0xffffffffu, scan - here, owner), base = __shfl_sync(0xffffffffu, off[r], owner);
+      u = sequence(p, 32 * r + owner);
+      u.first = (p.causal ? lo - base : rest - before) * tokens;
+      return u;
+    }
+    rest -= all;
+  }
+  return u;
+}
+
+// One thread's row of the output: CHUNKS times 32 dimensions from `first` on, out of tensor memory, over its sum.
+template <int CHUNKS>
+__device__ __forceinline__ void put_rows(const PromptParams& p, uint32_t o_addr, int first, bool some, float sum, float ref,
+                                         int q0, int tok, int lq, int head, bool with_lse) {
+  const bool none = sum == 0.f;
+  const float inv = none ? 0.f : 1.f / sum;
+  const int64_t at = static_cast<int64_t>(q0 + tok) * p.Hq + head;
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    uint32_t o[32];
+    if (some) {
+      tmem_ld_32x32b_x32(o_addr + 32 * c, o);
+      tmem_wait_ld();
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+    if (tok < lq) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (first + 32 * c + 8 * i < p.D) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(o[8 * i + 2 * e + 1]));
+          *reinterpret_cast<uint4*>(p.out + at * p.D + first + 32 * c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+  }
+  if (with_lse && tok < lq && p.lse) p.lse[at] = none ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+}
 
 template <int HD>
 struct PromptLayout {
@@ -93,23 +228,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto o_full = [&](int t) { return bar0 + 8 * (2 * S + 6 + t); };
   const uint32_t q_full = bar0 + 8 * (2 * S + 8), drain_bar = bar0 + 8 * (2 * S + 9);
   const uint32_t v_last = bar0 + 8 * (2 * S + 10), v_clean = bar0 + 8 * (2 * S + 11);
-  int* misc = reinterpret_cast<int*>(smem + L::kOffMisc);  // [0] TMEM base, [1] abort, [2..13] counts
+  int* misc = reinterpret_cast<int*>(smem + L::kOffMisc);  // [0] TMEM base, [1] abort, [2..7] the unit
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   grid_dep_launch();
   grid_dep_wait();
-  // Units of 2 row tiles are numbered from cu_q[b] / tokens + b for sequence b (at most
-  // n / tokens + 1 of them), heads fastest, the last (for causal prompts: the
-  // longest) rows first.
   const int tile_tokens = kRows >> p.gshift;
-  const int unit = p.units - 1 - static_cast<int>(blockIdx.x) / p.head_groups;
   const int head0 = static_cast<int>(blockIdx.x) % p.head_groups << p.gshift;
-  auto clampq = [&](int i) { return min(max(__ldg(p.cu_q + i), 0), p.Tq); };
-  int below = 0;
-  for (int i = tid; i < p.B; i += kThreads) below += clampq(i) / (2 * tile_tokens) + i <= unit;
-  below = __reduce_add_sync(0xffffffffu, below);
-  if (lane == 0) misc[2 + warp] = below;
-  if (tid == 0) {
+  if (warp == 0) {
+    const Unit u = pick_unit(p, static_cast<int>(blockIdx.x) / p.head_groups, 2 * tile_tokens, lane);
+    if (lane == 0) *reinterpret_cast<Unit*>(misc + 2) = u;
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_addr(&misc[0]), 512);
+    tmem_relinquish();
+  }
+  if (tid == 32) {
     for (int s = 0; s < S; ++s) {
       mbar_init(kv_full(s), 1);
       mbar_init(kv_empty(s), 1);
@@ -127,15 +261,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     misc[1] = 0;
     fence_mbarrier_init();
   }
+  tc_fence_before();
   __syncthreads();
-  int b = -1;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) b += misc[2 + w];
-  if (b < 0) return;
-  const int q0 = clampq(b), lq = clampq(b + 1) - q0;
-  const int k0 = min(max(__ldg(p.cu_k + b), 0), p.Tk), lk = min(max(__ldg(p.cu_k + b + 1), k0), p.Tk) - k0;
-  const int tok0 = (unit - (q0 / (2 * tile_tokens) + b)) * 2 * tile_tokens;
-  if (tok0 >= lq) return;
+  tc_fence_after();
+  if (misc[2] < 0) {
+    if (warp == 9) tmem_dealloc(static_cast<uint32_t>(misc[0]), 512);
+    return;
+  }
+  const int q0 = __shfl_sync(0xffffffffu, misc[3], 0), lq = __shfl_sync(0xffffffffu, misc[4], 0), k0 = __shfl_sync(0xffffffffu, misc[5], 0),
+            lk = __shfl_sync(0xffffffffu, misc[6], 0), tok0 = __shfl_sync(0xffffffffu, misc[7], 0);
   auto visible = [&](int tok) { return p.causal ? min(lk, tok + 1 + lk - lq) : lk; };
   int blocks[2], kmax[2];  // key blocks of a tile, keys that its last row sees
 #pragma unroll
@@ -148,13 +282,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // rows of the last V block that are not this sequence's but share a 16-key step with some that are
   const int past = lk - (num_blocks - 1) * kRows;
   const int tail_rows = num_blocks > 0 && past < kRows ? (16 - past) & 15 : 0;
-  if (warp == 9) {
-    tmem_alloc(smem_addr(&misc[0]), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
   const Watchdog wd{p.status, p.timeout_ns, reinterpret_cast<volatile int*>(&misc[1])};
 
@@ -386,32 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       float lo, hi;
       unpack_f32x2(add_f32x2(sum2[0], sum2[1]), lo, hi);
-      const float sum = lo + hi;
-      const bool none = sum == 0.f;
-      const float inv = none ? 0.f : 1.f / sum;
-      const int64_t at = static_cast<int64_t>(q0 + tok) * p.Hq + head;
-#pragma unroll
-      for (int c = 0; c < HD / 32; ++c) {
-        uint32_t o[32];
-        if (n > 0) {
-          tmem_ld_32x32b_x32(o_addr + 32 * c, o);
-          tmem_wait_ld();
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
-        if (tok < lq) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (32 * c + 8 * i < p.D) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(o[8 * i + 2 * e + 1]));
-              *reinterpret_cast<uint4*>(p.out + at * p.D + 32 * c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-      }
-      if (tok < lq && p.lse) p.lse[at] = none ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+      put_rows<HD / 32>(p, o_addr, 0, n > 0, lo + hi, ref, q0, tok, lq, head, true);
     }
   }
 
@@ -424,7 +526,289 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ---- one row tile a CTA --------------------------------------------------------
+//
+// Heads of 64 dimensions: an MMA is half as long and the softmax is not, so two tiles an SM leave
+// the tensor cores waiting.  Here a CTA owns one row tile with 64 columns of tensor memory
+// for scores of 64 keys (weights over them) and 64 for the output, and four
+// CTAs share an SM: four softmaxes hide each other's waits, and the tiles are dealt out one by one, which
+// ragged prompts need.
+//   warps 0-3  softmax and output, one thread a row
+//   warp 4     TMA producer: Q, then K_0, V_0, K_1, V_1, ...; then V rows past the sequence's end
+//   warp 5     MMA issuer, one elected thread
+
 template <int HD>
+struct TileLayout {
+  static constexpr int kCtas = 256 / HD;                  // an SM
+  static constexpr int kBoxes = HD / 64;
+  static constexpr int kQBox = kRows * 128;
+  static constexpr int kQTile = kBoxes * kQBox;
+  static constexpr int kBox = kTileKeys * 128;
+  static constexpr int kTile = kBoxes * kBox;             // a K or V block
+  static constexpr int kStages = 4;
+  static constexpr int kCols = 64 + HD <= 128 ? 128 : 256;  // tensor memory: S, then O
+  static constexpr int kOffKv = kQTile;
+  static constexpr int kOffBar = kOffKv + kStages * kTile;
+  static constexpr int kNumBars = 2 * kStages + 7;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kBytes = kOffMisc + 48;
+  static constexpr int kDynSmem = kBytes + 1024;
+  static_assert(kCtas * (kDynSmem + 1024) <= 233472 && (kCtas + 1) * kDynSmem > 233472, "shared memory of kCtas CTAs, and no more");
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kTileThreads, TileLayout<HD>::kCtas)
+    prompt_tile_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const PromptParams p) {
+  using L = TileLayout<HD>;
+  constexpr int S = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sQ = smem_addr(smem), sKv = smem_addr(smem + L::kOffKv), bar0 = smem_addr(smem + L::kOffBar);
+  auto kv_full = [&](int s) { return bar0 + 8 * s; };
+  auto kv_empty = [&](int s) { return bar0 + 8 * (S + s); };
+  const uint32_t s_full = bar0 + 8 * (2 * S), p_full = s_full + 8, o_full = s_full + 16, q_full = s_full + 24;
+  const uint32_t drain_bar = s_full + 32, v_last = s_full + 40, v_clean = s_full + 48;
+  int* misc = reinterpret_cast<int*>(smem + L::kOffMisc);  // [0] TMEM base, [1] abort, [2..7] the unit
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  grid_dep_launch();
+  grid_dep_wait();
+  const int tile_tokens = kRows >> p.gshift;
+  const int head0 = static_cast<int>(blockIdx.x) % p.head_groups << p.gshift;
+  if (warp == 0) {
+    const Unit u = pick_unit(p, static_cast<int>(blockIdx.x) / p.head_groups, tile_tokens, lane);
+    if (lane == 0) *reinterpret_cast<Unit*>(misc + 2) = u;
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_addr(&misc[0]), L::kCols);
+    tmem_relinquish();
+  }
+  if (tid == 32) {
+    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar0 + 8 * i, bar0 + 8 * i == p_full ? kRows : 1);
+    misc[1] = 0;
+    fence_mbarrier_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (misc[2] < 0) {
+    if (warp == 5) tmem_dealloc(static_cast<uint32_t>(misc[0]), L::kCols);
+    return;
+  }
+  const int q0 = __shfl_sync(0xffffffffu, misc[3], 0), lq = __shfl_sync(0xffffffffu, misc[4], 0), k0 = __shfl_sync(0xffffffffu, misc[5], 0),
+            lk = __shfl_sync(0xffffffffu, misc[6], 0), tok0 = __shfl_sync(0xffffffffu, misc[7], 0);
+  auto visible = [&](int tok) { return p.causal ? min(lk, tok + 1 + lk - lq) : lk; };
+  const int kmax = max(visible(min(tok0 + tile_tokens, lq) - 1), 0);  // keys that the last row sees
+  const int n = (kmax + kTileKeys - 1) / kTileKeys;
+  // rows of the last V block that are not this sequence's but share a 16-key step with some that are
+  const int past = lk - (n - 1) * kTileKeys;
+  const int tail_rows = n > 0 && past < kTileKeys ? (16 - past) & 15 : 0;
+  const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+  const Watchdog wd{p.status, p.timeout_ns, reinterpret_cast<volatile int*>(&misc[1])};
+
+  if (warp == 4) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0 && n > 0) {
+      const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
+      mbar_arrive_expect_tx(q_full, L::kQTile);
+      for (int x = 0; x < L::kBoxes; ++x)
+        tma_load_3d_hint(sQ + x * L::kQBox, &tmQ, x * 64, head0, q0 + tok0, q_full, once);
+      const int kv_head = head0 / p.group;
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, last_par = 0;
+      bool ok = true;
+      for (int i = 0; i < 2 * n; ++i) {
+        if (!mbar_wait(kv_empty(stage), phase ^ 1, wd, kWhereProducerEmpty)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(kv_full(stage), L::kTile);
+        for (int x = 0; x < L::kBoxes; ++x)
+          tma_load_3d_hint(sKv + stage * L::kTile + x * L::kBox, (i & 1) ? &tmV : &tmK, x * 64, kv_head,
+                           k0 + (i >> 1) * kTileKeys, kv_full(stage), keep);
+        issued |= 1u << stage;
+        last_par = (last_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) {  // loads in flight must land before the CTA can exit
+        mbar_wait_drain(q_full, 0, 200000000ull);
+        for (int s = 0; s < S; ++s)
+          if ((issued >> s) & 1) mbar_wait_drain(kv_full(s), (last_par >> s) & 1, 200000000ull);
+      }
+    }
+    __syncwarp();
+    if (tail_rows > 0 && __all_sync(0xffffffffu, mbar_wait(v_last, 0, wd, kWhereMmaFull))) {
+      const int st = (2 * n - 1) % S;
+      for (int i = lane; i < tail_rows * 8 * L::kBoxes; i += 32)
+        st_shared_v4(sKv + st * L::kTile + (i / (tail_rows * 8)) * L::kBox + past * 128 + (i % (tail_rows * 8)) * 16, 0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_clean);
+    }
+  } else if (warp == 5) {
+    // ---------------- MMA issuer ----------------
+    if (n > 0 && elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0;
+      auto advance = [&]() {
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1;
+        }
+      };
+      auto wait = [&](uint32_t bar, uint32_t parity, int where) {
+        const bool got = mbar_wait<true>(bar, parity, wd, where);
+        tc_fence_after();
+        return got;
+      };
+      auto scores = [&](int j) {  // S = Q K_j^T
+        const int keys = (min(kTileKeys, kmax - j * kTileKeys) + 15) & ~15;
+        const uint32_t idesc = instr_desc(1, 1, kRows, keys);
+        const uint64_t a = kmajor_sw128_desc(sQ), k = kmajor_sw128_desc(sKv + stage * L::kTile);
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i)
+          mma_f16_ss(tmem, desc_advance(a, (i / 4) * L::kQBox + (i % 4) * 32), desc_advance(k, (i / 4) * L::kBox + (i % 4) * 32),
+                     idesc, i != 0);
+        mma_commit(s_full);
+        mma_commit(kv_empty(stage));
+        advance();
+      };
+      bool ok = wait(q_full, 0, kWhereMmaFull) && wait(kv_full(0), 0, kWhereMmaFull);
+      if (ok) scores(0);
+      constexpr uint32_t idesc = instr_desc(1, 1, kRows, HD) | kIdescBMajorN;
+      for (int j = 0; j < n && ok; ++j) {
+        const int vs = stage;
+        ok = wait(kv_full(vs), phase, kWhereMmaFull);
+        advance();
+        if (ok && j + 1 == n && tail_rows > 0) {
+          mbar_arrive(v_last);
+          ok = wait(v_clean, 0, kWhereMmaFull);
+        }
+        // K_j+1 as well, so that nothing is waited for between the two products
+        if (ok && j + 1 < n) ok = wait(kv_full(stage), phase, kWhereMmaFull);
+        ok = ok && wait(p_full, j & 1, kWhereMmaTmemEmpty);
+        if (!ok) break;
+        const uint64_t v = smem_desc(sKv + vs * L::kTile, L::kBox, 1024, 2);
+        const int steps = (min(kTileKeys, kmax - j * kTileKeys) + 15) / 16;
+#pragma unroll
+        for (int i = 0; i < kTileKeys / 16; ++i)
+          if (i < steps) mma_f16_ts(tmem + 64, tmem + i * 8, desc_advance(v, i * 2048), idesc, (j | i) != 0);
+        if (j + 1 < n)
+          scores(j + 1);
+        else
+          mma_commit(o_full);
+        mma_commit(kv_empty(vs));
+      }
+      // every MMA has finished and every commit has landed before the CTA exits
+      mma_commit(drain_bar);
+      mbar_wait_drain(drain_bar, 0, 200000000ull);
+    }
+  } else {
+    // ---------------- softmax and output ----------------
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t s_addr = tmem + lanes, o_addr = s_addr + 64;
+    const int row = warp * 32 + lane;
+    const int tok = tok0 + (row >> p.gshift);
+    const int head = head0 + (row & ((1 << p.gshift) - 1));
+    const int lim = visible(tok);
+    const int lim_warp = visible(tok0 + (warp * 32 >> p.gshift));  // least of the warp's
+    const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
+    float ref = -INFINITY;      // r, in log2 units
+    uint64_t sum2[2] = {0, 0};  // four partial row sums
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      ok = __all_sync(0xffffffffu, mbar_wait(s_full, j & 1, wd, kWhereEpiTmemFull));
+      if (!ok) break;
+      tc_fence_after();
+      const int chunks = (min(kTileKeys, kmax - j * kTileKeys) + 31) / 32;
+      const int room = lim - j * kTileKeys;
+      const bool edge = lim_warp - j * kTileKeys < kTileKeys;
+      // twice over the scores, for the maximum and for the weights: 64 of them do not fit the registers
+      uint32_t s[32];
+      auto scores = [&](int c) {
+        tmem_ld_32x32b_x32(s_addr + 32 * c, s);
+        tmem_wait_ld();
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * c + i >= room) s[i] = 0xFF800000u;
+        }
+      };
+      float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {
+        scores(c);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2)
+          tops[(i >> 1) & 3] = max3(tops[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+      }
+      const float mx = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * p.scale_log2;
+      if (j == 0) {
+        ref = mx;
+      } else {
+        const bool move = mx > ref + kSlack;
+        if (__any_sync(0xffffffffu, move)) {
+          const float by = move ? ex2(ref - mx) : 1.f;
+          if (move) ref = mx;
+          const uint64_t by2 = pack_f32x2(by, by);
+          sum2[0] = mul_f32x2(sum2[0], by2);
+          sum2[1] = mul_f32x2(sum2[1], by2);
+#pragma unroll 1
+          for (int c = 0; c < HD / 16; ++c) {  // S fills the registers: a little of O at a time
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(o_addr + 16 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+            tmem_st_32x32b_x16(o_addr + 16 * c, o);
+          }
+        }
+      }
+      const float neg = ref == -INFINITY ? 0.f : -ref;
+      const uint64_t neg2 = pack_f32x2(neg, neg);
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {
+        scores(c);
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float x, y;
+          unpack_f32x2(fma_f32x2(pack_f32x2(s[2 * i], s[2 * i + 1]), scale2, neg2), x, y);
+          x = ex2(x);
+          y = ex2(y);
+          sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(x, y));
+          w[i] = pack_bf16x2(x, y);
+        }
+        tmem_st_32x32b_x16(s_addr + 16 * c, w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(p_full);
+    }
+    if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(o_full, 0, wd, kWhereEpiTmemFull));
+    if (ok) {
+      tc_fence_after();
+      float lo, hi;
+      unpack_f32x2(add_f32x2(sum2[0], sum2[1]), lo, hi);
+      put_rows<HD / 32>(p, o_addr, 0, n > 0, lo + hi, ref, q0, tok, lq, head, true);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kCols);
+  }
+}
+
+template <int HD, bool TILE>
 sg_status_t launch(const AttnShape& s, const AttnArgs& a) {
   PromptParams p{};
   p.cu_q = a.cu_q;
@@ -438,7 +822,7 @@ sg_status_t launch(const AttnShape& s, const AttnArgs& a) {
   p.group = s.Hq / s.Hk;
   while (p.gshift < 7 && p.group % (2 << p.gshift) == 0) ++p.gshift;
   p.head_groups = s.Hq >> p.gshift;
-  const int64_t units = a.Tq / (2 * (kRows >> p.gshift)) + a.B;
+  const int64_t units = a.Tq / ((TILE ? 1 : 2) * (kRows >> p.gshift)) + a.B;
   if (units * p.head_groups >= (int64_t(1) << 31)) return SG_ERR_UNSUPPORTED_SHAPE;
   p.units = static_cast<int>(units);
   p.scale_log2 = a.scale * 1.4426950408889634f;
@@ -455,14 +839,21 @@ sg_status_t launch(const AttnShape& s, const AttnArgs& a) {
   const uint64_t sk[2] = {D * el, static_cast<uint64_t>(keys ? a.k_stride : a.q_stride) * el};
   const uint64_t sv[2] = {D * el, static_cast<uint64_t>(keys ? a.v_stride : a.q_stride) * el};
   const uint32_t bq[3] = {64, 1u << p.gshift, static_cast<uint32_t>(kRows >> p.gshift)};
-  const uint32_t bk[3] = {64, 1, kRows};
+  const uint32_t bk[3] = {64, 1, TILE ? kTileKeys : kRows};
   CUtensorMap tmQ, tmK, tmV;
   if (!encode_3d(&tmQ, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, dq, sq, bq, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_3d(&tmK, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, keys ? a.k : a.q, dk, sk, bk, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_3d(&tmV, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, keys ? a.v : a.q, dk, sv, bk, CU_TENSOR_MAP_SWIZZLE_128B))
     return SG_ERR_CUDA;
-  GemmLaunch l(dim3(static_cast<unsigned>(units * p.head_groups)), dim3(kThreads), PromptLayout<HD>::kDynSmem, a.stream, 1);
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, prompt_kernel<HD>, tmQ, tmK, tmV, p);
+  const dim3 grid(static_cast<unsigned>(units * p.head_groups));
+  cudaError_t e;
+  if constexpr (TILE) {
+    GemmLaunch l(grid, dim3(kTileThreads), TileLayout<HD>::kDynSmem, a.stream, 1);
+    e = cudaLaunchKernelEx(&l.cfg, prompt_tile_kernel<HD>, tmQ, tmK, tmV, p);
+  } else {
+    GemmLaunch l(grid, dim3(kThreads), PromptLayout<HD>::kDynSmem, a.stream, 1);
+    e = cudaLaunchKernelEx(&l.cfg, prompt_kernel<HD>, tmQ, tmK, tmV, p);
+  }
   if (e != cudaSuccess) {
     note_cuda_error(e);
     cudaGetLastError();
@@ -474,12 +865,14 @@ sg_status_t launch(const AttnShape& s, const AttnArgs& a) {
 }  // namespace
 
 cudaError_t prompt_prepare() {
-  const cudaError_t e = cudaFuncSetAttribute(prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptLayout<64>::kDynSmem);
+  const cudaError_t e = cudaFuncSetAttribute(prompt_tile_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileLayout<64>::kDynSmem);
   return e == cudaSuccess
              ? cudaFuncSetAttribute(prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptLayout<128>::kDynSmem)
              : e;
 }
 
-sg_status_t prompt_launch(const AttnShape& s, const AttnArgs& a) { return s.D > 64 ? launch<128>(s, a) : launch<64>(s, a); }
+sg_status_t prompt_launch(const AttnShape& s, const AttnArgs& a) {
+  return s.D > 64 ? launch<128, false>(s, a) : launch<64, true>(s, a);
+}
 
 }  // namespace sg

@@ -473,6 +473,24 @@ def test_prompt(case):
     assert binding.scaled_attn_debug_status(plan.handle)[0] == 0
 
 
+@pytest.mark.parametrize("B", [40, 128, 150])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_many_sequences(B, causal, d):
+    # units are dealt out by the keys they see, up to 128 sequences, in their order beyond
+    rng = np.random.default_rng(B)
+    ql = [int(n) for n in rng.integers(0, 12, B)]
+    kl = [n + int(m) for n, m in zip(ql, rng.integers(0, 9, B))]
+    ql[7], kl[7], ql[B - 3], kl[B - 3], kl[5] = 290, 300, 140, 600, 0
+    hq, hk = 2, 1
+    q, k, v = _prompt_inputs(ql, kl, hq, hk, d, 60 + B)
+    plan = _pkg().PagedAttention(hq, hk, d)
+    out = torch.full((sum(ql), hq, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    _, lse = plan.prompt(q, k, v, _dev(_cum(ql)), _dev(_cum(kl)), causal=causal, out=out)
+    torch.cuda.synchronize()
+    _check_prompt(ql, kl, hq, hk, d, causal, q, k, v, out, lse)
+
+
 def test_prompt_sampled_rows_of_a_long_one():
     # long enough for several key tiles a row; a sample of rows against 64 bits
     hq, hk, d, n = 4, 1, 128, 3001
