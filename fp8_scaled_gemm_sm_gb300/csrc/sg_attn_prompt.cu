@@ -195,12 +195,12 @@ __device__ __forceinline__ void put_rows(const PromptParams& p, uint32_t o_addr,
   if (with_lse && tok < lq && p.lse) p.lse[at] = none ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
 }
 
-template <int HD>
 struct PromptLayout {
+  static constexpr int HD = 128;
   static constexpr int kBoxes = HD / 64;                  // 64-column (128-byte) boxes of a row
   static constexpr int kBox = kRows * 128;                // bytes of a box
   static constexpr int kTile = kBoxes * kBox;             // a Q, K or V tile
-  static constexpr int kStages = HD == 128 ? 5 : 8;
+  static constexpr int kStages = 5;
   static constexpr int kOffKv = 2 * kTile;
   static constexpr int kOffBar = kOffKv + kStages * kTile;
   static constexpr int kNumBars = 2 * kStages + 12;
@@ -210,11 +210,11 @@ struct PromptLayout {
   static_assert(kDynSmem <= 232448, "shared memory");
 };
 
-template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const PromptParams p) {
-  using L = PromptLayout<HD>;
+  using L = PromptLayout;
+  constexpr int HD = L::HD;
   constexpr int S = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -528,11 +528,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- one row tile a CTA --------------------------------------------------------
 //
-// Heads of 64 dimensions: an MMA is half as long and the softmax is not, so two tiles an SM leave
+// Heads of up to 64 dimensions: an MMA is half as long and the softmax is not, so two tiles an SM leave
 // the tensor cores waiting.  Here a CTA owns one row tile with 64 columns of tensor memory
 // for scores of 64 keys (weights over them) and 64 for the output, and four
 // CTAs share an SM: four softmaxes hide each other's waits, and the tiles are dealt out one by one, which
-// ragged prompts need.
+// ragged prompts need (29 of 1 to 2500 tokens, 16 heads of 64: 64.5 us, 94 with two tiles a CTA).  What bounds
+// it is the softmax's instructions.  With heads of 128, two CTAs an SM, it is for short sequences.
 //   warps 0-3  softmax and output, one thread a row
 //   warp 4     TMA producer: Q, then K_0, V_0, K_1, V_1, ...; then V rows past the sequence's end
 //   warp 5     MMA issuer, one elected thread
@@ -851,8 +852,8 @@ sg_status_t launch(const AttnShape& s, const AttnArgs& a) {
     GemmLaunch l(grid, dim3(kTileThreads), TileLayout<HD>::kDynSmem, a.stream, 1);
     e = cudaLaunchKernelEx(&l.cfg, prompt_tile_kernel<HD>, tmQ, tmK, tmV, p);
   } else {
-    GemmLaunch l(grid, dim3(kThreads), PromptLayout<HD>::kDynSmem, a.stream, 1);
-    e = cudaLaunchKernelEx(&l.cfg, prompt_kernel<HD>, tmQ, tmK, tmV, p);
+    GemmLaunch l(grid, dim3(kThreads), PromptLayout::kDynSmem, a.stream, 1);
+    e = cudaLaunchKernelEx(&l.cfg, prompt_kernel, tmQ, tmK, tmV, p);
   }
   if (e != cudaSuccess) {
     note_cuda_error(e);
@@ -864,15 +865,23 @@ sg_status_t launch(const AttnShape& s, const AttnArgs& a) {
 
 }  // namespace
 
+template <typename Kernel>
+cudaError_t allow(Kernel* kernel, int smem) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
 cudaError_t prompt_prepare() {
-  const cudaError_t e = cudaFuncSetAttribute(prompt_tile_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileLayout<64>::kDynSmem);
-  return e == cudaSuccess
-             ? cudaFuncSetAttribute(prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptLayout<128>::kDynSmem)
-             : e;
+  cudaError_t e = allow(prompt_tile_kernel<64>, TileLayout<64>::kDynSmem);
+  if (e == cudaSuccess) e = allow(prompt_tile_kernel<128>, TileLayout<128>::kDynSmem);
+  return e == cudaSuccess ? allow(prompt_kernel, PromptLayout::kDynSmem) : e;
 }
 
 sg_status_t prompt_launch(const AttnShape& s, const AttnArgs& a) {
-  return s.D > 64 ? launch<128, false>(s, a) : launch<64, true>(s, a);
+  if (s.D <= 64) return launch<64, true>(s, a);
+  // Two tiles a CTA read K and V half as often and overlap better, one a CTA starts sooner and
+  // deals out finer: by the keys a sequence has on average (32 heads over 8, one sequence of 256, 512, 1024 tokens: 9.6,
+  // 12.6, 19.2 us with two, 8.3, 12.4, 21.2 with one; 32 of 200: 64.6 and 56.5; 8 of 512: 44.1 and 45.9).
+  return a.Tk <= 384 * a.B ? launch<128, true>(s, a) : launch<128, false>(s, a);
 }
 
 }  // namespace sg

@@ -430,6 +430,14 @@ PROMPT = [
     ([0, 0, 9], [5, 0, 9], 2, 2, 64, True),
     ([260], [700], 12, 4, 128, True),
     ([600, 1], [600, 900], 1, 1, 128, True),
+    # more keys a sequence on average: two row tiles a CTA where heads are over 64 wide
+    ([40, 1, 0, 130, 3, 257], [1200, 1, 0, 130, 900, 700], 4, 1, 128, True),
+    ([40, 1, 0, 130, 3, 257], [1200, 1, 0, 130, 900, 700], 3, 3, 128, False),
+    ([33, 300, 5], [1000, 120, 403], 10, 2, 96, True),       # the first 180 queries of the second see nothing
+    ([1, 257], [2049, 513], 16, 1, 80, True),
+    ([70, 64], [1408, 16], 32, 4, 112, True),
+    ([200], [0], 2, 1, 128, True),
+    ([9, 500], [1500, 0], 2, 1, 128, False),
 ]
 
 
@@ -508,29 +516,31 @@ def test_prompt_sampled_rows_of_a_long_one():
 def test_prompt_sequences_do_not_reach_each_other():
     # the middle sequence is all NaN and infinity: only its own rows may show it
     hq, hk, d = 4, 2, 128
-    for ql in ([50, 60, 200], [129, 1, 127], [16, 300, 17]):
-        q, k, v = _prompt_inputs(ql, ql, hq, hk, d, 42)
-        cq = _cum(ql)
-        for t in (q, k, v):
-            t[cq[1]:cq[2]] = float("nan")
-            t[cq[1]:cq[2], :, ::3] = float("inf")
+    for ql, more in (([50, 60, 200], 0), ([129, 1, 127], 0), ([16, 300, 17], 0), ([50, 60, 200], 503), ([129, 1, 3], 450)):
+        kl = [n + more for n in ql]
+        q, k, v = _prompt_inputs(ql, kl, hq, hk, d, 42)
+        cq, ck = _cum(ql), _cum(kl)
+        for t, c in ((q, cq), (k, ck), (v, ck)):
+            t[c[1]:c[2]] = float("nan")
+            t[c[1]:c[2], :, ::3] = float("inf")
         plan = _pkg().PagedAttention(hq, hk, d)
-        out, lse = plan.prompt(q, k, v, _dev(cq))
+        out, lse = plan.prompt(q, k, v, _dev(cq), _dev(ck))
         torch.cuda.synchronize()
         for b in (0, 2):
-            r = slice(cq[b], cq[b + 1])
-            _check_prompt([ql[b]], [ql[b]], hq, hk, d, True, q[r], k[r], v[r], out[r], lse[r])
+            r, rk = slice(cq[b], cq[b + 1]), slice(ck[b], ck[b + 1])
+            _check_prompt([ql[b]], [kl[b]], hq, hk, d, True, q[r], k[rk], v[rk], out[r], lse[r])
 
 
-def test_prompt_masked_keys_may_be_nan_and_scores_may_be_large():
-    hq, hk, d, n = 2, 1, 64, 140
-    q, k, v = _prompt_inputs([n], [n], hq, hk, d, 43)
-    k[100:] = float("nan")           # rows below 100 see none of them
+@pytest.mark.parametrize("d,ctx", [(64, 0), (128, 0), (128, 400)])
+def test_prompt_masked_keys_may_be_nan_and_scores_may_be_large(d, ctx):
+    hq, hk, n = 2, 1, 140
+    q, k, v = _prompt_inputs([n], [ctx + n], hq, hk, d, 43)
+    k[ctx + 100:] = float("nan")     # rows below 100 see none of them
     q[:, 1] *= 100                   # scores of several hundred
     plan = _pkg().PagedAttention(hq, hk, d)
-    out, lse = plan.prompt(q, k, v, _dev(_cum([n])))
+    out, lse = plan.prompt(q, k, v, _dev(_cum([n])), _dev(_cum([ctx + n])))
     torch.cuda.synchronize()
-    o, ls, mag, big = ref.attend(_f64(q)[:100], _f64(k), _f64(v), np.arange(1, 101), d ** -0.5)
+    o, ls, mag, big = ref.attend(_f64(q)[:100], _f64(k), _f64(v), ctx + np.arange(1, 101), d ** -0.5)
     # scores of up to 2^big are known to 2^-22 of themselves: weights move by that much
     tol = ref.out_tolerance(o, mag, 8) + (2.0 ** -20 * big)[..., None] * mag
     assert (np.abs(_f64(out)[:100] - o) <= tol).all()
