@@ -4,9 +4,9 @@
 ``PagedAttention`` is a plan for one head layout; ``KVCache`` the cache it works
 on; ``rotary_table`` the positions' cosines and sines.  As in ``binding``, this
 is argument marshalling: every step runs in the library's kernels, launched on
-torch's current stream, and nothing synchronises.
+torch's current stream, and nothing synchronises.  The calls themselves are in
+``_attn.so`` (``csrc/sg_attn_torch.cpp``): checks, outputs and launch in one step.
 """
-import ctypes
 import math
 
 import torch
@@ -15,9 +15,22 @@ from . import binding
 
 BLOCK = 16  # tokens that share a scale
 
-# torch's current stream as a number; without the Stream object, building which takes longer than a launch
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+_EXT = None
+
+
+def _ext():
+    """The calls on tensors (built by ``fp8_scaled_gemm_sm_gb300.build``)."""
+    global _EXT
+    if _EXT is None:
+        binding.lib()
+        try:
+            from . import _attn
+        except ImportError as e:
+            raise RuntimeError("_attn.so is not built; run `python -c 'import __graft_entry__ as g; g.build()'` (%s)" % e)
+        _attn.set_error(binding.ScaledGemmError)
+        _EXT = _attn
+    return _EXT
 
 
 class KVCache:
@@ -43,8 +56,8 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.heads, self.page, self.dim, self.device = hk, page, d, k.device
         least = hk * page * d
-        self.args = binding.KvCacheArgs(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages,
-                                        k.stride(0) if pages > 1 else least, v.stride(0) if pages > 1 else least)
+        self._c = _ext().cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages,
+                               k.stride(0) if pages > 1 else least, v.stride(0) if pages > 1 else least, hk, page, d, k.device.index)
 
     @classmethod
     def new(cls, num_pages, heads, page, dim, device="cuda"):
@@ -96,54 +109,20 @@ class PagedAttention:
         dev = torch.cuda.current_device() if device is None else torch.device("cuda", device).index
         self.device = torch.device("cuda", dev)
         self.rotary = rotary
-        if rotary is None:
-            self._rot = binding.RotaryArgs(None, 0, 0, 0)
-        else:
+        rot = (0, 0, 0, 0)
+        if rotary is not None:
             if rotary.dtype != torch.float32 or rotary.dim() != 3 or rotary.shape[1] != 2 or not rotary.is_contiguous():
                 raise ValueError("rotary must be a contiguous float32 [max_pos, 2, rot / 2] tensor")
             if rotary.device != self.device:
                 raise ValueError("rotary must be on the plan's device")
-            self._rot = binding.RotaryArgs(rotary.data_ptr(), rotary.shape[0], 2 * rotary.shape[2], int(interleaved))
+            rot = (rotary.data_ptr(), rotary.shape[0], 2 * rotary.shape[2], int(interleaved))
+        ext = _ext()
         self.handle = binding.scaled_attn_create(q_heads, kv_heads, dim, page_size, dev)
+        self._p = ext.plan(self.handle, self.q_heads, self.kv_heads, self.dim, self.page_size, dev, *rot)
+        self._append, self._decode, self._prompt = ext.append, ext.decode, ext.prompt
 
     def new_cache(self, num_pages):
         return KVCache.new(num_pages, self.kv_heads, self.page_size, self.dim, self.device)
-
-    # -- checks -------------------------------------------------------------------
-
-    def _rows(self, t, heads, what):
-        if t.dim() != 3 or t.dtype != torch.bfloat16 or t.device != self.device:
-            raise ValueError("%s must be a bfloat16 [tokens, heads, dim] tensor on the plan's device" % what)
-        n, h, d = t.shape
-        s = t.stride()
-        if h != heads or d != self.dim or s[2] != 1 or (h > 1 and s[1] != d):
-            raise ValueError("%s must be [tokens, %d, %d] with its heads next to each other" % (what, heads, self.dim))
-        return n, (s[0] if n > 1 else heads * d)
-
-    def _cache(self, cache):
-        if cache.heads != self.kv_heads or cache.page != self.page_size or cache.dim != self.dim or cache.device != self.device:
-            raise ValueError("the cache's layout differs from the plan's")
-        return cache.args
-
-    def _ints(self, t, n, what):
-        if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or t.device != self.device or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous int32 [%d] tensor on the plan's device" % (what, n))
-        return t.data_ptr()
-
-    def _table(self, t, batch):
-        if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != batch or t.device != self.device or not t.is_contiguous():
-            raise ValueError("block_table must be a contiguous int32 [%d, pages] tensor on the plan's device" % batch)
-        return t.data_ptr(), t.shape[1]
-
-    def _out(self, t, shape, dtype, what):
-        if t is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        if t.shape != shape or t.dtype != dtype or t.device != self.device or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous %s %s tensor on the plan's device" % (what, dtype, tuple(shape)))
-        return t
-
-    def _stream(self, stream):
-        return _current_stream(self.device.index) if stream is None else stream
 
     # -- operators ----------------------------------------------------------------
 
@@ -151,60 +130,22 @@ class PagedAttention:
         """Rotate q and k, append k and v to the cache behind the ctx_lens [B] tokens that
         each sequence has there; sequence b's new rows are cu_seqlens[b] .. cu_seqlens[b + 1].
         Returns (rotated q, rotated k or None)."""
-        T, qs = self._rows(q, self.q_heads, "q")
-        tk, ks = self._rows(k, self.kv_heads, "k")
-        tv, vs = self._rows(v, self.kv_heads, "v")
-        if tk != T or tv != T:
-            raise ValueError("q, k and v must have the same number of rows")
-        B = ctx_lens.shape[0]
-        table, width = self._table(block_table, B)
-        q_out = self._out(q_out, (T, self.q_heads, self.dim), torch.bfloat16, "q_out")
-        if k_out is True or isinstance(k_out, torch.Tensor):
-            k_out = self._out(None if k_out is True else k_out, (T, self.kv_heads, self.dim), torch.bfloat16, "k_out")
-        else:
-            k_out = None
-        binding.scaled_attn_append(
-            self.handle, self._cache(cache), self._rot, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, table, width,
-            self._ints(ctx_lens, B, "ctx_lens"), self._ints(cu_seqlens, B + 1, "cu_seqlens"), T, B, q_out.data_ptr(),
-            None if k_out is None else k_out.data_ptr(), self._stream(stream))
-        return q_out, k_out
+        return self._append(self._p, q, k, v, cache._c, block_table, ctx_lens, cu_seqlens, k_out, q_out, stream)
 
     def decode(self, q, cache, block_table, kv_lens, q_tokens=1, scale=None, out=None, lse=None, stream=None):
         """Attention of each sequence's newest q_tokens tokens (q [B * q_tokens, Hq, dim]) over its
         first kv_lens [B] tokens in the cache, themselves included.  Returns (out, lse)."""
-        n, qs = self._rows(q, self.q_heads, "q")
-        B = kv_lens.shape[0]
-        if n != B * q_tokens:
-            raise ValueError("q must have q_tokens = %d rows for each of %d sequences" % (q_tokens, B))
-        table, width = self._table(block_table, B)
-        out = self._out(out, (n, self.q_heads, self.dim), torch.bfloat16, "out")
-        lse = self._out(lse, (n, self.q_heads), torch.float32, "lse")
-        binding.scaled_attn_decode(
-            self.handle, self._cache(cache), q.data_ptr(), qs, q_tokens, table, width, self._ints(kv_lens, B, "kv_lens"), B,
-            self.dim ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(), self._stream(stream))
-        return out, lse
+        return self._decode(self._p, q, cache._c, block_table, kv_lens, q_tokens, scale, out, lse, stream)
 
     def prompt(self, q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None, lse=None, stream=None):
         """Attention within each of the packed sequences: queries cu_q[b] .. cu_q[b + 1] over keys
         cu_k[b] .. cu_k[b + 1] (cu_k None: the same).  causal: the last query sees every
         key.  Returns (out, lse)."""
-        n, qs = self._rows(q, self.q_heads, "q")
-        m, ks = self._rows(k, self.kv_heads, "k")
-        mv, vs = self._rows(v, self.kv_heads, "v")
-        if mv != m:
-            raise ValueError("k and v must have the same number of rows")
-        cu_k = cu_q if cu_k is None else cu_k
-        B = cu_q.shape[0] - 1
-        out = self._out(out, (n, self.q_heads, self.dim), torch.bfloat16, "out")
-        lse = self._out(lse, (n, self.q_heads), torch.float32, "lse")
-        binding.scaled_attn_prompt(
-            self.handle, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, self._ints(cu_q, B + 1, "cu_q"),
-            self._ints(cu_k, B + 1, "cu_k"), n, m, B, int(causal), self.dim ** -0.5 if scale is None else scale,
-            out.data_ptr(), lse.data_ptr(), self._stream(stream))
-        return out, lse
+        return self._prompt(self._p, q, k, v, cu_q, cu_k, causal, scale, out, lse, stream)
 
     def close(self):
         if getattr(self, "handle", None):
+            self._p = None  # calls after this are refused
             binding.scaled_attn_destroy(self.handle)
             self.handle = None
 

@@ -1,10 +1,12 @@
-"""Build libscaledgemm.so (the sm_103a kernels + C ABI) in-tree with nvcc.
+"""Build libscaledgemm.so (the sm_103a kernels + C ABI) in-tree with nvcc, and the
+attention operators' torch binding beside it.
 
-Every translation unit under csrc/ is compiled in parallel for
+Every .cu under csrc/ is compiled in parallel for
 ``-gencode arch=compute_103a,code=sm_103a`` and linked into
 ``fp8_scaled_gemm_sm_gb300/libscaledgemm.so`` with the CUDA runtime linked
 statically, so the library loads on a machine without a GPU (its entry points
-then return SG_ERR_CUDA).
+then return SG_ERR_CUDA).  ``_attn.so`` (host code, the C++ compiler and torch's
+headers) is compiled at the same time and links to it.
 """
 import os
 import shutil
@@ -18,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libscaledgemm.so")
+EXT = os.path.join(PKG, "_attn.so")
+EXT_SRC = os.path.join(CSRC, "sg_attn_torch.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -38,15 +42,15 @@ def sources():
 
 
 def _deps():
-    return sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
+    return sources() + [EXT_SRC] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
         os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")
     ] + [os.path.abspath(__file__)]
 
 
 def up_to_date():
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -70,15 +74,55 @@ def build(force=False, verbose=False, extra_flags=()):
         return obj
 
     srcs = sources()
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        ext = ex.submit(_compile_ext, verbose)
         objs = list(ex.map(compile_one, srcs))
+        ext_obj = ext.result()
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [cc] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "--cudart", "static", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
+    _link_ext(ext_obj)
     return LIB
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s%s" % (what, r.stdout, r.stderr))
+
+
+def _torch_dirs():
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    return root, int(torch._C._GLIBCXX_USE_CXX11_ABI)
+
+
+def _compile_ext(verbose):
+    import sysconfig
+
+    torch_root, abi = _torch_dirs()
+    obj = os.path.join(BUILD, "sg_attn_torch.o")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=%d" % abi, "-c", EXT_SRC, "-o", obj,
+           "-I" + INCLUDE, "-isystem", os.path.join(torch_root, "include"),
+           "-isystem", os.path.join(torch_root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include")]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    _run(cmd, "compiling " + EXT_SRC)
+    return obj
+
+
+def _link_ext(obj):
+    libs = os.path.join(_torch_dirs()[0], "lib")
+    tmp = EXT + ".tmp.%d" % os.getpid()
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + libs, "-Wl,-rpath," + libs,
+          "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"], "linking " + EXT)
+    os.replace(tmp, EXT)
 
 
 if __name__ == "__main__":
