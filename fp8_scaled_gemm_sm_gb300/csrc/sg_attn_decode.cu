@@ -43,7 +43,6 @@ namespace sg {
 namespace {
 
 constexpr int kKeys = 32;       // keys of a tile
-constexpr int kMinTiles = 2;    // least tiles of a warp's range
 constexpr int kSegCost = 3;     // what a segment costs beside its tiles, in tiles
 constexpr int kUncut = 4;       // segments of up to 1 / kUncut of a range are not cut
 constexpr int kMaxWarps = 16;
@@ -226,72 +225,90 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
     for (int s = 0; s < S; ++s) mbar_init(bars + 8 * s, 1);
     fence_mbarrier_init();
   }
+  __syncthreads();
   grid_dep_launch();
   grid_dep_wait();
 
-  // Numbers before each run of `per` sequences, and in all.
+  // Numbers in all, and before each run of `per` sequences: up to 32 sequences every warp sums up for
+  // itself, one a lane; more are summed by the block.
   Walk walk{p, p.Hk * p.row_tiles, 0, 0, 0};
-  const int per = (p.B + kThreads - 1) / kThreads;
+  const bool few = p.B <= 32;
+  const int per = few ? 1 : (p.B + kThreads - 1) / kThreads;
   int64_t mine = 0;
-  for (int i = tid * per; i < min((tid + 1) * per, p.B); ++i) mine += walk.numbers(walk.len(i));
-  int64_t scan = mine;
+  const int first = few ? lane : tid * per;
+  for (int i = first; i < min(first + per, p.B); ++i) mine += walk.numbers(walk.len(i));
+  int64_t scan = mine;  // up to and with this lane's
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t up = __shfl_up_sync(0xffffffffu, scan, o);
     if (lane >= o) scan += up;
   }
-  if (lane == 31) warp_sums[warp] = scan;
-  __syncthreads();
-  int64_t base = 0;
-  for (int w = 0; w < warp; ++w) base += warp_sums[w];
-  sums[tid + 1] = (base + scan) * walk.segs;
-  if (tid == 0) sums[0] = 0;
-  __syncthreads();
-  const int64_t total = sums[kThreads];
+  int64_t total;
+  if (few) {
+    total = __shfl_sync(0xffffffffu, scan, 31) * walk.segs;
+  } else {
+    if (lane == 31) warp_sums[warp] = scan;
+    __syncthreads();
+    int64_t base = 0;
+    for (int w = 0; w < warp; ++w) base += warp_sums[w];
+    sums[tid + 1] = (base + scan) * walk.segs;
+    if (tid == 0) sums[0] = 0;
+    __syncthreads();
+    total = sums[kThreads];
+  }
 
-  // sequences with nothing to see
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x)
-    if (walk.len(b) == 0) {
-      const int64_t n = static_cast<int64_t>(p.qn) * p.Hq;
-      for (int64_t i = tid; i < n * p.D / 8; i += kThreads)
-        reinterpret_cast<uint4*>(p.out + b * n * p.D)[i] = make_uint4(0, 0, 0, 0);
-      if (p.lse)
-        for (int64_t i = tid; i < n; i += kThreads) p.lse[b * n + i] = -INFINITY;
-      if (p.by_segment)
-        for (int i = tid; i < walk.segs; i += kThreads) p.cuts[b * walk.segs + i].last = -1;
-    }
+  // Sequences with nothing to see; after the first loads are on their way.
+  auto write_empty = [&]() {
+    for (int b = blockIdx.x * kWarps + warp; b < p.B; b += gridDim.x * kWarps)
+      if (walk.len(b) == 0) {
+        const int64_t n = static_cast<int64_t>(p.qn) * p.Hq;
+        for (int64_t i = lane; i < n * p.D / 8; i += 32)
+          reinterpret_cast<uint4*>(p.out + b * n * p.D)[i] = make_uint4(0, 0, 0, 0);
+        if (p.lse)
+          for (int64_t i = lane; i < n; i += 32) p.lse[b * n + i] = -INFINITY;
+        if (p.by_segment)
+          for (int i = lane; i < walk.segs; i += 32) p.cuts[b * walk.segs + i].last = -1;
+      }
+  };
 
-  // As many ranges as there are warps, or as few as the least range allows; those few on as many SMs as there are.
-  const int64_t quota = max(quotient(total + gridDim.x * kWarps - 1, gridDim.x * kWarps), static_cast<int64_t>(kMinTiles + kSegCost));
+  // As many ranges as there are warps; fewer numbers than warps go to as many SMs as there are.
+  const int64_t quota = max(quotient(total + gridDim.x * kWarps - 1, gridDim.x * kWarps), static_cast<int64_t>(1));
   const int warps = static_cast<int>(quotient(quotient(total + quota - 1, quota) + gridDim.x - 1, gridDim.x));
   const int range = blockIdx.x * warps + warp;
   walk.begin = warp < warps ? min(range * quota, total) : total;
   walk.end = min(walk.begin + quota, total);
   walk.uncut = static_cast<int>(min(quota / kUncut, static_cast<int64_t>(1 << 20)));
-  if (!p.by_segment && lane == 0 && warp < kWarps) p.cuts[blockIdx.x + gridDim.x * warp].last = -1;
-  if (walk.begin >= walk.end) return;
+  if (!p.by_segment && lane == 0) p.cuts[blockIdx.x + gridDim.x * warp].last = -1;
+  if (walk.begin >= walk.end) {
+    write_empty();
+    return;
+  }
 
   Part c{};  // the part to compute
-  {
+  if (few) {
+    const uint32_t after = __ballot_sync(0xffffffffu, scan * walk.segs > walk.begin);  // not zero: begin < total
+    c.b = __ffs(after) - 1;
+    c.start = __shfl_sync(0xffffffffu, scan - mine, c.b) * walk.segs;
+  } else {
     int lo = 0;  // the run of sequences: sums[lo] <= begin < sums[lo + 1]
-#pragma unroll 1
+#pragma unroll 4
     for (int i = lane; i < kThreads; i += 32) lo += sums[i + 1] <= walk.begin;
     lo = __reduce_add_sync(0xffffffffu, lo);
     c.start = sums[lo];
     c.b = lo * per;
-    for (;;) {
-      c.len = walk.len(c.b);
-      const int64_t n = walk.numbers(c.len);
-      if (walk.begin < c.start + n * walk.segs) {
-        c.hr = static_cast<int>(quotient(walk.begin - c.start, n));
-        c.start += c.hr * n;
-        break;
-      }
-      c.start += n * walk.segs;
-      ++c.b;
-    }
-    c.tiles = walk.tiles(c.len);
   }
+  for (;;) {
+    c.len = walk.len(c.b);
+    const int64_t n = walk.numbers(c.len);
+    if (walk.begin < c.start + n * walk.segs) {
+      c.hr = static_cast<int>(quotient(walk.begin - c.start, n));
+      c.start += c.hr * n;
+      break;
+    }
+    c.start += n * walk.segs;
+    ++c.b;
+  }
+  c.tiles = walk.tiles(c.len);
   bool some = walk.find(c);
   Part ahead = c;  // the part to load, its tile `ahead.t`
   bool more = some;
@@ -352,10 +369,30 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
       more = walk.next(ahead);
     }
   };
-  int in_flight = 0;  // stages loaded and not yet consumed
-  for (int s = 0; s < S && more; ++s, ++in_flight) load(s);
-
+  // This lane's share of the part's query rows: row g8, runs c4 (and c4 + 4).
   const int g8 = lane >> 2, c4 = lane & 3;
+  uint4 q_raw[NR][2 * kRuns];
+  auto load_q = [&]() {
+    const int h = c.hr / p.row_tiles, rt = c.hr % p.row_tiles;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int row = (rt * NR + r) * 8 + g8;
+      const bool live = row < p.qn * p.group;
+      const uint16_t* src = p.q + (static_cast<int64_t>(c.b) * p.qn + (live ? row / p.group : 0)) * p.q_stride +
+                            (h * p.group + row % p.group) * p.D;
+#pragma unroll
+      for (int i = 0; i < 2 * kRuns; ++i) {
+        const int d = 64 * (i / 2) + 16 * c4 + 8 * (i % 2);
+        q_raw[r][i] = live && d < p.D ? *reinterpret_cast<const uint4*>(src + d) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  bool q_loaded = some;
+  if (some) load_q();  // before the pages are looked up
+  int in_flight = 0;   // stages loaded and not yet consumed
+  for (int s = 0; s < S && more; ++s, ++in_flight) load(s);
+  write_empty();
+
   const int kr = key_row<HD>(g8), kv0 = key_row<HD>(2 * c4), kv1 = key_row<HD>(2 * c4 + 1);
   const int run_d = HD == 128 ? 16 * kr : 8 * g8;  // first dimension of this lane's outputs
   int stage = 0;
@@ -368,19 +405,12 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
     uint32_t qf[NR][4 * kRuns][2];
     float q_scale[NR][2];
     int lim[NR][2];      // keys that rows 2 c4, 2 c4 + 1 see
+    if (!q_loaded) load_q();
+    q_loaded = false;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const int row = (rt * NR + r) * 8 + g8;
-      const bool live = row < p.qn * p.group;
-      const uint16_t* src = p.q + (static_cast<int64_t>(c.b) * p.qn + (live ? row / p.group : 0)) * p.q_stride +
-                            (h * p.group + row % p.group) * p.D;
-      uint4 w[2 * kRuns];
       float top = 0.f;
-#pragma unroll
-      for (int i = 0; i < 2 * kRuns; ++i) {
-        const int d = 64 * (i / 2) + 16 * c4 + 8 * (i % 2);
-        w[i] = live && d < p.D ? *reinterpret_cast<const uint4*>(src + d) : make_uint4(0, 0, 0, 0);
-      }
+      const uint4 (&w)[2 * kRuns] = q_raw[r];
       auto lo = [](uint32_t x) { return __uint_as_float(x << 16); };
       auto hi = [](uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); };
 #pragma unroll
