@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
     }
     const float m0 = m == -INFINITY ? 0.f : m, n0 = n == -INFINITY ? 0.f : n;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 4
     for (int k = many ? warp : 0; k < count; k += many ? kJoinWarps : 1) {
       const float4 ml = p.part_ml[at(k, row)];
       const float4 x = *reinterpret_cast<const float4*>(p.part_o + static_cast<int64_t>(at(k, row)) * HD + d);
