@@ -26,6 +26,11 @@
 // P is rounded to bf16 (V is bf16, and an MMA has one operand type): an error of at most 2^-9 of each weight,
 // against the 2^-9 of the rounded output; the row sums take the unrounded weights.
 //
+// What bounds it: the tensor pipe, short of the turns it waits for a softmax.  16384 tokens, 32 heads of 128 over
+// 8, causal: 1377 us, 1.60 PFLOP/s, 82% of what the library's bf16 GEMM reaches.  Measured beside it: one
+// S buffer a tile with P elsewhere 1509 us, 64-key blocks with two S buffers 1612, MMAs issued by lane 0 under a
+// plain branch instead of one elected thread for the whole loop 1520.
+//
 // V rows past a sequence's end belong to the next one: those that share a 16-key
 // MMA step with valid ones are zeroed in shared memory, the rest are not multiplied.
 #include <cuda.h>
@@ -40,11 +45,11 @@ namespace {
 
 constexpr int kRows = 128;   // rows of a tile, keys of a block
 constexpr int kThreads = 384;
-// Registers a thread of the softmax warpgroups and of the third (producer, MMA issuer, two
-// idle warps): 2 x 200 + 104 = 3 x 168, what the block is launched with.
+// Registers a thread of the softmax warpgroups and of the third (producer, MMA issuer, V's end,
+// an idle warp): 2 x 192 + 120 = 3 x 168, what the block is launched with.
 constexpr int kSoftmaxRegs = 192, kIssueRegs = 120;
 constexpr int kEarly = 4;  // 16-key steps of a block whose weights are handed over first
-constexpr int kTileKeys = 64, kTileThreads = 192;  // of the kernel with one row tile a CTA, for D <= 64
+constexpr int kTileKeys = 64, kTileThreads = 192;  // of the kernel with one row tile a CTA
 constexpr float kSlack = 8.f;  // log2 of the largest weight
 
 struct PromptParams {

@@ -35,10 +35,11 @@
  * or 128; rot a multiple of 16, 0 <= rot <= D; scale positive and finite.  Softmax statistics, sums and products are
  * accumulated in fp32; bf16 outputs are rounded once, to nearest even.
  *
- * NaN and infinity: what a row does not see does not reach it, with one exception: in
- * scaled_attn_prompt a non-finite VALUE (v) reaches the rows of its own sequence whose
- * keys are processed in the same tile of 128 keys, whether they see it or not (its weight
- * there is zero, and zero times infinity is NaN).
+ * NaN and infinity: what a row does not see does not reach it, with one exception, a non-finite
+ * VALUE (v) of the row's own sequence in a tile of keys that the row sees a part of (its weight
+ * there is zero, and zero times infinity is NaN): in scaled_attn_prompt tiles are of 64 or
+ * 128 keys, in scaled_attn_decode with several query tokens of 32 (a later
+ * token's value reaches the earlier rows).  Other sequences' values never do.
  *
  * Errors, streams and programmatic launches: as in scaled_gemm.h.  A handle owns a
  * workspace that scaled_attn_decode uses, so decodes on one handle must be ordered (one
