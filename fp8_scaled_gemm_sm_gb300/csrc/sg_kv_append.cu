@@ -14,13 +14,15 @@
 // written per token, each once.  One CTA takes the new tokens of one block of
 // positions of one sequence (so a block's scale has one owner: no atomics, no
 // order).  Lanes own 16 elements of a row (a run of 8 pairs, two 16-byte loads); the
-// rows that a warp holds at once are tokens times heads, as many tokens as there are, so
-// that one new token a sequence fills lanes as well as sixteen.  K and V rows
-// wait in shared memory, loaded there asynchronously, and are rotated twice, for the block's maximum and
-// for its codes: in registers their fp32 values would take the room of half the warps, and with those the
-// loads in flight; in shared memory, that of the cosines in L1.  48k prompt tokens, 32 heads of 128 over 8: 249 us, 84% of the
-// rate of a copy (281 with fp32 kept); 41 chunks of up to 1500 tokens, 24 heads of 64 over 24: 50 us; one token of
-// 512 sequences 8.7 us, of 8 sequences 4.4, most of it the launch and four dependent loads.
+// rows that a warp holds at once are up to 4 tokens times heads, so that one new token a sequence
+// fills lanes as well as sixteen.  A warp's work comes in items of 4 KB (a block's tokens of a key or value head, 4
+// tokens of query heads), loaded to shared memory asynchronously while the item before is worked on.  K and V rows
+// are rotated twice from there, for the block's maximum and for its codes: in registers their fp32 values would take
+// the room of half the warps.  The tokens' cosines and sines, which all heads use, wait in shared memory too: the
+// items leave L1 too little room for them.  48k prompt tokens, 32 heads of 128 over 8: 230 us, 91% of the
+// rate of a copy (249 without loading ahead and with cosines through L1, 281 with fp32 kept); 41 chunks of up to 1500
+// tokens, 24 heads of 64 over 24: 43 us (50), issue slots bind; one token of 512 sequences 6.6 us, of 8
+// sequences 3.6, most of it the launch and four dependent loads.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -39,9 +41,12 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPassBytes = 1024;  // shared memory of a warp's pass: 32 bytes a lane
-constexpr int kHeadPasses = 8;  // passes over query heads that reuse one set of cosines
-constexpr int kCtas = 6;        // resident CTAs an SM
-constexpr int kWaves = 5;       // CTAs wanted, in times what the GPU holds
+constexpr int kHeadPasses = 4;  // passes over query heads that reuse one set of cosines
+constexpr int kTokens = 4;      // tokens that a warp holds at once, where there are as many; its other lanes take heads
+constexpr int kPasses = kKvBlock / kTokens;  // passes over a block's tokens
+constexpr int kItemBytes = 4 * kPassBytes;   // shared memory of an item: 4 passes
+constexpr int kCtas = 4;        // resident CTAs an SM
+constexpr int kWaves = 4;       // CTAs wanted, in times what the GPU holds
 
 struct AppendParams {
   sg_kv_cache_t cache;
@@ -63,11 +68,11 @@ struct Run {
   bool live, rotated;
 };
 
-template <bool INTER>
+template <bool INTER, bool ROTATE>
 __device__ __forceinline__ Run make_run(int j, const AppendParams& p) {
   Run r;
   r.live = j < p.D / 16;
-  r.rotated = j < p.rot / 16;
+  r.rotated = ROTATE && j < p.rot / 16;
   if (r.rotated && !INTER) {
     r.off_a = 8 * j;
     r.off_b = p.rot / 2 + 8 * j;
@@ -76,17 +81,6 @@ __device__ __forceinline__ Run make_run(int j, const AppendParams& p) {
     r.off_b = 16 * j + 8;
   }
   return r;
-}
-
-struct Raw {
-  uint4 a, b;
-};
-
-__device__ __forceinline__ Raw load_raw(const uint16_t* row, const Run& r) {
-  Raw x;
-  x.a = *reinterpret_cast<const uint4*>(row + r.off_a);
-  x.b = *reinterpret_cast<const uint4*>(row + r.off_b);
-  return x;
 }
 
 __device__ __forceinline__ void widen(const uint4& w, float* f) {
@@ -108,22 +102,41 @@ __device__ __forceinline__ uint4 ld_shared_16(uint32_t a) {
   return v;
 }
 
+// What a CTA works on: new tokens [t0, t0 + n) at positions [pos, pos + n) of one
+// block of 16, `held` older tokens before them.
+struct Unit {
+  int t0, n, held;
+  int64_t pos;
+  int page_id;  // outside [0, num_pages): no page, nothing is written
+  int slot0;    // the block's first slot in the page
+};
+
 struct Angles {
   float c[8], s[8];
 };
 
-__device__ __forceinline__ void load_angles(const AppendParams& p, int64_t pos, int j, Angles& g) {
-  const int64_t row = pos < p.max_pos ? pos : p.max_pos - 1;
-  const float4* c = reinterpret_cast<const float4*>(p.rot_table + row * p.rot + 8 * j);
-  const float4* s = reinterpret_cast<const float4*>(p.rot_table + row * p.rot + p.rot / 2 + 8 * j);
-  // volatile: loaded where they are used, not for all of a warp's tokens ahead of time
-  auto load = [](float* f, const float4* a) {
-    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "l"(a));
-  };
-  load(g.c, c);
-  load(g.c + 4, c + 1);
-  load(g.s, s);
-  load(g.s + 4, s + 1);
+// The cosines and sines of a unit's tokens in shared memory: of a token, the first four of every run, then the
+// other four (a warp's 16-byte reads then lie side by side), cosines before sines.
+constexpr int kAngleRow = (128 + 16) * 4;
+
+__device__ __forceinline__ void stage_angles(const AppendParams& p, const Unit& u, uint32_t angles) {
+  const int vecs = p.rot / 4, runs = p.rot / 16;  // 16-byte pieces of a token, runs
+  for (int i = threadIdx.x; i < u.n * vecs; i += kThreads) {
+    const int t = i / vecs, x = i - t * vecs, sine = x >= 2 * runs, y = x - sine * 2 * runs;
+    const int64_t row = min(u.pos + t, p.max_pos - 1);
+    cp_async_16(angles + t * kAngleRow + (sine * 2 * runs + (y & 1) * runs + (y >> 1)) * 16, p.rot_table + row * p.rot + 4 * x, 16);
+  }
+}
+
+__device__ __forceinline__ Angles load_angles(const AppendParams& p, uint32_t angles, int t, int j) {
+  Angles g;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 v = ld_shared_16(angles + t * kAngleRow + (i * (p.rot / 16) + j) * 16);
+    float* f = (i < 2 ? g.c : g.s) + 4 * (i & 1);
+    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+  }
+  return g;
 }
 
 // f[0..7] and f[8..15]: the run's halves; rotated in place, two pairs an instruction.  The sum of two
@@ -175,46 +188,38 @@ __device__ __forceinline__ uint4 rescale16(uint4 c, float by) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// What a CTA works on: new tokens [t0, t0 + n) at positions [pos, pos + n) of one
-// block of 16, `held` older tokens before them.
-struct Unit {
-  int t0, n, held;
-  int64_t pos;
-  int page_id;  // outside [0, num_pages): no page, nothing is written
-  int slot0;    // the block's first slot in the page
-};
-
 // How a warp's rows are split into tokens and heads: row r is token r % tokens of
 // head r / tokens.
 struct Split {
   int tokens, heads, shift;  // tokens = 1 << shift
 };
 
-// The unit's tokens of `split.heads` K (or V) heads from `head0`; `keep`: this lane's shared memory.
+// Loads the unit's tokens of `split.heads` K (or V) heads from `head0`; `keep`: this lane's shared memory.
 template <int LPR, bool INTER, bool IS_K>
-__device__ __forceinline__ void append_heads(const AppendParams& p, const Unit& u, const Split& split, int head0, int lane,
-                                             uint32_t keep) {
-  constexpr int kRows = 32 / LPR;               // rows a pass
-  constexpr int kPasses = kKvBlock / kRows;
+__device__ __forceinline__ void load_heads(const AppendParams& p, const Unit& u, const Split& split, int head0, int lane, uint32_t keep) {
   const int j = lane % LPR, row = lane / LPR;
   const int t0 = row & (split.tokens - 1), head = head0 + (row >> split.shift);
-  Run run = make_run<INTER>(j, p);
-  if (!IS_K) {
-    run.rotated = false;
-    run.off_a = 16 * j;
-    run.off_b = 16 * j + 8;
-  }
-  run.live = run.live && head < p.Hk;
-  const uint16_t* src = (IS_K ? p.k : p.v) + static_cast<int64_t>(u.t0) * (IS_K ? p.k_stride : p.v_stride) + head * p.D;
+  const Run run = make_run<INTER, IS_K>(j, p);
   const int64_t stride = IS_K ? p.k_stride : p.v_stride;
+  const uint16_t* src = (IS_K ? p.k : p.v) + static_cast<int64_t>(u.t0) * stride + head * p.D;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int t = i * split.tokens + t0;
-    if (t < u.n && run.live) {
+    if (t < u.n && run.live && head < p.Hk) {
       cp_async_16(keep + i * kPassBytes, src + t * stride + run.off_a, 16);
       cp_async_16(keep + i * kPassBytes + 512, src + t * stride + run.off_b, 16);
     }
   }
+}
+
+// Appends them.
+template <int LPR, bool INTER, bool IS_K>
+__device__ __forceinline__ void append_heads(const AppendParams& p, const Unit& u, const Split& split, int head0, int lane,
+                                             uint32_t keep, uint32_t angles) {
+  const int j = lane % LPR, row = lane / LPR;
+  const int t0 = row & (split.tokens - 1), head = head0 + (row >> split.shift);
+  Run run = make_run<INTER, IS_K>(j, p);
+  run.live = run.live && head < p.Hk;
   uint8_t* scale = nullptr;
   uint8_t* codes = nullptr;
   int was = 0;
@@ -230,12 +235,10 @@ __device__ __forceinline__ void append_heads(const AppendParams& p, const Unit& 
     widen(ld_shared_16(keep + i * kPassBytes), f);
     widen(ld_shared_16(keep + i * kPassBytes + 512), f + 8);
     if (IS_K && run.rotated) {
-      Angles g;
-      load_angles(p, u.pos + i * split.tokens + t0, j, g);
+      const Angles g = load_angles(p, angles, i * split.tokens + t0, j);
       rotate<INTER>(f, g, p.one);
     }
   };
-  cp_async_wait_all();  // this lane's own: no other reads them
   float amax = 0.f;
 #pragma unroll 1
   for (int i = 0; i < kPasses; ++i) {
@@ -290,7 +293,8 @@ __device__ __forceinline__ void append_heads(const AppendParams& p, const Unit& 
 template <int LPR, bool INTER>
 __global__ void __launch_bounds__(kThreads, kCtas) kv_append_kernel(const AppendParams p) {
   __shared__ int4 found;  // sequence, its first row, the row past its last, its tokens in the cache
-  __shared__ __align__(16) uint8_t kept[kWarps][kKvBlock / (32 / LPR) * kPassBytes];
+  __shared__ __align__(16) uint8_t kept[kWarps][2 * kItemBytes];
+  __shared__ __align__(16) uint8_t turns[kKvBlock * kAngleRow];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) found.x = -1;
   __syncthreads();
@@ -330,8 +334,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv_append_kernel(const Append
   u.page_id = at < p.table_stride ? __ldg(p.table + b * p.table_stride + at) : -1;
   u.slot0 = static_cast<int>(block * kKvBlock % p.page);
 
-  constexpr int kRows = 32 / LPR;  // rows a warp takes at once
-  Split split{kRows, 1, LPR == 8 ? 2 : 3};
+  Split split{kTokens, 32 / LPR / kTokens, 2};
   while (split.tokens > 1 && split.tokens / 2 >= u.n) {
     split.tokens /= 2;
     split.heads *= 2;
@@ -341,47 +344,69 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv_append_kernel(const Append
   const int head_runs = (p.Hq + split.heads * kHeadPasses - 1) / (split.heads * kHeadPasses);
   const int items = 2 * kv_runs + (u.n + split.tokens - 1) / split.tokens * head_runs;
   const int j = lane % LPR, row = lane / LPR;
-  const Run run = make_run<INTER>(j, p);
+  const Run run = make_run<INTER, true>(j, p);
   const uint32_t keep = smem_addr(kept[warp]) + lane * 16;
-  for (int it = blockIdx.y * kWarps + warp; it < items; it += gridDim.y * kWarps) {
+  // query item qi: this lane's token and first head
+  auto query = [&](int qi, int& t, int& h0) {
+    t = (qi / head_runs << split.shift) + (row & (split.tokens - 1));
+    h0 = (qi % head_runs) * split.heads * kHeadPasses + (row >> split.shift);
+    return t < u.n && run.live;
+  };
+  auto load = [&](int it, uint32_t to) {
     if (it < kv_runs) {
-      append_heads<LPR, INTER, true>(p, u, split, it * split.heads, lane, keep);
-      continue;
-    }
-    if (it < 2 * kv_runs) {
-      append_heads<LPR, INTER, false>(p, u, split, (it - kv_runs) * split.heads, lane, keep);
-      continue;
-    }
-    const int qi = it - 2 * kv_runs;
-    const int t = (qi / head_runs << split.shift) + (row & (split.tokens - 1));
-    const int h0 = (qi % head_runs) * split.heads * kHeadPasses + (row >> split.shift);
-    if (t >= u.n || !run.live) continue;
-    Angles g;
-    if (run.rotated) load_angles(p, u.pos + t, j, g);
-    const uint16_t* src = p.q + (u.t0 + t) * p.q_stride;
-    uint16_t* dst = p.q_out + static_cast<int64_t>(u.t0 + t) * p.Hq * p.D;
-#pragma unroll 1
-    for (int i0 = 0; i0 < kHeadPasses; i0 += 2) {
-      Raw raw[2];
+      load_heads<LPR, INTER, true>(p, u, split, it * split.heads, lane, to);
+    } else if (it < 2 * kv_runs) {
+      load_heads<LPR, INTER, false>(p, u, split, (it - kv_runs) * split.heads, lane, to);
+    } else if (int t, h0; it < items && query(it - 2 * kv_runs, t, h0)) {
+      const uint16_t* src = p.q + (u.t0 + t) * p.q_stride;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int h = h0 + (i0 + i) * split.heads;
-        if (h < p.Hq) raw[i] = load_raw(src + h * p.D, run);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int h = h0 + (i0 + i) * split.heads;
+      for (int i = 0; i < kHeadPasses; ++i) {
+        const int h = h0 + i * split.heads;
         if (h < p.Hq) {
-          float f[16];
-          widen(raw[i].a, f);
-          widen(raw[i].b, f + 8);
-          if (run.rotated) rotate<INTER>(f, g, p.one);
-          *reinterpret_cast<uint4*>(dst + h * p.D + run.off_a) = narrow(f);
-          *reinterpret_cast<uint4*>(dst + h * p.D + run.off_b) = narrow(f + 8);
+          cp_async_16(to + i * kPassBytes, src + h * p.D + run.off_a, 16);
+          cp_async_16(to + i * kPassBytes + 512, src + h * p.D + run.off_b, 16);
         }
       }
     }
+    cp_async_commit();
+  };
+  const int step = gridDim.y * kWarps;
+  int it = blockIdx.y * kWarps + warp;
+  const uint32_t angles = smem_addr(turns);
+  if (p.rot) stage_angles(p, u, angles);
+  cp_async_commit();
+  load(it, keep);
+  cp_async_wait<1>();
+  __syncthreads();
+  for (uint32_t buf = 0; it < items; it += step, buf ^= kItemBytes) {
+    load(it + step, keep + (buf ^ kItemBytes));
+    cp_async_wait<1>();  // this lane's own: no other reads them
+    if (it < kv_runs) {
+      append_heads<LPR, INTER, true>(p, u, split, it * split.heads, lane, keep + buf, angles);
+      continue;
+    }
+    if (it < 2 * kv_runs) {
+      append_heads<LPR, INTER, false>(p, u, split, (it - kv_runs) * split.heads, lane, keep + buf, angles);
+      continue;
+    }
+    int t, h0;
+    if (!query(it - 2 * kv_runs, t, h0)) continue;
+    Angles g;
+    if (run.rotated) g = load_angles(p, angles, t, j);
+    uint16_t* dst = p.q_out + static_cast<int64_t>(u.t0 + t) * p.Hq * p.D;
+#pragma unroll 1
+    for (int i = 0; i < kHeadPasses; ++i) {
+      const int h = h0 + i * split.heads;
+      if (h >= p.Hq) break;
+      float f[16];
+      widen(ld_shared_16(keep + buf + i * kPassBytes), f);
+      widen(ld_shared_16(keep + buf + i * kPassBytes + 512), f + 8);
+      if (run.rotated) rotate<INTER>(f, g, p.one);
+      *reinterpret_cast<uint4*>(dst + h * p.D + run.off_a) = narrow(f);
+      *reinterpret_cast<uint4*>(dst + h * p.D + run.off_b) = narrow(f + 8);
+    }
   }
+  cp_async_wait_all();  // none is left in flight: the last load is empty
 }
 
 template <int LPR>
@@ -423,9 +448,9 @@ sg_status_t append_launch(const AttnShape& s, const AttnArgs& a) {
   // A CTA's warps take one or more items each: of 16 tokens, 2 Hk heads of K and V, and the
   // query heads 8 at a time for as many tokens as a warp holds.  Fewer units than some waves of
   // CTAs are split along the items, down to one a warp.
-  const int64_t rows = s.D > 64 ? 4 : 8;
-  const int64_t items = p.by_token ? 2 * ((s.Hk + rows - 1) / rows) + (s.Hq + rows * kHeadPasses - 1) / (rows * kHeadPasses)
-                                   : 2 * s.Hk + kKvBlock / rows * ((s.Hq + kHeadPasses - 1) / kHeadPasses);
+  const int64_t rows = s.D > 64 ? 4 : 8, heads = p.by_token ? rows : rows / kTokens;
+  const int64_t items = 2 * ((s.Hk + heads - 1) / heads) +
+                        (p.by_token ? 1 : kKvBlock / kTokens) * ((s.Hq + heads * kHeadPasses - 1) / (heads * kHeadPasses));
   const int64_t want = (p.by_token ? 1 : kWaves) * kCtas * s.num_sms / units, most = (items + kWarps - 1) / kWarps;
   const unsigned split = static_cast<unsigned>(want < 1 ? 1 : want < most ? want : most);
   GemmLaunch l(dim3(units, split), dim3(kThreads), 0, a.stream, 1);
