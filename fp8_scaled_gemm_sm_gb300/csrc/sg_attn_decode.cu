@@ -14,7 +14,7 @@
 //   * Products add up in fp32 in mma.sync with keys (or dimensions) as its M and the query rows of
 //     a key/value head, 8 a tile, as its N: groups of up to 8 rows leave nothing idle but unused columns.
 //     Codes become fp16 exactly (two a conversion); queries are scaled per row by a power of two and are then exact in
-//     fp16; weights are rounded to fp16 (2^-11 of each).  (mma.sync on e4m3 operands measured slower: it
+//     fp16; weights are rounded to fp16 (2^-11 of each, 2^-32 of the largest for those below 2^-21 of it).  (mma.sync on e4m3 operands measured slower: it
 //     converts them too, and a query takes two terms.)
 //   * The contraction order over dimensions is free, so a lane takes K as it
 //     lies: lane (g, c) holds 16-byte runs c (and c + 4) of keys g and g + 8, four dimensions a k-step.
@@ -50,7 +50,9 @@ constexpr int kSegCost = 3;     // what a segment costs beside its tiles, in til
 constexpr int kUncut = 4;       // segments of up to 1 / kUncut of a range are not cut
 constexpr int kMaxWarps = 16;
 constexpr int kJoinWarps = 8;
-constexpr float kSlack = 8.f;   // log2 of the largest weight
+constexpr float kSlack = 8.f;   // log2 of how far a maximum may pass its reference
+constexpr float kLift = 7.f;    // the output's weights at its reference are 2^kLift, the largest 2^15: the room that
+                                // fp16 has above 1 keeps light weights among its normal numbers, down to 2^-21
 
 // What the join kernel does for a segment (or range): ranges first .. last have parts of
 // segment (b, hr); last < 0: nothing.
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
             top = fmaxf(top, two);
             vtop = fmaxf(vtop, two + vx[j]);
           }
-          move |= top > m[r][e] + kSlack || vtop > n[r][e] + kSlack;
+          move |= top > m[r][e] + kSlack || vtop > n[r][e] + kLift + kSlack;
         }
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -539,9 +541,9 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
               sum[r][e] *= ex2(m[r][e] - top);
               m[r][e] = top;
             }
-            if (vtop > n[r][e]) {
-              const float by = ex2(n[r][e] - vtop);
-              n[r][e] = vtop;
+            if (vtop - kLift > n[r][e]) {
+              const float by = ex2(n[r][e] - (vtop - kLift));
+              n[r][e] = vtop - kLift;
 #pragma unroll
               for (int i = 0; i < kOut; ++i) {
                 o[r][i][e] *= by;

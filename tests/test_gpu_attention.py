@@ -303,6 +303,24 @@ def test_decode(case):
     assert binding.scaled_attn_debug_status(plan.handle)[0] == 0
 
 
+@pytest.mark.parametrize("B,hq,hk,d,qn,long", [
+    (70, 32, 32, 128, 1, 3000),     # 2240 segments on 152 x 12 ranges
+    (90, 32, 32, 64, 1, 3000),      # 2880 on 152 x 16
+    (60, 64, 32, 128, 5, 2000),     # 1920 of two row tiles each on 152 x 8
+    (700, 2, 1, 128, 1, 900),       # more sequences than a block has threads
+    (1500, 1, 1, 32, 2, 500),
+    (2600, 2, 2, 64, 1, 70),
+])
+def test_decode_many_short_sequences_and_a_few_long(B, hq, hk, d, qn, long):
+    rng = np.random.default_rng(B)
+    lens = [int(n) for n in rng.integers(0, 40, B)]
+    for b in (0, B // 2, B - 1):
+        lens[b] = long + b % 17
+    lens[1], lens[2] = 0, 1
+    _, args, host, out, lse = _decode(lens, hq, hk, d, 16, qn, 800 + B)
+    _check_decode(lens, hq, hk, d, 16, qn, host, args[0], out, lse)
+
+
 def test_decode_one_long_sequence():
     lens = [20011]
     _, args, host, out, lse = _decode(lens, 4, 1, 128, 64, 1, 31)
@@ -438,6 +456,10 @@ PROMPT = [
     ([70, 64], [1408, 16], 32, 4, 112, True),
     ([200], [0], 2, 1, 128, True),
     ([9, 500], [1500, 0], 2, 1, 128, False),
+    ([40, 1, 0, 130, 3, 257], [2000, 1, 0, 130, 1500, 700], 4, 1, 128, True),
+    ([40, 1, 0, 130, 3, 257], [2000, 1, 0, 130, 1500, 700], 3, 3, 128, False),
+    ([33, 300, 5], [1300, 120, 603], 10, 2, 96, True),
+    ([300, 2], [1009, 1030], 6, 2, 128, True),
 ]
 
 
@@ -497,6 +519,21 @@ def test_prompt_many_sequences(B, causal, d):
     _, lse = plan.prompt(q, k, v, _dev(_cum(ql)), _dev(_cum(kl)), causal=causal, out=out)
     torch.cuda.synchronize()
     _check_prompt(ql, kl, hq, hk, d, causal, q, k, v, out, lse)
+
+
+@pytest.mark.parametrize("B", [33, 130])
+def test_prompt_many_sequences_behind_contexts(B):
+    rng = np.random.default_rng(B)
+    ql = [int(n) for n in rng.integers(0, 12, B)]
+    kl = [n + 700 + int(m) for n, m in zip(ql, rng.integers(0, 300, B))]
+    ql[7], kl[7], ql[B - 3], kl[B - 3], kl[5] = 290, 300, 140, 600, 0
+    hq, hk, d = 2, 1, 128
+    q, k, v = _prompt_inputs(ql, kl, hq, hk, d, 70 + B)
+    plan = _pkg().PagedAttention(hq, hk, d)
+    out = torch.full((sum(ql), hq, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    _, lse = plan.prompt(q, k, v, _dev(_cum(ql)), _dev(_cum(kl)), out=out)
+    torch.cuda.synchronize()
+    _check_prompt(ql, kl, hq, hk, d, True, q, k, v, out, lse)
 
 
 def test_prompt_sampled_rows_of_a_long_one():
