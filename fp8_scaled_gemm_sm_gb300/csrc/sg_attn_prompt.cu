@@ -533,7 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // for scores of 64 keys (weights over them) and 64 for the output, and four
 // CTAs share an SM: four softmaxes hide each other's waits, and the tiles are dealt out one by one, which
 // ragged prompts need (29 of 1 to 2500 tokens, 16 heads of 64: 64.5 us, 94 with two tiles a CTA).  What bounds
-// it is the softmax's instructions.  With heads of 128, two CTAs an SM, it is for short sequences.
+// it is the softmax's instructions.  With heads of 128, two CTAs an SM, it is for short
+// sequences (77 tokens, 32 heads over 8: 5.4 us).
 //   warps 0-3  softmax and output, one thread a row
 //   warp 4     TMA producer: Q, then K_0, V_0, K_1, V_1, ...; then V rows past the sequence's end
 //   warp 5     MMA issuer, one elected thread
@@ -726,27 +727,32 @@ __global__ void __launch_bounds__(kTileThreads, TileLayout<HD>::kCtas)
       ok = __all_sync(0xffffffffu, mbar_wait(s_full, j & 1, wd, kWhereEpiTmemFull));
       if (!ok) break;
       tc_fence_after();
-      const int chunks = (min(kTileKeys, kmax - j * kTileKeys) + 31) / 32;
       const int room = lim - j * kTileKeys;
       const bool edge = lim_warp - j * kTileKeys < kTileKeys;
-      // twice over the scores, for the maximum and for the weights: 64 of them do not fit the registers
-      uint32_t s[32];
+      // Where registers hold all 64 scores (two CTAs an SM) they are read once, else 32 at a time and twice,
+      // for the maximum and for the weights.
+      constexpr int kHeld = HD == 128 ? 2 : 1;  // times 32 scores
+      const int chunks = kHeld == 2 ? 2 : (min(kTileKeys, kmax - j * kTileKeys) + 31) / 32;
+      uint32_t s[kHeld][32];
       auto scores = [&](int c) {
-        tmem_ld_32x32b_x32(s_addr + 32 * c, s);
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) tmem_ld_32x32b_x32(s_addr + 32 * (c + k), s[k]);
         tmem_wait_ld();
         if (edge) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * c + i >= room) s[i] = 0xFF800000u;
+          for (int k = 0; k < kHeld; ++k)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * (c + k) + i >= room) s[k][i] = 0xFF800000u;
         }
       };
       float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
+      for (int c = 0; c < chunks; c += kHeld) {
         scores(c);
 #pragma unroll
-        for (int i = 0; i < 32; i += 2)
-          tops[(i >> 1) & 3] = max3(tops[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+        for (int i = 0; i < 32 * kHeld; i += 2)
+          tops[(i >> 1) & 3] = max3(tops[(i >> 1) & 3], __uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1]));
       }
       const float mx = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * p.scale_log2;
       if (j == 0) {
@@ -773,19 +779,22 @@ __global__ void __launch_bounds__(kTileThreads, TileLayout<HD>::kCtas)
       const float neg = ref == -INFINITY ? 0.f : -ref;
       const uint64_t neg2 = pack_f32x2(neg, neg);
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
-        scores(c);
-        uint32_t w[16];
+      for (int c = 0; c < chunks; c += kHeld) {
+        if (kHeld == 1) scores(c);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float x, y;
-          unpack_f32x2(fma_f32x2(pack_f32x2(s[2 * i], s[2 * i + 1]), scale2, neg2), x, y);
-          x = ex2(x);
-          y = ex2(y);
-          sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(x, y));
-          w[i] = pack_bf16x2(x, y);
+        for (int k = 0; k < kHeld; ++k) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float x, y;
+            unpack_f32x2(fma_f32x2(pack_f32x2(s[k][2 * i], s[k][2 * i + 1]), scale2, neg2), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(x, y));
+            w[i] = pack_bf16x2(x, y);
+          }
+          tmem_st_32x32b_x16(s_addr + 16 * (c + k), w);
         }
-        tmem_st_32x32b_x16(s_addr + 16 * c, w);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -879,9 +888,10 @@ cudaError_t prompt_prepare() {
 sg_status_t prompt_launch(const AttnShape& s, const AttnArgs& a) {
   if (s.D <= 64) return launch<64, true>(s, a);
   // Two tiles a CTA read K and V half as often and overlap better, one a CTA starts sooner and
-  // deals out finer: by the keys a sequence has on average (32 heads over 8, one sequence of 256, 512, 1024 tokens: 9.6,
-  // 12.6, 19.2 us with two, 8.3, 12.4, 21.2 with one; 32 of 200: 64.6 and 56.5; 8 of 512: 44.1 and 45.9).
-  return a.Tk <= 384 * a.B ? launch<128, true>(s, a) : launch<128, false>(s, a);
+  // deals out finer: by the keys a sequence has on average (32 heads over 8, one sequence of 256, 512, 1024, 2048 tokens: 9.6,
+  // 12.5, 19.2, 35.1 us with two, 7.6, 11.1, 19.0, 39.4 with one; 8 of 512: 44.8 and 44.6; 32 of 200: 65.2 and 54.9; 8 heads
+  // over 8, one of 512, 1024: 11.4, 16.8 and 11.1, 17.8).
+  return a.Tk <= 512 * a.B ? launch<128, true>(s, a) : launch<128, false>(s, a);
 }
 
 }  // namespace sg
