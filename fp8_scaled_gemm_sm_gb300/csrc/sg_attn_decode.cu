@@ -50,6 +50,7 @@ constexpr int kSegCost = 3;     // what a segment costs beside its tiles, in til
 constexpr int kUncut = 4;       // segments of up to 1 / kUncut of a range are not cut
 constexpr int kMaxWarps = 16;
 constexpr int kJoinWarps = 8;
+constexpr int kFirst = 4;
 constexpr float kSlack = 8.f;   // log2 of how far a maximum may pass its reference
 constexpr float kLift = 7.f;    // the output's weights at its reference are 2^kLift, the largest 2^15: the room that
                                 // fp16 has above 1 keeps light weights among its normal numbers, down to 2^-21
@@ -690,6 +691,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
   const int d = 4 * lane < HD ? 4 * lane : 0;
   for (int row = many ? blockIdx.y : warp; row < rows; row += many ? gridDim.y : kJoinWarps) {
     float m = -INFINITY, n = -INFINITY, sum = 0.f;
+    // this warp's first parts are on their way while the references are looked up
+    const int step = many ? kJoinWarps : 1, k0 = many ? warp : 0;
+    float4 mls[kFirst], xs[kFirst];
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) {
+      const int k = min(k0 + i * step, count - 1);
+      mls[i] = p.part_ml[at(k, row)];
+      xs[i] = *reinterpret_cast<const float4*>(p.part_o + static_cast<int64_t>(at(k, row)) * HD + d);
+    }
     for (int k = lane; k < count; k += 32) {
       const float4 ml = p.part_ml[at(k, row)];
       m = fmaxf(m, ml.x);
@@ -702,17 +712,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
     }
     const float m0 = m == -INFINITY ? 0.f : m, n0 = n == -INFINITY ? 0.f : n;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = many ? warp : 0; k < count; k += many ? kJoinWarps : 1) {
-      const float4 ml = p.part_ml[at(k, row)];
-      const float4 x = *reinterpret_cast<const float4*>(p.part_o + static_cast<int64_t>(at(k, row)) * HD + d);
+    auto add = [&](const float4& ml, const float4& x) {
       sum += ml.z * ex2(ml.x - m0);
       const float by = ex2(ml.y - n0);
       o.x += x.x * by;
       o.y += x.y * by;
       o.z += x.z * by;
       o.w += x.w * by;
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i)
+      if (k0 + i * step < count) add(mls[i], xs[i]);
+#pragma unroll 4
+    for (int k = k0 + kFirst * step; k < count; k += step)
+      add(p.part_ml[at(k, row)], *reinterpret_cast<const float4*>(p.part_o + static_cast<int64_t>(at(k, row)) * HD + d));
     if (many) {
       __syncthreads();  // the last row's have been read
       shared_o[warp][lane] = o;
