@@ -9,7 +9,7 @@
 // makes rescaling the output rare.
 //
 // Rows are packed: a tile's 128 rows are 128 / G tokens times G query heads of one
-// key/value head (G the largest power of two in the group), so grouped heads share
+// key/value head (G the largest divisor of the group that leaves at most 8 rows idle), so grouped heads share
 // each K and V tile, the causal edge wastes less, and short prompts fill rows.
 // A CTA owns two such row tiles and runs them in opposition: while the tensor
 // cores work for one, the other's softmax runs.  Per CTA:
@@ -58,8 +58,8 @@ struct PromptParams {
   const int32_t *cu_q, *cu_k;
   int Tq, Tk, B, Hq, D, causal;
   int group;            // query heads of a key/value head
-  int gshift;           // log2 of the query heads packed into a tile
-  int head_groups;      // Hq >> gshift
+  int pack;             // query heads packed into a tile
+  int head_groups;      // Hq / pack
   int units;
   float scale_log2;
   uint16_t* out;
@@ -240,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   grid_dep_launch();
   grid_dep_wait();
-  const int tile_tokens = kRows >> p.gshift;
-  const int head0 = static_cast<int>(blockIdx.x) % p.head_groups << p.gshift;
+  const int tile_tokens = kRows / p.pack;
+  const int head0 = static_cast<int>(blockIdx.x) % p.head_groups * p.pack;
   if (warp == 0) {
     const Unit u = pick_unit(p, static_cast<int>(blockIdx.x) / p.head_groups, 2 * tile_tokens, lane);
     if (lane == 0) *reinterpret_cast<Unit*>(misc + 2) = u;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0 && num_blocks > 0) {
         const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
         const int tiles = tok0 + tile_tokens < lq ? 2 : 1;
-        mbar_arrive_expect_tx(q_full, tiles * L::kTile);
+        mbar_arrive_expect_tx(q_full, tiles * L::kBoxes * tile_tokens * p.pack * 128);
         for (int t = 0; t < tiles; ++t)
           for (int x = 0; x < L::kBoxes; ++x)
             tma_load_3d_hint(sQ + t * L::kTile + x * L::kBox, &tmQ, x * 64, head0, q0 + tok0 + t * tile_tokens, q_full, once);
@@ -428,10 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_addr = tmem + lanes + t * 128, o_addr = tmem + lanes + 256 + t * HD;
     const int row = quarter * 32 + lane;
-    const int tok = tok0 + t * tile_tokens + (row >> p.gshift);
-    const int head = head0 + (row & ((1 << p.gshift) - 1));
+    const int tok = row < tile_tokens * p.pack ? tok0 + t * tile_tokens + row / p.pack : lq;  // lq: an idle row
+    const int head = head0 + row % p.pack;
     const int lim = visible(tok);
-    const int lim_warp = visible(tok0 + t * tile_tokens + (quarter * 32 >> p.gshift));  // least of the warp's
+    const int lim_warp = visible(tok0 + t * tile_tokens + quarter * 32 / p.pack);  // least of the warp's
     const int n = blocks[t];
     const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
     float ref = -INFINITY;     // r, in log2 units
@@ -577,8 +577,8 @@ __global__ void __launch_bounds__(kTileThreads, TileLayout<HD>::kCtas)
 
   grid_dep_launch();
   grid_dep_wait();
-  const int tile_tokens = kRows >> p.gshift;
-  const int head0 = static_cast<int>(blockIdx.x) % p.head_groups << p.gshift;
+  const int tile_tokens = kRows / p.pack;
+  const int head0 = static_cast<int>(blockIdx.x) % p.head_groups * p.pack;
   if (warp == 0) {
     const Unit u = pick_unit(p, static_cast<int>(blockIdx.x) / p.head_groups, tile_tokens, lane);
     if (lane == 0) *reinterpret_cast<Unit*>(misc + 2) = u;
@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(kTileThreads, TileLayout<HD>::kCtas)
     // ---------------- TMA producer ----------------
     if (lane == 0 && n > 0) {
       const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
-      mbar_arrive_expect_tx(q_full, L::kQTile);
+      mbar_arrive_expect_tx(q_full, L::kBoxes * tile_tokens * p.pack * 128);
       for (int x = 0; x < L::kBoxes; ++x)
         tma_load_3d_hint(sQ + x * L::kQBox, &tmQ, x * 64, head0, q0 + tok0, q_full, once);
       const int kv_head = head0 / p.group;
@@ -715,10 +715,10 @@ __global__ void __launch_bounds__(kTileThreads, TileLayout<HD>::kCtas)
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t s_addr = tmem + lanes, o_addr = s_addr + 64;
     const int row = warp * 32 + lane;
-    const int tok = tok0 + (row >> p.gshift);
-    const int head = head0 + (row & ((1 << p.gshift) - 1));
+    const int tok = row < tile_tokens * p.pack ? tok0 + row / p.pack : lq;  // lq: an idle row
+    const int head = head0 + row % p.pack;
     const int lim = visible(tok);
-    const int lim_warp = visible(tok0 + (warp * 32 >> p.gshift));  // least of the warp's
+    const int lim_warp = visible(tok0 + warp * 32 / p.pack);  // least of the warp's
     const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
     float ref = -INFINITY;      // r, in log2 units
     uint64_t sum2[2] = {0, 0};  // four partial row sums
@@ -830,9 +830,11 @@ sg_status_t launch(const AttnShape& s, const AttnArgs& a) {
   p.D = s.D;
   p.causal = a.causal;
   p.group = s.Hq / s.Hk;
-  while (p.gshift < 7 && p.group % (2 << p.gshift) == 0) ++p.gshift;
-  p.head_groups = s.Hq >> p.gshift;
-  const int64_t units = a.Tq / ((TILE ? 1 : 2) * (kRows >> p.gshift)) + a.B;
+  p.pack = 1;
+  for (int g = 2; g <= p.group && g <= kRows; ++g)
+    if (p.group % g == 0 && kRows % g <= kRows / 16) p.pack = g;
+  p.head_groups = s.Hq / p.pack;
+  const int64_t units = a.Tq / ((TILE ? 1 : 2) * (kRows / p.pack)) + a.B;
   if (units * p.head_groups >= (int64_t(1) << 31)) return SG_ERR_UNSUPPORTED_SHAPE;
   p.units = static_cast<int>(units);
   p.scale_log2 = a.scale * 1.4426950408889634f;
@@ -848,7 +850,7 @@ sg_status_t launch(const AttnShape& s, const AttnArgs& a) {
   const uint64_t sq[2] = {D * el, static_cast<uint64_t>(a.q_stride) * el};
   const uint64_t sk[2] = {D * el, static_cast<uint64_t>(keys ? a.k_stride : a.q_stride) * el};
   const uint64_t sv[2] = {D * el, static_cast<uint64_t>(keys ? a.v_stride : a.q_stride) * el};
-  const uint32_t bq[3] = {64, 1u << p.gshift, static_cast<uint32_t>(kRows >> p.gshift)};
+  const uint32_t bq[3] = {64, static_cast<uint32_t>(p.pack), static_cast<uint32_t>(kRows / p.pack)};
   const uint32_t bk[3] = {64, 1, TILE ? kTileKeys : kRows};
   CUtensorMap tmQ, tmK, tmV;
   if (!encode_3d(&tmQ, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, dq, sq, bq, CU_TENSOR_MAP_SWIZZLE_128B) ||

@@ -536,6 +536,20 @@ def test_prompt_many_sequences_behind_contexts(B):
     _check_prompt(ql, kl, hq, hk, d, True, q, k, v, out, lse)
 
 
+@pytest.mark.parametrize("group", [3, 6, 11, 13, 24, 39, 60, 129])
+@pytest.mark.parametrize("d,ctx", [(64, 0), (128, 0), (128, 700)])
+def test_prompt_heads_of_a_group_share_rows(group, d, ctx):
+    # heads times tokens of a tile need not fill its rows
+    ql = [45, 1, 0, 23]
+    kl = [n + ctx for n in ql]
+    q, k, v = _prompt_inputs(ql, kl, group, 1, d, 90 + group)
+    plan = _pkg().PagedAttention(group, 1, d)
+    out = torch.full((sum(ql), group, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    _, lse = plan.prompt(q, k, v, _dev(_cum(ql)), _dev(_cum(kl)), out=out)
+    torch.cuda.synchronize()
+    _check_prompt(ql, kl, group, 1, d, True, q, k, v, out, lse)
+
+
 def test_prompt_sampled_rows_of_a_long_one():
     # long enough for several key tiles a row; a sample of rows against 64 bits
     hq, hk, d, n = 4, 1, 128, 3001
