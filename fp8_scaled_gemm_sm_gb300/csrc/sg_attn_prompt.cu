@@ -15,23 +15,28 @@
 // cores work for one, the other's softmax runs.  Per CTA:
 //   warps 0-3, 4-7  softmax of tile 0 / 1, one thread a row: S from tensor memory to
 //                   registers, maximum, 2^x, row sum, P = bf16 back over S's columns; at the end
-//                   the output row, divided by the sum, straight to memory.
-//   warp 8          TMA producer: both Q tiles once, then K_0, V_0, K_1, V_1, ... through a ring.
+//                   the output rows, divided by the sums, through shared memory to whole lines.
+//   warp 8          TMA producer: both Q tiles, then K_0, V_0, K_1, V_1, ... through a ring.
 //   warp 9          MMA issuer, one elected thread: S_t = Q_t K_j^T (operands in shared memory), O_t +=
 //                   P_t V_j (P in tensor memory, V as it lies in memory: N-major).
 //   warp 10         V rows past a sequence's end (below).
+//   warp 11         what to do: the unit that the CTA was launched for, then those of CTAs that have not
+//                   been launched yet, which it takes over before their time (cluster launch control): the next unit's
+//                   loads and first scores go with this one's last softmax and output.  Launched one by one, a CTA a
+//                   unit, a unit costs 6.7 us beside its blocks, taken over 3.5.
 // The tensor cores take the MMAs in order, so S_t of block j + 1, issued after
 // O_t += P_t V_j, cannot overwrite P_t early, and a softmax thread that sees it
 // complete may also touch O_t.
 // P is rounded to bf16 (V is bf16, and an MMA has one operand type): an error of at most 2^-9 of each weight,
 // against the 2^-9 of the rounded output; the row sums take the unrounded weights.
 //
-// What bounds it: the tensor pipe, short of the turns it waits for a softmax.  16384 tokens, 32 heads of 128 over
-// 8, causal: 1275 us, 1.72 PFLOP/s, 89% of what the library's bf16 GEMM reaches.  Measured beside it: key
-// columns past a block's last key skipped in the loads and exponentials (they are hidden, and only the last block
-// has any; the branches cost every block) 1377 us, and, of that form, one
-// S buffer a tile with P elsewhere 1509 us, 64-key blocks with two S buffers 1612, MMAs issued by lane 0 under a
-// plain branch instead of one elected thread for the whole loop 1520.
+// What bounds it: the tensor pipe, but for a unit's first and last softmax and its output: a block of both tiles
+// takes 1.34 us, 1.9 PFLOP/s.  16384 tokens, 32 heads of 128 over 8, causal: 1250 us, 1.75 PFLOP/s, 91% of what the
+// library's bf16 GEMM reaches; 6 chunks of 300 to 2048 tokens behind contexts, 40 heads over 8: 301 us.  Measured
+// beside it: a CTA a unit 1275 and 323 us; output a row a lane 1257 and 309; key columns past a block's last key
+// skipped in the loads and exponentials (they are hidden, and only the last block has any; the branches cost every
+// block) 1377 us for the 16384 tokens, and, of that form, one S buffer a tile with P elsewhere 1509 us, 64-key
+// blocks with two S buffers 1612, MMAs issued by lane 0 under a plain branch instead of one elected thread 1520.
 //
 // V rows past a sequence's end belong to the next one: those that share a 16-key
 // MMA step with valid ones are zeroed in shared memory, the rest are not multiplied.
@@ -47,9 +52,12 @@ namespace {
 
 constexpr int kRows = 128;   // rows of a tile, keys of a block
 constexpr int kThreads = 384;
-// Registers a thread of the softmax warpgroups and of the third (producer, MMA issuer, V's end,
-// an idle warp): 2 x 192 + 120 = 3 x 168, what the block is launched with.
-constexpr int kSoftmaxRegs = 192, kIssueRegs = 120;
+// Registers a thread of the softmax warpgroups and of the third: 2 x 208 + 88 = 3 x 168, what the block is
+// launched with (192 and 120: 334 us instead of 309 for the chunks above).
+constexpr int kSoftmaxRegs = 208, kIssueRegs = 88;
+constexpr int kWhereJob = 0x41;  // a wait for a job, beside those of sg_ptx.cuh
+constexpr int kJobReaders = 11;  // warps that take jobs
+constexpr int kAhead = 4;   // loads before a job's end at which the next one is looked for
 constexpr int kEarly = 4;  // 16-key steps of a block whose weights are handed over first
 constexpr int kTileKeys = 64, kTileThreads = 192;  // of the kernel with one row tile a CTA
 constexpr float kSlack = 8.f;  // log2 of the largest weight
@@ -171,15 +179,15 @@ __device__ __forceinline__ Unit pick_unit(const PromptParams& p, int x, int toke
   return u;
 }
 
-// One thread's row of the output: CHUNKS times 32 dimensions from `first` on, out of tensor memory, over its sum.
-template <int CHUNKS>
-__device__ __forceinline__ void put_rows(const PromptParams& p, uint32_t o_addr, int first, bool some, float sum, float ref,
-                                         int q0, int tok, int lq, int head, bool with_lse) {
+// One thread's row of the output: HD dimensions out of tensor memory, over its sum.
+template <int HD>
+__device__ __forceinline__ void put_row(const PromptParams& p, uint32_t o_addr, bool some, float sum, float ref, int q0, int tok,
+                                        int lq, int head) {
   const bool none = sum == 0.f;
   const float inv = none ? 0.f : 1.f / sum;
   const int64_t at = static_cast<int64_t>(q0 + tok) * p.Hq + head;
 #pragma unroll
-  for (int c = 0; c < CHUNKS; ++c) {
+  for (int c = 0; c < HD / 32; ++c) {
     uint32_t o[32];
     if (some) {
       tmem_ld_32x32b_x32(o_addr + 32 * c, o);
@@ -190,16 +198,64 @@ __device__ __forceinline__ void put_rows(const PromptParams& p, uint32_t o_addr,
     if (tok < lq) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (first + 32 * c + 8 * i < p.D) {
+        if (32 * c + 8 * i < p.D) {
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(o[8 * i + 2 * e + 1]));
-          *reinterpret_cast<uint4*>(p.out + at * p.D + first + 32 * c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(p.out + at * p.D + 32 * c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
   }
-  if (with_lse && tok < lq && p.lse) p.lse[at] = none ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+  if (tok < lq && p.lse) p.lse[at] = none ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+}
+
+// A warp's 32 rows of the output, a row a lane: HD dimensions out of tensor memory, over their sums, 64 at a time
+// through 4 KB of shared memory at `stage`, so that a store writes whole lines (eight lanes a row): a row a lane
+// wrote 32 lines at once, which took 2 us of a two-tile CTA's 128 x 2 rows.
+template <int HD>
+__device__ __forceinline__ void put_rows(const PromptParams& p, uint32_t o_addr, uint32_t stage, int lane, bool some, float sum,
+                                         float ref, int q0, int tok, int lq, int head) {
+  const bool none = sum == 0.f;
+  const float inv = none ? 0.f : 1.f / sum;
+  const int64_t at = static_cast<int64_t>(q0 + tok) * p.Hq + head;
+  const int64_t mine = tok < lq ? at * p.D : -1;
+#pragma unroll
+  for (int h = 0; h < HD / 64; ++h) {
+    __syncwarp();  // what was staged before has been read
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t o[32];
+      if (some) {
+        tmem_ld_32x32b_x32(o_addr + 64 * h + 32 * c, o);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(o[8 * i + 2 * e + 1]));
+        st_shared_v4(stage + lane * 128 + (((4 * c + i) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+      }
+    }
+    __syncwarp();
+    const int piece = lane & 7, d = 64 * h + 8 * piece;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      const int64_t to = __shfl_sync(0xffffffffu, mine, r);
+      uint4 v;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "r"(stage + r * 128 + ((piece ^ (r & 7)) << 4))
+                   : "memory");
+      if (to >= 0 && d < p.D) *reinterpret_cast<uint4*>(p.out + to + d) = v;
+    }
+  }
+  if (tok < lq && p.lse) p.lse[at] = none ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
 }
 
 struct PromptLayout {
@@ -207,14 +263,23 @@ struct PromptLayout {
   static constexpr int kBoxes = HD / 64;                  // 64-column (128-byte) boxes of a row
   static constexpr int kBox = kRows * 128;                // bytes of a box
   static constexpr int kTile = kBoxes * kBox;             // a Q, K or V tile
-  static constexpr int kStages = 5;
+  static constexpr int kStages = 4;
   static constexpr int kOffKv = 2 * kTile;
-  static constexpr int kOffBar = kOffKv + kStages * kTile;
-  static constexpr int kNumBars = 2 * kStages + 12;
+  static constexpr int kOffOut = kOffKv + kStages * kTile;  // 4 KB a softmax warp
+  static constexpr int kOffBar = kOffOut + 8 * 4096;
+  static constexpr int kNumBars = 2 * kStages + 20;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kBytes = kOffMisc + 64;
+  static constexpr int kOffJobs = kOffMisc + 16;
+  static constexpr int kOffAnswer = kOffJobs + 2 * 32;
+  static constexpr int kBytes = kOffAnswer + 16;
   static constexpr int kDynSmem = kBytes + 1024;
-  static_assert(kDynSmem <= 232448, "shared memory");
+  static_assert(kOffAnswer % 16 == 0 && kDynSmem <= 232448, "shared memory");
+};
+
+// A unit and the first query head of its rows.  u.b: -1 nothing, -2 no more.
+struct Job {
+  Unit u;
+  int head0, unused;
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -233,19 +298,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto p_full = [&](int t) { return bar0 + 8 * (2 * S + 2 + t); };
   auto p_half = [&](int t) { return bar0 + 8 * (2 * S + 4 + t); };
   auto o_full = [&](int t) { return bar0 + 8 * (2 * S + 6 + t); };
-  const uint32_t q_full = bar0 + 8 * (2 * S + 8), drain_bar = bar0 + 8 * (2 * S + 9);
-  const uint32_t v_last = bar0 + 8 * (2 * S + 10), v_clean = bar0 + 8 * (2 * S + 11);
-  int* misc = reinterpret_cast<int*>(smem + L::kOffMisc);  // [0] TMEM base, [1] abort, [2..7] the unit
+  auto job_full = [&](int s) { return bar0 + 8 * (2 * S + 8 + s); };
+  auto job_empty = [&](int s) { return bar0 + 8 * (2 * S + 10 + s); };
+  const uint32_t q_full = bar0 + 8 * (2 * S + 12), q_empty = bar0 + 8 * (2 * S + 13), drain_bar = bar0 + 8 * (2 * S + 14);
+  const uint32_t v_last = bar0 + 8 * (2 * S + 15), v_clean = bar0 + 8 * (2 * S + 16);
+  const uint32_t more_wanted = bar0 + 8 * (2 * S + 17), answered = bar0 + 8 * (2 * S + 18);
+  int* misc = reinterpret_cast<int*>(smem + L::kOffMisc);  // [0] TMEM base, [1] abort
+  Job* jobs = reinterpret_cast<Job*>(smem + L::kOffJobs);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   grid_dep_launch();
   grid_dep_wait();
   const int tile_tokens = kRows / p.pack;
-  const int head0 = static_cast<int>(blockIdx.x) % p.head_groups * p.pack;
-  if (warp == 0) {
-    const Unit u = pick_unit(p, static_cast<int>(blockIdx.x) / p.head_groups, 2 * tile_tokens, lane);
-    if (lane == 0) *reinterpret_cast<Unit*>(misc + 2) = u;
-  }
   if (warp == 9) {
     tmem_alloc(smem_addr(&misc[0]), 512);
     tmem_relinquish();
@@ -261,105 +325,184 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(p_full(t), kRows);
       mbar_init(o_full(t), 1);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(job_full(s), 1);
+      mbar_init(job_empty(s), kJobReaders);
+    }
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     mbar_init(v_last, 1);
     mbar_init(v_clean, 1);
     mbar_init(drain_bar, 1);
+    mbar_init(more_wanted, 1);
+    mbar_init(answered, 1);
     misc[1] = 0;
     fence_mbarrier_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (misc[2] < 0) {
-    if (warp == 9) tmem_dealloc(static_cast<uint32_t>(misc[0]), 512);
-    return;
-  }
-  const int q0 = __shfl_sync(0xffffffffu, misc[3], 0), lq = __shfl_sync(0xffffffffu, misc[4], 0), k0 = __shfl_sync(0xffffffffu, misc[5], 0),
-            lk = __shfl_sync(0xffffffffu, misc[6], 0), tok0 = __shfl_sync(0xffffffffu, misc[7], 0);
-  auto visible = [&](int tok) { return p.causal ? min(lk, tok + 1 + lk - lq) : lk; };
-  int blocks[2], kmax[2];  // key blocks of a tile, keys that its last row sees
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int first = tok0 + t * tile_tokens;
-    kmax[t] = first < lq ? max(visible(min(first + tile_tokens, lq) - 1), 0) : 0;
-    blocks[t] = (kmax[t] + kRows - 1) / kRows;
-  }
-  const int num_blocks = max(blocks[0], blocks[1]);
-  // rows of the last V block that are not this sequence's but share a 16-key step with some that are
-  const int past = lk - (num_blocks - 1) * kRows;
-  const int tail_rows = num_blocks > 0 && past < kRows ? (16 - past) & 15 : 0;
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
   const Watchdog wd{p.status, p.timeout_ns, reinterpret_cast<volatile int*>(&misc[1])};
+  // Job i of this CTA; false: no more, or the CTA gives up.  A warp that has what it needs of it says so.
+  auto read = [&](int i, Job& job) {
+    const int4* from = reinterpret_cast<const int4*>(jobs + (i & 1));
+    const int4 x = from[0], y = from[1];
+    auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    job.u.b = same(x.x), job.u.q0 = same(x.y), job.u.lq = same(x.z), job.u.k0 = same(x.w);
+    job.u.lk = same(y.x), job.u.first = same(y.y), job.head0 = same(y.z);
+  };
+  auto done = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(job_empty(i & 1));
+  };
+  auto peek = [&](int i, Job& job) {
+    if (!__all_sync(0xffffffffu, mbar_wait(job_full(i & 1), (i >> 1) & 1, wd, kWhereJob))) return false;
+    read(i, job);
+    return job.u.b != -2;
+  };
+  auto take = [&](int i, Job& job) {
+    const bool got = peek(i, job);
+    if (got) done(i);
+    return got;
+  };
+  // What follows from a job.
+  struct Plan {
+    int kmax[2], blocks[2];  // keys that a tile's last row sees, its key blocks
+    int num_blocks, past, tail_rows;
+  };
+  auto visible = [&](const Unit& u, int tok) { return p.causal ? min(u.lk, tok + 1 + u.lk - u.lq) : u.lk; };
+  auto plan = [&](const Unit& u) {
+    Plan x{};
+    if (u.b < 0) return x;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int first = u.first + t * tile_tokens;
+      x.kmax[t] = first < u.lq ? max(visible(u, min(first + tile_tokens, u.lq) - 1), 0) : 0;
+      x.blocks[t] = (x.kmax[t] + kRows - 1) / kRows;
+    }
+    x.num_blocks = max(x.blocks[0], x.blocks[1]);
+    // rows of the last V block that are not this sequence's but share a 16-key step with some that are
+    x.past = u.lk - (x.num_blocks - 1) * kRows;
+    x.tail_rows = x.num_blocks > 0 && x.past < kRows ? (16 - x.past) & 15 : 0;
+    return x;
+  };
 
   if (warp >= 8) {
     reg_dec<kIssueRegs>();
+    Job job;
     if (warp == 8) {
       // ---------------- TMA producer ----------------
-      if (lane == 0 && num_blocks > 0) {
-        const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
-        const int tiles = tok0 + tile_tokens < lq ? 2 : 1;
-        mbar_arrive_expect_tx(q_full, tiles * L::kBoxes * tile_tokens * p.pack * 128);
-        for (int t = 0; t < tiles; ++t)
-          for (int x = 0; x < L::kBoxes; ++x)
-            tma_load_3d_hint(sQ + t * L::kTile + x * L::kBox, &tmQ, x * 64, head0, q0 + tok0 + t * tile_tokens, q_full, once);
-        const int kv_head = head0 / p.group;
-        int stage = 0;
-        uint32_t phase = 0, issued = 0, last_par = 0;
-        bool ok = true;
-        for (int i = 0; i < 2 * num_blocks; ++i) {
-          if (!mbar_wait(kv_empty(stage), phase ^ 1, wd, kWhereProducerEmpty)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(kv_full(stage), L::kTile);
-          for (int x = 0; x < L::kBoxes; ++x)
-            tma_load_3d_hint(sKv + stage * L::kTile + x * L::kBox, (i & 1) ? &tmV : &tmK, x * 64, kv_head,
-                             k0 + (i >> 1) * kRows, kv_full(stage), keep);
-          issued |= 1u << stage;
-          last_par = (last_par & ~(1u << stage)) | (phase << stage);
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1;
+      const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
+      int stage = 0, q_fills = 0;
+      uint32_t phase = 0, issued = 0, last_par = 0;
+      bool ok = true;
+      for (int it = 0; ok && take(it, job); ++it) {
+        const Plan x = plan(job.u);
+        if (lane == 0) {
+          if (x.num_blocks == 0) mbar_arrive(more_wanted);
+          const int tiles = job.u.first + tile_tokens < job.u.lq ? 2 : 1;
+          const int kv_head = job.head0 / p.group;
+          for (int i = 0; i < 2 * x.num_blocks; ++i) {
+            if (i == 0) {
+              ok = q_fills == 0 || mbar_wait(q_empty, (q_fills - 1) & 1, wd, kWhereProducerEmpty);
+              if (!ok) break;
+              mbar_arrive_expect_tx(q_full, tiles * L::kBoxes * tile_tokens * p.pack * 128);
+              for (int t = 0; t < tiles; ++t)
+                for (int b = 0; b < L::kBoxes; ++b)
+                  tma_load_3d_hint(sQ + t * L::kTile + b * L::kBox, &tmQ, b * 64, job.head0, job.u.q0 + job.u.first + t * tile_tokens,
+                                   q_full, once);
+              ++q_fills;
+            }
+            if (i == max(2 * x.num_blocks - kAhead, 0)) mbar_arrive(more_wanted);
+            ok = mbar_wait(kv_empty(stage), phase ^ 1, wd, kWhereProducerEmpty);
+            if (!ok) break;
+            mbar_arrive_expect_tx(kv_full(stage), L::kTile);
+            for (int b = 0; b < L::kBoxes; ++b)
+              tma_load_3d_hint(sKv + stage * L::kTile + b * L::kBox, (i & 1) ? &tmV : &tmK, b * 64, kv_head,
+                               job.u.k0 + (i >> 1) * kRows, kv_full(stage), keep);
+            issued |= 1u << stage;
+            last_par = (last_par & ~(1u << stage)) | (phase << stage);
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
         }
-        if (!ok) {  // loads in flight must land before the CTA can exit
-          mbar_wait_drain(q_full, 0, 200000000ull);
-          for (int s = 0; s < S; ++s)
-            if ((issued >> s) & 1) mbar_wait_drain(kv_full(s), (last_par >> s) & 1, 200000000ull);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (lane == 0) {  // loads in flight must land before the CTA can exit (all have, unless it gave up)
+        if (q_fills > 0) mbar_wait_drain(q_full, (q_fills - 1) & 1, 200000000ull);
+        for (int s = 0; s < S; ++s)
+          if ((issued >> s) & 1) mbar_wait_drain(kv_full(s), (last_par >> s) & 1, 200000000ull);
+      }
+    } else if (warp == 11) {
+      // ---------------- jobs: this CTA's own, then those of CTAs not yet launched ----------------
+      int next = static_cast<int>(blockIdx.x);
+      for (int it = 0;; ++it) {
+        if (it >= 2 && !__all_sync(0xffffffffu, mbar_wait(job_empty(it & 1), ((it >> 1) - 1) & 1, wd, kWhereJob))) break;
+        Unit u{};
+        u.b = -2;
+        if (next >= 0) u = pick_unit(p, next / p.head_groups, 2 * tile_tokens, lane);
+        if (lane == 0) {
+          jobs[it & 1] = Job{u, max(next, 0) % p.head_groups * p.pack, 0};
+          mbar_arrive(job_full(it & 1));
         }
+        if (next < 0 || !__all_sync(0xffffffffu, mbar_wait(more_wanted, it & 1, wd, kWhereJob))) break;
+        if (lane == 0) {
+          fence_proxy_async_smem();  // the last answer has been read
+          mbar_arrive_expect_tx(answered, 16);
+          take_cta(smem_addr(smem + L::kOffAnswer), answered);
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(answered, it & 1, wd, kWhereJob))) {
+          mbar_wait_drain(answered, it & 1, 200000000ull);  // before the CTA can exit
+          break;
+        }
+        next = taken_cta(smem_addr(smem + L::kOffAnswer));
+        __syncwarp();
       }
     } else if (warp == 10) {
       // ---------------- V rows past the sequence's end ----------------
-      if (tail_rows > 0) {
-        const int st = (2 * num_blocks - 1) % S;  // the last V block's: all other loads come before it
-        const bool ok = __all_sync(0xffffffffu, mbar_wait(v_last, 0, wd, kWhereMmaFull));
-        if (ok) {
-          for (int i = lane; i < tail_rows * 8 * L::kBoxes; i += 32)
-            st_shared_v4(sKv + st * L::kTile + (i / (tail_rows * 8)) * L::kBox + past * 128 + (i % (tail_rows * 8)) * 16, 0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(v_clean);
-        }
+      int loads = 0, tails = 0;  // before this job
+      for (int it = 0; take(it, job); ++it) {
+        const Plan x = plan(job.u);
+        loads += 2 * x.num_blocks;
+        if (x.tail_rows == 0) continue;
+        const int st = (loads - 1) % S;  // the job's last V block
+        if (!__all_sync(0xffffffffu, mbar_wait(v_last, tails++ & 1, wd, kWhereMmaFull))) break;
+        for (int i = lane; i < x.tail_rows * 8 * L::kBoxes; i += 32)
+          st_shared_v4(sKv + st * L::kTile + (i / (x.tail_rows * 8)) * L::kBox + x.past * 128 + (i % (x.tail_rows * 8)) * 16, 0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_clean);
       }
-    } else if (warp == 9) {
-      // ---------------- MMA issuer ----------------
-      if (num_blocks > 0 && elect_one()) {
-        int stage = 0;
-        uint32_t phase = 0;
-        auto advance = [&]() {
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1;
-          }
-        };
-        auto wait = [&](uint32_t bar, uint32_t parity, int where) {
-          const bool got = mbar_wait<true>(bar, parity, wd, where);
-          tc_fence_after();
-          return got;
-        };
+    } else if (elect_one()) {
+      // ---------------- MMA issuer: one thread for all of it ----------------
+      int stage = 0, q_uses = 0, tails = 0;
+      uint32_t phase = 0, turn[2] = {0, 0};  // parity of a tile's next weights
+      auto advance = [&]() {
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1;
+        }
+      };
+      auto wait = [&](uint32_t bar, uint32_t parity, int where) {
+        const bool got = mbar_wait<true>(bar, parity, wd, where);
+        tc_fence_after();
+        return got;
+      };
+      bool ok = true;
+      for (int it = 0; ok; ++it) {
+        ok = wait(job_full(it & 1), (it >> 1) & 1, kWhereJob);
+        if (!ok) break;
+        job = jobs[it & 1];
+        mbar_arrive(job_empty(it & 1));
+        if (job.u.b == -2) break;
+        const Plan x = plan(job.u);
+        if (x.num_blocks == 0) continue;
+        const int num_blocks = x.num_blocks;
         auto scores = [&](int t, int j) {  // S_t = Q_t K_j^T
-          const int n = (min(kRows, kmax[t] - j * kRows) + 15) & ~15;
+          const int n = (min(kRows, x.kmax[t] - j * kRows) + 15) & ~15;
           const uint32_t idesc = instr_desc(1, 1, kRows, n);
           const uint64_t a = kmajor_sw128_desc(sQ + t * L::kTile), k = kmajor_sw128_desc(sKv + stage * L::kTile);
 #pragma unroll
@@ -369,41 +512,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mma_commit(s_full(t));
         };
-        bool ok = wait(q_full, 0, kWhereMmaFull) && wait(kv_full(0), 0, kWhereMmaFull);
+        ok = wait(q_full, q_uses & 1, kWhereMmaFull) && wait(kv_full(stage), phase, kWhereMmaFull);
         if (ok) {
-          if (blocks[0] > 0) scores(0, 0);
-          if (blocks[1] > 0) scores(1, 0);
-          mma_commit(kv_empty(0));
+          if (x.blocks[0] > 0) scores(0, 0);
+          if (x.blocks[1] > 0) scores(1, 0);
+          mma_commit(kv_empty(stage));
+          if (num_blocks == 1) mma_commit(q_empty);
+          advance();
         }
-        advance();
         for (int j = 0; j < num_blocks && ok; ++j) {
           ok = wait(kv_full(stage), phase, kWhereMmaFull);  // V_j
           const int vs = stage;
           advance();
-          if (ok && j + 1 == num_blocks && tail_rows > 0) {
+          if (ok && j + 1 == num_blocks && x.tail_rows > 0) {
             mbar_arrive(v_last);
-            ok = wait(v_clean, 0, kWhereMmaFull);
+            ok = wait(v_clean, tails & 1, kWhereMmaFull);
           }
           bool k_ready = false;
           const uint64_t v = smem_desc(sKv + vs * L::kTile, L::kBox, 1024, 2);
           constexpr uint32_t idesc = instr_desc(1, 1, kRows, HD) | kIdescBMajorN;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (ok && j < blocks[t]) {
-              const int steps = (min(kRows, kmax[t] - j * kRows) + 15) / 16;
+            if (ok && j < x.blocks[t]) {
+              const int steps = (min(kRows, x.kmax[t] - j * kRows) + 15) / 16;
               // O_t += P_t V_j: what is stored first, then the rest
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                ok = ok && wait(h ? p_full(t) : p_half(t), j & 1, kWhereMmaTmemEmpty);
+                ok = ok && wait(h ? p_full(t) : p_half(t), turn[t], kWhereMmaTmemEmpty);
                 if (ok) {
 #pragma unroll
                   for (int i = h ? kEarly : 0; i < (h ? 8 : kEarly); ++i)
                     if (i < steps)
                       mma_f16_ts(tmem + 256 + t * HD, tmem + t * 128 + i * 8, desc_advance(v, i * 2048), idesc, (j | i) != 0);
-                  if (h && j + 1 == blocks[t]) mma_commit(o_full(t));
+                  if (h && j + 1 == x.blocks[t]) mma_commit(o_full(t));
                 }
               }
-              if (ok && j + 1 < blocks[t]) {
+              turn[t] ^= 1;
+              if (ok && j + 1 < x.blocks[t]) {
                 if (!k_ready) ok = wait(kv_full(stage), phase, kWhereMmaFull);
                 k_ready = true;
                 if (ok) scores(t, j + 1);
@@ -414,12 +559,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (k_ready) {
             mma_commit(kv_empty(stage));
             advance();
+            if (j + 2 == num_blocks) mma_commit(q_empty);  // the job's last scores
           }
         }
-        // every MMA has finished and every commit has landed before the CTA exits
-        mma_commit(drain_bar);
-        mbar_wait_drain(drain_bar, 0, 200000000ull);
+        ++q_uses;
+        tails += x.tail_rows > 0;
       }
+      // every MMA has finished and every commit has landed before the CTA exits
+      mma_commit(drain_bar);
+      mbar_wait_drain(drain_bar, 0, 200000000ull);
     }
   } else {
     reg_inc<kSoftmaxRegs>();
@@ -428,92 +576,116 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_addr = tmem + lanes + t * 128, o_addr = tmem + lanes + 256 + t * HD;
     const int row = quarter * 32 + lane;
-    const int tok = row < tile_tokens * p.pack ? tok0 + t * tile_tokens + row / p.pack : lq;  // lq: an idle row
-    const int head = head0 + row % p.pack;
-    const int lim = visible(tok);
-    const int lim_warp = visible(tok0 + t * tile_tokens + quarter * 32 / p.pack);  // least of the warp's
-    const int n = blocks[t];
     const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
-    float ref = -INFINITY;     // r, in log2 units
-    uint64_t sum2[2] = {0, 0};  // four partial row sums
+    uint32_t turn = 0, outputs = 0;  // parities of the next scores, of the next output
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      ok = __all_sync(0xffffffffu, mbar_wait(s_full(t), j & 1, wd, kWhereEpiTmemFull));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t s[4][32];
+#pragma unroll 1
+    for (int it = 0; ok; ++it) {
+      int n, lim;  // key blocks; keys that this row sees
+      bool nothing;
+      {
+        Job job;
+        if (!peek(it, job)) break;
+        nothing = job.u.b < 0;
+        const Plan pl = plan(job.u);
+        const int tok0 = job.u.first + t * tile_tokens;
+        n = pl.blocks[t];
+        lim = visible(job.u, row < tile_tokens * p.pack ? tok0 + row / p.pack : job.u.lq);
+        
+      }
+      float ref = -INFINITY;      // r, in log2 units
+      uint64_t sum2[2] = {0, 0};  // four partial row sums
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full(t), turn, wd, kWhereEpiTmemFull));
+        turn ^= 1;
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[4][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        tmem_ld_32x32b_x32(s_addr + 32 * c, s[c]);  // past the block's last key: hidden below
-      tmem_wait_ld();
-      const int room = lim - j * kRows;
-      if (lim_warp - j * kRows < kRows) {
+        for (int c = 0; c < 4; ++c)
+          tmem_ld_32x32b_x32(s_addr + 32 * c, s[c]);  // past the last key: hidden below
+        tmem_wait_ld();
+        const int room = lim - j * kRows;
+        if (__shfl_sync(0xffffffffu, room, 0) < kRows) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= room) s[c][i] = 0xFF800000u;
+        }
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains: one would wait for itself
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * c + i >= room) s[c][i] = 0xFF800000u;
-      }
-      float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains: one would wait for itself
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int i = 0; i < 32; i += 2)
-          tops[(i >> 1) & 3] = max3(tops[(i >> 1) & 3], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
-      float mx = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
-      mx *= p.scale_log2;
-      if (j == 0) {
-        ref = mx;
-      } else {
-        const bool move = mx > ref + kSlack;
-        if (__any_sync(0xffffffffu, move)) {
-          const float by = move ? ex2(ref - mx) : 1.f;
-          if (move) ref = mx;
-          const uint64_t by2 = pack_f32x2(by, by);
-          sum2[0] = mul_f32x2(sum2[0], by2);
-          sum2[1] = mul_f32x2(sum2[1], by2);
+          for (int i = 0; i < 32; i += 2)
+            tops[(i >> 1) & 3] = max3(tops[(i >> 1) & 3], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+        float mx = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
+        mx *= p.scale_log2;
+        if (j == 0) {
+          ref = mx;
+        } else {
+          const bool move = mx > ref + kSlack;
+          if (__any_sync(0xffffffffu, move)) {
+            const float by = move ? ex2(ref - mx) : 1.f;
+            if (move) ref = mx;
+            const uint64_t by2 = pack_f32x2(by, by);
+            sum2[0] = mul_f32x2(sum2[0], by2);
+            sum2[1] = mul_f32x2(sum2[1], by2);
 #pragma unroll 1
-          for (int c = 0; c < HD / 16; ++c) {  // S fills the registers: a little of O at a time
-            uint32_t o[16];
-            tmem_ld_32x32b_x16(o_addr + 16 * c, o);
-            tmem_wait_ld();
+            for (int c = 0; c < HD / 16; ++c) {  // S fills the registers: a little of O at a time
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(o_addr + 16 * c, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
-            tmem_st_32x32b_x16(o_addr + 16 * c, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+              tmem_st_32x32b_x16(o_addr + 16 * c, o);
+            }
           }
         }
-      }
-      const float neg = ref == -INFINITY ? 0.f : -ref;
-      const uint64_t neg2 = pack_f32x2(neg, neg);
+        const float neg = ref == -INFINITY ? 0.f : -ref;
+        const uint64_t neg2 = pack_f32x2(neg, neg);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t w[16];
+        for (int c = 0; c < 4; ++c) {
+          {
+            uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float x, y;
-          unpack_f32x2(fma_f32x2(pack_f32x2(s[c][2 * i], s[c][2 * i + 1]), scale2, neg2), x, y);
-          x = ex2(x);
-          y = ex2(y);
-          sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(x, y));
-          w[i] = pack_bf16x2(x, y);
-        }
-        if (c == kEarly / 2) {  // by now what was stored before is there
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(p_half(t));
-        }
-        tmem_st_32x32b_x16(s_addr + 16 * c, w);
+            for (int i = 0; i < 16; ++i) {
+              float x, y;
+              unpack_f32x2(fma_f32x2(pack_f32x2(s[c][2 * i], s[c][2 * i + 1]), scale2, neg2), x, y);
+              x = ex2(x);
+              y = ex2(y);
+              sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(x, y));
+              w[i] = pack_bf16x2(x, y);
+            }
+            if (c == kEarly / 2) {  // by now what was stored before is there
+              tmem_wait_st();
+              tc_fence_before();
+              mbar_arrive(p_half(t));
+            }
+            tmem_st_32x32b_x16(s_addr + 16 * c, w);
+          }
       }
       tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(p_full(t));
-    }
-    if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), 0, wd, kWhereEpiTmemFull));
-    if (ok) {
-      tc_fence_after();
-      float lo, hi;
-      unpack_f32x2(add_f32x2(sum2[0], sum2[1]), lo, hi);
-      put_rows<HD / 32>(p, o_addr, 0, n > 0, lo + hi, ref, q0, tok, lq, head, true);
+        tc_fence_before();
+        mbar_arrive(p_full(t));
+      }
+      if (n > 0 && ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), outputs, wd, kWhereEpiTmemFull));
+        outputs ^= 1;
+      }
+      if (ok && !nothing) {
+        tc_fence_after();
+        float lo, hi;
+        unpack_f32x2(add_f32x2(sum2[0], sum2[1]), lo, hi);
+        Job job;
+        read(it, job);  // again: scores left no room to keep it
+        put_rows<HD>(p, o_addr, smem_addr(smem + L::kOffOut) + warp * 4096, lane, n > 0, lo + hi, ref, job.u.q0,
+                     row < tile_tokens * p.pack ? job.u.first + t * tile_tokens + row / p.pack : job.u.lq, job.u.lq,
+                     job.head0 + row % p.pack);
+        tc_fence_before();  // the next job's weights are handed over after these loads
+      }
+      done(it);
     }
   }
 
@@ -805,7 +977,7 @@ __global__ void __launch_bounds__(kTileThreads, TileLayout<HD>::kCtas)
       tc_fence_after();
       float lo, hi;
       unpack_f32x2(add_f32x2(sum2[0], sum2[1]), lo, hi);
-      put_rows<HD / 32>(p, o_addr, 0, n > 0, lo + hi, ref, q0, tok, lq, head, true);
+      put_row<HD>(p, o_addr, n > 0, lo + hi, ref, q0, tok, lq, head);
     }
   }
 

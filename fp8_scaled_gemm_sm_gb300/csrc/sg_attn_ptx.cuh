@@ -149,4 +149,27 @@ __device__ __forceinline__ void cp_async_wait() {  // for all but the last N gro
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Asks to run a CTA of this grid that has not been launched yet in this one: 16 bytes at `answer`,
+// counted by the mbarrier.  Not to be asked again once there was none.
+__device__ __forceinline__ void take_cta(uint32_t answer, uint32_t mbar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer), "r"(mbar)
+               : "memory");
+}
+// blockIdx.x of the CTA that was taken; -1: none.
+__device__ __forceinline__ int taken_cta(uint32_t answer) {
+  uint32_t yes, x;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .b64 lo, hi;\n\t.reg .b32 y, z, w;\n\t.reg .pred p;\n\t"
+      "ld.shared.v2.b64 {lo, hi}, [%2];\n\t"
+      "mov.b128 r, {lo, hi};\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
+      : "=&r"(yes), "=&r"(x)
+      : "r"(answer)
+      : "memory");
+  return yes ? static_cast<int>(x) : -1;
+}
+
 }  // namespace sg
