@@ -990,6 +990,13 @@ __global__ void __launch_bounds__(kTileThreads, TileLayout<HD>::kCtas)
   }
 }
 
+int heads_packed(int group) {
+  int pack = 1;
+  for (int g = 2; g <= group && g <= kRows; ++g)
+    if (group % g == 0 && kRows % g <= kRows / 16) pack = g;
+  return pack;
+}
+
 template <int HD, bool TILE>
 sg_status_t launch(const AttnShape& s, const AttnArgs& a) {
   PromptParams p{};
@@ -1002,9 +1009,7 @@ sg_status_t launch(const AttnShape& s, const AttnArgs& a) {
   p.D = s.D;
   p.causal = a.causal;
   p.group = s.Hq / s.Hk;
-  p.pack = 1;
-  for (int g = 2; g <= p.group && g <= kRows; ++g)
-    if (p.group % g == 0 && kRows % g <= kRows / 16) p.pack = g;
+  p.pack = heads_packed(p.group);
   p.head_groups = s.Hq / p.pack;
   const int64_t units = a.Tq / ((TILE ? 1 : 2) * (kRows / p.pack)) + a.B;
   if (units * p.head_groups >= (int64_t(1) << 31)) return SG_ERR_UNSUPPORTED_SHAPE;
@@ -1061,11 +1066,16 @@ cudaError_t prompt_prepare() {
 
 sg_status_t prompt_launch(const AttnShape& s, const AttnArgs& a) {
   if (s.D <= 64) return launch<64, true>(s, a);
-  // Two tiles a CTA read K and V half as often and overlap better, one a CTA starts sooner and
-  // deals out finer: by the keys a sequence has on average (32 heads over 8, one sequence of 256, 512, 1024, 2048 tokens: 9.6,
-  // 12.5, 19.2, 35.1 us with two, 7.6, 11.1, 19.0, 39.4 with one; 8 of 512: 44.8 and 44.6; 32 of 200: 65.2 and 54.9; 8 heads
-  // over 8, one of 512, 1024: 11.4, 16.8 and 11.1, 17.8).
-  return a.Tk <= 512 * a.B ? launch<128, true>(s, a) : launch<128, false>(s, a);
+  // Two tiles a CTA read K and V half as often and overlap better, one a CTA starts sooner and deals out finer.
+  // Judged by the mean sequence: where two-tile units fill the SMs three times over, they win unless an odd tile leaves
+  // half of too many units empty (32 heads over 8, 32 sequences of 200 tokens: 52.2 us with two, 54.3 with one; 8 of
+  // 512: 35.6, 44.3; 128 of 100: 94.8, 122.6; but 8 heads over 8, 128 of 100, one tile each: 50.9, 37.9; 64 of 300, three: 69.2,
+  // 58.3); with fewer units it is the keys that decide (32 over 8, one of 512, 1024, 2048 tokens: 13.0, 20.2, 33.2 with two,
+  // 11.1, 18.9, 39.0 with one; 8 over 8, one of 1024, 2048: 18.0, 29.3 and 18.1, 32.3).
+  const int pack = heads_packed(s.Hq / s.Hk);
+  const int64_t tiles = (a.Tq * pack / a.B + kRows - 1) / kRows, units = (tiles + 1) / 2 * a.B * (s.Hq / pack);
+  const bool two = units >= 3 * s.num_sms ? tiles % 2 == 0 || tiles > 4 : a.Tk > 512 * a.B;
+  return two ? launch<128, false>(s, a) : launch<128, true>(s, a);
 }
 
 }  // namespace sg

@@ -550,6 +550,17 @@ def test_prompt_heads_of_a_group_share_rows(group, d, ctx):
     _check_prompt(ql, kl, group, 1, d, True, q, k, v, out, lse)
 
 
+@pytest.mark.parametrize("hq,hk", [(64, 64), (120, 40)])
+def test_prompt_many_short_ones_of_many_heads(hq, hk):
+    ql = [129, 0, 257, 1, 130, 300, 128, 96, 127, 200, 256, 31]
+    q, k, v = _prompt_inputs(ql, ql, hq, hk, 128, 80 + hq)
+    plan = _pkg().PagedAttention(hq, hk, 128)
+    out = torch.full((sum(ql), hq, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    _, lse = plan.prompt(q, k, v, _dev(_cum(ql)), out=out)
+    torch.cuda.synchronize()
+    _check_prompt(ql, ql, hq, hk, 128, True, q, k, v, out, lse)
+
+
 def test_prompt_sampled_rows_of_a_long_one():
     # long enough for several key tiles a row; a sample of rows against 64 bits
     hq, hk, d, n = 4, 1, 128, 3001
