@@ -591,7 +591,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok0 = job.u.first + t * tile_tokens;
         n = pl.blocks[t];
         lim = visible(job.u, row < tile_tokens * p.pack ? tok0 + row / p.pack : job.u.lq);
-        
       }
       float ref = -INFINITY;      // r, in log2 units
       uint64_t sum2[2] = {0, 0};  // four partial row sums
@@ -607,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_32x32b_x32(s_addr + 32 * c, s[c]);  // past the last key: hidden below
         tmem_wait_ld();
         const int room = lim - j * kRows;
-        if (__shfl_sync(0xffffffffu, room, 0) < kRows) {
+        if (__shfl_sync(0xffffffffu, room, 0) < kRows) {  // the first row sees least
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
