@@ -31,8 +31,8 @@
 // against the 2^-9 of the rounded output; the row sums take the unrounded weights.
 //
 // What bounds it: the tensor pipe, but for a unit's first and last softmax and its output: a block of both tiles
-// takes 1.34 us, 1.9 PFLOP/s.  16384 tokens, 32 heads of 128 over 8, causal: 1250 us, 1.75 PFLOP/s, 91% of what the
-// library's bf16 GEMM reaches; 6 chunks of 300 to 2048 tokens behind contexts, 40 heads over 8: 301 us.  Measured
+// takes 1.33 us, 1.9 PFLOP/s.  16384 tokens, 32 heads of 128 over 8, causal: 1240 us, 1.77 PFLOP/s, 91% of what the
+// library's bf16 GEMM reaches; 6 chunks of 300 to 2048 tokens behind contexts, 40 heads over 8: 295 us.  Measured
 // beside it: a CTA a unit 1275 and 323 us; output a row a lane 1257 and 309; key columns past a block's last key
 // skipped in the loads and exponentials (they are hidden, and only the last block has any; the branches cost every
 // block) 1377 us for the 16384 tokens, and, of that form, one S buffer a tile with P elsewhere 1509 us, 64-key
@@ -57,7 +57,7 @@ constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 208, kIssueRegs = 88;
 constexpr int kWhereJob = 0x41;  // a wait for a job, beside those of sg_ptx.cuh
 constexpr int kJobReaders = 11;  // warps that take jobs
-constexpr int kAhead = 4;   // loads before a job's end at which the next one is looked for
+constexpr int kAhead = 8;  // loads before a job's end at which the next one is looked for (chunks: 294.7 us, 298 with 4)
 constexpr int kEarly = 4;  // 16-key steps of a block whose weights are handed over first
 constexpr int kTileKeys = 64, kTileThreads = 192;  // of the kernel with one row tile a CTA
 constexpr float kSlack = 8.f;  // log2 of the largest weight
@@ -179,12 +179,20 @@ __device__ __forceinline__ Unit pick_unit(const PromptParams& p, int x, int toke
   return u;
 }
 
+// Two elements of an output row over its sum, as bf16.
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t x, uint32_t y, uint64_t by2) {
+  float a, b;
+  unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(x), __uint_as_float(y)), by2), a, b);
+  return pack_bf16x2(a, b);
+}
+
 // One thread's row of the output: HD dimensions out of tensor memory, over its sum.
 template <int HD>
 __device__ __forceinline__ void put_row(const PromptParams& p, uint32_t o_addr, bool some, float sum, float ref, int q0, int tok,
                                         int lq, int head) {
   const bool none = sum == 0.f;
   const float inv = none ? 0.f : 1.f / sum;
+  const uint64_t inv2 = pack_f32x2(inv, inv);
   const int64_t at = static_cast<int64_t>(q0 + tok) * p.Hq + head;
 #pragma unroll
   for (int c = 0; c < HD / 32; ++c) {
@@ -193,8 +201,6 @@ __device__ __forceinline__ void put_row(const PromptParams& p, uint32_t o_addr, 
       tmem_ld_32x32b_x32(o_addr + 32 * c, o);
       tmem_wait_ld();
     }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
     if (tok < lq) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -202,7 +208,7 @@ __device__ __forceinline__ void put_row(const PromptParams& p, uint32_t o_addr, 
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(o[8 * i + 2 * e + 1]));
+            w[e] = none ? 0u : scaled_pair(o[8 * i + 2 * e], o[8 * i + 2 * e + 1], inv2);
           *reinterpret_cast<uint4*>(p.out + at * p.D + 32 * c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
@@ -218,6 +224,7 @@ __device__ __forceinline__ void put_rows(const PromptParams& p, uint32_t o_addr,
                                          float ref, int q0, int tok, int lq, int head) {
   const bool none = sum == 0.f;
   const float inv = none ? 0.f : 1.f / sum;
+  const uint64_t inv2 = pack_f32x2(inv, inv);
   const int64_t at = static_cast<int64_t>(q0 + tok) * p.Hq + head;
   const int64_t mine = tok < lq ? at * p.D : -1;
 #pragma unroll
@@ -231,13 +238,11 @@ __device__ __forceinline__ void put_rows(const PromptParams& p, uint32_t o_addr,
         tmem_wait_ld();
       }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
-#pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(o[8 * i + 2 * e + 1]));
+          w[e] = none ? 0u : scaled_pair(o[8 * i + 2 * e], o[8 * i + 2 * e + 1], inv2);
         st_shared_v4(stage + lane * 128 + (((4 * c + i) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
       }
     }
