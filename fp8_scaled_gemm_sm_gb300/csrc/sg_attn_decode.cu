@@ -32,7 +32,7 @@
 // by a second kernel in the order of its ranges, so results do not depend on timing.
 // Measured, main kernel and join: 64 sequences of up to 16k tokens, 32 heads of 128 over 8: 94 + 4 us, the
 // main kernel at 92% of a copy's rate; 2 long ones 84 + 6; 200 sequences with 4 drafted tokens, 16 heads of 64 over 16:
-// 57 + 6 (issue slots bound it: 64-wide heads have as many weights to make for half the bytes); one of 777 tokens 8.9.
+// 57 + 5 (issue slots bound it: 64-wide heads have as many weights to make for half the bytes); one of 777 tokens 8.9.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -673,10 +673,10 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
 
 // Joins the parts of a cut segment; a lane owns 4 dimensions.  Few parts: a warp a row, in the first
 // block of the segment.  Many: a block a row, whose warps share out the parts.
-template <int HD, int NR>
-__global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const DecodeParams p) {
-  __shared__ float4 shared_o[kJoinWarps][32];
-  __shared__ float shared_sum[kJoinWarps];
+template <int HD, int NR, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) decode_join_kernel(const DecodeParams p) {
+  __shared__ float4 shared_o[WARPS][32];
+  __shared__ float shared_sum[WARPS];
   grid_dep_launch();
   grid_dep_wait();
   const Cut cut = p.cuts[blockIdx.x];
@@ -685,14 +685,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
   const int row0 = cut.hr % p.row_tiles * NR * 8, head = cut.hr / p.row_tiles * p.group;
   const int rows = min(8 * NR, p.qn * p.group - row0);
   const int count = cut.last - cut.first + 1;
-  const bool many = count > 2 * kJoinWarps;
+  const bool many = count > 2 * WARPS;
   if (!many && blockIdx.y > 0) return;
   auto at = [&](int k, int row) { return (2 * (cut.first + k) + (k == 0)) * (8 * NR) + row; };
   const int d = 4 * lane < HD ? 4 * lane : 0;
-  for (int row = many ? blockIdx.y : warp; row < rows; row += many ? gridDim.y : kJoinWarps) {
+  for (int row = many ? blockIdx.y : warp; row < rows; row += many ? gridDim.y : WARPS) {
     float m = -INFINITY, n = -INFINITY, sum = 0.f;
     // this warp's first parts are on their way while the references are looked up
-    const int step = many ? kJoinWarps : 1, k0 = many ? warp : 0;
+    const int step = many ? WARPS : 1, k0 = many ? warp : 0;
     float4 mls[kFirst], xs[kFirst];
 #pragma unroll
     for (int i = 0; i < kFirst; ++i) {
@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
       __syncthreads();
       if (warp != 0) continue;
 #pragma unroll
-      for (int i = 1; i < kJoinWarps; ++i) {
+      for (int i = 1; i < WARPS; ++i) {
         const float4 x = shared_o[i][lane];
         o.x += x.x;
         o.y += x.y;
@@ -783,8 +783,16 @@ sg_status_t launch(const AttnShape& s, const AttnArgs& a, DecodeParams& p) {
   // blocks for a row each where that many fit the GPU at once
   const int64_t joins = p.by_segment ? segments : ranges, fit = 8 * s.num_sms / joins;
   const unsigned per_row = static_cast<unsigned>(fit < 1 ? 1 : fit < 8 * NR ? fit : 8 * NR);
+  // where not even a block a segment fits, up to 4 rows take half the warps (200 sequences, 4 drafted tokens: 61.4 us,
+  // 63.0 with 8 warps)
+  if constexpr (NR == 1) {
+    if (fit < 1 && p.qn * p.group <= kJoinWarps / 2) {
+      GemmLaunch j(dim3(static_cast<unsigned>(joins), per_row), dim3(16 * kJoinWarps), 0, a.stream, 1);
+      return launch_error(cudaLaunchKernelEx(&j.cfg, decode_join_kernel<HD, NR, kJoinWarps / 2>, p));
+    }
+  }
   GemmLaunch j(dim3(static_cast<unsigned>(joins), per_row), dim3(32 * kJoinWarps), 0, a.stream, 1);
-  return launch_error(cudaLaunchKernelEx(&j.cfg, decode_join_kernel<HD, NR>, p));
+  return launch_error(cudaLaunchKernelEx(&j.cfg, decode_join_kernel<HD, NR, kJoinWarps>, p));
 }
 
 template <int HD, int NR>
