@@ -27,8 +27,8 @@
 // The tensor cores take the MMAs in order, so S_t of block j + 1, issued after
 // O_t += P_t V_j, cannot overwrite P_t early, and a softmax thread that sees it
 // complete may also touch O_t.
-// P is rounded to bf16 (V is bf16, and an MMA has one operand type): an error of at most 2^-9 of each weight,
-// against the 2^-9 of the rounded output; the row sums take the unrounded weights.
+// P is rounded to bf16 (V is bf16, and an MMA has one operand type): an error of at most 2^-8 of each weight,
+// as the output's own rounding; the row sums take the unrounded weights.
 //
 // What bounds it: the tensor pipe, but for a unit's first and last softmax and its output: a block of both tiles
 // takes 1.33 us, 1.9 PFLOP/s.  16384 tokens, 32 heads of 128 over 8, causal: 1240 us, 1.77 PFLOP/s, 91% of what the
@@ -1071,7 +1071,7 @@ cudaError_t prompt_prepare() {
 sg_status_t prompt_launch(const AttnShape& s, const AttnArgs& a) {
   if (s.D <= 64) return launch<64, true>(s, a);
   // Two tiles a CTA read K and V half as often and overlap better, one a CTA starts sooner and deals out finer.
-  // Judged by the mean sequence: where two-tile units fill the SMs three times over, they win unless an odd tile leaves
+  // By the mean sequence: where two-tile units fill the SMs three times over, they win unless an odd tile leaves
   // half of too many units empty (32 heads over 8, 32 sequences of 200 tokens: 52.2 us with two, 54.3 with one; 8 of
   // 512: 35.6, 44.3; 128 of 100: 94.8, 122.6; but 8 heads over 8, 128 of 100, one tile each: 50.9, 37.9; 64 of 300, three: 69.2,
   // 58.3); with fewer units it is the keys that decide (32 over 8, one of 512, 1024, 2048 tokens: 13.0, 20.2, 33.2 with two,
