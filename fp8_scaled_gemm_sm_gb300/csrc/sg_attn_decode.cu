@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int pg = i ? page1 : page0;
-      if (pg >= 0) {
+      if (pg >= 0 && key + 16 * i < ahead.len) {  // a block past the end may hold any byte, NaN's among them
         const int64_t at = ((static_cast<int64_t>(pg) * p.Hk + ahead_head) << block_shift) + (((key + 16 * i) & in_page) >> 4);
         scales |= static_cast<uint32_t>(__ldg(p.k_scale + at)) << (8 * i) | static_cast<uint32_t>(__ldg(p.v_scale + at)) << (16 + 8 * i);
       }
