@@ -5,9 +5,10 @@
 // (K, V codes, a, b the exponents of their block),
 //     s_j = c x . k_j   (c = scale log2 e),   o = sum_j 2^(s_j) v_j / sum_j 2^(s_j).
 // In one pass over tiles of 32 keys, with two references that follow running
-// maxima: m for s_j (the denominator's weights 2^(s_j - m)) and n for s_j + b_j (the
-// output's weights 2^(s_j + b_j - n), the value scale inside, so that the
-// tensor cores multiply codes): o = 2^(n - m) sum_j 2^(s_j + b_j - n) V_j / sum_j 2^(s_j - m).
+// maxima: m for s_j (the denominator's weights 2^(s_j - m)) and m + n for s_j + b_j (the
+// output's weights 2^((s_j - m) + b_j - n), the value scale inside, so that the
+// tensor cores multiply codes): o = 2^n sum_j 2^((s_j - m) + b_j - n) V_j / sum_j 2^(s_j - m).
+// n is held relative to m, and s_j - m is formed first: beside a score of 2^24 or more b_j would be lost.
 //
 // The bound is memory: every code is read once, 2 D bytes a token and head.  What
 // competes with it is the arithmetic on codes, so a warp does as little of it as it can, in registers:
@@ -37,6 +38,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
+
 #include "sg_attn.h"
 #include "sg_attn_ptx.cuh"
 #include "sg_mx.cuh"
@@ -53,6 +56,7 @@ constexpr int kMaxWarps = 16;
 constexpr int kJoinWarps = 8;
 constexpr int kFirst = 4;
 constexpr float kSlack = 8.f;   // log2 of how far a maximum may pass its reference
+constexpr float kUnset = -FLT_MAX;  // references before a row has seen a key: finite, so that differences with them are
 constexpr float kLift = 7.f;    // the output's weights at its reference are 2^kLift, the largest 2^15: the room that
                                 // fp16 has above 1 keeps light weights among its normal numbers, down to 2^-21
 
@@ -74,7 +78,7 @@ struct DecodeParams {
   uint16_t* out;
   float* lse;
   float* part_o;      // [2 ranges][rows][HD]: the part that begins a segment (odd), one that does not
-  float4* part_ml;    // [2 ranges][rows]: m, n, sum
+  float4* part_ml;    // [2 ranges][rows]: m, n (relative to m), sum
   Cut* cuts;          // by segment, or by range where there are fewer of those
   int by_segment;
   int* status;
@@ -459,7 +463,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
         for (int e = 0; e < 4; ++e) o[r][i][e] = 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[r][e] = n[r][e] = -INFINITY;
+        m[r][e] = n[r][e] = kUnset;
         sum[r][e] = 0.f;
       }
     }
@@ -512,13 +516,13 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
             const float by = kx[j] * q_scale[r][e];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float x = s[r][j][2 * i + e] * by;
+              float x = __fmul_rn(s[r][j][2 * i + e], by);  // rounded, as m is, so that their difference is exact near m
               if (edge && (key0 + 16 * j + 8 * i + kr >= lim[r][e] || ((about.y >> j) & 1))) x = -INFINITY;
               s[r][j][2 * i + e] = x;
             }
             const float two = fmaxf(s[r][j][e], s[r][j][2 + e]);
             top = fmaxf(top, two);
-            vtop = fmaxf(vtop, two + vx[j]);
+            vtop = fmaxf(vtop, (two - m[r][e]) + vx[j]);
           }
           move |= top > m[r][e] + kSlack || vtop > n[r][e] + kLift + kSlack;
         }
@@ -527,22 +531,22 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
         for (int r = 0; r < NR; ++r)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = -INFINITY, vtop = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float two = fmaxf(s[r][j][e], s[r][j][2 + e]);
-              top = fmaxf(top, two);
-              vtop = fmaxf(vtop, two + vx[j]);
-            }
+            const float a = fmaxf(s[r][0][e], s[r][0][2 + e]), b = fmaxf(s[r][1][e], s[r][1][2 + e]);
+            float top = fmaxf(fmaxf(a, b), kUnset);
+            float vtop = fmaxf((a - top) + vx[0], (b - top) + vx[1]);  // relative to top
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) {
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-              vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, x));
+              const float other = __shfl_xor_sync(0xffffffffu, top, x), vother = __shfl_xor_sync(0xffffffffu, vtop, x);
+              const float both = fmaxf(top, other);
+              vtop = fmaxf(vtop + (top - both), vother + (other - both));
+              top = both;
             }
             if (top > m[r][e]) {
               sum[r][e] *= ex2(m[r][e] - top);
+              n[r][e] += m[r][e] - top;
               m[r][e] = top;
             }
+            vtop += top - m[r][e];
             if (vtop - kLift > n[r][e]) {
               const float by = ex2(n[r][e] - (vtop - kLift));
               n[r][e] = vtop - kLift;
@@ -560,17 +564,12 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
       for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float neg_m[2], by[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            neg_m[e] = m[r][e] == -INFINITY ? 0.f : -m[r][e];
-            by[e] = n[r][e] == -INFINITY ? 0.f : vx[j] - n[r][e];
-          }
+          const float by[2] = {vx[j] - n[r][0], vx[j] - n[r][1]};
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float x = s[r][j][2 * i], y = s[r][j][2 * i + 1];
-            sum[r][0] += ex2(x + neg_m[0]);
-            sum[r][1] += ex2(y + neg_m[1]);
+            const float x = s[r][j][2 * i] - m[r][0], y = s[r][j][2 * i + 1] - m[r][1];
+            sum[r][0] += ex2(x);
+            sum[r][1] += ex2(y);
             w[r][j][i] = transpose8(pack_f16x2(ex2(x + by[0]), ex2(y + by[1])));
           }
         }
@@ -632,7 +631,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
         if (whole) {
           const int64_t at = (static_cast<int64_t>(c.b) * p.qn + row / p.group) * p.Hq + h * p.group + row % p.group;
           const bool none = sum[r][e] == 0.f;
-          const float by = none ? 0.f : ex2(n[r][e] - m[r][e]) / sum[r][e];
+          const float by = none ? 0.f : ex2(n[r][e]) / sum[r][e];
           if (run_d < p.D) {
 #pragma unroll
             for (int i = 0; i < kOut; i += 4) {
@@ -691,7 +690,7 @@ __global__ void __launch_bounds__(32 * WARPS) decode_join_kernel(const DecodePar
   auto at = [&](int k, int row) { return (2 * (cut.first + k) + (k == 0)) * (8 * NR) + row; };
   const int d = 4 * lane < HD ? 4 * lane : 0;
   for (int row = many ? blockIdx.y : warp; row < rows; row += many ? gridDim.y : WARPS) {
-    float m = -INFINITY, n = -INFINITY, sum = 0.f;
+    float m = kUnset, n = kUnset, sum = 0.f;
     // this warp's first parts are on their way while the references are looked up
     const int step = many ? WARPS : 1, k0 = many ? warp : 0;
     float4 mls[kFirst], xs[kFirst];
@@ -704,18 +703,19 @@ __global__ void __launch_bounds__(32 * WARPS) decode_join_kernel(const DecodePar
     for (int k = lane; k < count; k += 32) {
       const float4 ml = p.part_ml[at(k, row)];
       m = fmaxf(m, ml.x);
-      n = fmaxf(n, ml.y);
+      n = fmaxf(n, ml.x + ml.y);
     }
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
       n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, x));
     }
-    const float m0 = m == -INFINITY ? 0.f : m, n0 = n == -INFINITY ? 0.f : n;
+    n = fabsf(m) < 1048576.f ? n - m : 0.f;  // any reference does that keeps 2^n in range; beside a larger m it would be lost
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](const float4& ml, const float4& x) {
-      sum += ml.z * ex2(ml.x - m0);
-      const float by = ex2(ml.y - n0);
+      const float below = ml.x - m;
+      sum += ml.z * ex2(below);
+      const float by = ex2(below + (ml.y - n));
       o.x += x.x * by;
       o.y += x.y * by;
       o.z += x.z * by;
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(32 * WARPS) decode_join_kernel(const DecodePar
     const int r = row0 + row;
     const int64_t to = (static_cast<int64_t>(cut.b) * p.qn + r / p.group) * p.Hq + head + r % p.group;
     const bool none = sum == 0.f;
-    const float by = none ? 0.f : ex2(n - m) / sum;
+    const float by = none ? 0.f : ex2(n) / sum;
     if (4 * lane < p.D)
       *reinterpret_cast<uint2*>(p.out + to * p.D + d) =
           none ? make_uint2(0, 0) : make_uint2(pack_bf16x2(o.x * by, o.y * by), pack_bf16x2(o.z * by, o.w * by));

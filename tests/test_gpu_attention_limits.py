@@ -2,7 +2,8 @@
 import numpy as np
 import pytest
 
-from test_gpu_attention import _check_decode, _decode, lib  # noqa: F401
+import attn_ref as ref
+from test_gpu_attention import _check_decode, _decode, _f64, lib  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -23,3 +24,40 @@ def test_decode_scales_of_blocks_that_nothing_wrote(page, hq, hk, d, qn):
 
     _, args, host, out, lse = _decode(lens, hq, hk, d, page, qn, 400 + page, edit)
     _check_decode(lens, hq, hk, d, page, qn, host, args[0], out, lse)
+
+
+def _sure(q, k, vis, scale):
+    """[n, Hq]: rows whose largest score is ahead of the others by more than scores summed in fp32 can be off
+    (2^-18 of sum |q k| each, as lse_tolerance has it) and another 32."""
+    g = q.shape[1] // k.shape[1]
+    kk = np.repeat(k, g, 1)
+    s = np.where(vis[:, None, :], np.einsum("nhd,mhd->nhm", q, kk) * scale, -np.inf)
+    big = np.einsum("nhd,mhd->nhm", np.abs(q), np.abs(kk)).max(-1) * scale
+    top = -np.sort(-s, -1)[..., :2]
+    return top[..., 0] - top[..., 1] > 2 * 2.0 ** -18 * big + 32 if top.shape[-1] > 1 else np.ones(s.shape[:2], bool)
+
+
+def _check_large(q, k, v, vis, scale, out, lse, bits):
+    """Of rows that are sure of their key, the output; of all, the logarithm of the sum."""
+    o, ls, mag, big = ref.attend(q, k, v, vis, scale)
+    sure = _sure(q, k, vis, scale)
+    assert sure.any()
+    assert np.isfinite(out).all()
+    err = np.abs(out - o)
+    assert (err <= ref.out_tolerance(o, mag, bits))[sure].all(), float((err / ref.out_tolerance(o, mag, bits))[sure].max())
+    assert (np.abs(lse - ls) <= ref.lse_tolerance(ls, big)).all()
+
+
+@pytest.mark.parametrize("scale", [1e4, 1e5, 1e7, 1e12, 1e24])
+@pytest.mark.parametrize("lens,hq,hk,d,qn", [([150, 33, 16], 4, 2, 64, 1), ([260, 40], 6, 2, 128, 3), ([90], 24, 1, 96, 1), ([6011], 2, 1, 128, 1)])
+def test_decode_scores_of_any_size(lens, hq, hk, d, qn, scale):
+    page = 16
+    _, args, host, out, lse = _decode(lens, hq, hk, d, page, qn, 500, scale=scale)
+    table, codes, scales = host
+    q, go, gl = _f64(args[0]), _f64(out), _f64(lse)
+    for b, n in enumerate(lens):
+        k, _ = ref.cached(codes[0], scales[0], table[b], hk, page, n)
+        v, _ = ref.cached(codes[1], scales[1], table[b], hk, page, n)
+        vis = np.arange(n)[None, :] < np.array([n - (qn - 1 - i) for i in range(qn)])[:, None]
+        r = slice(b * qn, (b + 1) * qn)
+        _check_large(q[r], k, v, vis, np.float64(np.float32(scale)), go[r], gl[r], 11)
