@@ -43,6 +43,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
+
 #include "sg_attn.h"
 #include "sg_attn_ptx.cuh"
 
@@ -61,6 +63,7 @@ constexpr int kAhead = 8;  // loads before a job's end at which the next one is 
 constexpr int kEarly = 4;  // 16-key steps of a block whose weights are handed over first
 constexpr int kTileKeys = 64, kTileThreads = 192;  // of the kernel with one row tile a CTA
 constexpr float kSlack = 8.f;  // log2 of the largest weight
+constexpr float kFar = 1073741824.f;  // references past this are not stood by (row_sum)
 
 struct PromptParams {
   const int32_t *cu_q, *cu_k;
@@ -177,6 +180,14 @@ __device__ __forceinline__ Unit pick_unit(const PromptParams& p, int x, int toke
     rest -= all;
   }
   return u;
+}
+
+// A row's sum; NaN where its reference is too large.  The weights come of fma's exact product less the rounded reference,
+// off by up to half a unit in the reference's last place: all of a row share that, but past 2^31 it is a factor of
+// 2^128, and sums are infinite or, worse, zero.  (Subtracting from the rounded product, for all rows or by a branch to the
+// rows that need it, costs every call 2 to 3%.)
+__device__ __forceinline__ float row_sum(float sum, float ref) {
+  return fabsf(ref) > kFar && fabsf(ref) <= FLT_MAX ? __uint_as_float(0x7FC00000u) : sum;
 }
 
 // Two elements of an output row over its sum, as bf16.
@@ -684,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         unpack_f32x2(add_f32x2(sum2[0], sum2[1]), lo, hi);
         Job job;
         read(it, job);  // again: scores left no room to keep it
-        put_rows<HD>(p, o_addr, smem_addr(smem + L::kOffOut) + warp * 4096, lane, n > 0, lo + hi, ref, job.u.q0,
+        put_rows<HD>(p, o_addr, smem_addr(smem + L::kOffOut) + warp * 4096, lane, n > 0, row_sum(lo + hi, ref), ref, job.u.q0,
                      row < tile_tokens * p.pack ? job.u.first + t * tile_tokens + row / p.pack : job.u.lq, job.u.lq,
                      job.head0 + row % p.pack);
         tc_fence_before();  // the next job's weights are handed over after these loads
@@ -981,7 +992,7 @@ __global__ void __launch_bounds__(kTileThreads, TileLayout<HD>::kCtas)
       tc_fence_after();
       float lo, hi;
       unpack_f32x2(add_f32x2(sum2[0], sum2[1]), lo, hi);
-      put_row<HD>(p, o_addr, n > 0, lo + hi, ref, q0, tok, lq, head);
+      put_row<HD>(p, o_addr, n > 0, row_sum(lo + hi, ref), ref, q0, tok, lq, head);
     }
   }
 

@@ -32,7 +32,8 @@
  *                for a row that sees no key, whose output is zero.  NULL: not written.
  *
  * Rules: 1 <= Hq, Hk <= 1024, Hq a multiple of Hk; D a multiple of 16, 16 <= D <= 128; page 16, 32, 64
- * or 128; rot a multiple of 16, 0 <= rot <= D; scale positive and finite.  Softmax statistics, sums and products are
+ * or 128; rot a multiple of 16, 0 <= rot <= D; scale positive and finite; in scaled_attn_prompt scores scale q.k of up to 2^29
+ * in magnitude (a row whose largest is past 2^30 gets NaN).  Softmax statistics, sums and products are
  * accumulated in fp32; bf16 outputs are rounded once, to nearest even.
  *
  * NaN and infinity: what a row does not see does not reach it, with one exception, a non-finite

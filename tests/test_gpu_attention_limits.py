@@ -1,9 +1,10 @@
 """GPU tests of the attention operators at the limits of what they are given, against the 64-bit implementations of attn_ref."""
 import numpy as np
 import pytest
+import torch
 
 import attn_ref as ref
-from test_gpu_attention import _check_decode, _decode, _f64, lib  # noqa: F401
+from test_gpu_attention import _check_decode, _cum, _decode, _dev, _f64, _pkg, _prompt_inputs, lib  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +62,22 @@ def test_decode_scores_of_any_size(lens, hq, hk, d, qn, scale):
         vis = np.arange(n)[None, :] < np.array([n - (qn - 1 - i) for i in range(qn)])[:, None]
         r = slice(b * qn, (b + 1) * qn)
         _check_large(q[r], k, v, vis, np.float64(np.float32(scale)), go[r], gl[r], 11)
+
+
+@pytest.mark.parametrize("scale", [1e4, 1e6, 1e7, 1e8, 1e9, 1e12, 1e24])
+@pytest.mark.parametrize("n,m,hq,hk,d", [(140, 140, 4, 1, 64), (70, 200, 2, 2, 128), (140, 840, 4, 1, 128), (130, 130, 5, 1, 128)])
+def test_prompt_large_scores_are_right_or_nan(n, m, hq, hk, d, scale):
+    q, k, v = _prompt_inputs([n], [m], hq, hk, d, 510)
+    plan = _pkg().PagedAttention(hq, hk, d)
+    out, lse = plan.prompt(q, k, v, _dev(_cum([n])), _dev(_cum([m])), scale=scale)
+    torch.cuda.synchronize()
+    vis = np.arange(m)[None, :] < np.arange(n)[:, None] + 1 + m - n
+    q, k, v, out, lse, scale = _f64(q), _f64(k), _f64(v), _f64(out), _f64(lse), np.float64(np.float32(scale))
+    o, ls, mag, big = ref.attend(q, k, v, vis, scale)
+    top = np.abs(np.where(vis[:, None, :], np.einsum("nhd,mhd->nhm", q, np.repeat(k, hq // hk, 1)) * scale, -np.inf).max(-1))
+    near, far = top <= 2.0 ** 29, top > 2.0 ** 30
+    assert np.isnan(out[far]).all() and np.isnan(lse[far]).all()
+    sure = near & _sure(q, k, vis, scale)
+    assert (np.abs(out - o) <= ref.out_tolerance(o, mag, 8))[sure].all()
+    assert (np.abs(lse - ls) <= ref.lse_tolerance(ls, big))[near].all()
+    assert sure.any() if scale < 1e8 else far.any()
