@@ -323,7 +323,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   Job* jobs = reinterpret_cast<Job*>(smem + L::kOffJobs);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  grid_dep_launch();
   grid_dep_wait();
   const int tile_tokens = kRows / p.pack;
   if (warp == 9) {
@@ -358,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dep_launch();  // not before tensor memory is there: a kernel that starts early may take all of an SM's and wait for this one
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
   const Watchdog wd{p.status, p.timeout_ns, reinterpret_cast<volatile int*>(&misc[1])};
   // Job i of this CTA; false: no more, or the CTA gives up.  A warp that has what it needs of it says so.
@@ -762,7 +762,6 @@ __global__ void __launch_bounds__(kTileThreads, TileLayout<HD>::kCtas)
   int* misc = reinterpret_cast<int*>(smem + L::kOffMisc);  // [0] TMEM base, [1] abort, [2..7] the unit
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  grid_dep_launch();
   grid_dep_wait();
   const int tile_tokens = kRows / p.pack;
   const int head0 = static_cast<int>(blockIdx.x) % p.head_groups * p.pack;
@@ -782,6 +781,7 @@ __global__ void __launch_bounds__(kTileThreads, TileLayout<HD>::kCtas)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dep_launch();  // not before tensor memory is there
   if (misc[2] < 0) {
     if (warp == 5) tmem_dealloc(static_cast<uint32_t>(misc[0]), L::kCols);
     return;

@@ -142,6 +142,8 @@ __device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity, u
 // (grid_dep_wait; at once when there is no such kernel).  Ordering in the stream
 // is therefore that of plain launches; what overlaps is the next kernel's
 // launch, barrier set-up and TMEM allocation with this kernel's last tiles.
+// A kernel with tensor memory allocates it before grid_dep_launch: a next kernel that has started holds its own until this
+// one has completed, so an allocation after it could wait for the very kernel that waits for it.
 
 __device__ __forceinline__ void grid_dep_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
