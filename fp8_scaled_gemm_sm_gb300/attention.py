@@ -102,6 +102,12 @@ class PagedAttention:
     `rotary` is a table from ``rotary_table`` (None: positions are not rotated);
     `interleaved` rotates pairs (2i, 2i + 1) instead of (i, i + rot / 2).  q, k and v
     are bfloat16 [tokens, heads, dim], possibly views of a projection's rows.
+
+    Calls run on torch's current stream, or on `stream` (a CUDA stream's number, such as
+    ``torch.cuda.Stream.cuda_stream``).  Outputs that a call allocates may be dropped at
+    once either way.  What the caller passes (inputs, the cache, outputs of its own) has to
+    be ready on `stream` and to live until that has used it: ``wait_stream`` and
+    ``record_stream`` are the caller's.
     """
 
     def __init__(self, q_heads, kv_heads, dim, page_size=64, rotary=None, interleaved=False, device=None):

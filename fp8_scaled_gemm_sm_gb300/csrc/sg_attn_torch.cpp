@@ -7,6 +7,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/Functions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <cstring>
@@ -104,9 +105,35 @@ const int32_t* table(PyObject* o, int64_t batch, const Plan& p, int64_t* width) 
   return static_cast<const int32_t*>(t.data_ptr());
 }
 
-at::Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const Plan& p, const char* what) {
-  if (o == Py_None)
-    return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(p.device))));
+// The stream that a call runs on; torch's current one, and whether the two differ.
+struct Streams {
+  sg_stream_t handle;
+  c10::cuda::CUDAStream current;
+  bool side;
+};
+
+Streams streams(PyObject* o, const Plan& p) {
+  const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(p.device));
+  const sg_stream_t now = current.stream();
+  if (o == Py_None) return {now, current, false};
+  const auto s = static_cast<sg_stream_t>(PyLong_AsVoidPtr(o));
+  if (PyErr_Occurred()) throw BadArgument{"stream"};
+  return {s, current, s != now};
+}
+
+// An output that the caller has, or a new one.  On a stream of the caller's choice a new one is that stream's memory, so
+// whoever used it before or gets it next is ordered there; and it is recorded on the current stream, where results are
+// read as a rule, so that dropping it does not give it away before the reads so far.
+at::Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const Plan& p, const Streams& s, const char* what) {
+  if (o == Py_None) {
+    const auto options = at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(p.device)));
+    if (!s.side) return at::empty(shape, options);
+    const c10::cuda::CUDAStreamGuard guard(
+        c10::cuda::getStreamFromExternal(s.handle, static_cast<c10::DeviceIndex>(p.device)));
+    const at::Tensor t = at::empty(shape, options);
+    t.record_stream(s.current.unwrap());
+    return t;
+  }
   const at::Tensor& t = tensor(o, what);
   if (t.sizes() != shape || t.scalar_type() != type || !on(t, p.device) || !t.is_contiguous())
     throw BadArgument{std::string(what) + " must be a contiguous tensor of the result's shape and type on the plan's device"};
@@ -125,13 +152,6 @@ const sg_kv_cache_t* cache(PyObject* o, const Plan& p) {
   if (c->heads != p.kv_heads || c->page != p.page || c->dim != p.dim || c->device != p.device)
     throw BadArgument{"the cache's layout differs from the plan's"};
   return &c->args;
-}
-
-sg_stream_t stream(PyObject* o, const Plan& p) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(p.device)).stream();
-  void* s = PyLong_AsVoidPtr(o);
-  if (PyErr_Occurred()) throw BadArgument{"stream"};
-  return static_cast<sg_stream_t>(s);
 }
 
 int64_t number(PyObject* o) {
@@ -214,13 +234,13 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* t = table(a[5], batch, p, &width);
     const int32_t* ctx = ints(a[6], batch, p, "ctx_lens");
     const int32_t* cu = ints(a[7], batch + 1, p, "cu_seqlens");
-    const sg_stream_t s = stream(a[10], p);
-    const at::Tensor q_out = output(a[9], {q.n, p.q_heads, p.dim}, at::kBFloat16, p, "q_out");
+    const Streams s = streams(a[10], p);
+    const at::Tensor q_out = output(a[9], {q.n, p.q_heads, p.dim}, at::kBFloat16, p, s, "q_out");
     at::Tensor k_out;
     if (a[8] == Py_True || (a[8] != Py_None && a[8] != Py_False))
-      k_out = output(a[8] == Py_True ? Py_None : a[8], {q.n, p.kv_heads, p.dim}, at::kBFloat16, p, "k_out");
+      k_out = output(a[8] == Py_True ? Py_None : a[8], {q.n, p.kv_heads, p.dim}, at::kBFloat16, p, s, "k_out");
     check(scaled_attn_append(p.handle, c, &p.rotary, q.data, q.stride, k.data, k.stride, v.data, v.stride, t, width, ctx, cu,
-                             q.n, batch, q_out.data_ptr(), k_out.defined() ? k_out.data_ptr() : nullptr, s),
+                             q.n, batch, q_out.data_ptr(), k_out.defined() ? k_out.data_ptr() : nullptr, s.handle),
           "scaled_attn_append");
     PyObject* second = Py_None;
     if (k_out.defined())
@@ -245,11 +265,11 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* t = table(a[3], batch, p, &width);
     const int32_t* lens = ints(a[4], batch, p, "kv_lens");
     const float scale = scale_or(a[6], p);
-    const sg_stream_t s = stream(a[9], p);
-    const at::Tensor out = output(a[7], {q.n, p.q_heads, p.dim}, at::kBFloat16, p, "out");
-    const at::Tensor lse = output(a[8], {q.n, p.q_heads}, at::kFloat, p, "lse");
+    const Streams s = streams(a[9], p);
+    const at::Tensor out = output(a[7], {q.n, p.q_heads, p.dim}, at::kBFloat16, p, s, "out");
+    const at::Tensor lse = output(a[8], {q.n, p.q_heads}, at::kFloat, p, s, "lse");
     check(scaled_attn_decode(p.handle, c, q.data, q.stride, qn, t, width, lens, batch, scale, out.data_ptr(),
-                             static_cast<float*>(lse.data_ptr()), s),
+                             static_cast<float*>(lse.data_ptr()), s.handle),
           "scaled_attn_decode");
     return pair(out, THPVariable_Wrap(lse));
   });
@@ -268,11 +288,11 @@ PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int causal = PyObject_IsTrue(a[6]);
     if (causal < 0) throw BadArgument{"causal"};
     const float scale = scale_or(a[7], p);
-    const sg_stream_t s = stream(a[10], p);
-    const at::Tensor out = output(a[8], {q.n, p.q_heads, p.dim}, at::kBFloat16, p, "out");
-    const at::Tensor lse = output(a[9], {q.n, p.q_heads}, at::kFloat, p, "lse");
+    const Streams s = streams(a[10], p);
+    const at::Tensor out = output(a[8], {q.n, p.q_heads, p.dim}, at::kBFloat16, p, s, "out");
+    const at::Tensor lse = output(a[9], {q.n, p.q_heads}, at::kFloat, p, s, "lse");
     check(scaled_attn_prompt(p.handle, q.data, q.stride, k.data, k.stride, v.data, v.stride, cu_q, cu_k, q.n, k.n, batch, causal,
-                             scale, out.data_ptr(), static_cast<float*>(lse.data_ptr()), s),
+                             scale, out.data_ptr(), static_cast<float*>(lse.data_ptr()), s.handle),
           "scaled_attn_prompt");
     return pair(out, THPVariable_Wrap(lse));
   });

@@ -81,3 +81,61 @@ def test_prompt_large_scores_are_right_or_nan(n, m, hq, hk, d, scale):
     assert (np.abs(out - o) <= ref.out_tolerance(o, mag, 8))[sure].all()
     assert (np.abs(lse - ls) <= ref.lse_tolerance(ls, big))[near].all()
     assert sure.any() if scale < 1e8 else far.any()
+
+
+def _calls(seed):
+    """append, decode and prompt on inputs of their own: functions of (stream) that return their outputs."""
+    pkg = _pkg()
+    hq, hk, d, page, n = 8, 2, 128, 32, 96
+    plan = pkg.PagedAttention(hq, hk, d, page, rotary=pkg.rotary_table(n, d))
+    cache = plan.new_cache(3)
+    x = torch.randn(n, hq + 2 * hk, d, generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+    q, k, v = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+    table, cu = _dev(np.array([[2, 0, 1]], np.int32)), _dev(_cum([n]))
+    each, lens = _dev(np.array([0], np.int32)), _dev(np.array([n], np.int32))
+    plan.append(q, k, v, cache, table, each, cu)
+    many, ones = table.expand(n, 3).contiguous(), lens.expand(n).contiguous()
+    return [lambda s: plan.append(q, k, v, cache, table, each, cu, k_out=True, stream=s),
+            lambda s: plan.decode(q, cache, many, ones, stream=s),
+            lambda s: plan.prompt(q, k, v, cu, stream=s)]
+
+
+@pytest.mark.parametrize("op", range(3))
+def test_outputs_on_a_stream_of_the_callers(op):
+    # the side stream is kept busy, so that its kernels run after the host has gone on
+    call, other = _calls(1)[op], _calls(2)[op]
+    want = [t.clone() for t in call(None)]
+    side, current = torch.cuda.Stream(), torch.cuda.current_stream()
+    side.wait_stream(current)
+    torch.cuda.synchronize()
+
+    def wait_on(stream):
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(50_000_000)
+
+    # an output that is dropped at once is still the kernel's
+    wait_on(side)
+    first, _ = call(side.cuda_stream)
+    del _
+    fresh = [torch.full_like(t, 7.0) for t in want for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(first, want[0]) and all(bool((t == 7.0).all()) for t in fresh)
+    del fresh, first
+
+    # memory that the current stream still reads is not the kernel's
+    old = [torch.full_like(t, 3.0) for t in want]
+    wait_on(current)
+    read = [t.clone() for t in old]
+    del old
+    got = call(side.cuda_stream)
+    torch.cuda.synchronize()
+    assert all(bool((t == 3.0).all()) for t in read) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+    # results that the current stream reads may be dropped before it has
+    current.wait_stream(side)
+    wait_on(current)
+    read = [t.clone() for t in got]
+    del got
+    other(side.cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(read, want))
