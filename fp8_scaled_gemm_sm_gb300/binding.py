@@ -63,6 +63,7 @@ SIGNATURES = {
                                   _vp, _vp, _vp]),
     "scaled_attn_decode": (_int, [_vp, _cache_p, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _f32, _vp, _vp, _vp]),
     "scaled_attn_prompt": (_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _int, _f32, _vp, _vp, _vp]),
+    "scaled_attn_set_debug": (_int, [_vp, _i64, _i64]),
     "scaled_attn_debug_status": (_int, [_vp, _vp, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]),
 }
 DTYPES = {"bf16": 0, "f32": 1}
@@ -216,6 +217,10 @@ def scaled_attn_decode(h, cache, q, q_stride, qn, table, table_stride, kv_lens, 
 def scaled_attn_prompt(h, q, q_stride, k, k_stride, v, v_stride, cu_q, cu_k, Tq, Tk, B, causal, scale, out, lse, stream=0):
     _check(lib().scaled_attn_prompt(h, q, q_stride, k, k_stride, v, v_stride, cu_q, cu_k, Tq, Tk, B, causal, scale, out, lse,
                                     stream), "scaled_attn_prompt")
+
+
+def scaled_attn_set_debug(h, timeout_ns=0, skip_tile=-1):
+    _check(lib().scaled_attn_set_debug(h, int(timeout_ns), int(skip_tile)), "scaled_attn_set_debug")
 
 
 def scaled_attn_debug_status(h, stream=0):

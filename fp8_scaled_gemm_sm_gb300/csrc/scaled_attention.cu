@@ -103,6 +103,7 @@ sg_status_t scaled_attn_create(sg_attn_t* out, int64_t Hq, int64_t Hk, int64_t D
   h->shape.page = static_cast<int>(page);
   h->shape.num_sms = sms;
   h->shape.timeout_ns = kTimeoutNs;
+  h->shape.skip_tile = -1;
   int prev = -1;
   cudaGetDevice(&prev);
   if (prev != dev && cudaSetDevice(dev) != cudaSuccess) {
@@ -142,6 +143,14 @@ sg_status_t scaled_attn_destroy(sg_attn_t h) {
   if (prev >= 0 && prev != h->device) cudaSetDevice(prev);
   delete h;
   return e == cudaSuccess ? SG_OK : SG_ERR_CUDA;
+}
+
+sg_status_t scaled_attn_set_debug(sg_attn_t h, int64_t timeout_ns, int64_t skip_tile) {
+  if (!h) return refuse(SG_ERR_INVALID_ARG, "attn set_debug: NULL handle");
+  if (timeout_ns < 0 || skip_tile < -1 || skip_tile > kMaxDim) return refuse(SG_ERR_INVALID_ARG, "attn set_debug: bad value");
+  h->shape.timeout_ns = timeout_ns ? static_cast<uint64_t>(timeout_ns) : kTimeoutNs;
+  h->shape.skip_tile = static_cast<int>(skip_tile);
+  return SG_OK;
 }
 
 sg_status_t scaled_attn_debug_status(sg_attn_t h, sg_stream_t stream, int32_t* code, int32_t* where) {

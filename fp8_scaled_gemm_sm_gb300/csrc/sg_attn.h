@@ -19,6 +19,7 @@ struct AttnShape {
   int num_sms;
   int* status;          // device status word of the plan
   uint64_t timeout_ns;  // limit of every wait in a kernel
+  int skip_tile;        // tests: a key tile that is not loaded; -1: none
   void* workspace;      // decode: partial results
 };
 

@@ -81,6 +81,7 @@ struct DecodeParams {
   float4* part_ml;    // [2 ranges][rows]: m, n (relative to m), sum
   Cut* cuts;          // by segment, or by range where there are fewer of those
   int by_segment;
+  int skip;           // number of a tile that is not loaded (scaled_attn_set_debug); -1: none
   int* status;
   uint64_t timeout_ns;
 };
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
     if (batch < 0 || ahead.t >= batch + 32) refresh();
     const int from = ahead.t - batch;
     const int pg0 = __shfl_sync(0xffffffffu, page0, from), pg1 = __shfl_sync(0xffffffffu, page1, from);
-    if (lane == 0) {
+    if (lane == 0 && ahead.t != p.skip) {
       const uint32_t bar = bars + 8 * stage, k = ring + 2 * stage * L::kTile, v = k + L::kTile;
       const int row = (ahead_head << p.page_shift) + (ahead.t * kKeys & in_page);
       mbar_arrive_expect_tx(bar, 2 * L::kTile);
@@ -659,7 +660,13 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
     }
     some = walk.next(c);
   }
-  if (!ok) {  // loads in flight must land before the CTA can exit
+  if (!ok) {
+    // the join must not find what an earlier call left for the segments that begin here
+    while (some) {
+      if (c.t == 0 && lane == 0 && p.by_segment) p.cuts[c.b * walk.segs + c.hr].last = -1;
+      some = walk.next(c);
+    }
+    // loads in flight must land before the CTA can exit
     for (int i = 0; i < in_flight; ++i) {
       if (lane == 0) mbar_wait_drain(bars + 8 * stage, phase, 200000000ull);
       if (++stage == S) {
@@ -838,6 +845,7 @@ sg_status_t decode_launch(const AttnShape& s, const AttnArgs& a) {
   p.part_o = static_cast<float*>(s.workspace);
   p.part_ml = reinterpret_cast<float4*>(p.part_o + max_ranges(s) * 2 * 16 * 128);
   p.cuts = reinterpret_cast<Cut*>(p.part_ml + max_ranges(s) * 2 * 16);
+  p.skip = s.skip_tile;
   p.status = s.status;
   p.timeout_ns = s.timeout_ns;
   AttnArgs args = a;

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import attn_ref as ref
-from test_gpu_attention import _check_decode, _cum, _decode, _dev, _f64, _pkg, _prompt_inputs, lib  # noqa: F401
+from test_gpu_attention import _check_decode, _cum, _decode, _dev, _f64, _pkg, _prompt_inputs, _table, lib  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -139,3 +139,82 @@ def test_outputs_on_a_stream_of_the_callers(op):
     other(side.cuda_stream)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(read, want))
+
+
+TIMEOUT = 6  # SG_ERR_TIMEOUT
+
+
+def _large(lens, hq, hk, d, page, qn, seed):
+    """A plan and a decode's arguments, made on the GPU."""
+    pkg = _pkg()
+    plan = pkg.PagedAttention(hq, hk, d, page)
+    table, pages = _table(lens, page, seed)
+    cache = plan.new_cache(pages)
+    g = torch.Generator("cuda").manual_seed(seed)
+    for codes, scales in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        codes.copy_(torch.randint(0, 127, codes.shape, generator=g, device="cuda") | torch.randint(0, 2, codes.shape, generator=g, device="cuda") << 7)
+        scales.copy_(torch.randint(116, 120, scales.shape, generator=g, device="cuda"))
+    q = torch.randn(len(lens) * qn, hq, d, generator=g, device="cuda").bfloat16()
+    return plan, (q, cache, _dev(table), _dev(np.array(lens, np.int32)))
+
+
+@pytest.mark.parametrize("hq,hk,d", [(4, 1, 128), (4, 1, 64), (16, 1, 128), (16, 1, 64), (32, 8, 128)])
+def test_decode_that_gives_up_leaves_other_memory_alone(hq, hk, d):
+    # a call over many sequences, then one over two of them, where a tile never comes: what the first left in the plan's
+    # workspace (parts of cut segments of sequences that the second does not have) must not be joined into outputs that are not there
+    from fp8_scaled_gemm_sm_gb300 import binding
+
+    B, n, page = 60, 1700, 64
+    plan, args = _large([n] * B, hq, hk, d, page, 1, 600)
+    q, cache, table, lens = args
+    keep = plan.decode(*args)
+    buf = torch.full((B + 4, hq, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    lbuf = torch.full((B + 4, hq), 5.0, device="cuda")
+    two = (q[:2].contiguous(), cache, table[:2].contiguous(), lens[:2].contiguous())
+    host = (table.cpu().numpy(), [t.cpu().numpy() for t in (cache.k, cache.v)], [t.cpu().numpy() for t in (cache.k_scale, cache.v_scale)])
+    for tile in (0, 40):
+        plan.decode(*args)
+        binding.scaled_attn_set_debug(plan.handle, 50_000_000, tile)
+        plan.decode(*two, out=buf[:2], lse=lbuf[:2])
+        torch.cuda.synchronize()
+        code, where = binding.scaled_attn_debug_status(plan.handle)
+        assert code == TIMEOUT and where != 0
+        assert bool((buf[2:] == 5.0).all()) and bool((lbuf[2:] == 5.0).all())
+        # the context and the plan are as before
+        binding.scaled_attn_set_debug(plan.handle)
+        plan.decode(*two, out=buf[:2], lse=lbuf[:2])
+        out, lse = plan.decode(*args)
+        torch.cuda.synchronize()
+        assert binding.scaled_attn_debug_status(plan.handle)[0] == 0
+        assert torch.equal(out, keep[0]) and torch.equal(lse, keep[1])
+        _check_decode([n] * 2, hq, hk, d, page, 1, host, q[:2], buf[:2], lbuf[:2])
+        buf[:2], lbuf[:2] = 5.0, 5.0
+
+
+# segments by range, several to a warp, rows in two tiles
+@pytest.mark.parametrize("lens,hq,hk,d,qn", [([40, 700] * 40, 64, 32, 128, 1), ([2000] * 100, 64, 32, 64, 2), ([90, 16, 500] * 40, 36, 12, 128, 5)])
+def test_decode_gives_up_in_every_form(lens, hq, hk, d, qn):
+    from fp8_scaled_gemm_sm_gb300 import binding
+
+    plan, args = _large(lens, hq, hk, d, 16, qn, 610)
+    keep = plan.decode(*args, q_tokens=qn)
+    binding.scaled_attn_set_debug(plan.handle, 50_000_000, 1)
+    plan.decode(*args, q_tokens=qn)
+    torch.cuda.synchronize()
+    assert binding.scaled_attn_debug_status(plan.handle)[0] == TIMEOUT
+    binding.scaled_attn_set_debug(plan.handle)
+    out, lse = plan.decode(*args, q_tokens=qn)
+    torch.cuda.synchronize()
+    assert binding.scaled_attn_debug_status(plan.handle)[0] == 0
+    assert torch.equal(out, keep[0]) and torch.equal(lse, keep[1])
+
+
+def test_debug_limits_are_checked():
+    from fp8_scaled_gemm_sm_gb300 import binding
+
+    plan = _pkg().PagedAttention(4, 2, 64, 32)
+    for bad in ((-1, -1), (0, -2), (0, 1 << 31)):
+        with pytest.raises(binding.ScaledGemmError) as e:
+            binding.scaled_attn_set_debug(plan.handle, *bad)
+        assert e.value.status == 1
+    assert binding.lib().scaled_attn_set_debug(None, 0, -1) == 1
