@@ -72,6 +72,7 @@ struct PromptParams {
   int pack;             // query heads packed into a tile
   int head_groups;      // Hq / pack
   int units;
+  int skip;             // number of a key block that is not loaded (scaled_attn_set_debug); -1: none
   float scale_log2;
   uint16_t* out;
   float* lse;
@@ -433,12 +434,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i == max(2 * x.num_blocks - kAhead, 0)) mbar_arrive(more_wanted);
             ok = mbar_wait(kv_empty(stage), phase ^ 1, wd, kWhereProducerEmpty);
             if (!ok) break;
-            mbar_arrive_expect_tx(kv_full(stage), L::kTile);
-            for (int b = 0; b < L::kBoxes; ++b)
-              tma_load_3d_hint(sKv + stage * L::kTile + b * L::kBox, (i & 1) ? &tmV : &tmK, b * 64, kv_head,
-                               job.u.k0 + (i >> 1) * kRows, kv_full(stage), keep);
-            issued |= 1u << stage;
-            last_par = (last_par & ~(1u << stage)) | (phase << stage);
+            if (i != 2 * p.skip) {
+              mbar_arrive_expect_tx(kv_full(stage), L::kTile);
+              for (int b = 0; b < L::kBoxes; ++b)
+                tma_load_3d_hint(sKv + stage * L::kTile + b * L::kBox, (i & 1) ? &tmV : &tmK, b * 64, kv_head,
+                                 job.u.k0 + (i >> 1) * kRows, kv_full(stage), keep);
+              issued |= 1u << stage;
+              last_par = (last_par & ~(1u << stage)) | (phase << stage);
+            }
             if (++stage == S) {
               stage = 0;
               phase ^= 1;
@@ -797,6 +800,7 @@ __global__ void __launch_bounds__(kTileThreads, TileLayout<HD>::kCtas)
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
   const Watchdog wd{p.status, p.timeout_ns, reinterpret_cast<volatile int*>(&misc[1])};
 
+  uint32_t issued = 0, last_par = 0;  // the producer's loads: stages, and the parities of their last
   if (warp == 4) {
     // ---------------- TMA producer ----------------
     if (lane == 0 && n > 0) {
@@ -806,28 +810,21 @@ __global__ void __launch_bounds__(kTileThreads, TileLayout<HD>::kCtas)
         tma_load_3d_hint(sQ + x * L::kQBox, &tmQ, x * 64, head0, q0 + tok0, q_full, once);
       const int kv_head = head0 / p.group;
       int stage = 0;
-      uint32_t phase = 0, issued = 0, last_par = 0;
-      bool ok = true;
+      uint32_t phase = 0;
       for (int i = 0; i < 2 * n; ++i) {
-        if (!mbar_wait(kv_empty(stage), phase ^ 1, wd, kWhereProducerEmpty)) {
-          ok = false;
-          break;
+        if (!mbar_wait(kv_empty(stage), phase ^ 1, wd, kWhereProducerEmpty)) break;
+        if (i != 2 * p.skip) {
+          mbar_arrive_expect_tx(kv_full(stage), L::kTile);
+          for (int x = 0; x < L::kBoxes; ++x)
+            tma_load_3d_hint(sKv + stage * L::kTile + x * L::kBox, (i & 1) ? &tmV : &tmK, x * 64, kv_head,
+                             k0 + (i >> 1) * kTileKeys, kv_full(stage), keep);
+          issued |= 1u << stage;
+          last_par = (last_par & ~(1u << stage)) | (phase << stage);
         }
-        mbar_arrive_expect_tx(kv_full(stage), L::kTile);
-        for (int x = 0; x < L::kBoxes; ++x)
-          tma_load_3d_hint(sKv + stage * L::kTile + x * L::kBox, (i & 1) ? &tmV : &tmK, x * 64, kv_head,
-                           k0 + (i >> 1) * kTileKeys, kv_full(stage), keep);
-        issued |= 1u << stage;
-        last_par = (last_par & ~(1u << stage)) | (phase << stage);
         if (++stage == S) {
           stage = 0;
           phase ^= 1;
         }
-      }
-      if (!ok) {  // loads in flight must land before the CTA can exit
-        mbar_wait_drain(q_full, 0, 200000000ull);
-        for (int s = 0; s < S; ++s)
-          if ((issued >> s) & 1) mbar_wait_drain(kv_full(s), (last_par >> s) & 1, 200000000ull);
       }
     }
     __syncwarp();
@@ -999,6 +996,11 @@ __global__ void __launch_bounds__(kTileThreads, TileLayout<HD>::kCtas)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (misc[1] && warp == 4 && lane == 0 && n > 0) {  // somebody gave up: loads in flight must land before the CTA can exit
+    mbar_wait_drain(q_full, 0, 200000000ull);
+    for (int s = 0; s < S; ++s)
+      if ((issued >> s) & 1) mbar_wait_drain(kv_full(s), (last_par >> s) & 1, 200000000ull);
+  }
   if (warp == 5) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kCols);
@@ -1032,6 +1034,7 @@ sg_status_t launch(const AttnShape& s, const AttnArgs& a) {
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.out = static_cast<uint16_t*>(a.out);
   p.lse = a.lse;
+  p.skip = s.skip_tile;
   p.status = s.status;
   p.timeout_ns = s.timeout_ns;
   // q as [tokens][heads][D]; without keys nothing reads the other two maps

@@ -122,8 +122,9 @@ sg_status_t scaled_attn_prompt(sg_attn_t h, const void* q, int64_t q_stride, con
 sg_status_t scaled_attn_debug_status(sg_attn_t h, sg_stream_t stream, int32_t* code, int32_t* where);
 
 /* Set the time limit of every kernel-side wait of the plan (nanoseconds; 0 = the default, 4 s) and, for tests only,
- * leave out the load of key tile `skip_tile` (-1: none) of every sequence in scaled_attn_decode, so that
- * the wait for it runs out.  After a timeout the call's outputs are undefined; nothing else is written.
+ * leave out the load of key tile `skip_tile` (-1: none) of every sequence (scaled_attn_decode) or of every few
+ * query tokens (scaled_attn_prompt), so that the wait for it runs out.  After a timeout the call's outputs are undefined;
+ * nothing else is written.
  * Not to be called while a launch on the plan is being made. */
 sg_status_t scaled_attn_set_debug(sg_attn_t h, int64_t timeout_ns, int64_t skip_tile);
 

@@ -209,6 +209,37 @@ def test_decode_gives_up_in_every_form(lens, hq, hk, d, qn):
     assert torch.equal(out, keep[0]) and torch.equal(lse, keep[1])
 
 
+# one row tile a CTA, two, units taken over, sequences without keys; a block that is the only one, the second, one far in
+@pytest.mark.parametrize("tile", [0, 1, 5])
+@pytest.mark.parametrize("ql,more,hq,hk,d", [
+    ([77], 0, 8, 2, 128), ([500, 1, 300], 0, 4, 4, 64), ([40, 1, 0, 130], 900, 4, 1, 128), ([1500] * 12, 700, 16, 8, 128), ([30] * 400, 0, 5, 1, 64),
+])
+def test_prompt_gives_up(ql, more, hq, hk, d, tile):
+    from fp8_scaled_gemm_sm_gb300 import binding
+
+    kl = [n + more for n in ql]
+    g = torch.Generator("cuda").manual_seed(620)
+    q, k, v = (torch.randn(n, h, d, generator=g, device="cuda").bfloat16() for n, h in ((sum(ql), hq), (sum(kl), hk), (sum(kl), hk)))
+    cq, ck = _dev(_cum(ql)), _dev(_cum(kl))
+    plan = _pkg().PagedAttention(hq, hk, d)
+    keep = plan.prompt(q, k, v, cq, ck)
+    T = sum(ql)
+    buf = torch.full((T + 64, hq, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    lbuf = torch.full((T + 64, hq), 5.0, device="cuda")
+    binding.scaled_attn_set_debug(plan.handle, 50_000_000, tile)
+    plan.prompt(q, k, v, cq, ck, out=buf[:T], lse=lbuf[:T])
+    torch.cuda.synchronize()
+    code, where = binding.scaled_attn_debug_status(plan.handle)
+    reached = max(kl) > tile * (128 if d == 128 and sum(kl) > 512 * len(kl) else 64)
+    assert (code, where != 0) == ((TIMEOUT, True) if reached else (0, False))
+    assert bool((buf[T:] == 5.0).all()) and bool((lbuf[T:] == 5.0).all())
+    binding.scaled_attn_set_debug(plan.handle)
+    out, lse = plan.prompt(q, k, v, cq, ck)
+    torch.cuda.synchronize()
+    assert binding.scaled_attn_debug_status(plan.handle)[0] == 0
+    assert torch.equal(out, keep[0]) and torch.equal(lse, keep[1])
+
+
 def test_debug_limits_are_checked():
     from fp8_scaled_gemm_sm_gb300 import binding
 
