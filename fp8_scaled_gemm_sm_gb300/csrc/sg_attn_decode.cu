@@ -181,7 +181,7 @@ struct Walk {
     const int64_t cap = p.table_stride * p.page;  // below 2^31
     return static_cast<int>(min(static_cast<int64_t>(max(__ldg(p.lens + b), 0)), cap));
   }
-  __device__ __forceinline__ static int tiles(int len) { return (len + kKeys - 1) / kKeys; }
+  __device__ __forceinline__ static int tiles(int len) { return static_cast<int>((static_cast<uint32_t>(len) + kKeys - 1) / kKeys); }
   __device__ __forceinline__ static int64_t numbers(int len) { return len > 0 ? tiles(len) + kSegCost : 0; }
   // The first part at or after segment c; false: none.
   __device__ __forceinline__ bool find(Part& c) const {
@@ -336,10 +336,10 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
   auto refresh = [&]() {
     batch = ahead.t;
     ahead_head = ahead.hr / p.row_tiles;
-    const int key = (ahead.t + lane) * kKeys;
+    const uint32_t key = static_cast<uint32_t>(ahead.t + lane) * kKeys, len = ahead.len;  // past 2^31 for lanes past the last tile
     const int32_t* row = p.table + ahead.b * p.table_stride;
-    auto page_of = [&](int k) {
-      if (k >= ahead.len) return -1;
+    auto page_of = [&](uint32_t k) {
+      if (k >= len) return -1;
       const int pg = __ldg(row + (k >> p.page_shift));
       return pg >= 0 && pg < p.num_pages ? pg : -1;
     };
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int pg = i ? page1 : page0;
-      if (pg >= 0 && key + 16 * i < ahead.len) {  // a block past the end may hold any byte, NaN's among them
+      if (pg >= 0 && key + 16 * i < len) {  // a block past the end may hold any byte, NaN's among them
         const int64_t at = ((static_cast<int64_t>(pg) * p.Hk + ahead_head) << block_shift) + (((key + 16 * i) & in_page) >> 4);
         scales |= static_cast<uint32_t>(__ldg(p.k_scale + at)) << (8 * i) | static_cast<uint32_t>(__ldg(p.v_scale + at)) << (16 + 8 * i);
       }
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
         kx[j] = kc == 255 ? __uint_as_float(0x7FC00000u) : exp2_code(kc);
         vx[j] = vc == 255 ? __uint_as_float(0x7FC00000u) : static_cast<float>(vc - 127);
       }
-      const bool edge = key0 + kKeys > c.len - (p.qn - 1) || about.y != 0;
+      const bool edge = key0 > c.len - (p.qn - 1) - kKeys || about.y != 0;
       bool move = false;
 #pragma unroll
       for (int r = 0; r < NR; ++r)

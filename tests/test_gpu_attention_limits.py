@@ -27,6 +27,38 @@ def test_decode_scales_of_blocks_that_nothing_wrote(page, hq, hk, d, qn):
     _check_decode(lens, hq, hk, d, page, qn, host, args[0], out, lse)
 
 
+@pytest.mark.parametrize("hq,qn", [(2, 1), (12, 3)])
+def test_decode_lengths_up_to_31_bits(hq, qn):
+    # a table of 2^24 - 1 entries that name three pages over and over: 2^31 - 128 tokens, the most that there can be
+    page, d, pages = 128, 16, 3
+    pkg = _pkg()
+    plan = pkg.PagedAttention(hq, 1, d, page)
+    rng = np.random.default_rng(8)
+    codes = [ref.e4m3_round(rng.normal(size=(pages, 1, page, d)) * 100) for _ in range(2)]
+    scales = [rng.integers(116, 121, (pages, 1, page // 16)).astype(np.uint8) for _ in range(2)]
+    width = (1 << 24) - 1
+    table = (torch.arange(width, dtype=torch.int32, device="cuda") % pages)[None]
+    n = width * page
+    for length in (n, n - 1, n - 113, 2 ** 31 - 1, n - 4000):
+        q = torch.randn(qn, hq, d, generator=torch.Generator().manual_seed(9)).bfloat16().cuda()
+        cache = pkg.KVCache(*[_dev(c) for c in codes], *[_dev(s) for s in scales])
+        out, lse = plan.decode(q, cache, table, _dev(np.array([length], np.int32)), q_tokens=qn)
+        torch.cuda.synchronize()
+        for i in range(qn):
+            see = min(length, n) - (qn - 1 - i)
+            full, rest = divmod(see, page)
+            times = np.array([(full - p + pages - 1) // pages for p in range(pages)])[:, None] + (np.arange(pages) == full % pages)[:, None] * (np.arange(page) < rest)
+            k, v = (ref.E4M3[c[:, 0]] * np.repeat(ref.pow2(s[:, 0]), 16, -1)[..., None] for c, s in zip(codes, scales))
+            x = k @ _f64(q)[i].T * d ** -0.5                       # [pages, page, hq]
+            w = np.exp(x - x.max((0, 1))) * times[..., None]
+            o = np.einsum("pth,ptd->hd", w, v) / w.sum((0, 1))[:, None]
+            mag = np.einsum("pth,ptd->hd", w, np.abs(v)) / w.sum((0, 1))[:, None]
+            # a warp adds up 2^31 / 1216 keys at most, in four fp32 sums a lane group of eight: 2^17 roundings of 2^-24 each
+            assert (np.abs(_f64(out)[i] - o) <= ref.out_tolerance(o, mag, 11) + 2.0 ** -7 * mag).all()
+            ls = x.max((0, 1)) + np.log(w.sum((0, 1)))
+            assert (np.abs(_f64(lse)[i] - ls) <= 2.0 ** -7 + ref.lse_tolerance(ls, np.abs(x).max())).all()
+
+
 def _sure(q, k, vis, scale):
     """[n, Hq]: rows whose largest score is ahead of the others by more than scores summed in fp32 can be off
     (2^-18 of sum |q k| each, as lse_tolerance has it) and another 32."""
