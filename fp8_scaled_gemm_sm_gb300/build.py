@@ -6,8 +6,11 @@ Every .cu under csrc/ is compiled in parallel for
 ``fp8_scaled_gemm_sm_gb300/libscaledgemm.so`` with the CUDA runtime linked
 statically, so the library loads on a machine without a GPU (its entry points
 then return SG_ERR_CUDA).  ``_attn.so`` (host code, the C++ compiler and torch's
-headers) is compiled at the same time and links to it.
+headers) is compiled at the same time and links to it.  The library does not depend
+on it: without torch only the library is built, and where ``_attn.so`` does not build
+the library is there before the error is raised.
 """
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -47,10 +50,15 @@ def _deps():
     ] + [os.path.abspath(__file__)]
 
 
+def have_torch():
+    return importlib.util.find_spec("torch") is not None
+
+
 def up_to_date():
-    if not os.path.exists(LIB) or not os.path.exists(EXT):
+    made = [LIB, EXT] if have_torch() else [LIB]
+    if not all(os.path.exists(f) for f in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
+    t = min(os.path.getmtime(f) for f in made)
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -75,16 +83,16 @@ def build(force=False, verbose=False, extra_flags=()):
 
     srcs = sources()
     with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        ext = ex.submit(_compile_ext, verbose)
+        ext = ex.submit(_compile_ext, verbose) if have_torch() else None
         objs = list(ex.map(compile_one, srcs))
-        ext_obj = ext.result()
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [cc] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "--cudart", "static", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
-    _link_ext(ext_obj)
+    if ext is not None:
+        _link_ext(ext.result())
     return LIB
 
 
