@@ -32,8 +32,10 @@ sg_status_t check_rows(const void* p, int64_t stride, int64_t heads, int64_t D, 
 }
 
 sg_status_t check_cache(const sg_attn* h, const sg_kv_cache_t* c) {
-  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return refuse(SG_ERR_INVALID_ARG, "attn: NULL cache");
+  if (!c) return refuse(SG_ERR_INVALID_ARG, "attn: NULL cache");
   if (c->num_pages < 0) return refuse(SG_ERR_INVALID_ARG, "attn: negative num_pages");
+  if (c->num_pages == 0) return SG_OK;  // nothing is read or written
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return refuse(SG_ERR_INVALID_ARG, "attn: NULL cache");
   if (c->num_pages > kMaxDim) return refuse(SG_ERR_UNSUPPORTED_SHAPE, "attn: num_pages >= 2^31");
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->k_page_stride % 16 != 0 || c->v_page_stride % 16 != 0)
     return refuse(SG_ERR_MISALIGNED, "attn: cache codes");

@@ -849,7 +849,11 @@ sg_status_t decode_launch(const AttnShape& s, const AttnArgs& a) {
   p.status = s.status;
   p.timeout_ns = s.timeout_ns;
   AttnArgs args = a;
-  if (args.cache.num_pages == 0) args.cache.num_pages = 1;  // a tensor map has no empty dimension; nothing reads it
+  if (args.cache.num_pages == 0) {  // a tensor map has no empty dimension; nothing reads it
+    args.cache.num_pages = 1;
+    args.cache.k = args.cache.v = const_cast<void*>(a.q);
+    args.cache.k_page_stride = args.cache.v_page_stride = static_cast<int64_t>(s.Hk) * s.page * s.D;
+  }
   // Up to 8 query rows of a key/value head take half the registers, which
   // more warps use; more rows go 16 at a time, so that the cache is read half as often.
   if (p.qn * p.group <= 8) return s.D > 64 ? launch<128, 1>(s, args, p) : launch<64, 1>(s, args, p);

@@ -21,6 +21,7 @@
  *                apart (a multiple of 16, at least Hk * page * D); k_scale, v_scale: e8m0 codes
  *                [num_pages][Hk][page / 16] (any alignment), one scale for each block of
  *                16 tokens and head: value = e4m3(code) * 2^(scale - 127).  Scale code 255 is NaN.
+ *                With num_pages 0 the pointers and strides are not looked at.
  *   table        int32 [B][table_stride] (4-byte aligned): the pages of each sequence in order.
  *                An entry outside [0, num_pages) has no page: nothing is written for its tokens
  *                and attention does not see them.

@@ -115,6 +115,21 @@ def test_prompt_large_scores_are_right_or_nan(n, m, hq, hk, d, scale):
     assert sure.any() if scale < 1e8 else far.any()
 
 
+def test_cache_without_pages():
+    pkg = _pkg()
+    plan = pkg.PagedAttention(4, 2, 64, 32)
+    cache = plan.new_cache(0)
+    q = torch.ones(2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    kv = torch.ones(2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    for width in (0, 3):
+        table = torch.zeros(2, width, dtype=torch.int32, device="cuda")
+        lens = torch.tensor([9, 0], dtype=torch.int32, device="cuda")
+        out, lse = plan.decode(q, cache, table, lens)
+        rotated, _ = plan.append(q, kv, kv, cache, table, lens, torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda"))
+        torch.cuda.synchronize()
+        assert bool((out == 0).all()) and bool(torch.isinf(lse).all()) and torch.equal(rotated, q)
+
+
 def _calls(seed):
     """append, decode and prompt on inputs of their own: functions of (stream) that return their outputs."""
     pkg = _pkg()
