@@ -38,10 +38,11 @@
  * accumulated in fp32; bf16 outputs are rounded once, to nearest even.
  *
  * NaN and infinity: what a row does not see does not reach it, with one exception, a non-finite
- * VALUE (v) of the row's own sequence in a tile of keys that the row sees a part of (its weight
- * there is zero, and zero times infinity is NaN): in scaled_attn_prompt tiles are of 64 or
- * 128 keys, in scaled_attn_decode with several query tokens of 32 (a later
- * token's value reaches the earlier rows).  Other sequences' values never do.
+ * VALUE (v) of the row's own sequence behind the causal edge: its weight is zero, but the matrix product takes it with
+ * keys that other rows see, and zero times infinity is NaN.  In scaled_attn_prompt such a value of a key up to 142 past the last that the
+ * row sees may make the value's dimension of the row NaN (the rest of its tile of 128 rows, rounded up to 16 keys); in scaled_attn_decode
+ * with several query tokens, one of those tokens may do so to the rows before it.  Keys (k), bytes of the cache that no
+ * token has been written to, and other sequences never do.
  *
  * Errors, streams and programmatic launches: as in scaled_gemm.h.  A handle owns a
  * workspace that scaled_attn_decode uses, so decodes on one handle must be ordered (one

@@ -115,6 +115,55 @@ def test_prompt_large_scores_are_right_or_nan(n, m, hq, hk, d, scale):
     assert sure.any() if scale < 1e8 else far.any()
 
 
+# The rows that a non-finite value behind the causal edge may reach: those whose last key is up to 142 before it.
+@pytest.mark.parametrize("back", [1, 17, 90, 130, 255])
+@pytest.mark.parametrize("n,m,hq,hk,d", [(300, 300, 1, 1, 64), (300, 300, 4, 1, 64), (260, 330, 1, 1, 128), (300, 300, 5, 1, 128),
+                                         (300, 900, 2, 1, 128), (300, 907, 1, 1, 128), (400, 800, 3, 1, 96)])
+def test_prompt_values_that_are_not_finite(n, m, hq, hk, d, back):
+    q, k, v = _prompt_inputs([n], [m], hq, hk, d, 520)
+    plan = _pkg().PagedAttention(hq, hk, d)
+    cu = _dev(_cum([n])), _dev(_cum([m]))
+    clean, clean_lse = plan.prompt(q, k, v, *cu)
+    at = m - back
+    for value in (float("inf"), float("nan")):
+        v = v.clone()
+        v[at, :, 3] = value
+        out, lse = plan.prompt(q, k, v, *cu)
+        torch.cuda.synchronize()
+        last = np.arange(n) + m - n                       # the last key that a row sees
+        bad = ~torch.isfinite(out).cpu().numpy()
+        assert bad[last >= at][:, :, 3].all()             # who sees it shows it
+        assert not bad[last + 142 < at].any()             # who is far before it does not
+        bad[:, :, 3] = False
+        assert not bad.any()                              # nor does any other dimension
+        same = torch.isfinite(out)
+        assert torch.equal(out[same], clean[same]) and torch.equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("qn", [1, 4, 40])
+@pytest.mark.parametrize("hq,hk,d,page", [(4, 2, 64, 16), (8, 1, 128, 64)])
+def test_decode_values_that_are_not_finite(hq, hk, d, page, qn):
+    lens = [90, 200]
+    plan, (q, cache, table, dl), host, clean, clean_lse = _decode(lens, hq, hk, d, page, qn, 530)
+    for back in (1, 2, qn, qn + 1):
+        at = lens[0] - back
+        kept = cache.v.clone()
+        cache.v[int(table[0, at // page]), :, at % page, 5] = 0x7F
+        out, lse = plan.decode(q, cache, table, dl, q_tokens=qn)
+        torch.cuda.synchronize()
+        bad = torch.isnan(out).cpu().numpy()
+        last = lens[0] - 1 - (qn - 1 - np.arange(qn))
+        assert bad[:qn][last >= at][:, :, 5].all()
+        if back > qn - 1:                                 # every row sees it: nothing else to say
+            assert bad[:qn, :, 5].all()
+        assert not bad[qn:].any()                         # the other sequence
+        bad[:, :, 5] = False
+        assert not bad.any()
+        same = ~torch.isnan(out)
+        assert torch.equal(out[same], clean[same]) and torch.equal(lse, clean_lse)
+        cache.v.copy_(kept)
+
+
 def test_cache_without_pages():
     pkg = _pkg()
     plan = pkg.PagedAttention(4, 2, 64, 32)
