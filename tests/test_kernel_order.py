@@ -1,4 +1,5 @@
-"""Order of a kernel's first steps, read from the sources (a deadlock is not to be tried on a GPU).
+"""What is read from the kernels' sources: helpers that nothing calls, and the order of a kernel's first steps (a deadlock is not
+to be tried on a GPU).
 
 A kernel launched early holds tensor memory while it waits for the one before it.  So a kernel that allocates
 tensor memory does so, on every path, before it lets the next one start."""
@@ -32,3 +33,10 @@ def test_tensor_memory_is_allocated_before_the_next_kernel_may_start(f, name, pa
     assert alloc < launch
     assert "__syncthreads()" in part[alloc:launch]  # all warps know of it
     assert part.count("grid_dep_launch()") == 1
+
+
+def test_every_device_helper_is_called():
+    text = "".join(re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, f)).read()) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh")))
+    names = set(re.findall(r"__device__ __forceinline__ (?:static )?[\w:<>]+[ &*]+(\w+)\(", text))
+    assert len(names) > 60
+    assert sorted(n for n in names if len(re.findall(r"\b%s\b" % n, text)) == 1) == []
