@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import attn_ref as ref
-from test_gpu_attention import _check_decode, _cum, _decode, _dev, _f64, _pkg, _prompt_inputs, _table, lib  # noqa: F401
+from test_gpu_attention import _check_decode, _check_prompt, _cum, _decode, _dev, _f64, _pkg, _prompt_inputs, _table, lib  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -345,3 +345,58 @@ def test_debug_limits_are_checked():
             binding.scaled_attn_set_debug(plan.handle, *bad)
         assert e.value.status == 1
     assert binding.lib().scaled_attn_set_debug(None, 0, -1) == 1
+
+
+@pytest.mark.parametrize("d,page,rot,inter", [(128, 64, 128, 0), (64, 16, 32, 1), (96, 32, 0, 0)])
+def test_raw_calls_agree_and_outputs_may_be_left_out(d, page, rot, inter):
+    # the C ABI by its binding's names, with k_out and lse NULL, against the calls on tensors
+    from fp8_scaled_gemm_sm_gb300 import binding
+
+    pkg = _pkg()
+    hq, hk, n = 6, 2, 75
+    cs = pkg.rotary_table(n, rot) if rot else None
+    plan = pkg.PagedAttention(hq, hk, d, page, rotary=cs, interleaved=bool(inter))
+    x = torch.randn(n, hq + 2 * hk, d, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    q, k, v = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+    pages = -(-n // page)
+    table, cu = torch.arange(pages, dtype=torch.int32, device="cuda")[None], _dev(_cum([n]))
+    zero, lens = _dev(np.array([0], np.int32)), _dev(np.array([n], np.int32))
+    cache, other = plan.new_cache(pages), plan.new_cache(pages)
+    want_q, _ = plan.append(q, k, v, cache, table, zero, cu)
+    want_d, _ = plan.decode(want_q[-1:], cache, table, lens)
+    want_p, _ = plan.prompt(want_q, k, v, cu)
+
+    least = hk * page * d
+    args = binding.KvCacheArgs(other.k.data_ptr(), other.v.data_ptr(), other.k_scale.data_ptr(), other.v_scale.data_ptr(), pages, least, least)
+    turn = binding.RotaryArgs(cs.data_ptr() if rot else None, n if rot else 0, rot, inter)
+    wide, s = x.stride(0), torch.cuda.current_stream().cuda_stream
+    got_q, got_d, got_p = (torch.empty_like(t) for t in (want_q, want_d, want_p))
+    binding.scaled_attn_append(plan.handle, args, turn, q.data_ptr(), wide, k.data_ptr(), wide, v.data_ptr(), wide, table.data_ptr(), pages,
+                               zero.data_ptr(), cu.data_ptr(), n, 1, got_q.data_ptr(), None, s)
+    binding.scaled_attn_decode(plan.handle, args, got_q[-1:].data_ptr(), hq * d, 1, table.data_ptr(), pages, lens.data_ptr(), 1, d ** -0.5,
+                               got_d.data_ptr(), None, s)
+    binding.scaled_attn_prompt(plan.handle, got_q.data_ptr(), hq * d, k.data_ptr(), wide, v.data_ptr(), wide, cu.data_ptr(), cu.data_ptr(), n, n, 1, 1,
+                               d ** -0.5, got_p.data_ptr(), None, s)
+    torch.cuda.synchronize()
+    for a, b in ((got_q, want_q), (got_d, want_d), (got_p, want_p), (other.k, cache.k), (other.v, cache.v), (other.k_scale, cache.k_scale), (other.v_scale, cache.v_scale)):
+        assert torch.equal(a, b)
+
+
+def test_scale_and_outputs_of_the_callers():
+    lens, hq, hk, d, page = [70, 33, 0], 4, 2, 64, 16
+    for scale in (0.03, 1.0):
+        plan, args, host, out, lse = _decode(lens, hq, hk, d, page, 1, 540, scale=scale, q_scale=0.5)
+        _check_decode(lens, hq, hk, d, page, 1, host, args[0], out, lse, scale=np.float64(np.float32(scale)))
+        mine = torch.full_like(out, 9.0), torch.full_like(lse, 9.0)
+        got = plan.decode(*args, scale=scale, out=mine[0], lse=mine[1])
+        assert all(a.data_ptr() == b.data_ptr() for a, b in zip(got, mine))
+        assert torch.equal(mine[0], out) and torch.equal(mine[1], lse)
+        ql = [50, 1, 90]
+        q, k, v = _prompt_inputs(ql, ql, hq, hk, d, 541)
+        q = q * 0.5
+        cu = _dev(_cum(ql))
+        out, lse = plan.prompt(q, k, v, cu, scale=scale)
+        _check_prompt(ql, ql, hq, hk, d, True, q, k, v, out, lse, scale=np.float64(np.float32(scale)))
+        mine = torch.full_like(out, 9.0), torch.full_like(lse, 9.0)
+        plan.prompt(q, k, v, cu, scale=scale, out=mine[0], lse=mine[1])
+        assert torch.equal(mine[0], out) and torch.equal(mine[1], lse)
