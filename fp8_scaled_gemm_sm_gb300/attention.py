@@ -108,6 +108,12 @@ class PagedAttention:
     once either way.  What the caller passes (inputs, the cache, outputs of its own) has to
     be ready on `stream` and to live until that has used it: ``wait_stream`` and
     ``record_stream`` are the caller's.
+
+    A plan owns a workspace that ``decode`` uses, so decodes on one plan have to be ordered
+    (one stream, ordered streams, or a plan a stream); ``append`` and ``prompt`` may
+    overlap with anything that leaves their buffers alone.  Nothing here has a backward
+    pass: results carry no gradient, whatever the inputs do.  Output rows past
+    cu_seqlens[B] (a batch padded for a graph) are not written.
     """
 
     def __init__(self, q_heads, kv_heads, dim, page_size=64, rotary=None, interleaved=False, device=None):

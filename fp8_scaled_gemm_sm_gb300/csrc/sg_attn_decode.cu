@@ -31,9 +31,11 @@
 // the device; each CTA sums them up), loaded into its own ring by TMA ahead of use, across
 // segments.  Segments that are short beside a range are not cut; the parts of a cut one are joined
 // by a second kernel in the order of its ranges, so results do not depend on timing.
-// Measured, main kernel and join: 64 sequences of up to 16k tokens, 32 heads of 128 over 8: 94 + 4 us, the
-// main kernel at 92% of a copy's rate; 2 long ones 84 + 6; 200 sequences with 4 drafted tokens, 16 heads of 64 over 16:
-// 57 + 5 (issue slots bound it: 64-wide heads have as many weights to make for half the bytes); one of 777 tokens 8.9.
+// Measured, main kernel and join: 64 sequences of up to 16k tokens, 32 heads of 128 over 8: 98 us (the join 4; the
+// main kernel at 92% of a copy's rate); 2 long ones 90 (6); 200 sequences with 4 drafted tokens, 16 heads of 64 over 16:
+// 60 (5; 62% of the issue slots, DRAM at 59%: 64-wide heads have as many weights to make for half the bytes); one of 777 tokens
+// 8.7.  With 16 query rows a key/value head (128 heads over 8, or 4 drafted tokens of 32 over 8) the 64 sequences take 118:
+// 255 registers leave two warps a scheduler, which wait for one another's results (issue 46%, DRAM 64%).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

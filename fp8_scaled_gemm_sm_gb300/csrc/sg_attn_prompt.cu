@@ -31,9 +31,10 @@
 // as the output's own rounding; the row sums take the unrounded weights.
 //
 // What bounds it: the tensor pipe, but for a unit's first and last softmax and its output: a block of both tiles
-// takes 1.33 us, 1.9 PFLOP/s.  16384 tokens, 32 heads of 128 over 8, causal: 1240 us, 1.77 PFLOP/s, 91% of what the
-// library's bf16 GEMM reaches; 6 chunks of 300 to 2048 tokens behind contexts, 40 heads over 8: 295 us.  Measured
-// beside it: a CTA a unit 1275 and 323 us; output a row a lane 1257 and 309; key columns past a block's last key
+// takes 1.33 us, 1.9 PFLOP/s.  16384 tokens, 32 heads of 128 over 8, causal: 1240 us a launch by itself, 1.77 PFLOP/s, 91% of
+// what the library's bf16 GEMM reaches in a burst; launched on and on, under the power cap, 1376 us, 1.60 PFLOP/s, 92% of what that
+// reaches for seconds.  6 chunks of 300 to 2048 tokens behind contexts, 40 heads over 8: 295 us, 316 in a loop.  Measured
+// beside it, launches by themselves: a CTA a unit 1275 and 323 us; output a row a lane 1257 and 309; key columns past a block's last key
 // skipped in the loads and exponentials (they are hidden, and only the last block has any; the branches cost every
 // block) 1377 us for the 16384 tokens, and, of that form, one S buffer a tile with P elsewhere 1509 us, 64-key
 // blocks with two S buffers 1612, MMAs issued by lane 0 under a plain branch instead of one elected thread 1520.
@@ -722,9 +723,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the tensor cores waiting.  Here a CTA owns one row tile with 64 columns of tensor memory
 // for scores of 64 keys (weights over them) and 64 for the output, and four
 // CTAs share an SM: four softmaxes hide each other's waits, and the tiles are dealt out one by one, which
-// ragged prompts need (29 of 1 to 2500 tokens, 16 heads of 64: 64.5 us, 94 with two tiles a CTA).  What bounds
+// ragged prompts need (29 of 1 to 2500 tokens, 16 heads of 64: 63.8 us, 94 with two tiles a CTA).  What bounds
 // it is the softmax's instructions.  With heads of 128, two CTAs an SM, it is for short
-// sequences (77 tokens, 32 heads over 8: 5.4 us).
+// sequences (77 tokens, 32 heads over 8: 5.3 us).
 //   warps 0-3  softmax and output, one thread a row
 //   warp 4     TMA producer: Q, then K_0, V_0, K_1, V_1, ...; then V rows past the sequence's end
 //   warp 5     MMA issuer, one elected thread
@@ -1086,10 +1087,10 @@ sg_status_t prompt_launch(const AttnShape& s, const AttnArgs& a) {
   if (s.D <= 64) return launch<64, true>(s, a);
   // Two tiles a CTA read K and V half as often and overlap better, one a CTA starts sooner and deals out finer.
   // By the mean sequence: where two-tile units fill the SMs three times over, they win unless an odd tile leaves
-  // half of too many units empty (32 heads over 8, 32 sequences of 200 tokens: 52.2 us with two, 54.3 with one; 8 of
-  // 512: 35.6, 44.3; 128 of 100: 94.8, 122.6; but 8 heads over 8, 128 of 100, one tile each: 50.9, 37.9; 64 of 300, three: 69.2,
-  // 58.3); with fewer units it is the keys that decide (32 over 8, one of 512, 1024, 2048 tokens: 13.0, 20.2, 33.2 with two,
-  // 11.1, 18.9, 39.0 with one; 8 over 8, one of 1024, 2048: 18.0, 29.3 and 18.1, 32.3).
+  // half of too many units empty (32 heads over 8, 32 sequences of 200 tokens: 51.3 us with two, 56.2 with one; 8 of
+  // 512: 34.8, 44.0; 128 of 100: 94.8, 128.4; one of 8000 and 63 of 100: 363, 542; but 8 heads over 8, 128 of 100, one tile each:
+  // 50.2, 40.3; 64 of 300, three: 66.3, 63.8); with fewer units it is the keys that decide (32 over 8, one of 512, 1024, 2048
+  // tokens: 12.6, 19.1, 32.6 with two, 11.4, 18.8, 40.5 with one; 8 over 8, one of 1024, 2048: 17.9, 28.5 and 18.1, 31.4).
   const int pack = heads_packed(s.Hq / s.Hk);
   const int64_t tiles = (a.Tq * pack / a.B + kRows - 1) / kRows, units = (tiles + 1) / 2 * a.B * (s.Hq / pack);
   const bool two = units >= 3 * s.num_sms ? tiles % 2 == 0 || tiles > 4 : a.Tk > 512 * a.B;

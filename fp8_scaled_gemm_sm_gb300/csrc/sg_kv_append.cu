@@ -21,8 +21,8 @@
 // the room of half the warps.  The tokens' cosines and sines, which all heads use, wait in shared memory too: the
 // items leave L1 too little room for them.  48k prompt tokens, 32 heads of 128 over 8: 230 us, 91% of the
 // rate of a copy (249 without loading ahead and with cosines through L1, 281 with fp32 kept); 41 chunks of up to 1500
-// tokens, 24 heads of 64 over 24: 43 us (50), half of the issue slots and of the memory; one token of 512 sequences 6.6 us, of 8
-// sequences 3.6, most of it the launch and four dependent loads.
+// tokens, 24 heads of 64 over 24: 43 us (50), half of the issue slots and of the memory; one token of 512 sequences 6.5 us, of 8
+// sequences 3.4, most of it the launch and four dependent loads.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>

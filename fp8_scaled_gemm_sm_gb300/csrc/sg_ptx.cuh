@@ -315,7 +315,8 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// tma_store_2d with an L2 cache policy.
+// 2D tiled store of a shared-memory box to (x, y), with an L2 cache policy; the box
+// is clipped at the tensor's bounds.
 __device__ __forceinline__ void tma_store_2d_hint(const CUtensorMap* map, uint32_t src, int32_t x,
                                                   int32_t y, uint64_t policy) {
   asm volatile(

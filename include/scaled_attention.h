@@ -26,7 +26,8 @@
  *                An entry outside [0, num_pages) has no page: nothing is written for its tokens
  *                and attention does not see them.
  *   cu_seqlens   int32 [B + 1] (4-byte aligned), non-decreasing, cu_seqlens[0] = 0: sequence b's rows are
- *                [cu_seqlens[b], cu_seqlens[b + 1]).  Values are clamped to the rows there are.
+ *                [cu_seqlens[b], cu_seqlens[b + 1]).  Values are clamped to the rows there are.  Output rows
+ *                past cu_seqlens[B] (a batch padded for a graph) are not written.
  *   rotary       float [max_pos][2][rot / 2] (cos, then sin) by position; a position past
  *                the table uses its last row.
  *   lse          float [rows][Hq] (4-byte aligned): natural logarithm of the softmax's denominator; -infinity
@@ -34,15 +35,21 @@
  *
  * Rules: 1 <= Hq, Hk <= 1024, Hq a multiple of Hk; D a multiple of 16, 16 <= D <= 128; page 16, 32, 64
  * or 128; rot a multiple of 16, 0 <= rot <= D; scale positive and finite; in scaled_attn_prompt scores scale q.k of up to 2^29
- * in magnitude (a row whose largest is past 2^30 gets NaN).  Softmax statistics, sums and products are
- * accumulated in fp32; bf16 outputs are rounded once, to nearest even.
+ * in magnitude (a row whose largest is past 2^30 gets NaN).
+ *
+ * Precision: scores, softmax statistics and sums are held in fp32; bf16 outputs are rounded once, to nearest even.
+ * The weights of the product with v are rounded to what the tensor cores take, each to nearest: in
+ * scaled_attn_prompt to bf16 (by at most 2^-8 of itself), in scaled_attn_decode to fp16 (2^-11; with its value block's
+ * scale inside, and to no finer than 2^-32 of the row's largest such weight: where one visible block's value scale is 2^22 or
+ * more above the others', their light weights lose bits in every dimension).  The denominator takes them unrounded.
  *
  * NaN and infinity: what a row does not see does not reach it, with one exception, a non-finite
- * VALUE (v) of the row's own sequence behind the causal edge: its weight is zero, but the matrix product takes it with
- * keys that other rows see, and zero times infinity is NaN.  In scaled_attn_prompt such a value of a key up to 142 past the last that the
- * row sees may make the value's dimension of the row NaN (the rest of its tile of 128 rows, rounded up to 16 keys); in scaled_attn_decode
- * with several query tokens, one of those tokens may do so to the rows before it.  Keys (k), bytes of the cache that no
- * token has been written to, and other sequences never do.
+ * VALUE (v) of the row's own sequence behind the causal edge: its weight is zero, but the matrix
+ * product takes it with keys that other rows see, and zero times infinity is NaN.  In
+ * scaled_attn_prompt the value of a key up to 142 past the last that a row sees (the rest of its
+ * tile of 128 rows, rounded up to 16 keys) may make that dimension of the row NaN; in
+ * scaled_attn_decode with several query tokens, one of them may do so to the rows before it.
+ * Keys (k), bytes of the cache that no token has been written to, and other sequences never do.
  *
  * Errors, streams and programmatic launches: as in scaled_gemm.h.  A handle owns a
  * workspace that scaled_attn_decode uses, so decodes on one handle must be ordered (one

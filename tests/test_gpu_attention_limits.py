@@ -400,3 +400,20 @@ def test_scale_and_outputs_of_the_callers():
         mine = torch.full_like(out, 9.0), torch.full_like(lse, 9.0)
         plan.prompt(q, k, v, cu, scale=scale, out=mine[0], lse=mine[1])
         assert torch.equal(mine[0], out) and torch.equal(mine[1], lse)
+
+
+def test_rows_past_the_last_sequence_are_not_written():
+    # a batch padded for a graph: more rows than the sequences have
+    pkg = _pkg()
+    hq, hk, d, page, n, rows = 4, 2, 64, 16, 20, 150
+    plan = pkg.PagedAttention(hq, hk, d, page, rotary=pkg.rotary_table(n, d))
+    x = torch.randn(rows, hq + 2 * hk, d, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    q, k, v = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+    cu, zero = _dev(np.array([0, n], np.int32)), _dev(np.array([0], np.int32))
+    table = torch.arange(2, dtype=torch.int32, device="cuda")[None]
+    mine = [torch.full((rows, h, d), 5.0, dtype=torch.bfloat16, device="cuda") for h in (hq, hk, hq)]
+    lse = torch.full((rows, hq), 5.0, device="cuda")
+    plan.append(q, k, v, plan.new_cache(2), table, zero, cu, k_out=mine[1], q_out=mine[0])
+    plan.prompt(q, k, v, cu, out=mine[2], lse=lse)
+    torch.cuda.synchronize()
+    assert all(bool((t[n:] == 5.0).all()) and not bool((t[:n] == 5.0).all()) for t in mine + [lse])
