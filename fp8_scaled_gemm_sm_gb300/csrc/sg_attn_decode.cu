@@ -634,14 +634,14 @@ __global__ void __launch_bounds__(DecodeLayout<HD, NR>::kThreads, 1)
         if (whole) {
           const int64_t at = (static_cast<int64_t>(c.b) * p.qn + row / p.group) * p.Hq + h * p.group + row % p.group;
           const bool none = sum[r][e] == 0.f;
-          const float by = none ? 0.f : ex2(n[r][e]) / sum[r][e];
+          const float half = ex2(0.5f * n[r][e]), by = half / sum[r][e];  // 2^n in two steps: by itself it may leave fp32's range
           if (run_d < p.D) {
 #pragma unroll
             for (int i = 0; i < kOut; i += 4) {
               uint32_t u[4];
 #pragma unroll
               for (int x = 0; x < 4; ++x)
-                u[x] = none ? 0u : pack_bf16x2(o[r][i + x][e] * by, o[r][i + x][2 + e] * by);
+                u[x] = none ? 0u : pack_bf16x2(o[r][i + x][e] * half * by, o[r][i + x][2 + e] * half * by);
               *reinterpret_cast<uint4*>(p.out + at * p.D + run_d + 2 * i) = make_uint4(u[0], u[1], u[2], u[3]);
             }
           }
@@ -755,10 +755,11 @@ __global__ void __launch_bounds__(32 * WARPS) decode_join_kernel(const DecodePar
     const int r = row0 + row;
     const int64_t to = (static_cast<int64_t>(cut.b) * p.qn + r / p.group) * p.Hq + head + r % p.group;
     const bool none = sum == 0.f;
-    const float by = none ? 0.f : ex2(n) / sum;
+    const float half = ex2(0.5f * n), by = half / sum;
     if (4 * lane < p.D)
       *reinterpret_cast<uint2*>(p.out + to * p.D + d) =
-          none ? make_uint2(0, 0) : make_uint2(pack_bf16x2(o.x * by, o.y * by), pack_bf16x2(o.z * by, o.w * by));
+          none ? make_uint2(0, 0)
+               : make_uint2(pack_bf16x2(o.x * half * by, o.y * half * by), pack_bf16x2(o.z * half * by, o.w * half * by));
     if (lane == 0 && p.lse) p.lse[to] = none ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
   }
 }

@@ -96,6 +96,27 @@ def test_decode_scores_of_any_size(lens, hq, hk, d, qn, scale):
         _check_large(q[r], k, v, vis, np.float64(np.float32(scale)), go[r], gl[r], 11)
 
 
+# Values of a whole sequence near the ends of fp32's range: e4m3 codes at scales of 2^-127 .. 2^-110 and 2^112 .. 2^118.
+@pytest.mark.parametrize("low,high", [(0, 6), (6, 17), (239, 245)])
+@pytest.mark.parametrize("lens,hq,hk,d,qn", [([150, 33, 16], 4, 2, 64, 1), ([260, 40], 6, 2, 128, 3), ([90], 24, 1, 96, 1), ([6011], 2, 1, 128, 1)])
+def test_decode_values_at_the_ends_of_the_range(lens, hq, hk, d, qn, low, high):
+    def edit(table, codes, scales):
+        scales[1][:] = np.random.default_rng(3).integers(low, high, scales[1].shape)
+        codes[1][:] = ref.e4m3_round(np.random.default_rng(4).uniform(64, 400, codes[1].shape))   # one sign: sums do not cancel
+
+    _, args, host, out, lse = _decode(lens, hq, hk, d, 16, qn, 505, edit)
+    table, codes, scales = host
+    q, go = _f64(args[0]), _f64(out)
+    for b, n in enumerate(lens):
+        k, _ = ref.cached(codes[0], scales[0], table[b], hk, 16, n)
+        v, _ = ref.cached(codes[1], scales[1], table[b], hk, 16, n)
+        r = slice(b * qn, (b + 1) * qn)
+        o, _, mag, _ = ref.attend(q[r], k, v, np.array([n - (qn - 1 - i) for i in range(qn)]), d ** -0.5)
+        assert o.min() > 2.0 ** -126
+        # as out_tolerance, without its allowance of 1e-30
+        assert (np.abs(go[r] - o) <= 2.0 ** -8 * np.abs(o) + (2.0 ** -11 + 2.0 ** -13) * mag).all(), float((np.abs(go[r] - o) / o).max())
+
+
 @pytest.mark.parametrize("scale", [1e4, 1e6, 1e7, 1e8, 1e9, 1e12, 1e24])
 @pytest.mark.parametrize("n,m,hq,hk,d", [(140, 140, 4, 1, 64), (70, 200, 2, 2, 128), (140, 840, 4, 1, 128), (130, 130, 5, 1, 128)])
 def test_prompt_large_scores_are_right_or_nan(n, m, hq, hk, d, scale):
