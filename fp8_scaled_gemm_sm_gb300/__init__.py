@@ -11,7 +11,9 @@ the library is loaded by the first call.
 
 ``PagedAttention`` is the attention between two such GEMMs: rotary positions and
 append to a paged 8-bit key/value cache, attention of the newest tokens over it,
-and attention over whole prompts (``include/scaled_attention.h``).
+and attention over whole prompts (``include/scaled_attention.h``); ``PagePool`` shares
+the cache's pages out among sequences.  ``norm_quantize`` is the step before a GEMM: a residual's
+addition, root-mean-square norm and quantisation.
 """
 from .binding import MODES, ScaledGemm, ScaledGemmError  # noqa: F401
 
@@ -22,4 +24,12 @@ def __getattr__(name):
         from . import attention
 
         return getattr(attention, name)
+    if name == "PagePool":
+        from .pages import PagePool
+
+        return PagePool
+    if name == "norm_quantize":
+        from .norm import norm_quantize
+
+        return norm_quantize
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

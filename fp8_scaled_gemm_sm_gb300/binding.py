@@ -43,7 +43,15 @@ class RotaryArgs(ctypes.Structure):
     _fields_ = [("table", _vp), ("max_pos", _i64), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
+class PagePoolArgs(ctypes.Structure):
+    """sg_page_pool_t"""
+
+    _fields_ = [("table", _vp), ("lens", _vp), ("refs", _vp), ("rows", _i64), ("table_stride", _i64), ("num_pages", _i64),
+                ("scratch", _vp)]
+
+
 _cache_p = ctypes.POINTER(KvCacheArgs)
+_pool_p = ctypes.POINTER(PagePoolArgs)
 _rotary_p = ctypes.POINTER(RotaryArgs)
 SIGNATURES = {
     "scaled_gemm_create": (_int, [ctypes.POINTER(_vp), _int, _i64, _i64, _i64, _int]),
@@ -57,12 +65,18 @@ SIGNATURES = {
     "scaled_gemm_set_debug": (_int, [_vp, _i64, _i64]),
     "scaled_gemm_launch_noalloc": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp]),
     "scaled_gemm_quantize": (_int, [_int, _int, _vp, _i64, _i64, _vp, _vp, _vp]),
+    "scaled_gemm_norm_quantize": (_int, [_int, _int, _vp, _vp, _vp, _vp, ctypes.c_double, _i64, _i64, _vp, _vp, _vp]),
     "scaled_attn_create": (_int, [ctypes.POINTER(_vp), _i64, _i64, _i64, _i64, _int]),
     "scaled_attn_destroy": (_int, [_vp]),
     "scaled_attn_append": (_int, [_vp, _cache_p, _rotary_p, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64,
                                   _vp, _vp, _vp]),
     "scaled_attn_decode": (_int, [_vp, _cache_p, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _f32, _vp, _vp, _vp]),
     "scaled_attn_prompt": (_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _int, _f32, _vp, _vp, _vp]),
+    "scaled_attn_pool_scratch_bytes": (_i64, [_i64, _i64]),
+    "scaled_attn_pool_release": (_int, [_vp, _pool_p, _vp, _i64, _vp]),
+    "scaled_attn_pool_grow": (_int, [_vp, _pool_p, _vp, _vp, _i64, _vp, _vp]),
+    "scaled_attn_pool_fork": (_int, [_vp, _pool_p, _cache_p, _i64, _vp, _vp, _i64, _vp, _vp]),
+    "scaled_attn_pool_compact": (_int, [_vp, _pool_p, _cache_p, _i64, _vp, _vp]),
     "scaled_attn_set_debug": (_int, [_vp, _i64, _i64]),
     "scaled_attn_debug_status": (_int, [_vp, _vp, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]),
 }
@@ -167,6 +181,14 @@ def quantize(mode, x, stream=None):
     return q, s
 
 
+def scaled_gemm_norm_quantize(mode, x_dtype, X, residual, residual_out, weight, eps, R, C, Q, scale, stream=0):
+    """Residual addition, norm and quantisation of X [R, C] (device pointers; see the C header)."""
+    m = MODES[mode] if isinstance(mode, str) else int(mode)
+    dt = DTYPES[x_dtype] if isinstance(x_dtype, str) else int(x_dtype)
+    _check(lib().scaled_gemm_norm_quantize(m, dt, X, residual or None, residual_out or None, weight, float(eps), int(R), int(C), Q,
+                                           scale or None, stream or None), "scaled_gemm_norm_quantize")
+
+
 def scaled_gemm_destroy(h):
     _check(lib().scaled_gemm_destroy(h), "scaled_gemm_destroy")
 
@@ -217,6 +239,28 @@ def scaled_attn_decode(h, cache, q, q_stride, qn, table, table_stride, kv_lens, 
 def scaled_attn_prompt(h, q, q_stride, k, k_stride, v, v_stride, cu_q, cu_k, Tq, Tk, B, causal, scale, out, lse, stream=0):
     _check(lib().scaled_attn_prompt(h, q, q_stride, k, k_stride, v, v_stride, cu_q, cu_k, Tq, Tk, B, causal, scale, out, lse,
                                     stream), "scaled_attn_prompt")
+
+
+def scaled_attn_pool_scratch_bytes(rows, num_pages):
+    return lib().scaled_attn_pool_scratch_bytes(int(rows), int(num_pages))
+
+
+def scaled_attn_pool_release(h, pool, which, n, stream=0):
+    """Pages of a pool (see include/scaled_attention.h); pool is a PagePoolArgs."""
+    _check(lib().scaled_attn_pool_release(h, pool, which, n, stream), "scaled_attn_pool_release")
+
+
+def scaled_attn_pool_grow(h, pool, which, add, n, ok, stream=0):
+    _check(lib().scaled_attn_pool_grow(h, pool, which, add, n, ok, stream), "scaled_attn_pool_grow")
+
+
+def scaled_attn_pool_fork(h, pool, caches, layers, src, dst, n, ok, stream=0):
+    """caches: an array of `layers` KvCacheArgs."""
+    _check(lib().scaled_attn_pool_fork(h, pool, caches, layers, src, dst, n, ok, stream), "scaled_attn_pool_fork")
+
+
+def scaled_attn_pool_compact(h, pool, caches, layers, in_use, stream=0):
+    _check(lib().scaled_attn_pool_compact(h, pool, caches, layers, in_use, stream), "scaled_attn_pool_compact")
 
 
 def scaled_attn_set_debug(h, timeout_ns=0, skip_tile=-1):

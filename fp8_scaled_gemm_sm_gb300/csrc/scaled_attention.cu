@@ -66,6 +66,30 @@ sg_status_t check_device(const sg_attn* h) {
   return cur == h->device ? SG_OK : refuse(SG_ERR_INVALID_ARG, "attn: current device differs from the plan's");
 }
 
+sg_status_t check_pool(const sg_page_pool_t* p) {
+  if (!p) return refuse(SG_ERR_INVALID_ARG, "pool: NULL pool");
+  if (p->rows < 0 || p->table_stride < 0 || p->num_pages < 0) return refuse(SG_ERR_INVALID_ARG, "pool: negative size");
+  if (p->rows > kMaxDim || p->num_pages > kMaxDim || p->table_stride > kMaxDim || p->rows * p->table_stride > kMaxDim)
+    return refuse(SG_ERR_UNSUPPORTED_SHAPE, "pool: size >= 2^31");
+  if (!p->table || !p->lens || !p->refs || !p->scratch) return refuse(SG_ERR_INVALID_ARG, "pool: NULL pointer");
+  if (!aligned(p->table, 4) || !aligned(p->lens, 4) || !aligned(p->refs, 16) || !aligned(p->scratch, 16))
+    return refuse(SG_ERR_MISALIGNED, "pool: pointer");
+  return SG_OK;
+}
+
+// The caches of a pool's layers: each of the pool's pages, none of them twice.
+sg_status_t check_layers(const sg_attn* h, const sg_page_pool_t* pool, const sg_kv_cache_t* caches, int64_t layers) {
+  if (layers < 0) return refuse(SG_ERR_INVALID_ARG, "pool: negative number of layers");
+  if (layers > 65536) return refuse(SG_ERR_UNSUPPORTED_SHAPE, "pool: layers > 65536");
+  if (!caches && layers > 0) return refuse(SG_ERR_INVALID_ARG, "pool: NULL caches");
+  for (int64_t i = 0; i < layers; ++i) {
+    const sg_status_t r = check_cache(h, caches + i);
+    if (r != SG_OK) return r;
+    if (caches[i].num_pages < pool->num_pages) return refuse(SG_ERR_INVALID_ARG, "pool: a cache has fewer pages than the pool");
+  }
+  return SG_OK;
+}
+
 // The bytes that rows of a strided operand cover.
 int64_t row_bytes(int64_t rows, int64_t stride, int64_t width) {
   return rows > 0 ? 2 * ((rows - 1) * stride + width) : 0;
@@ -315,6 +339,64 @@ sg_status_t scaled_attn_prompt(sg_attn_t h, const void* q, int64_t q_stride, con
   a.stream = reinterpret_cast<cudaStream_t>(stream);
   const sg_status_t r = sg::prompt_launch(s, a);
   return r == SG_OK ? SG_OK : refuse(r, "prompt: kernel launch");
+}
+
+int64_t scaled_attn_pool_scratch_bytes(int64_t rows, int64_t num_pages) {
+  if (rows < 0 || num_pages < 0 || rows > kMaxDim || num_pages > kMaxDim) return 0;
+  return sg::pool_scratch_bytes(rows, num_pages);
+}
+
+sg_status_t scaled_attn_pool_release(sg_attn_t h, const sg_page_pool_t* pool, const int32_t* which, int64_t n,
+                                     sg_stream_t stream) {
+  if (!h) return refuse(SG_ERR_INVALID_ARG, "pool release: NULL handle");
+  SG_TRY(check_pool(pool));
+  if (n < 0) return refuse(SG_ERR_INVALID_ARG, "pool release: negative n");
+  if (n > kMaxDim) return refuse(SG_ERR_UNSUPPORTED_SHAPE, "pool release: n >= 2^31");
+  if (n == 0) return SG_OK;
+  SG_TRY(check_ints(which, "pool release: which"));
+  SG_TRY(check_device(h));
+  const sg_status_t r = sg::pool_release(h->shape, *pool, which, n, reinterpret_cast<cudaStream_t>(stream));
+  return r == SG_OK ? SG_OK : refuse(r, "pool release: kernel launch");
+}
+
+sg_status_t scaled_attn_pool_grow(sg_attn_t h, const sg_page_pool_t* pool, const int32_t* which, const int32_t* add,
+                                  int64_t n, int32_t* ok, sg_stream_t stream) {
+  if (!h) return refuse(SG_ERR_INVALID_ARG, "pool grow: NULL handle");
+  SG_TRY(check_pool(pool));
+  if (n < 0 || n > pool->rows) return refuse(SG_ERR_INVALID_ARG, "pool grow: n outside [0, rows]");
+  if (n == 0) return SG_OK;
+  SG_TRY(check_ints(which, "pool grow: which"));
+  SG_TRY(check_ints(add, "pool grow: add"));
+  SG_TRY(check_ints(ok, "pool grow: ok"));
+  SG_TRY(check_device(h));
+  const sg_status_t r = sg::pool_grow(h->shape, *pool, which, add, n, ok, reinterpret_cast<cudaStream_t>(stream));
+  return r == SG_OK ? SG_OK : refuse(r, "pool grow: kernel launch");
+}
+
+sg_status_t scaled_attn_pool_fork(sg_attn_t h, const sg_page_pool_t* pool, const sg_kv_cache_t* caches, int64_t layers,
+                                  const int32_t* src, const int32_t* dst, int64_t n, int32_t* ok, sg_stream_t stream) {
+  if (!h) return refuse(SG_ERR_INVALID_ARG, "pool fork: NULL handle");
+  SG_TRY(check_pool(pool));
+  SG_TRY(check_layers(h, pool, caches, layers));
+  if (n < 0 || n > pool->rows) return refuse(SG_ERR_INVALID_ARG, "pool fork: n outside [0, rows]");
+  if (n == 0) return SG_OK;
+  SG_TRY(check_ints(src, "pool fork: src"));
+  SG_TRY(check_ints(dst, "pool fork: dst"));
+  SG_TRY(check_ints(ok, "pool fork: ok"));
+  SG_TRY(check_device(h));
+  const sg_status_t r = sg::pool_fork(h->shape, *pool, caches, layers, src, dst, n, ok, reinterpret_cast<cudaStream_t>(stream));
+  return r == SG_OK ? SG_OK : refuse(r, "pool fork: kernel launch");
+}
+
+sg_status_t scaled_attn_pool_compact(sg_attn_t h, const sg_page_pool_t* pool, const sg_kv_cache_t* caches, int64_t layers,
+                                     int32_t* in_use, sg_stream_t stream) {
+  if (!h) return refuse(SG_ERR_INVALID_ARG, "pool compact: NULL handle");
+  SG_TRY(check_pool(pool));
+  SG_TRY(check_layers(h, pool, caches, layers));
+  SG_TRY(check_ints(in_use, "pool compact: in_use"));
+  SG_TRY(check_device(h));
+  const sg_status_t r = sg::pool_compact(h->shape, *pool, caches, layers, in_use, reinterpret_cast<cudaStream_t>(stream));
+  return r == SG_OK ? SG_OK : refuse(r, "pool compact: kernel launch");
 }
 
 }  // extern "C"

@@ -410,4 +410,44 @@ sg_status_t scaled_gemm_quantize(int mode, int x_dtype, const void* X, int64_t R
   return r == SG_OK ? SG_OK : fail(r, "quantize: kernel launch");
 }
 
+sg_status_t scaled_gemm_norm_quantize(int mode, int x_dtype, const void* X, const void* residual, void* residual_out,
+                                      const void* weight, double eps, int64_t R, int64_t C, void* Q, void* scale,
+                                      sg_stream_t stream) {
+  if (mode < SG_MODE_BF16 || mode > SG_MODE_MXFP8) return fail(SG_ERR_INVALID_ARG, "norm_quantize: bad mode");
+  if (x_dtype != SG_DTYPE_BF16 && x_dtype != SG_DTYPE_F32) return fail(SG_ERR_INVALID_ARG, "norm_quantize: bad x_dtype");
+  if (R < 0 || C < 0) return fail(SG_ERR_INVALID_ARG, "norm_quantize: negative size");
+  if (!(eps >= 0x1p-60 && eps <= 0x1p60)) return fail(SG_ERR_INVALID_ARG, "norm_quantize: eps outside [2^-60, 2^60]");
+  if (R > kMaxDim || C > sg::quantize_max_cols()) return fail(SG_ERR_UNSUPPORTED_SHAPE, "norm_quantize: R >= 2^31 or C > 32768");
+  if (C % k_multiple(mode) != 0) return fail(SG_ERR_UNSUPPORTED_SHAPE, "norm_quantize: C not a multiple of the mode's block");
+  if (R == 0 || C == 0) return SG_OK;
+  if (!X || !weight || !Q || (mode != SG_MODE_BF16 && !scale) || (residual && !residual_out))
+    return fail(SG_ERR_INVALID_ARG, "norm_quantize: NULL pointer");
+  const void* const all[] = {X, residual, residual ? residual_out : nullptr, weight, Q, mode != SG_MODE_BF16 ? scale : nullptr};
+  for (const void* p : all)
+    if (!aligned16(p)) return fail(SG_ERR_MISALIGNED, "norm_quantize: pointer");
+  // residual_out may be X or the residual (each element is read before it is written, by the thread
+  // that writes it), and so may a bf16 output be a bf16 X; any other overlap with an output is refused.
+  const int64_t n = R * C, size = x_dtype == SG_DTYPE_BF16 ? 2 : 4;
+  const struct { const void* p; int64_t bytes; bool self; } in[] = {{X, n * size, true}, {residual, n * size, true}, {weight, C * size, false}};
+  const struct { const void* p; int64_t bytes; bool whole; } outs[] = {
+      {residual ? residual_out : nullptr, n * size, true},
+      {Q, mode == SG_MODE_BF16 ? 2 * n : n, mode == SG_MODE_BF16 && x_dtype == SG_DTYPE_BF16},
+      {mode != SG_MODE_BF16 ? scale : nullptr, sg::scale_bytes_a(mode, R, C), false}};
+  for (int o = 0; o < 3; ++o) {
+    for (const auto& i : in)
+      if (!(i.self && outs[o].whole && outs[o].p == i.p) && sg::ranges_overlap(outs[o].p, outs[o].bytes, i.p, i.bytes))
+        return fail(SG_ERR_INVALID_ARG, "norm_quantize: an output overlaps an input");
+    for (int other = 0; other < o; ++other)
+      if (sg::ranges_overlap(outs[o].p, outs[o].bytes, outs[other].p, outs[other].bytes))
+        return fail(SG_ERR_INVALID_ARG, "norm_quantize: outputs overlap");
+  }
+  int dev = -1, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return fail(SG_ERR_CUDA, "norm_quantize: device query");
+  const sg_status_t r = sg::norm_launch(mode, x_dtype == SG_DTYPE_BF16, X, residual, residual_out, weight, eps, R, C, Q, scale,
+                                        sms, reinterpret_cast<cudaStream_t>(stream));
+  return r == SG_OK ? SG_OK : fail(r, "norm_quantize: kernel launch");
+}
+
 }  // extern "C"

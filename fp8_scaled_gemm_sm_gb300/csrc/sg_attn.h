@@ -42,6 +42,15 @@ struct AttnArgs {
 
 sg_status_t append_launch(const AttnShape& s, const AttnArgs& a);
 
+int64_t pool_scratch_bytes(int64_t rows, int64_t num_pages);
+sg_status_t pool_release(const AttnShape& s, const sg_page_pool_t& pool, const int32_t* rows, int64_t n, cudaStream_t stream);
+sg_status_t pool_grow(const AttnShape& s, const sg_page_pool_t& pool, const int32_t* rows, const int32_t* add, int64_t n, int32_t* ok,
+                      cudaStream_t stream);
+sg_status_t pool_fork(const AttnShape& s, const sg_page_pool_t& pool, const sg_kv_cache_t* caches, int64_t layers, const int32_t* src,
+                      const int32_t* dst, int64_t n, int32_t* ok, cudaStream_t stream);
+sg_status_t pool_compact(const AttnShape& s, const sg_page_pool_t& pool, const sg_kv_cache_t* caches, int64_t layers, int32_t* in_use,
+                         cudaStream_t stream);
+
 size_t decode_workspace_bytes(const AttnShape& s);
 cudaError_t decode_prepare();
 sg_status_t decode_launch(const AttnShape& s, const AttnArgs& a);

@@ -1,6 +1,6 @@
 // sg_attn_ptx.cuh -- inline-PTX building blocks of the attention kernels beside
 // those of sg_ptx.cuh: MMAs with an operand in tensor memory, tensor memory
-// stores, 3D tiled loads, packed fp32 sums and exponentials.
+// stores, 3D tiled loads and exponentials.
 #pragma once
 
 #include <cstdint>
@@ -40,13 +40,6 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-// d = a + b, element-wise on two fp32 lanes, round to nearest even.
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 

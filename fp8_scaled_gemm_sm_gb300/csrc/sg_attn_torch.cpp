@@ -1,5 +1,5 @@
-// sg_attn_torch.cpp -- the calls of attention.py on torch tensors, in one step each:
-// checks, outputs, the C ABI (include/scaled_attention.h).
+// sg_attn_torch.cpp -- the calls of attention.py, pages.py and norm.py on torch tensors, in one step each:
+// checks, outputs, the C ABI (include/scaled_attention.h, include/scaled_gemm.h).
 //
 // A decode step of a small batch runs in 5 to 10 us on the GPU; the same marshalling in Python
 // took 12 to 20 us a call, most of it for outputs, the stream and the checks.  Nothing is
@@ -13,6 +13,7 @@
 #include <cstring>
 #include <exception>
 #include <string>
+#include <vector>
 
 #include "scaled_attention.h"
 
@@ -33,6 +34,14 @@ struct Cache {
   int device;
 };
 
+struct Pool {
+  sg_page_pool_t args;
+  std::vector<sg_kv_cache_t> layers;
+  int64_t heads, page, dim;
+  int device;
+};
+
+constexpr const char* kPool = "sg_attn pool";
 constexpr const char* kPlan = "sg_attn plan";
 constexpr const char* kCache = "sg_attn cache";
 
@@ -112,32 +121,36 @@ struct Streams {
   bool side;
 };
 
-Streams streams(PyObject* o, const Plan& p) {
-  const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(p.device));
+Streams streams(PyObject* o, int device) {
+  const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device));
   const sg_stream_t now = current.stream();
   if (o == Py_None) return {now, current, false};
   const auto s = static_cast<sg_stream_t>(PyLong_AsVoidPtr(o));
   if (PyErr_Occurred()) throw BadArgument{"stream"};
   return {s, current, s != now};
 }
+Streams streams(PyObject* o, const Plan& p) { return streams(o, p.device); }
 
 // An output that the caller has, or a new one.  On a stream of the caller's choice a new one is that stream's memory, so
 // whoever used it before or gets it next is ordered there; and it is recorded on the current stream, where results are
 // read as a rule, so that dropping it does not give it away before the reads so far.
-at::Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const Plan& p, const Streams& s, const char* what) {
+at::Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, int device, const Streams& s, const char* what) {
   if (o == Py_None) {
-    const auto options = at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(p.device)));
+    const auto options = at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(device)));
     if (!s.side) return at::empty(shape, options);
     const c10::cuda::CUDAStreamGuard guard(
-        c10::cuda::getStreamFromExternal(s.handle, static_cast<c10::DeviceIndex>(p.device)));
+        c10::cuda::getStreamFromExternal(s.handle, static_cast<c10::DeviceIndex>(device)));
     const at::Tensor t = at::empty(shape, options);
     t.record_stream(s.current.unwrap());
     return t;
   }
   const at::Tensor& t = tensor(o, what);
-  if (t.sizes() != shape || t.scalar_type() != type || !on(t, p.device) || !t.is_contiguous())
+  if (t.sizes() != shape || t.scalar_type() != type || !on(t, device) || !t.is_contiguous())
     throw BadArgument{std::string(what) + " must be a contiguous tensor of the result's shape and type on the plan's device"};
   return t;
+}
+at::Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const Plan& p, const Streams& s, const char* what) {
+  return output(o, shape, type, p.device, s, what);
 }
 
 const Plan& plan(PyObject* o) {
@@ -298,13 +311,159 @@ PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// pool(plan, table, lens, refs, scratch, caches): sizes and devices were checked in pages.py
+PyObject* make_pool(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 6);
+    const Plan& p = plan(a[0]);
+    const at::Tensor &t = tensor(a[1], "table"), &lens = tensor(a[2], "lens"), &refs = tensor(a[3], "refs"), &scratch = tensor(a[4], "scratch");
+    std::vector<sg_kv_cache_t> layers;
+    for (Py_ssize_t i = 0; i < PyList_Size(a[5]); ++i) layers.push_back(*cache(PyList_GetItem(a[5], i), p));
+    if (PyErr_Occurred()) throw BadArgument{"caches"};
+    auto* pool = new Pool{{static_cast<int32_t*>(t.data_ptr()), static_cast<int32_t*>(lens.data_ptr()), static_cast<int32_t*>(refs.data_ptr()),
+                           t.size(0), t.size(1), refs.size(0), scratch.data_ptr()},
+                          std::move(layers), p.kv_heads, p.page, p.dim, p.device};
+    return PyCapsule_New(pool, kPool, free_capsule<Pool>);
+  });
+}
+
+const Pool& pool(PyObject* o, const Plan& p) {
+  auto* x = static_cast<Pool*>(PyCapsule_GetPointer(o, kPool));
+  if (!x) throw BadArgument{"not a pool"};
+  return *x;
+}
+
+PyObject* wrapped(const at::Tensor& t) { return THPVariable_Wrap(t); }
+
+// pool_release(plan, pool, rows, stream)
+PyObject* pool_release(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 4);
+    const Plan& p = plan(a[0]);
+    const Pool& x = pool(a[1], p);
+    const int64_t count = length(a[2], "rows");
+    const int32_t* rows = ints(a[2], count, p, "rows");
+    const Streams s = streams(a[3], p);
+    check(scaled_attn_pool_release(p.handle, &x.args, rows, count, s.handle), "scaled_attn_pool_release");
+    Py_RETURN_NONE;
+  });
+}
+
+// pool_grow(plan, pool, rows, add, ok, stream)
+PyObject* pool_grow(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 6);
+    const Plan& p = plan(a[0]);
+    const Pool& x = pool(a[1], p);
+    const int64_t count = length(a[2], "rows");
+    const int32_t *rows = ints(a[2], count, p, "rows"), *add = ints(a[3], count, p, "tokens");
+    const Streams s = streams(a[5], p);
+    const at::Tensor ok = output(a[4], {count}, at::kInt, p, s, "ok");
+    check(scaled_attn_pool_grow(p.handle, &x.args, rows, add, count, static_cast<int32_t*>(ok.data_ptr()), s.handle),
+          "scaled_attn_pool_grow");
+    return wrapped(ok);
+  });
+}
+
+// pool_fork(plan, pool, src, dst, ok, stream)
+PyObject* pool_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 6);
+    const Plan& p = plan(a[0]);
+    const Pool& x = pool(a[1], p);
+    const int64_t count = length(a[2], "src");
+    const int32_t *src = ints(a[2], count, p, "src"), *dst = ints(a[3], count, p, "dst");
+    const Streams s = streams(a[5], p);
+    const at::Tensor ok = output(a[4], {count}, at::kInt, p, s, "ok");
+    check(scaled_attn_pool_fork(p.handle, &x.args, x.layers.data(), static_cast<int64_t>(x.layers.size()), src, dst, count,
+                                static_cast<int32_t*>(ok.data_ptr()), s.handle),
+          "scaled_attn_pool_fork");
+    return wrapped(ok);
+  });
+}
+
+// pool_compact(plan, pool, in_use, stream)
+PyObject* pool_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 4);
+    const Plan& p = plan(a[0]);
+    const Pool& x = pool(a[1], p);
+    const Streams s = streams(a[3], p);
+    const at::Tensor in_use = output(a[2], {1}, at::kInt, p, s, "in_use");
+    check(scaled_attn_pool_compact(p.handle, &x.args, x.layers.data(), static_cast<int64_t>(x.layers.size()),
+                                   static_cast<int32_t*>(in_use.data_ptr()), s.handle),
+          "scaled_attn_pool_compact");
+    return wrapped(in_use);
+  });
+}
+
+// norm_quantize(mode, x, weight, eps, residual, residual_out, stream)
+PyObject* norm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 7);
+    const int64_t mode = number(a[0]);
+    const at::Tensor& x = tensor(a[1], "x");
+    if (x.dim() != 2 || (x.scalar_type() != at::kBFloat16 && x.scalar_type() != at::kFloat) || !x.is_cuda() || !x.is_contiguous())
+      throw BadArgument{"x must be a contiguous 2-D bfloat16 or float32 CUDA tensor"};
+    const int64_t R = x.size(0), C = x.size(1);
+    const int device = x.device().index();
+    auto same = [&](PyObject* o, at::IntArrayRef shape, const char* what) -> const at::Tensor& {
+      const at::Tensor& t = tensor(o, what);
+      if (t.sizes() != shape || t.scalar_type() != x.scalar_type() || !on(t, device) || !t.is_contiguous())
+        throw BadArgument{std::string(what) + " must be contiguous, of x's type, on its device, and as long as its rows (weight) or of its shape"};
+      return t;
+    };
+    const at::Tensor& weight = same(a[2], {C}, "weight");
+    const double eps = PyFloat_AsDouble(a[3]);
+    if (eps == -1.0 && PyErr_Occurred()) throw BadArgument{"eps"};
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
+    const Streams s = streams(a[6], device);
+    at::Tensor kept = x;
+    const void* residual = nullptr;
+    if (a[4] != Py_None) {
+      residual = same(a[4], {R, C}, "residual").data_ptr();
+      kept = output(a[5], {R, C}, x.scalar_type(), device, s, "residual_out");
+    } else if (a[5] != Py_None) {
+      throw BadArgument{"residual_out without a residual"};
+    }
+    const at::Tensor q = output(Py_None, {R, C}, mode == SG_MODE_BF16 ? at::kBFloat16 : at::kByte, device, s, "codes");
+    at::Tensor scale;
+    if (mode == SG_MODE_PTPC) scale = output(Py_None, {R}, at::kFloat, device, s, "scale");
+    if (mode == SG_MODE_BLOCKSCALE) scale = output(Py_None, {C / 128, R}, at::kFloat, device, s, "scale");
+    if (mode == SG_MODE_MXFP8) scale = output(Py_None, {C / 32, R}, at::kByte, device, s, "scale");
+    check(scaled_gemm_norm_quantize(static_cast<int>(mode), x.scalar_type() == at::kFloat ? SG_DTYPE_F32 : SG_DTYPE_BF16, x.data_ptr(), residual,
+                                    residual ? kept.data_ptr() : nullptr, weight.data_ptr(), eps, R, C, q.data_ptr(),
+                                    scale.defined() ? scale.data_ptr() : nullptr, s.handle),
+          "scaled_gemm_norm_quantize");
+    PyObject* second = Py_None;
+    if (scale.defined())
+      second = THPVariable_Wrap(scale);
+    else
+      Py_INCREF(second);
+    PyObject *first = THPVariable_Wrap(q), *third = THPVariable_Wrap(kept);
+    PyObject* t = first && second && third ? PyTuple_Pack(3, first, second, third) : nullptr;
+    Py_XDECREF(first);
+    Py_XDECREF(second);
+    Py_XDECREF(third);
+    return t;
+  });
+}
+
+#define SG_METHOD(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
+
 PyMethodDef g_methods[] = {
     {"set_error", set_error, METH_O, nullptr},
-    {"plan", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(make_plan)), METH_FASTCALL, nullptr},
-    {"cache", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(make_cache)), METH_FASTCALL, nullptr},
-    {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append)), METH_FASTCALL, nullptr},
-    {"decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode)), METH_FASTCALL, nullptr},
-    {"prompt", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prompt)), METH_FASTCALL, nullptr},
+    SG_METHOD("plan", make_plan),
+    SG_METHOD("cache", make_cache),
+    SG_METHOD("append", append),
+    SG_METHOD("decode", decode),
+    SG_METHOD("prompt", prompt),
+    SG_METHOD("pool", make_pool),
+    SG_METHOD("pool_release", pool_release),
+    SG_METHOD("pool_grow", pool_grow),
+    SG_METHOD("pool_fork", pool_fork),
+    SG_METHOD("pool_compact", pool_compact),
+    SG_METHOD("norm_quantize", norm_quantize),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_attn", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

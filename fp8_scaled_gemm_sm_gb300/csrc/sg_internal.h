@@ -127,6 +127,9 @@ int64_t quantize_max_cols();
 sg_status_t quantize_launch(int mode, bool bf16, const void* X, int64_t R, int64_t C, void* Q,
                             void* scale, int num_sms, cudaStream_t st);
 
+sg_status_t norm_launch(int mode, bool bf16, const void* x, const void* residual, void* residual_out, const void* weight,
+                        double eps, int64_t R, int64_t C, void* out, void* scale, int num_sms, cudaStream_t st);
+
 cudaError_t dense_prepare(int mode);
 sg_status_t dense_launch(const LaunchArgs& a);
 sg_status_t dense_launch_gather(const LaunchArgs& a);  // ptpc, A rows gathered by a.gather_idx

@@ -11,6 +11,8 @@
  *   scaled_attn_decode   attention of each sequence's newest tokens over the cache
  *   scaled_attn_prompt   attention over whole prompts, packed one after another
  *
+ * and scaled_attn_pool_* share the cache's pages out among sequences: release, grow, fork, compact.
+ *
  * Layouts (device pointers, owned by the caller, never retained after the call
  * returns; 16-byte aligned unless stated):
  *   q, k, v      bf16 [rows][heads][D]: heads D apart and rows `*_stride` elements apart
@@ -125,6 +127,48 @@ sg_status_t scaled_attn_prompt(sg_attn_t h, const void* q, int64_t q_stride, con
                                const void* v, int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k,
                                int64_t Tq, int64_t Tk, int64_t B, int causal, float scale, void* out,
                                float* lse, sg_stream_t stream);
+
+/* The pages of a cache and the sequences that hold them, all in device memory.  The caches of a
+ * model's layers share one pool: a page number means that page of each. */
+typedef struct sg_page_pool {
+  int32_t* table;  /* [rows][table_stride]: the pages of each row's tokens in order, -1 past the last (4-byte aligned) */
+  int32_t* lens;   /* [rows]: tokens of each row; a negative one counts as 0 (4-byte aligned) */
+  int32_t* refs;   /* [num_pages]: table entries that name the page; free at 0 (16-byte aligned) */
+  int64_t rows, table_stride, num_pages;
+  void* scratch;   /* scaled_attn_pool_scratch_bytes(rows, num_pages) bytes, 16-byte aligned */
+} sg_page_pool_t;
+
+/* Pool calls change table, lens and refs, so calls on a pool (or on a scratch) must be ordered, as must attention over
+ * rows that they change.  Requests are served in their order and pages taken lowest first: results do not depend on timing.
+ * Entries outside [0, num_pages) name no page.  Row numbers outside [0, rows) name no row.  Where a call names a
+ * row twice to be changed, the first request has it and the others are refused (release: it is released).  ok[i] (int32) is 1
+ * where request i was carried out, 0 where it was refused, which leaves its row as it was.  Once the free
+ * pages do not suffice for a request, later ones that need any are refused too.  rows, num_pages < 2^31; rows * table_stride < 2^31;
+ * n <= rows but for release. */
+
+/* Bytes of a pool's scratch; 0 for sizes that no pool has. */
+int64_t scaled_attn_pool_scratch_bytes(int64_t rows, int64_t num_pages);
+
+/* Rows which[0 .. n) give their pages back: entries -1, length 0. */
+sg_status_t scaled_attn_pool_release(sg_attn_t h, const sg_page_pool_t* pool, const int32_t* which, int64_t n,
+                                     sg_stream_t stream);
+
+/* Row which[i] gets the pages for add[i] >= 0 more tokens, and its length grows by them; refused where the
+ * row's entries or the free pages do not suffice. */
+sg_status_t scaled_attn_pool_grow(sg_attn_t h, const sg_page_pool_t* pool, const int32_t* which, const int32_t* add,
+                                  int64_t n, int32_t* ok, sg_stream_t stream);
+
+/* Row dst[i], which is empty (length 0), becomes a copy of row src[i] as it was before the call: pages that
+ * src's tokens fill are shared, and of a last page that they do not fill, dst gets a copy in each of the
+ * `layers` caches.  What src or dst append after that, the other does not see.  Refused where dst is not empty or
+ * there is no page for the copy.  A src of length 0 leaves dst empty. */
+sg_status_t scaled_attn_pool_fork(sg_attn_t h, const sg_page_pool_t* pool, const sg_kv_cache_t* caches, int64_t layers,
+                                  const int32_t* src, const int32_t* dst, int64_t n, int32_t* ok, sg_stream_t stream);
+
+/* The pages in use move to the numbers [0, *in_use), each by the table and in all caches: those past it, in order, to
+ * the free ones below it, in order.  in_use: int32, device memory. */
+sg_status_t scaled_attn_pool_compact(sg_attn_t h, const sg_page_pool_t* pool, const sg_kv_cache_t* caches, int64_t layers,
+                                     int32_t* in_use, sg_stream_t stream);
 
 /* Synchronise `stream` and report (and clear) the plan's status word, as
  * scaled_gemm_debug_status does. */

@@ -215,6 +215,22 @@ typedef enum { SG_DTYPE_BF16 = 0, SG_DTYPE_F32 = 1 } sg_dtype_t;
 sg_status_t scaled_gemm_quantize(int mode, int x_dtype, const void* X, int64_t R, int64_t C, void* Q,
                                  void* scale, sg_stream_t stream);
 
+/* A residual's addition, root-mean-square norm and quantisation in one step, for X [R][C]
+ * (row-major, x_dtype) before a GEMM of `mode`:
+ *   r = x_dtype(X + residual), kept in residual_out   (residual NULL: r = X, nothing is kept)
+ *   y = (r * g) * weight,  g = 1 / sqrt(mean of r^2 over the row + eps)
+ * and Q, scale hold y as scaled_gemm_quantize would hold a y given to it in fp32; in
+ * SG_MODE_BF16 Q is bf16 [R][C], y rounded once, and scale is not looked at.
+ * residual, residual_out and weight [C] are of x_dtype.  Sums and products are in fp32: g is the fp32
+ * number nearest to its value but for about one row in 2^16, where it is the next, and the two products of y
+ * are rounded one after the other.  Finite values; 2^-60 <= eps <= 2^60.  Shape rules of scaled_gemm_quantize
+ * (SG_MODE_BF16: C % 8 == 0); pointers 16-byte aligned, device memory, caller-owned.  residual_out may be X or
+ * residual, and Q may be X where both are bf16; no other output may overlap an input or
+ * another output (checked: SG_ERR_INVALID_ARG).  Asynchronous on `stream`, which is of the current device. */
+sg_status_t scaled_gemm_norm_quantize(int mode, int x_dtype, const void* X, const void* residual, void* residual_out,
+                                      const void* weight, double eps, int64_t R, int64_t C, void* Q, void* scale,
+                                      sg_stream_t stream);
+
 /* ptpc GEMM for callers that cannot allocate device memory.  (The paper has no
  * counterpart: this entry point belongs to this library's interface only.)
  *

@@ -1,0 +1,162 @@
+"""The norm before a GEMM (scaled_gemm_norm_quantize) against 64-bit arithmetic and the CPU oracle's quantiser.
+
+The header states each fp32 step: the kept sum, the nearest fp32 number to the inverse root, two products.
+So y is formed here by the same steps from a 64-bit root, and codes and scales have to match
+bit for bit; a row may have the root's neighbour instead (about one in 2^16 does)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+MODES = ["bf16", "ptpc", "blockscale", "mxfp8"]
+
+
+@pytest.fixture(scope="module")
+def norm():
+    if not torch.cuda.is_available():
+        pytest.fail("a GPU test ran without a GPU")
+    import gpu_util
+
+    gpu_util.lib_ready()
+    from fp8_scaled_gemm_sm_gb300 import norm_quantize
+
+    return norm_quantize
+
+
+def _make(R, C, seed, dtype):
+    g = torch.Generator("cpu").manual_seed(seed)
+    x = torch.randn(R, C, generator=g) * torch.exp2(torch.randint(-12, 12, (R, 1), generator=g).float())
+    r = torch.randn(R, C, generator=g) * torch.exp2(torch.randint(-3, 6, (1, C), generator=g).float())
+    w = 1 + 0.5 * torch.randn(C, generator=g)
+    if R > 4:
+        x[1], r[1] = 0.0, 0.0               # y is zero
+        x[2] *= 1e-12                       # eps decides
+        r[2] = 0.0
+        x[3, 3 % C] = 2.0 ** 60             # one value outweighs the rest
+        x[4] *= 2.0 ** 80                   # squares past fp32's largest
+    return x.to(dtype), r.to(dtype), w.to(dtype)
+
+
+def _expect(mode, kept, w, eps, root):
+    y = (kept * root[:, None]).astype(np.float32) * w[None, :]
+    assert y.dtype == np.float32
+    if mode == "bf16":
+        return torch.from_numpy(y).bfloat16().view(torch.int16).numpy(), None
+    return oracle.quantize(mode, y)
+
+
+def _check(mode, x, r, w, eps, got):
+    codes, scale, kept = (None if t is None else t.cpu() for t in got)
+    total = x if r is None else (x.float() + r.float()).to(x.dtype)
+    assert torch.equal(kept.view(torch.int16 if x.dtype == torch.bfloat16 else torch.int32),
+                       total.view(torch.int16 if x.dtype == torch.bfloat16 else torch.int32))
+    t = total.float().numpy()
+    root = (1.0 / np.sqrt((t.astype(np.float64) ** 2).mean(1) + eps)).astype(np.float32)
+    have = codes.view(torch.int16).numpy() if mode == "bf16" else codes.numpy()
+    per_row = (lambda s: s) if mode in ("ptpc", "bf16") else (lambda s: s.T)
+
+    def wrong(root):
+        q, s = _expect(mode, t, w.float().numpy(), eps, root)
+        bad = (have != q).any(1)
+        if s is not None:
+            differ = per_row(scale.numpy()).reshape(len(t), -1) != per_row(s).reshape(len(t), -1)
+            bad |= differ.any(1)
+        return bad
+
+    bad = wrong(root)
+    near = [wrong(np.nextafter(root, np.float32(to))) for to in (np.inf, 0)]
+    assert not (bad & near[0] & near[1]).any(), np.flatnonzero(bad & near[0] & near[1])[:5]
+    assert bad.sum() <= 2, bad.sum()
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("R,C", [(1, 128), (7, 1792), (301, 2048), (40, 7168), (9, 8320), (5, 16512), (3, 32768), (1400, 256)])
+def test_steps(norm, mode, dtype, R, C):
+    x, r, w = _make(R, C, R + C, dtype)
+    got = norm(mode, x.cuda(), w.cuda(), 1e-6, residual=r.cuda())
+    _check(mode, x, r, w, 1e-6, got)
+
+
+@pytest.mark.parametrize("mode,C", [("bf16", 8), ("bf16", 200), ("ptpc", 16), ("ptpc", 2064), ("mxfp8", 32), ("mxfp8", 2080), ("bf16", 2056)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_odd_widths_without_residual(norm, mode, C, dtype):
+    x, _, w = _make(6, C, C, dtype)
+    dx = x.cuda()
+    codes, scale, kept = norm(mode, dx, w.cuda(), 0.5)
+    assert kept.data_ptr() == dx.data_ptr()
+    _check(mode, x, None, w, 0.5, (codes, scale, kept))
+
+
+def test_in_place(norm):
+    x, r, w = _make(33, 2048, 3, torch.bfloat16)
+    want = norm("ptpc", x.cuda(), w.cuda(), residual=r.cuda())
+    for target in (0, 1):
+        dev = [x.cuda(), r.cuda()]
+        got = norm("ptpc", dev[0], w.cuda(), residual=dev[1], residual_out=dev[target])
+        assert got[2].data_ptr() == dev[target].data_ptr()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_bf16_over_its_input(norm):
+    from fp8_scaled_gemm_sm_gb300 import binding
+
+    x, r, w = (t.cuda() for t in _make(20, 1024, 4, torch.bfloat16))
+    want = norm("bf16", x, w, residual=r)[0]
+    kept = torch.empty_like(x)
+    binding.scaled_gemm_norm_quantize("bf16", "bf16", x.data_ptr(), r.data_ptr(), kept.data_ptr(), w.data_ptr(), 1e-6, 20, 1024, x.data_ptr(), 0,
+                                      torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(x, want)
+
+
+def test_the_quantiser_gives_the_same_codes(norm):
+    """What the norm quantises is what binding.quantize makes of the same y in fp32."""
+    from fp8_scaled_gemm_sm_gb300 import binding
+
+    x, r, w = (t.cuda() for t in _make(50, 1024, 5, torch.float32))
+    kept = norm("bf16", x, w, residual=r)[2]
+    root = (1.0 / (kept.double().square().mean(1, keepdim=True) + 1e-6).sqrt()).float()
+    for mode in MODES[1:]:
+        q, s = binding.quantize(mode, kept * root * w)
+        codes, scale, _ = norm(mode, x, w, residual=r)
+        assert (codes != q).any(1).sum() <= 1 and torch.equal(scale.view(torch.uint8), s.view(torch.uint8))
+
+
+def test_graph_and_stream(norm):
+    x, r, w = (t.cuda() for t in _make(17, 7168, 6, torch.bfloat16))
+    want = norm("mxfp8", x, w, residual=r)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = norm("mxfp8", x, w, residual=r)
+    for t in got:
+        t.zero_()
+    graph.replay()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = norm("mxfp8", x, w, residual=r, stream=side.cuda_stream)
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_tensor_refusals(norm):
+    from fp8_scaled_gemm_sm_gb300 import ScaledGemmError
+
+    x, r, w = (t.cuda() for t in _make(4, 256, 7, torch.bfloat16))
+    for bad in (dict(x=x.cpu()), dict(x=x.half()), dict(x=x[:, ::2]), dict(x=x[0]), dict(weight=w[:-8]), dict(weight=w.float()),
+                dict(residual=r[:2]), dict(residual=r.float()), dict(residual=None, residual_out=r), dict(residual_out=r[:2]), dict(mode="fp4")):
+        a = dict(dict(mode="ptpc", x=x, weight=w, residual=r), **bad)
+        with pytest.raises((ValueError, TypeError)):
+            norm(**a)
+    for eps in (0.0, -1.0, float("nan"), float("inf")):
+        with pytest.raises(ScaledGemmError):
+            norm("ptpc", x, w, eps)
+    with pytest.raises(ScaledGemmError):
+        norm("blockscale", x[:, :144].contiguous(), w[:144].contiguous())
+    assert norm("ptpc", x[:0], w)[0].shape == (0, 256)
