@@ -109,7 +109,7 @@ class PagedAttention:
     be ready on `stream` and to live until that has used it: ``wait_stream`` and
     ``record_stream`` are the caller's.
 
-    A plan owns a workspace that ``decode`` uses, so decodes on one plan have to be ordered
+    A plan owns a workspace that ``decode`` and ``chunk`` use, so those calls on one plan have to be ordered
     (one stream, ordered streams, or a plan a stream); ``append`` and ``prompt`` may
     overlap with anything that leaves their buffers alone.  Nothing here has a backward
     pass: results carry no gradient, whatever the inputs do.  Output rows past
@@ -131,7 +131,7 @@ class PagedAttention:
         ext = _ext()
         self.handle = binding.scaled_attn_create(q_heads, kv_heads, dim, page_size, dev)
         self._p = ext.plan(self.handle, self.q_heads, self.kv_heads, self.dim, self.page_size, dev, *rot)
-        self._append, self._decode, self._prompt = ext.append, ext.decode, ext.prompt
+        self._append, self._decode, self._chunk, self._prompt = ext.append, ext.decode, ext.chunk, ext.prompt
 
     def new_cache(self, num_pages):
         return KVCache.new(num_pages, self.kv_heads, self.page_size, self.dim, self.device)
@@ -148,6 +148,12 @@ class PagedAttention:
         """Attention of each sequence's newest q_tokens tokens (q [B * q_tokens, Hq, dim]) over its
         first kv_lens [B] tokens in the cache, themselves included.  Returns (out, lse)."""
         return self._decode(self._p, q, cache._c, block_table, kv_lens, q_tokens, scale, out, lse, stream)
+
+    def chunk(self, q, cache, block_table, kv_lens, cu_q, scale=None, out=None, lse=None, stream=None):
+        """Attention of chunks of new tokens over the cache, as many for each sequence as there are: rows cu_q[b] .. cu_q[b + 1]
+        of q are sequence b's newest tokens, over its first kv_lens [B] tokens in the cache, themselves
+        included (causal).  Returns (out, lse)."""
+        return self._chunk(self._p, q, cache._c, block_table, kv_lens, cu_q, scale, out, lse, stream)
 
     def prompt(self, q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None, lse=None, stream=None):
         """Attention within each of the packed sequences: queries cu_q[b] .. cu_q[b + 1] over keys

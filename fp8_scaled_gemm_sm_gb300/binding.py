@@ -71,6 +71,7 @@ SIGNATURES = {
     "scaled_attn_append": (_int, [_vp, _cache_p, _rotary_p, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64,
                                   _vp, _vp, _vp]),
     "scaled_attn_decode": (_int, [_vp, _cache_p, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _f32, _vp, _vp, _vp]),
+    "scaled_attn_chunk": (_int, [_vp, _cache_p, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _f32, _vp, _vp, _vp]),
     "scaled_attn_prompt": (_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _int, _f32, _vp, _vp, _vp]),
     "scaled_attn_pool_scratch_bytes": (_i64, [_i64, _i64]),
     "scaled_attn_pool_release": (_int, [_vp, _pool_p, _vp, _i64, _vp]),
@@ -234,6 +235,11 @@ def scaled_attn_append(h, cache, rotary, q, q_stride, k, k_stride, v, v_stride, 
 def scaled_attn_decode(h, cache, q, q_stride, qn, table, table_stride, kv_lens, B, scale, out, lse, stream=0):
     _check(lib().scaled_attn_decode(h, cache, q, q_stride, qn, table, table_stride, kv_lens, B, scale, out, lse, stream),
            "scaled_attn_decode")
+
+
+def scaled_attn_chunk(h, cache, q, q_stride, table, table_stride, kv_lens, cu_q, T, B, scale, out, lse, stream=0):
+    _check(lib().scaled_attn_chunk(h, cache, q, q_stride, table, table_stride, kv_lens, cu_q, T, B, scale, out, lse, stream),
+           "scaled_attn_chunk")
 
 
 def scaled_attn_prompt(h, q, q_stride, k, k_stride, v, v_stride, cu_q, cu_k, Tq, Tk, B, causal, scale, out, lse, stream=0):

@@ -136,8 +136,10 @@ sg_status_t scaled_attn_create(sg_attn_t* out, int64_t Hq, int64_t Hk, int64_t D
     delete h;
     return refuse(SG_ERR_CUDA, "attn create: cudaSetDevice");
   }
-  const size_t ws = sg::decode_workspace_bytes(h->shape);
+  const size_t decode_ws = sg::decode_workspace_bytes(h->shape), chunk_ws = sg::chunk_workspace_bytes(h->shape);
+  const size_t ws = decode_ws > chunk_ws ? decode_ws : chunk_ws;
   cudaError_t e = sg::decode_prepare();
+  if (e == cudaSuccess) e = sg::chunk_prepare();
   if (e == cudaSuccess) e = sg::prompt_prepare();
   if (e == cudaSuccess) e = cudaMalloc(&h->shape.status, 16);
   if (e == cudaSuccess) e = cudaMemset(h->shape.status, 0, 16);
@@ -293,6 +295,44 @@ sg_status_t scaled_attn_decode(sg_attn_t h, const sg_kv_cache_t* cache, const vo
   a.stream = reinterpret_cast<cudaStream_t>(stream);
   const sg_status_t r = sg::decode_launch(s, a);
   return r == SG_OK ? SG_OK : refuse(r, "decode: kernel launch");
+}
+
+sg_status_t scaled_attn_chunk(sg_attn_t h, const sg_kv_cache_t* cache, const void* q, int64_t q_stride,
+                              const int32_t* table, int64_t table_stride, const int32_t* kv_lens,
+                              const int32_t* cu_q, int64_t T, int64_t B, float scale, void* out, float* lse,
+                              sg_stream_t stream) {
+  if (!h) return refuse(SG_ERR_INVALID_ARG, "chunk: NULL handle");
+  const sg::AttnShape& s = h->shape;
+  if (T < 0 || B < 0) return refuse(SG_ERR_INVALID_ARG, "chunk: negative size");
+  if (T > kMaxDim - 1024 || B > (1 << 24)) return refuse(SG_ERR_UNSUPPORTED_SHAPE, "chunk: T >= 2^31 - 1024 or B > 2^24");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return refuse(SG_ERR_INVALID_ARG, "chunk: scale");
+  if (T == 0 || B == 0) return SG_OK;
+  SG_TRY(check_cache(h, cache));
+  SG_TRY(check_rows(q, q_stride, s.Hq, s.D, "chunk: q"));
+  SG_TRY(check_table(table, table_stride, s.page));
+  SG_TRY(check_ints(kv_lens, "chunk: kv_lens"));
+  SG_TRY(check_ints(cu_q, "chunk: cu_q"));
+  if (!out) return refuse(SG_ERR_INVALID_ARG, "chunk: out is NULL");
+  if (!aligned(out, 16) || !aligned(lse, 4)) return refuse(SG_ERR_MISALIGNED, "chunk: outputs");
+  if (sg::ranges_overlap(out, 2 * T * s.Hq * s.D, q, row_bytes(T, q_stride, int64_t(s.Hq) * s.D)))
+    return refuse(SG_ERR_INVALID_ARG, "chunk: out overlaps q");
+  SG_TRY(check_device(h));
+  sg::AttnArgs a{};
+  a.cache = *cache;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.table = table;
+  a.table_stride = table_stride;
+  a.lens = kv_lens;
+  a.cu_q = cu_q;
+  a.Tq = T;
+  a.B = B;
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
+  a.stream = reinterpret_cast<cudaStream_t>(stream);
+  const sg_status_t r = sg::chunk_launch(s, a);
+  return r == SG_OK ? SG_OK : refuse(r, "chunk: kernel launch");
 }
 
 sg_status_t scaled_attn_prompt(sg_attn_t h, const void* q, int64_t q_stride, const void* k, int64_t k_stride,

@@ -20,7 +20,7 @@ struct AttnShape {
   int* status;          // device status word of the plan
   uint64_t timeout_ns;  // limit of every wait in a kernel
   int skip_tile;        // tests: a key tile that is not loaded; -1: none
-  void* workspace;      // decode: partial results
+  void* workspace;      // decode and chunk: partial results
 };
 
 // Validated arguments of one call; unused fields are zero.
@@ -54,6 +54,10 @@ sg_status_t pool_compact(const AttnShape& s, const sg_page_pool_t& pool, const s
 size_t decode_workspace_bytes(const AttnShape& s);
 cudaError_t decode_prepare();
 sg_status_t decode_launch(const AttnShape& s, const AttnArgs& a);
+
+size_t chunk_workspace_bytes(const AttnShape& s);
+cudaError_t chunk_prepare();
+sg_status_t chunk_launch(const AttnShape& s, const AttnArgs& a);
 
 cudaError_t prompt_prepare();
 sg_status_t prompt_launch(const AttnShape& s, const AttnArgs& a);

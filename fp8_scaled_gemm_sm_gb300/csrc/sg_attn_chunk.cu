@@ -1,0 +1,1187 @@
+// sg_attn_chunk.cu -- attention of chunks of new tokens over the paged e4m3 cache
+// (scaled_attn_chunk).
+//
+// For query row i of a sequence's n and the keys j < m - (n - 1 - i) of its m, with k_j = 2^a_j K_j and
+// v_j = 2^b_j V_j (K, V codes, a, b the exponents of their block of 16 keys),
+//     s_j = c q_i . k_j   (c = scale log2 e),   o_i = sum_j 2^(s_j) v_j / sum_j 2^(s_j),
+// in one pass over tiles of 128 keys, as sg_attn_prompt.cu goes, with the cache's codes as operands:
+//   * Scores: K as it lies in the cache, through the fp8 tensor cores.  A query row, scaled by a power of two so that its largest
+//     value lies in [2^7, 2^8), is the sum of two terms: e4m3 (4 significant bits), and what that leaves of bf16's 8 in
+//     e5m2 (3 bits hold every remainder).  Elements down to 2^-13 of the row's largest are exact, smaller ones off by at most
+//     2^-22 of it.  Two products at twice bf16's rate: nothing is converted and nothing is lost, as K has no copy.
+//   * K's block scales are part of the factor that every score takes on its way to the exponential.
+//   * Values: codes to fp16, which holds them exactly, by two warps; their block scales go into the weights, 2^(s_j - m + b_j - n)
+//     in fp16 (2^-11 of each), and out of the row sum again, a block's sum at a time.  m follows the maximum of s_j, m + n
+//     that of s_j + b_j, as in sg_attn_decode.cu; both are whole numbers here, so that one fma a score forms the exponent
+//     with a single rounding.  Rows whose scores pass 2^22, or whose value scales lie 2^96 apart, take a
+//     slower way that forms score, difference and sum one by one.
+// Rows are packed as in sg_attn_prompt.cu: a tile's 128 rows are tokens times query heads of one key/value head.  A CTA
+// works on two row tiles in opposition, or, where a unit has but one (few tokens), on the even and the odd
+// key blocks of that one, whose halves it joins at the end out of tensor memory.  Warps: 0-3, 4-7 softmax and output, one thread a row;
+// 8 work and TMA; 9 MMA, one thread; 10, 11 queries to their two terms, values to fp16.
+//
+// Work: units (two row tiles of a sequence and head) are numbered by what they cost, and every CTA takes
+// an equal range of the numbers, so a few tokens over a long cache fill the GPU as well as many over a short one.
+// Units that are short beside a range are not cut; the parts of a cut one are joined by a second
+// kernel in the order of their ranges, so results do not depend on timing.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cfloat>
+
+#include "sg_attn.h"
+#include "sg_attn_ptx.cuh"
+#include "sg_mx.cuh"
+
+namespace sg {
+
+namespace {
+
+constexpr int kRows = 128;  // rows of a tile, keys of a block
+constexpr int kThreads = 384;
+constexpr int kSoftmaxRegs = 208, kIssueRegs = 88;  // 2 x 208 + 88 = 3 x 168
+constexpr int kWhereJob = 0x41, kWhereMerge = 0x42, kWhereConvert = 0x43;  // waits beside those of sg_ptx.cuh
+constexpr int kJobReaders = 11;  // warps that take jobs
+constexpr int kEarly = 4;        // 16-key steps of a block whose weights are handed over first
+constexpr int kUnitCost = 512;   // what a unit costs beside its keys, in keys of one row tile
+constexpr int kUncut = 8;        // units of up to 1 / kUncut of a range are not cut
+constexpr int kLeast = 1024;     // of a range; at least 256, so that every range of a cut unit has a block of it
+constexpr float kSlack = 8.f;    // log2 of how far a maximum may pass its reference
+constexpr float kLift = 7.f;     // the output's weights at its reference are 2^kLift, the largest 2^15
+constexpr float kUnset = -FLT_MAX;
+constexpr float kExact = 4194304.f;  // references past this take the slow way
+constexpr float kSpread = -96.f;     // so do value scales this far below their reference, in log2
+
+// A unit that was cut: its rows, and the ranges that have parts of it; last < 0: none begins in this range.
+struct Cut {
+  int q0, lq, first, head0, tiles, from, last, unused;
+};
+
+struct ChunkParams {
+  const uint16_t* q;
+  int64_t q_stride;
+  const int32_t *table, *lens, *cu;
+  int64_t table_stride;
+  const uint8_t *k_scale, *v_scale;
+  int64_t num_pages;
+  int T, B, Hq, Hk, D, page, page_shift;
+  int group;            // query heads of a key/value head
+  int pack;             // query heads packed into a tile
+  int head_groups;      // Hq / pack
+  int skip;             // number of a key block that is not loaded (scaled_attn_set_debug); -1: none
+  float scale_log2;
+  uint16_t* out;
+  float* lse;
+  float* part_o;        // [2 ranges][2 tiles][HD / 4][kRows][4]: the part that begins a unit (odd), one that does not
+  float4* part_ml;      // [2 ranges][2 tiles][kRows]: m, n, sum
+  Cut* cuts;            // [ranges]
+  int* status;
+  uint64_t timeout_ns;
+};
+
+template <int HD>
+struct ChunkLayout {
+  static constexpr int kTile = kRows * 128;          // a term of a query tile, a K block
+  static constexpr int kKStages = 3, kVStages = 2, kHalfStages = 2;
+  static constexpr int kRaw = kRows * HD;            // codes of a V block
+  static constexpr int kBox = kRows * 128;           // 64 dimensions of it in fp16
+  static constexpr int kHalf = HD / 64 * kBox;
+  static constexpr int kOffK = 4 * kTile;            // after two terms of two query tiles
+  static constexpr int kOffHalf = kOffK + kKStages * kTile;
+  static constexpr int kOffRaw = kOffHalf + kHalfStages * kHalf;
+  static constexpr int kOffOut = kOffRaw + kVStages * kRaw;  // 1 KB a softmax warp
+  static constexpr int kInfo = 8;                    // key blocks whose scales are held
+  static constexpr int kOffInfo = kOffOut + 8 * 1024;        // float2 for each 16 keys
+  static constexpr int kOffMask = kOffInfo + kInfo * 64;     // and a word a block: pages that are not there, scales that are NaN
+  static constexpr int kOffRow = kOffMask + kInfo * 4;       // a query row's factor, by job and row
+  static constexpr int kOffBar = kOffRow + 2 * 2 * kRows * 4;
+  static constexpr int kNumBars = 2 * (kKStages + kVStages + kHalfStages) + 8 + 4 + 4;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kOffJobs = kOffMisc + 16;
+  static constexpr int kOffStats = kOffOut;          // of two halves that are joined: float4 a row and half, before their output
+  static constexpr int kOffSums = kOffOut;           // while work is planned: int64 per thread
+  static constexpr int kBytes = kOffJobs + 2 * 48;
+  static constexpr int kDynSmem = kBytes + 1024;
+  static_assert(kOffBar % 8 == 0 && kOffJobs % 16 == 0 && kDynSmem <= 232448, "shared memory");
+};
+
+// Key blocks; sizes reach 2^31.
+__device__ __forceinline__ int blocks_of(int keys) { return static_cast<int>((static_cast<uint32_t>(keys) + kRows - 1) / kRows); }
+
+// Tokens of a sequence, its keys, and units: a unit has `span` tokens, a row tile half of that.
+struct Sequence {
+  int q0, lq, lk, units;
+};
+
+__device__ __forceinline__ Sequence sequence(const ChunkParams& p, int b, int span) {
+  Sequence s;
+  s.q0 = min(max(__ldg(p.cu + b), 0), p.T);
+  s.lq = max(min(max(__ldg(p.cu + b + 1), 0), p.T) - s.q0, 0);
+  const int64_t cap = p.table_stride * p.page;
+  s.lk = static_cast<int>(min(static_cast<int64_t>(max(__ldg(p.lens + b), 0)), cap));
+  s.units = (s.lq + span - 1) / span;
+  return s;
+}
+
+// Keys that the unit's last token sees, and its row tiles.
+__device__ __forceinline__ int unit_keys(const Sequence& s, int i, int span) {
+  return max(s.lk - s.lq + min((i + 1) * span, s.lq), 0);
+}
+__device__ __forceinline__ int unit_tiles(const Sequence& s, int i, int span) { return s.lq - i * span > span / 2 ? 2 : 1; }
+
+// What the units before unit i (at most the last) cost; all but the last have two tiles and see lk - lq + span (x + 1) keys.
+__device__ __forceinline__ int64_t cost_before(const Sequence& s, int i, int span) {
+  const int64_t a = static_cast<int64_t>(s.lk) - s.lq, n = i;
+  const int64_t none = a >= 0 ? 0 : min(n, -a / span);
+  return n * kUnitCost + 2 * ((n - none) * a + span * (n * (n + 1) / 2 - none * (none + 1) / 2));
+}
+__device__ __forceinline__ int64_t cost(const Sequence& s, int span) {  // of one head group
+  if (s.units == 0) return 0;
+  return cost_before(s, s.units - 1, span) + kUnitCost + static_cast<int64_t>(unit_tiles(s, s.units - 1, span)) * s.lk;
+}
+
+// What a CTA works on: blocks [t0, t1) of a unit.  b: -2 no more.
+struct Job {
+  int b, q0, lq, lk;     // sequence, its first row, tokens, keys
+  int first, tiles;      // the unit's first token, its row tiles
+  int t0, t1;
+  int head0, whole, slot, unused;
+};
+
+// The jobs of a range [begin, end) of the numbers.
+struct Walk {
+  const ChunkParams& p;
+  int span;
+  int64_t begin, end, quota;
+  Sequence s;
+  int b, hg, unit;
+  int64_t start;  // the unit's number
+  // The first job at or after the unit; false: none.
+  __device__ __forceinline__ bool find(Job& job, Cut& cut) {
+    for (;;) {
+      if (start >= end) return false;
+      const int keys = unit_keys(s, unit, span), tiles = unit_tiles(s, unit, span), blocks = blocks_of(keys);
+      const int64_t each = kRows * tiles, first = start + kUnitCost;
+      int t0 = 0, t1 = blocks;
+      bool mine;
+      if (static_cast<int64_t>(tiles) * keys * kUncut <= quota) {
+        mine = start >= begin;
+      } else {
+        if (begin > first) t0 = static_cast<int>(min((begin - first + each - 1) / each, static_cast<int64_t>(blocks)));
+        t1 = static_cast<int>(max(min((end - first + each - 1) / each, static_cast<int64_t>(blocks)), static_cast<int64_t>(0)));
+        mine = t0 < t1;
+      }
+      if (mine) {
+        const bool whole = t0 == 0 && t1 == blocks;
+        const int range = static_cast<int>(begin / quota);
+        job = Job{b, s.q0, s.lq, s.lk, unit * span, tiles, t0, t1, hg * p.pack, whole, 2 * range + (t0 == 0), 0};
+        if (t0 == 0 && !whole)
+          cut = Cut{s.q0, s.lq, unit * span, hg * p.pack, tiles, range, static_cast<int>((first + each * (blocks - 1)) / quota), 0};
+      }
+      // the next unit
+      start += kUnitCost + static_cast<int64_t>(tiles) * keys;
+      if (++unit == s.units) {
+        unit = 0;
+        if (++hg == p.head_groups) {
+          hg = 0;
+          do {
+            if (++b >= p.B) {
+              start = end;
+              break;
+            }
+            s = sequence(p, b, span);
+          } while (s.units == 0);
+        }
+      }
+      if (mine) return true;
+    }
+  }
+};
+
+// Two fp32 values to two e4m3 (e5m2) codes, to nearest even; two e4m3 codes to fp16.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t to_e5m2x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t from_e4m3x2(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+  return r;
+}
+__device__ __forceinline__ void half2_floats(uint32_t x, float& lo, float& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(lo), "=f"(hi) : "r"(x));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
+  const uint4 v = ld_shared_v4(a);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ uint32_t ld_shared(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared(uint32_t a, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
+__device__ __forceinline__ void st_shared_v2(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const ChunkParams p) {
+  using L = ChunkLayout<HD>;
+  constexpr int KS = L::kKStages, VS = L::kVStages, HS = L::kHalfStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t base = smem_addr(smem), bar0 = base + L::kOffBar;
+  auto q_tile = [&](int t, int term) { return base + (2 * t + term) * L::kTile; };
+  auto k_full = [&](int s) { return bar0 + 8 * s; };
+  auto k_empty = [&](int s) { return bar0 + 8 * (KS + s); };
+  auto v_full = [&](int s) { return bar0 + 8 * (2 * KS + s); };
+  auto v_empty = [&](int s) { return bar0 + 8 * (2 * KS + VS + s); };
+  auto h_full = [&](int s) { return bar0 + 8 * (2 * KS + 2 * VS + s); };
+  auto h_empty = [&](int s) { return bar0 + 8 * (2 * KS + 2 * VS + HS + s); };
+  constexpr int kMore = 2 * (KS + VS + HS);
+  auto s_full = [&](int t) { return bar0 + 8 * (kMore + t); };
+  auto p_full = [&](int t) { return bar0 + 8 * (kMore + 2 + t); };
+  auto p_half = [&](int t) { return bar0 + 8 * (kMore + 4 + t); };
+  auto o_full = [&](int t) { return bar0 + 8 * (kMore + 6 + t); };
+  auto job_full = [&](int s) { return bar0 + 8 * (kMore + 8 + s); };
+  auto job_empty = [&](int s) { return bar0 + 8 * (kMore + 10 + s); };
+  const uint32_t q_full = bar0 + 8 * (kMore + 12), q_empty = bar0 + 8 * (kMore + 13), drain_bar = bar0 + 8 * (kMore + 14);
+  const uint32_t merge_bar = bar0 + 8 * (kMore + 15);
+  int* misc = reinterpret_cast<int*>(smem + L::kOffMisc);  // [0] TMEM base, [1] abort
+  Job* jobs = reinterpret_cast<Job*>(smem + L::kOffJobs);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tile_tokens = kRows / p.pack, span = 2 * tile_tokens;
+
+  grid_dep_wait();
+  if (warp == 9) {
+    tmem_alloc(smem_addr(&misc[0]), 512);
+    tmem_relinquish();
+  }
+  if (tid == 32) {
+    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar0 + 8 * i, 1);
+    for (int s = 0; s < VS; ++s) mbar_init(v_empty(s), 2);
+    for (int s = 0; s < HS; ++s) mbar_init(h_full(s), 2);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(p_half(t), kRows);
+      mbar_init(p_full(t), kRows);
+      mbar_init(job_empty(t), kJobReaders);
+    }
+    mbar_init(q_full, 2);
+    mbar_init(merge_bar, 2 * kRows);
+    misc[1] = 0;
+    fence_mbarrier_init();
+  }
+  // Numbers before each run of `per` sequences, by thread.
+  int64_t* sums = reinterpret_cast<int64_t*>(smem + L::kOffSums);
+  const int per = (p.B + kThreads - 1) / kThreads;
+  {
+    int64_t mine = 0;
+    for (int b = tid * per; b < min((tid + 1) * per, p.B); ++b) mine += cost(sequence(p, b, span), span) * p.head_groups;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, mine, o);
+      if (lane >= o) mine += up;
+    }
+    sums[tid] = mine;  // up to and with this thread's, within the warp
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dep_launch();  // not before tensor memory is there
+  const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+  const Watchdog wd{p.status, p.timeout_ns, reinterpret_cast<volatile int*>(&misc[1])};
+  auto read = [&](int i, Job& job) {
+    const int4* from = reinterpret_cast<const int4*>(jobs + (i & 1));
+    const int4 x = from[0], y = from[1], z = from[2];
+    auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    job.b = same(x.x), job.q0 = same(x.y), job.lq = same(x.z), job.lk = same(x.w);
+    job.first = same(y.x), job.tiles = same(y.y), job.t0 = same(y.z), job.t1 = same(y.w);
+    job.head0 = same(z.x), job.whole = same(z.y), job.slot = same(z.z);
+  };
+  auto done = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(job_empty(i & 1));
+  };
+  auto peek = [&](int i, Job& job) {  // false: no more, or the CTA gives up
+    if (!__all_sync(0xffffffffu, mbar_wait(job_full(i & 1), (i >> 1) & 1, wd, kWhereJob))) return false;
+    read(i, job);
+    return job.b != -2;
+  };
+  // Keys that a token's row sees, a row tile's last row, and its blocks in the job.  A unit with one row tile has
+  // two halves of the job's blocks instead, the even ones and the odd ones.
+  auto visible = [&](const Job& j, int tok) { return max(min(j.lk, j.lk - j.lq + tok + 1), 0); };
+  auto tile_keys = [&](const Job& j, int t) {
+    const int first = j.first + (j.tiles == 2 ? t * tile_tokens : 0);
+    return first < j.lq ? visible(j, min(first + tile_tokens, j.lq) - 1) : 0;
+  };
+  auto tile_blocks = [&](const Job& j, int t) {
+    if (j.tiles == 1) return (j.t1 - j.t0 + 1 - t) / 2;
+    return max(min(blocks_of(tile_keys(j, t)), j.t1) - j.t0, 0);
+  };
+
+  if (warp >= 8) {
+    reg_dec<kIssueRegs>();
+    if (warp == 8) {
+      // ---------------- work and TMA ----------------
+      int64_t run = 0, total = 0;  // numbers before this lane's warp, in all
+      for (int w = 0; w < kThreads / 32; ++w) {
+        const int64_t x = sums[32 * w + 31];
+        total += x;
+        if (w < lane) run += x;
+      }
+      __syncwarp();
+      const int64_t quota = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kLeast));
+      Walk walk{p, span, min(static_cast<int64_t>(blockIdx.x) * quota, total), 0, quota, Sequence{0, 0, 0, 0}, 0, 0, 0, 0};
+      walk.end = min(walk.begin + quota, total);
+      bool some = walk.begin < walk.end;
+      if (some) {
+        // the run of sequences, the sequence in it, the head group and the unit with number `begin`
+        const int w = __popc(__ballot_sync(0xffffffffu, lane < kThreads / 32 && run <= walk.begin)) - 1;
+        walk.start = __shfl_sync(0xffffffffu, run, w);
+        const int64_t upto = sums[32 * w + lane] + walk.start;
+        const unsigned after = __ballot_sync(0xffffffffu, upto > walk.begin);  // not zero: begin is in this warp's
+        const int l = __ffs(after) - 1;
+        const int64_t before = __shfl_up_sync(0xffffffffu, upto, 1);
+        if (l > 0) walk.start = __shfl_sync(0xffffffffu, before, l);
+        walk.b = (32 * w + l) * per;
+        for (;;) {
+          walk.s = sequence(p, walk.b, span);
+          const int64_t each = cost(walk.s, span);
+          if (walk.begin < walk.start + each * p.head_groups) {
+            walk.hg = static_cast<int>((walk.begin - walk.start) / each);
+            walk.start += walk.hg * each;
+            break;
+          }
+          walk.start += each * p.head_groups;
+          ++walk.b;
+        }
+        int64_t lo = 0, step = walk.s.units;  // the unit is in [lo, lo + step)
+        while (step > 1) {
+          const int64_t next = (step + 31) / 32, i = lo + lane * next;
+          const bool below = i < min(lo + step, static_cast<int64_t>(walk.s.units)) &&
+                             walk.start + cost_before(walk.s, static_cast<int>(i), span) <= walk.begin;
+          lo += (__popc(__ballot_sync(0xffffffffu, below)) - 1) * next;
+          step = next;
+        }
+        walk.unit = static_cast<int>(lo);
+        walk.start += cost_before(walk.s, walk.unit, span);
+      }
+      Cut cut{};
+      cut.last = -1;
+      const uint64_t policy = l2_policy_evict_last();
+      int k_stage = 0, v_stage = 0, count = 0;
+      uint32_t k_phase = 0, v_phase = 0, k_issued = 0, v_issued = 0, k_par = 0, v_par = 0;
+      const int block_shift = p.page_shift - 4, boxes = min(kRows / p.page, 8);
+      const uint32_t k_box = kRows / boxes * 128, v_box = kRows / boxes * HD;
+      const int c8 = lane & 7;
+      bool ok = true;
+      for (int it = 0; ok; ++it) {
+        Job job{};
+        if (some) some = walk.find(job, cut);
+        if (!some) job.b = -2;
+        if (it >= 2) ok = __all_sync(0xffffffffu, mbar_wait(job_empty(it & 1), ((it >> 1) - 1) & 1, wd, kWhereJob));
+        if (!ok) break;
+        if (lane == 0) {
+          jobs[it & 1] = job;
+          mbar_arrive(job_full(it & 1));
+        }
+        if (!some) break;
+        const int head = job.head0 / p.group;
+        const int32_t* row = p.table + job.b * p.table_stride;
+        int page = -1;
+        float2 about = make_float2(0.f, 0.f);
+        uint32_t gone = 0, nan = 0;  // by lane
+        for (int t = job.t0; t < job.t1; ++t) {
+          const int in = (t - job.t0) & 3;
+          if (in == 0) {  // pages and scales of four blocks, 16 keys a lane
+            const int64_t key = static_cast<int64_t>(t) * kRows + 16 * lane;
+            page = -1;
+            about = make_float2(0.f, 0.f);
+            bool v_nan = false;
+            if (key < job.lk) {
+              const int pg = __ldg(row + (key >> p.page_shift));
+              if (pg >= 0 && pg < p.num_pages) {
+                page = pg;
+                const int64_t at = ((static_cast<int64_t>(pg) * p.Hk + head) << block_shift) + ((key & (p.page - 1)) >> 4);
+                const int kc = __ldg(p.k_scale + at), vc = __ldg(p.v_scale + at);
+                about = make_float2(kc == 255 ? __uint_as_float(0x7FC00000u) : p.scale_log2 * exp2_code(kc), vc == 255 ? 0.f : static_cast<float>(vc - 127));
+                v_nan = vc == 255;
+              }
+            }
+            gone = __ballot_sync(0xffffffffu, page < 0);
+            nan = __ballot_sync(0xffffffffu, v_nan);
+          }
+          // K
+          ok = __all_sync(0xffffffffu, mbar_wait(k_empty(k_stage), k_phase ^ 1, wd, kWhereProducerEmpty));
+          if (!ok) break;
+          const uint32_t slot = count++ & (L::kInfo - 1);
+          if ((lane >> 3) == in) st_shared_v2(base + L::kOffInfo + slot * 64 + c8 * 8, __float_as_uint(about.x), __float_as_uint(about.y));
+          if (lane == 0) st_shared(base + L::kOffMask + slot * 4, ((gone >> (8 * in)) & 255) | ((nan >> (8 * in)) & 255) << 8);
+          const bool mine = (lane >> 3) == in && c8 % (8 / boxes) == 0;
+          const int y = (head << p.page_shift) + ((t * kRows + 16 * c8) & (p.page - 1)), part = c8 / (8 / boxes);
+          __syncwarp();
+          if (t != p.skip) {
+            if (lane == 0) mbar_arrive_expect_tx(k_full(k_stage), L::kTile);
+            __syncwarp();
+            if (mine) tma_load_3d_hint(base + L::kOffK + k_stage * L::kTile + part * k_box, &tmK, 0, y, page, k_full(k_stage), policy);
+            k_issued |= 1u << k_stage;
+            k_par = (k_par & ~(1u << k_stage)) | (k_phase << k_stage);
+          }
+          if (++k_stage == KS) {
+            k_stage = 0;
+            k_phase ^= 1;
+          }
+          // V
+          ok = __all_sync(0xffffffffu, mbar_wait(v_empty(v_stage), v_phase ^ 1, wd, kWhereProducerEmpty));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(v_full(v_stage), L::kRaw);
+          __syncwarp();
+          if (mine) tma_load_3d_hint(base + L::kOffRaw + v_stage * L::kRaw + part * v_box, &tmV, 0, y, page, v_full(v_stage), policy);
+          v_issued |= 1u << v_stage;
+          v_par = (v_par & ~(1u << v_stage)) | (v_phase << v_stage);
+          if (++v_stage == VS) {
+            v_stage = 0;
+            v_phase ^= 1;
+          }
+        }
+      }
+      // a call that gives up leaves nothing for the join: its outputs are undefined, but no row outside them may be written
+      if (lane == 0) {
+        if (!ok) cut.last = -1;
+        p.cuts[blockIdx.x] = cut;
+        // loads in flight must land before the CTA can exit
+        for (int s = 0; s < KS; ++s)
+          if ((k_issued >> s) & 1) mbar_wait_drain(k_full(s), (k_par >> s) & 1, 200000000ull);
+        for (int s = 0; s < VS; ++s)
+          if ((v_issued >> s) & 1) mbar_wait_drain(v_full(s), (v_par >> s) & 1, 200000000ull);
+      }
+    } else if (warp >= 10) {
+      // ---------------- queries to two terms, values to fp16 ----------------
+      const int me = warp - 10;
+      int q_fills = 0, v_stage = 0, h_stage = 0, count = 0;
+      uint32_t v_phase = 0, h_phase = 0;
+      Job job;
+      bool ok = true;
+      for (int it = 0; ok && peek(it, job); ++it) {
+        const int blocks = job.t1 - job.t0;
+        if (blocks > 0) {
+          if (q_fills > 0) ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (q_fills - 1) & 1, wd, kWhereConvert));
+          if (!ok) break;
+          ++q_fills;
+          // HD / 8 lanes a row, 8 dimensions each; tokens past the unit's last have no rows
+          constexpr int kLanes = HD / 8, kAtOnce = 32 / kLanes;
+          const int d = 8 * (lane % kLanes);
+          const int live = min(job.lq - job.first, job.tiles * tile_tokens);
+#pragma unroll 1
+          for (int t = 0; t < job.tiles; ++t) {
+            const int rows = min(live - t * tile_tokens, tile_tokens) * p.pack;
+            const uint32_t hi_tile = q_tile(t, 0), lo_tile = q_tile(t, 1), factors = base + L::kOffRow + (((it & 1) * 2 + t) * kRows) * 4;
+            // rows without a query are zeros, so that what their threads find does not vary
+            for (int i = max(rows, 0) * 8 + me * 32 + lane; i < kRows * 8; i += 64) {
+              st_shared_v4(hi_tile + i * 16, 0, 0, 0, 0);
+              st_shared_v4(lo_tile + i * 16, 0, 0, 0, 0);
+            }
+            constexpr int kBatch = 4;  // rows a lane has on their way
+#pragma unroll 1
+            for (int r0 = me * kAtOnce * kBatch; r0 < rows; r0 += 2 * kAtOnce * kBatch) {
+              uint4 raw[kBatch];
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) {
+                const int r = r0 + i * kAtOnce + lane / kLanes;
+                raw[i] = make_uint4(0, 0, 0, 0);
+                if (r < rows && d < p.D)
+                  raw[i] = *reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(job.q0 + job.first + t * tile_tokens + r / p.pack) * p.q_stride +
+                                                           (job.head0 + r % p.pack) * p.D + d);
+              }
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) {
+                const int r = r0 + i * kAtOnce + lane / kLanes;
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                float x[8];
+                float top = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  x[2 * e] = __uint_as_float(w[e] << 16);
+                  x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+                  top = fmaxf(top, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
+                }
+#pragma unroll
+                for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                // the row's largest value to [2^7, 2^8)
+                const int field = min(261 - static_cast<int>(__float_as_uint(top) >> 23), 253);
+                const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
+                uint32_t hi[2], lo[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  hi[e] = lo[e] = 0;
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    const float a = x[4 * e + 2 * k] * up, b = x[4 * e + 2 * k + 1] * up;
+                    const uint32_t code = to_e4m3x2(a, b);
+                    float ha, hb;
+                    half2_floats(from_e4m3x2(code), ha, hb);
+                    hi[e] |= code << (16 * k);
+                    lo[e] |= to_e5m2x2(a - ha, b - hb) << (16 * k);
+                  }
+                }
+                if (r < rows) {
+                  const uint32_t at = r * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 8);
+                  st_shared_v2(hi_tile + at, hi[0], hi[1]);
+                  st_shared_v2(lo_tile + at, lo[0], lo[1]);
+                  if (d == 0)  // 1 / up; a row with an infinity is NaN
+                    st_shared(factors + r * 4, top == INFINITY ? 0x7FC00000u : static_cast<uint32_t>(254 - field) << 23);
+                }
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full);
+        }
+        for (int j = 0; j < blocks; ++j) {
+          ok = __all_sync(0xffffffffu, mbar_wait(v_full(v_stage), v_phase, wd, kWhereConvert) &&
+                                           mbar_wait(h_empty(h_stage), h_phase ^ 1, wd, kWhereConvert));
+          if (!ok) break;
+          const uint32_t from = base + L::kOffRaw + v_stage * L::kRaw, to = base + L::kOffHalf + h_stage * L::kHalf;
+          const uint32_t nan = ld_shared(base + L::kOffMask + (count++ & (L::kInfo - 1)) * 4) >> 8;
+          const int past = job.lk - (job.t0 + j) * kRows;  // rows from here on are not this sequence's
+          constexpr int kChunks = HD / 16;                 // 16-byte runs of a row of codes
+          const int chunk = lane % kChunks;
+#pragma unroll 4
+          for (int r0 = 0; r0 < kRows / 2; r0 += 32 / kChunks) {
+            const int r = me * (kRows / 2) + r0 + lane / kChunks;
+            uint4 x = ld_shared_v4(from + r * HD + chunk * 16);
+            if (past < kRows && r >= past) x = make_uint4(0, 0, 0, 0);
+            if (nan && ((nan >> (r >> 4)) & 1) && r < past) x = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y[2 * e] = from_e4m3x2(w[e]);
+              y[2 * e + 1] = from_e4m3x2(w[e] >> 16);
+            }
+            // runs 2 c and 2 c + 1 of the fp16 row; a row's upper half of lanes writes them the other way round, so that
+            // the eight lanes of a row meet in no bank
+            const uint32_t box = to + chunk / 4 * L::kBox + r * 128;
+            const int run = 2 * (chunk % 4), flip = HD == 128 ? chunk >> 2 : 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int h = k ^ flip;
+              st_shared_v4(box + (((run + h) ^ (r & 7)) << 4), h ? y[4] : y[0], h ? y[5] : y[1], h ? y[6] : y[2], h ? y[7] : y[3]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(h_full(h_stage));
+            mbar_arrive(v_empty(v_stage));
+          }
+          if (++v_stage == VS) {
+            v_stage = 0;
+            v_phase ^= 1;
+          }
+          if (++h_stage == HS) {
+            h_stage = 0;
+            h_phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        done(it);
+      }
+    } else if (elect_one()) {
+      // ---------------- MMA issuer: one thread for all of it ----------------
+      int k_stage = 0, h_stage = 0, q_uses = 0;
+      uint32_t k_phase = 0, h_phase = 0, turn[2] = {0, 0};  // parity of a tile's next weights
+      auto wait = [&](uint32_t bar, uint32_t parity, int where) {
+        const bool got = mbar_wait<true>(bar, parity, wd, where);
+        tc_fence_after();
+        return got;
+      };
+      bool ok = true;
+      Job job;
+      for (int it = 0; ok; ++it) {
+        ok = wait(job_full(it & 1), (it >> 1) & 1, kWhereJob);
+        if (!ok) break;
+        job = jobs[it & 1];
+        mbar_arrive(job_empty(it & 1));
+        if (job.b == -2) break;
+        const int blocks = job.t1 - job.t0;
+        if (blocks == 0) continue;
+        const bool pair = job.tiles == 2;
+        const int keys[2] = {tile_keys(job, 0) - job.t0 * kRows, tile_keys(job, 1) - job.t0 * kRows};
+        const int mine[2] = {tile_blocks(job, 0), tile_blocks(job, 1)};
+        auto scores = [&](int t, int j) {  // S_t = Q K_j^T, in two terms
+          const int n = (min(kRows, keys[pair ? t : 0] - j * kRows) + 15) & ~15;
+          const uint64_t k = kmajor_sw128_desc(base + L::kOffK + k_stage * L::kTile);
+#pragma unroll
+          for (int term = 0; term < 2; ++term) {
+            const uint64_t a = kmajor_sw128_desc(q_tile(pair ? t : 0, term));
+            const uint32_t idesc = instr_desc(term, 0, kRows, n);  // e4m3, then e5m2
+#pragma unroll
+            for (int i = 0; i < HD / 32; ++i) mma_f8f6f4(tmem + t * 128, desc_advance(a, i * 32), desc_advance(k, i * 32), idesc, (term | i) != 0);
+          }
+          mma_commit(s_full(t));
+        };
+        auto next_k = [&]() {
+          mma_commit(k_empty(k_stage));
+          if (++k_stage == KS) {
+            k_stage = 0;
+            k_phase ^= 1;
+          }
+        };
+        auto output = [&](int t, int j, bool last) {  // O_t += P_t V_j: what is stored first, then the rest
+          const uint64_t v = smem_desc(base + L::kOffHalf + h_stage * L::kHalf, L::kBox, 1024, 2);
+          constexpr uint32_t idesc = instr_desc(0, 0, kRows, HD) | kIdescBMajorN;
+          const int steps = (min(kRows, keys[pair ? t : 0] - j * kRows) + 15) / 16;
+          const bool first = pair ? j == 0 : j < 2;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && wait(h ? p_full(t) : p_half(t), turn[t], kWhereMmaTmemEmpty);
+            if (ok) {
+#pragma unroll
+              for (int i = h ? kEarly : 0; i < (h ? 8 : kEarly); ++i)
+                if (i < steps) mma_f16_ts(tmem + 256 + t * 128, tmem + t * 128 + i * 8, desc_advance(v, i * 2048), idesc, !(first && i == 0));
+              if (h && last) mma_commit(o_full(t));
+            }
+          }
+          turn[t] ^= 1;
+        };
+        auto next_v = [&]() {
+          mma_commit(h_empty(h_stage));
+          if (++h_stage == HS) {
+            h_stage = 0;
+            h_phase ^= 1;
+          }
+        };
+        auto k_ready = [&]() { return wait(k_full(k_stage), k_phase, kWhereMmaFull); };
+        auto v_ready = [&]() { return wait(h_full(h_stage), h_phase, kWhereMmaFull); };
+        ok = wait(q_full, q_uses & 1, kWhereMmaFull);
+        ++q_uses;
+        if (pair) {
+          ok = ok && k_ready();
+          if (ok) {
+            if (mine[0] > 0) scores(0, 0);
+            if (mine[1] > 0) scores(1, 0);
+            next_k();
+            if (blocks == 1) mma_commit(q_empty);
+          }
+          for (int j = 0; j < blocks && ok; ++j) {
+            ok = v_ready();
+            bool k = false;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              if (ok && j < mine[t]) {
+                output(t, j, j + 1 == mine[t]);
+                if (ok && j + 1 < mine[t]) {
+                  if (!k) ok = k_ready();
+                  k = true;
+                  if (ok) scores(t, j + 1);
+                }
+              }
+            next_v();
+            if (k) {
+              next_k();
+              if (j + 2 == blocks) mma_commit(q_empty);  // the job's last scores
+            }
+          }
+        } else {
+          for (int j = 0; j < min(blocks, 2) && ok; ++j) {
+            ok = k_ready();
+            if (ok) {
+              scores(j, j);
+              next_k();
+            }
+          }
+          if (blocks <= 2) mma_commit(q_empty);
+          for (int j = 0; j < blocks && ok; ++j) {
+            const int t = j & 1;
+            ok = v_ready();
+            if (ok) {
+              if (t == 0) output(0, j, j + 2 >= blocks); else output(1, j, j + 2 >= blocks);
+              next_v();
+            }
+            if (ok && j + 2 < blocks) {
+              ok = k_ready();
+              if (ok) {
+                if (t == 0) scores(0, j + 2); else scores(1, j + 2);
+                next_k();
+                if (j + 3 == blocks) mma_commit(q_empty);
+              }
+            }
+          }
+        }
+      }
+      // every MMA has finished and every commit has landed before the CTA exits
+      mma_commit(drain_bar);
+      mbar_wait_drain(drain_bar, 0, 200000000ull);
+    }
+  } else {
+    reg_inc<kSoftmaxRegs>();
+    // ---------------- softmax and output ----------------
+    const int t = warp >> 2, quarter = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_addr = tmem + lanes + t * 128, o_addr = tmem + lanes + 256;
+    const int row = quarter * 32 + lane;
+    uint32_t turn = 0, outputs = 0, merges = 0;  // parities of the next scores, the next output, the next meeting of the halves
+    int count = 0;                               // key blocks of the jobs before
+    bool ok = true;
+#pragma unroll 1
+    for (int it = 0; ok; ++it) {
+      int n, lim, t0, each, blocks;  // key blocks of this tile; keys that this row sees; the job's first block; blocks from one to the next
+      bool halves, idle;
+      {
+        Job job;
+        if (!peek(it, job)) break;
+        halves = job.tiles == 1;
+        n = tile_blocks(job, t);
+        blocks = job.t1 - job.t0;
+        t0 = job.t0 + (halves ? t : 0);
+        each = halves ? 2 : 1;
+        const int tok = job.first + (halves ? 0 : t * tile_tokens) + row / p.pack;
+        idle = row >= tile_tokens * p.pack || tok >= job.lq;
+        lim = idle ? tile_keys(job, halves ? 0 : t) : visible(job, tok);  // past a tile's keys its scores are not formed
+      }
+      const uint32_t info = base + L::kOffInfo, mask = base + L::kOffMask;
+      float factor = 0.f;                 // of the query row's codes
+      float m = kUnset, nn = kUnset;      // references, in log2 units: of scores, of the output's weights (relative to m)
+      uint64_t sum2 = 0;                  // two partial row sums
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full(t), turn, wd, kWhereEpiTmemFull));
+        turn ^= 1;
+        if (!ok) break;
+        tc_fence_after();
+        if (j == 0) factor = idle ? 1.f : __uint_as_float(ld_shared(base + L::kOffRow + (((it & 1) * 2 + (halves ? 0 : t)) * kRows + row) * 4));
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_addr + 32 * c, s[c]);  // past the last key: hidden below
+        const uint32_t slot = (count + (halves ? 2 * j + t : j)) & (L::kInfo - 1);
+        const uint32_t gone = ld_shared(mask + slot * 4) & 255;
+        float g[8], b[8];  // factors of the scores, exponents of the values, by 16 keys
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float4 x = ld_shared_f4(info + slot * 64 + c * 16);
+          g[2 * c] = x.x * factor, b[2 * c] = x.y, g[2 * c + 1] = x.z * factor, b[2 * c + 1] = x.w;
+        }
+        tmem_wait_ld();
+        const int room = lim - (t0 + each * j) * kRows;
+        if (__any_sync(0xffffffffu, room < kRows) || gone) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const int left = (gone >> c) & 1 ? 0 : room - 16 * c;
+            // no score of this row takes the block's scale, which may be NaN; and hidden ones are not to meet a zero
+            if (left <= 0) g[c] = 1.f;
+            if (g[c] == 0.f) g[c] = FLT_MIN;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (i >= left) s[c / 2][c % 2 * 16 + i] = 0xFF800000u;
+          }
+        }
+        float top[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          float x = -INFINITY, y = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            x = max3(x, __uint_as_float(s[c / 2][c % 2 * 16 + i]), __uint_as_float(s[c / 2][c % 2 * 16 + i + 1]));
+            y = max3(y, __uint_as_float(s[c / 2][c % 2 * 16 + i + 2]), __uint_as_float(s[c / 2][c % 2 * 16 + i + 3]));
+          }
+          top[c] = fmaxf(x, y) * g[c];
+        }
+        const float mx = fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]), max3(top[5], top[6], top[7]));
+        auto v_top = [&](float ref) {
+          float x[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) x[c] = (top[c] - ref) + b[c];
+          return fmaxf(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(x[5], x[6], x[7]));
+        };
+        if (__any_sync(0xffffffffu, mx > m + kSlack || v_top(m) > nn + (kLift + kSlack))) {
+          const float up = ceilf(mx);
+          if (up > m) {
+            const float by = ex2(m - up);
+            sum2 = mul_f32x2(sum2, pack_f32x2(by, by));
+            nn += m - up;
+            m = up;
+          }
+          const float vx = ceilf(v_top(m)) - kLift;
+          const bool lift = vx > nn;
+          const float by = lift ? ex2(nn - vx) : 1.f;
+          if (lift) nn = vx;
+          if (j > 0) {
+#pragma unroll 1
+            for (int c = 0; c < HD / 16; ++c) {  // S fills the registers: a little of O at a time
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(o_addr + t * 128 + 16 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+              tmem_st_32x32b_x16(o_addr + t * 128 + 16 * c, o);
+            }
+          }
+        }
+        // before a row has seen a key its references are unset: any do
+        const float ref = m == kUnset ? 0.f : m, vref = m == kUnset ? 0.f : nn;
+        float least = fminf(fminf(fminf(b[0], b[1]), fminf(b[2], b[3])), fminf(fminf(b[4], b[5]), fminf(b[6], b[7])));
+        const bool slow = __any_sync(0xffffffffu, fabsf(ref) > kExact || least - vref < kSpread);
+        if (slow) {
+          float more = 0.f;
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              uint32_t& x = s[c / 2][c % 2 * 16 + i];
+              const float y = __fsub_rn(__fmul_rn(__uint_as_float(x), g[c]), ref);
+              more += ex2(y);
+              x = __float_as_uint(y);
+            }
+          sum2 = add_f32x2(sum2, pack_f32x2(more, 0.f));
+        }
+        uint32_t w[16];  // two blocks' weights
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float by = slow ? 1.f : g[c], off = slow ? b[c] - vref : (b[c] - vref) - ref;
+          const uint64_t g2 = pack_f32x2(by, by), off2 = pack_f32x2(off, off);
+          uint64_t part = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float x, y;
+            unpack_f32x2(fma_f32x2(pack_f32x2(s[c / 2][c % 2 * 16 + 2 * i], s[c / 2][c % 2 * 16 + 2 * i + 1]), g2, off2), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            part = i ? add_f32x2(part, pack_f32x2(x, y)) : pack_f32x2(x, y);
+            w[c % 2 * 8 + i] = pack_f16x2(x, y);
+          }
+          if (!slow) {  // the weights without the values' scale
+            const float out = ex2(vref - b[c]);
+            sum2 = fma_f32x2(part, pack_f32x2(out, out), sum2);
+          }
+          if (c & 1) {
+            if (c / 2 == kEarly / 2) {  // by now what was stored before is there
+              tmem_wait_st();
+              tc_fence_before();
+              mbar_arrive(p_half(t));
+            }
+            tmem_st_32x32b_x16(s_addr + 16 * (c / 2), w);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_full(t));
+      }
+      count += blocks;
+      if (n > 0 && ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), outputs, wd, kWhereEpiTmemFull));
+        outputs ^= 1;
+        tc_fence_after();
+      }
+      if (!ok) break;
+      float lo, hi;
+      unpack_f32x2(sum2, lo, hi);
+      float sum = lo + hi;
+      // A tile's output is what its thread has; a unit of one tile has two halves, which meet here: each then
+      // writes half of the dimensions of both.
+      float part[2] = {0.f, 0.f};  // what the halves' outputs are multiplied by
+      bool has[2] = {n > 0, false};
+      if (halves) {
+        const uint32_t stats = base + L::kOffStats;
+        st_shared_v4(stats + (t * kRows + row) * 16, __float_as_uint(m), __float_as_uint(nn), __float_as_uint(sum), n > 0);
+        mbar_arrive(merge_bar);
+        ok = __all_sync(0xffffffffu, mbar_wait(merge_bar, merges & 1, wd, kWhereMerge));
+        if (!ok) break;
+        const uint4 x = ld_shared_v4(stats + ((t ^ 1) * kRows + row) * 16);
+        const float m1 = __uint_as_float(x.x), n1 = __uint_as_float(x.y), sum1 = __uint_as_float(x.z);
+        const float both = fmaxf(m, m1);
+        const float d0 = m == kUnset ? kUnset : (m - both) + nn, d1 = m1 == kUnset ? kUnset : (m1 - both) + n1;
+        const float top = fmaxf(d0, d1);
+        // in the order of the halves, so that both form the same sum
+        const float a0 = sum * ex2(m - both), a1 = sum1 * ex2(m1 - both);
+        sum = t == 0 ? a0 + a1 : a1 + a0;
+        part[t] = ex2(d0 - top);
+        part[t ^ 1] = ex2(d1 - top);
+        has[t] = n > 0;
+        has[t ^ 1] = x.w != 0;
+        m = both;
+        nn = top;
+        ++merges;
+      }
+      Job job;
+      read(it, job);  // again: scores left no room to keep it
+      const int tok = job.first + (halves ? 0 : t * tile_tokens) + row / p.pack;
+      const bool mine = row < tile_tokens * p.pack && tok < job.lq;
+      // dimensions [from, from + width) of this row, 32 at a time
+      const int width = halves ? HD / 2 : HD, from = halves ? t * (HD / 2) : 0;
+      auto load = [&](int c, float (&o)[32]) {
+        uint32_t x[32];
+        if (!halves) {
+          if (has[0]) {
+            tmem_ld_32x32b_x32(o_addr + t * 128 + c, x);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = has[0] ? __uint_as_float(x[i]) : 0.f;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (has[h]) {
+              tmem_ld_32x32b_x32(o_addr + h * 128 + c, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = fmaf(__uint_as_float(x[i]), part[h], o[i]);
+            }
+        }
+      };
+      if (job.whole) {
+        const bool none = sum == 0.f;
+        const float half = ex2(0.5f * nn), by = half / sum;  // 2^n in two steps: by itself it may leave fp32's range
+        const int64_t at = static_cast<int64_t>(job.q0 + tok) * p.Hq + job.head0 + row % p.pack;
+        const int64_t to = mine ? at * p.D : -1;
+        const uint32_t stage = base + L::kOffOut + warp * 1024;
+        // the halves' numbers lie where the output is staged
+        if (halves) {
+          mbar_arrive(merge_bar);
+          ok = __all_sync(0xffffffffu, mbar_wait(merge_bar, merges & 1, wd, kWhereMerge));
+          ++merges;
+          if (!ok) break;
+        }
+#pragma unroll 1
+        for (int c = from; c < from + width; c += 32) {
+          float o[32];
+          load(c, o);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // 16 dimensions of 32 rows: a store writes whole sectors, two lanes a row
+            __syncwarp();                // what was staged before has been read
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int k = 16 * h + 8 * i + 2 * e;
+                w[e] = none ? 0u : pack_bf16x2(o[k] * half * by, o[k + 1] * half * by);
+              }
+              st_shared_v4(stage + lane * 32 + ((i ^ ((lane >> 2) & 1)) << 4), w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+            const int piece = lane & 1, d = c + 16 * h + 8 * piece;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int r = 16 * i + (lane >> 1);
+              const int64_t there = __shfl_sync(0xffffffffu, to, r);
+              const uint4 v = ld_shared_v4(stage + r * 32 + ((piece ^ ((r >> 2) & 1)) << 4));
+              if (there >= 0 && d < p.D) *reinterpret_cast<uint4*>(p.out + there + d) = v;
+            }
+          }
+        }
+        if (mine && p.lse && (t == 0 || !halves)) p.lse[at] = none ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+      } else {
+        const int64_t tile = 2 * static_cast<int64_t>(job.slot) + (halves ? 0 : t);
+        if (!halves || t == 0) p.part_ml[tile * kRows + row] = make_float4(m, nn, sum, 0.f);
+        float* const out = p.part_o + tile * (kRows * HD);
+        if (halves || has[0]) {
+#pragma unroll 1
+          for (int c = from; c < from + width; c += 32) {
+            float o[32];
+            load(c, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(out + ((c / 4 + i) * kRows + row) * 4) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+      }
+      if (halves) {  // neither half goes on while the other reads its output or its numbers
+        tc_fence_before();
+        mbar_arrive(merge_bar);
+        ok = __all_sync(0xffffffffu, mbar_wait(merge_bar, merges & 1, wd, kWhereMerge));
+        ++merges;
+        if (!ok) break;
+      }
+      tc_fence_before();  // the next job's weights are handed over after these loads
+      done(it);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of a cut unit, a quarter of a row tile (32 rows, one a lane) a block; a warp has every eighth
+// group of four dimensions.
+constexpr int kJoinWarps = 8;
+
+template <int HD>
+__global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const ChunkParams p) {
+  constexpr int kGroups = HD / 4 / kJoinWarps;
+  __shared__ uint2 staged[32][HD / 4 + 1];
+  grid_dep_launch();
+  grid_dep_wait();
+  const Cut cut = p.cuts[blockIdx.x];
+  if (cut.last < 0) return;
+  const int tile_tokens = kRows / p.pack, t = blockIdx.y >> 2;
+  if (t >= cut.tiles) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = (blockIdx.y & 3) * 32 + lane;
+  const int tok = cut.first + t * tile_tokens + row / p.pack;
+  const bool mine = row < tile_tokens * p.pack && tok < cut.lq;
+  if (!__syncthreads_or(mine)) return;
+  const int parts = cut.last - cut.from + 1;
+  auto tile_of = [&](int k) { return 2 * static_cast<int64_t>(2 * (cut.from + k) + (k == 0)) + t; };
+  // the references: the largest of the parts'
+  float m = kUnset;
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k) m = fmaxf(m, p.part_ml[tile_of(k) * kRows + row].x);
+  float n = kUnset;
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k) {
+    const float4 ml = p.part_ml[tile_of(k) * kRows + row];
+    if (ml.x != kUnset) n = fmaxf(n, (ml.x - m) + ml.y);
+  }
+  float sum = 0.f;
+  float4 o[kGroups];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) o[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int k = 0; k < parts; ++k) {
+    const int64_t tile = tile_of(k);
+    const float4 ml = p.part_ml[tile * kRows + row];
+    sum += ml.z * ex2(ml.x - m);
+    if (ml.x == kUnset && ml.z == 0.f) continue;  // it saw nothing, and its output may not be there
+    const float by = ex2((ml.x - m) + (ml.y - n));
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const float4 x = *reinterpret_cast<const float4*>(p.part_o + tile * (kRows * HD) + ((warp + kJoinWarps * g) * kRows + row) * 4);
+      o[g].x = fmaf(x.x, by, o[g].x);
+      o[g].y = fmaf(x.y, by, o[g].y);
+      o[g].z = fmaf(x.z, by, o[g].z);
+      o[g].w = fmaf(x.w, by, o[g].w);
+    }
+  }
+  const bool none = sum == 0.f;
+  const float half = ex2(0.5f * n), by = half / sum;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g)
+    staged[lane][warp + kJoinWarps * g] =
+        none ? make_uint2(0, 0)
+             : make_uint2(pack_bf16x2(o[g].x * half * by, o[g].y * half * by), pack_bf16x2(o[g].z * half * by, o[g].w * half * by));
+  const int64_t at = static_cast<int64_t>(cut.q0 + tok) * p.Hq + cut.head0 + row % p.pack;
+  if (warp == 0 && mine && p.lse) p.lse[at] = none ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+  __syncthreads();
+  const int64_t to = mine ? at * p.D : -1;
+#pragma unroll
+  for (int r = warp; r < 32; r += kJoinWarps) {
+    const int64_t there = __shfl_sync(0xffffffffu, to, r);
+    if (there >= 0 && 4 * lane < p.D) *reinterpret_cast<uint2*>(p.out + there + 4 * lane) = staged[r][lane];
+  }
+}
+
+int heads_packed(int group) {
+  int pack = 1;
+  for (int g = 2; g <= group && g <= kRows; ++g)
+    if (group % g == 0 && kRows % g <= kRows / 16) pack = g;
+  return pack;
+}
+
+sg_status_t launch_error(cudaError_t e) {
+  if (e == cudaSuccess) return SG_OK;
+  note_cuda_error(e);
+  cudaGetLastError();
+  return SG_ERR_CUDA;
+}
+
+template <int HD>
+sg_status_t launch(const AttnShape& s, const AttnArgs& a, const ChunkParams& p) {
+  const uint64_t D = s.D, rows = static_cast<uint64_t>(s.Hk) * s.page;
+  const uint64_t dims[3] = {D, rows, static_cast<uint64_t>(a.cache.num_pages)};
+  const uint64_t sk[2] = {D, static_cast<uint64_t>(a.cache.k_page_stride)}, sv[2] = {D, static_cast<uint64_t>(a.cache.v_page_stride)};
+  // K rows take 128 bytes whatever D is, the rest of them zeros: one layout for the tensor cores
+  const uint32_t bk[3] = {128, static_cast<uint32_t>(s.page), 1}, bv[3] = {HD, static_cast<uint32_t>(s.page), 1};
+  CUtensorMap tmK, tmV;
+  if (!encode_3d(&tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.cache.k, dims, sk, bk, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_3d(&tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.cache.v, dims, sv, bv, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return SG_ERR_CUDA;
+  GemmLaunch l(dim3(s.num_sms), dim3(kThreads), ChunkLayout<HD>::kDynSmem, a.stream, 1);
+  const sg_status_t r = launch_error(cudaLaunchKernelEx(&l.cfg, chunk_kernel<HD>, tmK, tmV, p));
+  if (r != SG_OK) return r;
+  GemmLaunch j(dim3(s.num_sms, 8), dim3(32 * kJoinWarps), 0, a.stream, 1);
+  return launch_error(cudaLaunchKernelEx(&j.cfg, chunk_join_kernel<HD>, p));
+}
+
+template <int HD>
+cudaError_t prepare() {
+  return cudaFuncSetAttribute(chunk_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkLayout<HD>::kDynSmem);
+}
+
+}  // namespace
+
+size_t chunk_workspace_bytes(const AttnShape& s) {
+  return static_cast<size_t>(s.num_sms) * (2 * 2 * kRows * (128 * sizeof(float) + sizeof(float4)) + sizeof(Cut));
+}
+
+cudaError_t chunk_prepare() {
+  const cudaError_t e = prepare<64>();
+  return e == cudaSuccess ? prepare<128>() : e;
+}
+
+sg_status_t chunk_launch(const AttnShape& s, const AttnArgs& a) {
+  ChunkParams p{};
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.q_stride = a.q_stride;
+  p.table = a.table;
+  p.lens = a.lens;
+  p.cu = a.cu_q;
+  p.table_stride = a.cache.num_pages > 0 ? a.table_stride : 0;  // no page, no keys
+  p.k_scale = a.cache.k_scale;
+  p.v_scale = a.cache.v_scale;
+  p.num_pages = a.cache.num_pages;
+  p.T = static_cast<int>(a.Tq);
+  p.B = static_cast<int>(a.B);
+  p.Hq = s.Hq;
+  p.Hk = s.Hk;
+  p.D = s.D;
+  p.page = s.page;
+  while ((1 << p.page_shift) < s.page) ++p.page_shift;
+  p.group = s.Hq / s.Hk;
+  p.pack = heads_packed(p.group);
+  p.head_groups = s.Hq / p.pack;
+  p.skip = s.skip_tile;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.out = static_cast<uint16_t*>(a.out);
+  p.lse = a.lse;
+  p.part_o = static_cast<float*>(s.workspace);
+  p.part_ml = reinterpret_cast<float4*>(p.part_o + static_cast<size_t>(s.num_sms) * 2 * 2 * kRows * 128);
+  p.cuts = reinterpret_cast<Cut*>(p.part_ml + static_cast<size_t>(s.num_sms) * 2 * 2 * kRows);
+  p.status = s.status;
+  p.timeout_ns = s.timeout_ns;
+  AttnArgs args = a;
+  if (args.cache.num_pages == 0) {  // a tensor map has no empty dimension; nothing reads it
+    args.cache.num_pages = 1;
+    args.cache.k = args.cache.v = const_cast<void*>(a.q);
+    args.cache.k_page_stride = args.cache.v_page_stride = static_cast<int64_t>(s.Hk) * s.page * s.D;
+  }
+  return s.D > 64 ? launch<128>(s, args, p) : launch<64>(s, args, p);
+}
+
+}  // namespace sg

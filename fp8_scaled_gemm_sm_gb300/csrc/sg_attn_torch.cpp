@@ -288,6 +288,29 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// chunk(plan, q, cache, block_table, kv_lens, cu_q, scale, out, lse, stream)
+PyObject* chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 10);
+    const Plan& p = plan(a[0]);
+    const Rows q = rows(a[1], p.q_heads, p, "q");
+    const sg_kv_cache_t* c = cache(a[2], p);
+    const int64_t batch = length(a[4], "kv_lens");
+    int64_t width;
+    const int32_t* t = table(a[3], batch, p, &width);
+    const int32_t* lens = ints(a[4], batch, p, "kv_lens");
+    const int32_t* cu = ints(a[5], batch + 1, p, "cu_q");
+    const float scale = scale_or(a[6], p);
+    const Streams s = streams(a[9], p);
+    const at::Tensor out = output(a[7], {q.n, p.q_heads, p.dim}, at::kBFloat16, p, s, "out");
+    const at::Tensor lse = output(a[8], {q.n, p.q_heads}, at::kFloat, p, s, "lse");
+    check(scaled_attn_chunk(p.handle, c, q.data, q.stride, t, width, lens, cu, q.n, batch, scale, out.data_ptr(),
+                            static_cast<float*>(lse.data_ptr()), s.handle),
+          "scaled_attn_chunk");
+    return pair(out, THPVariable_Wrap(lse));
+  });
+}
+
 // prompt(plan, q, k, v, cu_q, cu_k, causal, scale, out, lse, stream)
 PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -457,6 +480,7 @@ PyMethodDef g_methods[] = {
     SG_METHOD("cache", make_cache),
     SG_METHOD("append", append),
     SG_METHOD("decode", decode),
+    SG_METHOD("chunk", chunk),
     SG_METHOD("prompt", prompt),
     SG_METHOD("pool", make_pool),
     SG_METHOD("pool_release", pool_release),

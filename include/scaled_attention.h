@@ -9,6 +9,7 @@
  *   scaled_attn_append   rotate queries and keys by their positions; append keys and
  *                        values to the cache
  *   scaled_attn_decode   attention of each sequence's newest tokens over the cache
+ *   scaled_attn_chunk    attention of chunks of new tokens, as many for each sequence as there are, over the cache
  *   scaled_attn_prompt   attention over whole prompts, packed one after another
  *
  * and scaled_attn_pool_* share the cache's pages out among sequences: release, grow, fork, compact.
@@ -119,6 +120,14 @@ sg_status_t scaled_attn_decode(sg_attn_t h, const sg_kv_cache_t* cache, const vo
                                int64_t qn, const int32_t* table, int64_t table_stride,
                                const int32_t* kv_lens, int64_t B, float scale, void* out, float* lse,
                                sg_stream_t stream);
+
+/* The same for chunks of new tokens, as many for each sequence as there are: q and out have the T rows of B packed
+ * sequences, [cu_q[b], cu_q[b + 1]) the newest tokens of sequence b in order, whose first kv_lens[b] tokens (themselves
+ * included) are in the cache.  Row i of n sees the first kv_lens[b] - (n - 1 - i). */
+sg_status_t scaled_attn_chunk(sg_attn_t h, const sg_kv_cache_t* cache, const void* q, int64_t q_stride,
+                              const int32_t* table, int64_t table_stride, const int32_t* kv_lens,
+                              const int32_t* cu_q, int64_t T, int64_t B, float scale, void* out, float* lse,
+                              sg_stream_t stream);
 
 /* out [Tq][Hq][D] = softmax(scale q k^T) v within each of B packed sequences: queries
  * [cu_q[b], cu_q[b+1]) over keys [cu_k[b], cu_k[b+1]).  causal: with n queries and m keys, query
