@@ -93,7 +93,8 @@ struct ChunkLayout {
   static constexpr int kInfo = 8;                    // key blocks whose scales are held
   static constexpr int kOffInfo = kOffOut + 8 * 1024;        // float2 for each 16 keys
   static constexpr int kOffMask = kOffInfo + kInfo * 64;     // and a word a block: pages that are not there, scales that are NaN
-  static constexpr int kOffRow = kOffMask + kInfo * 4;       // a query row's factor, by job and row
+  static constexpr int kOffLeast = kOffMask + kInfo * 4;     // the least exponent of a block's values
+  static constexpr int kOffRow = kOffLeast + kInfo * 4;      // a query row's factor, by job and row
   static constexpr int kOffBar = kOffRow + 2 * 2 * kRows * 4;
   static constexpr int kNumBars = 2 * (kKStages + kVStages + kHalfStages) + 8 + 4 + 4;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
@@ -435,6 +436,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           const uint32_t slot = count++ & (L::kInfo - 1);
           if ((lane >> 3) == in) st_shared_v2(base + L::kOffInfo + slot * 64 + c8 * 8, __float_as_uint(about.x), __float_as_uint(about.y));
+          float least = about.y;
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+          if (lane == 8 * in) st_shared(base + L::kOffLeast + slot * 4, __float_as_uint(least));
           if (lane == 0) st_shared(base + L::kOffMask + slot * 4, ((gone >> (8 * in)) & 255) | ((nan >> (8 * in)) & 255) << 8);
           const bool mine = (lane >> 3) == in && c8 % (8 / boxes) == 0;
           const int y = (head << p.page_shift) + ((t * kRows + 16 * c8) & (p.page - 1)), part = c8 / (8 / boxes);
@@ -610,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (elect_one()) {
       // ---------------- MMA issuer: one thread for all of it ----------------
       int k_stage = 0, h_stage = 0, q_uses = 0;
-      uint32_t k_phase = 0, h_phase = 0, turn[2] = {0, 0};  // parity of a tile's next weights
+      uint32_t k_phase = 0, h_phase = 0, turn = 0;  // turn: parities of the tiles' next weights, a bit each
       auto wait = [&](uint32_t bar, uint32_t parity, int where) {
         const bool got = mbar_wait<true>(bar, parity, wd, where);
         tc_fence_after();
@@ -627,10 +632,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int blocks = job.t1 - job.t0;
         if (blocks == 0) continue;
         const bool pair = job.tiles == 2;
-        const int keys[2] = {tile_keys(job, 0) - job.t0 * kRows, tile_keys(job, 1) - job.t0 * kRows};
-        const int mine[2] = {tile_blocks(job, 0), tile_blocks(job, 1)};
+        const int keys0 = tile_keys(job, 0) - job.t0 * kRows, keys1 = pair ? tile_keys(job, 1) - job.t0 * kRows : keys0;
+        const int mine0 = tile_blocks(job, 0), mine1 = tile_blocks(job, 1);
         auto scores = [&](int t, int j) {  // S_t = Q K_j^T, in two terms
-          const int n = (min(kRows, keys[pair ? t : 0] - j * kRows) + 15) & ~15;
+          const int n = (min(kRows, (t ? keys1 : keys0) - j * kRows) + 15) & ~15;
           const uint64_t k = kmajor_sw128_desc(base + L::kOffK + k_stage * L::kTile);
 #pragma unroll
           for (int term = 0; term < 2; ++term) {
@@ -651,11 +656,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto output = [&](int t, int j, bool last) {  // O_t += P_t V_j: what is stored first, then the rest
           const uint64_t v = smem_desc(base + L::kOffHalf + h_stage * L::kHalf, L::kBox, 1024, 2);
           constexpr uint32_t idesc = instr_desc(0, 0, kRows, HD) | kIdescBMajorN;
-          const int steps = (min(kRows, keys[pair ? t : 0] - j * kRows) + 15) / 16;
+          const int steps = (min(kRows, (t ? keys1 : keys0) - j * kRows) + 15) / 16;
           const bool first = pair ? j == 0 : j < 2;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            ok = ok && wait(h ? p_full(t) : p_half(t), turn[t], kWhereMmaTmemEmpty);
+            ok = ok && wait(h ? p_full(t) : p_half(t), (turn >> t) & 1, kWhereMmaTmemEmpty);
             if (ok) {
 #pragma unroll
               for (int i = h ? kEarly : 0; i < (h ? 8 : kEarly); ++i)
@@ -663,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (h && last) mma_commit(o_full(t));
             }
           }
-          turn[t] ^= 1;
+          turn ^= 1u << t;
         };
         auto next_v = [&]() {
           mma_commit(h_empty(h_stage));
@@ -679,8 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (pair) {
           ok = ok && k_ready();
           if (ok) {
-            if (mine[0] > 0) scores(0, 0);
-            if (mine[1] > 0) scores(1, 0);
+            if (mine0 > 0) scores(0, 0);
+            if (mine1 > 0) scores(1, 0);
             next_k();
             if (blocks == 1) mma_commit(q_empty);
           }
@@ -688,15 +693,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = v_ready();
             bool k = false;
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-              if (ok && j < mine[t]) {
-                output(t, j, j + 1 == mine[t]);
-                if (ok && j + 1 < mine[t]) {
+            for (int t = 0; t < 2; ++t) {
+              const int mine = t ? mine1 : mine0;
+              if (ok && j < mine) {
+                output(t, j, j + 1 == mine);
+                if (ok && j + 1 < mine) {
                   if (!k) ok = k_ready();
                   k = true;
                   if (ok) scores(t, j + 1);
                 }
               }
+            }
             next_v();
             if (k) {
               next_k();
@@ -704,13 +711,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         } else {
-          for (int j = 0; j < min(blocks, 2) && ok; ++j) {
-            ok = k_ready();
-            if (ok) {
-              scores(j, j);
-              next_k();
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (ok && j < blocks) {
+              ok = k_ready();
+              if (ok) {
+                scores(j, j);
+                next_k();
+              }
             }
-          }
           if (blocks <= 2) mma_commit(q_empty);
           for (int j = 0; j < blocks && ok; ++j) {
             const int t = j & 1;
@@ -776,11 +785,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_addr + 32 * c, s[c]);  // past the last key: hidden below
         const uint32_t slot = (count + (halves ? 2 * j + t : j)) & (L::kInfo - 1);
         const uint32_t gone = ld_shared(mask + slot * 4) & 255;
-        float g[8], b[8];  // factors of the scores, exponents of the values, by 16 keys
+        float g[8];  // factors of the scores by 16 keys; the exponents of their values are read where they are needed
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float4 x = ld_shared_f4(info + slot * 64 + c * 16);
-          g[2 * c] = x.x * factor, b[2 * c] = x.y, g[2 * c + 1] = x.z * factor, b[2 * c + 1] = x.w;
+          g[2 * c] = x.x * factor, g[2 * c + 1] = x.z * factor;
         }
         tmem_wait_ld();
         const int room = lim - (t0 + each * j) * kRows;
@@ -811,7 +820,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto v_top = [&](float ref) {
           float x[8];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) x[c] = (top[c] - ref) + b[c];
+          for (int c = 0; c < 4; ++c) {
+            const float4 y = ld_shared_f4(info + slot * 64 + c * 16);
+            x[2 * c] = (top[2 * c] - ref) + y.y, x[2 * c + 1] = (top[2 * c + 1] - ref) + y.w;
+          }
           return fmaxf(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(x[5], x[6], x[7]));
         };
         if (__any_sync(0xffffffffu, mx > m + kSlack || v_top(m) > nn + (kLift + kSlack))) {
@@ -840,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // before a row has seen a key its references are unset: any do
         const float ref = m == kUnset ? 0.f : m, vref = m == kUnset ? 0.f : nn;
-        float least = fminf(fminf(fminf(b[0], b[1]), fminf(b[2], b[3])), fminf(fminf(b[4], b[5]), fminf(b[6], b[7])));
+        const float least = __uint_as_float(ld_shared(base + L::kOffLeast + slot * 4));
         const bool slow = __any_sync(0xffffffffu, fabsf(ref) > kExact || least - vref < kSpread);
         if (slow) {
           float more = 0.f;
@@ -858,7 +870,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t w[16];  // two blocks' weights
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const float by = slow ? 1.f : g[c], off = slow ? b[c] - vref : (b[c] - vref) - ref;
+          const float b = __uint_as_float(ld_shared(info + slot * 64 + c * 8 + 4));
+          const float by = slow ? 1.f : g[c], off = slow ? b - vref : (b - vref) - ref;
           const uint64_t g2 = pack_f32x2(by, by), off2 = pack_f32x2(off, off);
           uint64_t part = 0;
 #pragma unroll
@@ -871,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[c % 2 * 8 + i] = pack_f16x2(x, y);
           }
           if (!slow) {  // the weights without the values' scale
-            const float out = ex2(vref - b[c]);
+            const float out = ex2(vref - b);
             sum2 = fma_f32x2(part, pack_f32x2(out, out), sum2);
           }
           if (c & 1) {
@@ -899,8 +912,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sum = lo + hi;
       // A tile's output is what its thread has; a unit of one tile has two halves, which meet here: each then
       // writes half of the dimensions of both.
-      float part[2] = {0.f, 0.f};  // what the halves' outputs are multiplied by
-      bool has[2] = {n > 0, false};
+      float part0 = 0.f, part1 = 0.f;  // what the halves' outputs are multiplied by
+      bool has0 = n > 0, has1 = false; // of a tile of its own: has0
       if (halves) {
         const uint32_t stats = base + L::kOffStats;
         st_shared_v4(stats + (t * kRows + row) * 16, __float_as_uint(m), __float_as_uint(nn), __float_as_uint(sum), n > 0);
@@ -915,10 +928,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // in the order of the halves, so that both form the same sum
         const float a0 = sum * ex2(m - both), a1 = sum1 * ex2(m1 - both);
         sum = t == 0 ? a0 + a1 : a1 + a0;
-        part[t] = ex2(d0 - top);
-        part[t ^ 1] = ex2(d1 - top);
-        has[t] = n > 0;
-        has[t ^ 1] = x.w != 0;
+        const float mine = ex2(d0 - top), other = ex2(d1 - top);
+        part0 = t ? other : mine;
+        part1 = t ? mine : other;
+        has0 = t ? x.w != 0 : n > 0;
+        has1 = t ? n > 0 : x.w != 0;
         m = both;
         nn = top;
         ++merges;
@@ -931,24 +945,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int width = halves ? HD / 2 : HD, from = halves ? t * (HD / 2) : 0;
       auto load = [&](int c, float (&o)[32]) {
         uint32_t x[32];
-        if (!halves) {
-          if (has[0]) {
-            tmem_ld_32x32b_x32(o_addr + t * 128 + c, x);
-            tmem_wait_ld();
-          }
+        // the halves as they lie, a tile of its own by 1 and 0
+        const uint32_t at0 = o_addr + (halves ? 0 : t * 128) + c;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = has[0] ? __uint_as_float(x[i]) : 0.f;
-        } else {
+        for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        if (has0) {
+          tmem_ld_32x32b_x32(at0, x);
+          tmem_wait_ld();
+          const float by = halves ? part0 : 1.f;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(x[i]) * by;
+        }
+        if (has1) {
+          tmem_ld_32x32b_x32(o_addr + 128 + c, x);
+          tmem_wait_ld();
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (has[h]) {
-              tmem_ld_32x32b_x32(o_addr + h * 128 + c, x);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = fmaf(__uint_as_float(x[i]), part[h], o[i]);
-            }
+          for (int i = 0; i < 32; ++i) o[i] = fmaf(__uint_as_float(x[i]), part1, o[i]);
         }
       };
       if (job.whole) {
@@ -997,7 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t tile = 2 * static_cast<int64_t>(job.slot) + (halves ? 0 : t);
         if (!halves || t == 0) p.part_ml[tile * kRows + row] = make_float4(m, nn, sum, 0.f);
         float* const out = p.part_o + tile * (kRows * HD);
-        if (halves || has[0]) {
+        if (halves || has0) {
 #pragma unroll 1
           for (int c = from; c < from + width; c += 32) {
             float o[32];
