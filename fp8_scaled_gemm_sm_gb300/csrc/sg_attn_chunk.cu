@@ -67,6 +67,7 @@ struct ChunkParams {
   int T, B, Hq, Hk, D, page, page_shift;
   int group;            // query heads of a key/value head
   int pack;             // query heads packed into a tile
+  int pack_inverse;     // a row's token: row * pack_inverse >> 16
   int head_groups;      // Hq / pack
   int skip;             // number of a key block that is not loaded (scaled_attn_set_debug); -1: none
   float scale_log2;
@@ -93,8 +94,8 @@ struct ChunkLayout {
   static constexpr int kInfo = 8;                    // key blocks whose scales are held
   static constexpr int kOffInfo = kOffOut + 8 * 1024;        // float2 for each 16 keys
   static constexpr int kOffMask = kOffInfo + kInfo * 64;     // and a word a block: pages that are not there, scales that are NaN
-  static constexpr int kOffLeast = kOffMask + kInfo * 4;     // the least exponent of a block's values
-  static constexpr int kOffRow = kOffLeast + kInfo * 4;      // a query row's factor, by job and row
+  static constexpr int kOffRange = kOffMask + kInfo * 4;     // the least and the largest exponent of a block's values
+  static constexpr int kOffRow = kOffRange + kInfo * 8;      // a query row's factor, by job and row
   static constexpr int kOffBar = kOffRow + 2 * 2 * kRows * 4;
   static constexpr int kNumBars = 2 * (kKStages + kVStages + kHalfStages) + 8 + 4 + 4;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
@@ -199,6 +200,11 @@ struct Walk {
   }
 };
 
+template <bool V>
+struct Flag {
+  static constexpr bool value = V;
+};
+
 // Two fp32 values to two e4m3 (e5m2) codes, to nearest even; two e4m3 codes to fp16.
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   uint16_t r;
@@ -231,6 +237,11 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
   const uint4 v = ld_shared_v4(a);
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
 }
 __device__ __forceinline__ uint32_t ld_shared(uint32_t a) {
   uint32_t v;
@@ -286,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(p_full(t), kRows);
       mbar_init(job_empty(t), kJobReaders);
     }
-    mbar_init(q_full, 2);
+    mbar_init(q_full, 8);
     mbar_init(merge_bar, 2 * kRows);
     misc[1] = 0;
     fence_mbarrier_init();
@@ -436,10 +447,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           const uint32_t slot = count++ & (L::kInfo - 1);
           if ((lane >> 3) == in) st_shared_v2(base + L::kOffInfo + slot * 64 + c8 * 8, __float_as_uint(about.x), __float_as_uint(about.y));
-          float least = about.y;
+          float least = about.y, most = about.y;
 #pragma unroll
-          for (int o = 1; o < 8; o <<= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
-          if (lane == 8 * in) st_shared(base + L::kOffLeast + slot * 4, __float_as_uint(least));
+          for (int o = 1; o < 8; o <<= 1) {
+            least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          }
+          if (lane == 8 * in) st_shared_v2(base + L::kOffRange + slot * 8, __float_as_uint(least), __float_as_uint(most));
           if (lane == 0) st_shared(base + L::kOffMask + slot * 4, ((gone >> (8 * in)) & 255) | ((nan >> (8 * in)) & 255) << 8);
           const bool mine = (lane >> 3) == in && c8 % (8 / boxes) == 0;
           const int y = (head << p.page_shift) + ((t * kRows + 16 * c8) & (p.page - 1)), part = c8 / (8 / boxes);
@@ -480,88 +494,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((v_issued >> s) & 1) mbar_wait_drain(v_full(s), (v_par >> s) & 1, 200000000ull);
       }
     } else if (warp >= 10) {
-      // ---------------- queries to two terms, values to fp16 ----------------
+      // ---------------- values to fp16 ----------------
       const int me = warp - 10;
-      int q_fills = 0, v_stage = 0, h_stage = 0, count = 0;
+      int v_stage = 0, h_stage = 0, count = 0;
       uint32_t v_phase = 0, h_phase = 0;
       Job job;
       bool ok = true;
       for (int it = 0; ok && peek(it, job); ++it) {
         const int blocks = job.t1 - job.t0;
-        if (blocks > 0) {
-          if (q_fills > 0) ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (q_fills - 1) & 1, wd, kWhereConvert));
-          if (!ok) break;
-          ++q_fills;
-          // HD / 8 lanes a row, 8 dimensions each; tokens past the unit's last have no rows
-          constexpr int kLanes = HD / 8, kAtOnce = 32 / kLanes;
-          const int d = 8 * (lane % kLanes);
-          const int live = min(job.lq - job.first, job.tiles * tile_tokens);
-#pragma unroll 1
-          for (int t = 0; t < job.tiles; ++t) {
-            const int rows = min(live - t * tile_tokens, tile_tokens) * p.pack;
-            const uint32_t hi_tile = q_tile(t, 0), lo_tile = q_tile(t, 1), factors = base + L::kOffRow + (((it & 1) * 2 + t) * kRows) * 4;
-            // rows without a query are zeros, so that what their threads find does not vary
-            for (int i = max(rows, 0) * 8 + me * 32 + lane; i < kRows * 8; i += 64) {
-              st_shared_v4(hi_tile + i * 16, 0, 0, 0, 0);
-              st_shared_v4(lo_tile + i * 16, 0, 0, 0, 0);
-            }
-            constexpr int kBatch = 4;  // rows a lane has on their way
-#pragma unroll 1
-            for (int r0 = me * kAtOnce * kBatch; r0 < rows; r0 += 2 * kAtOnce * kBatch) {
-              uint4 raw[kBatch];
-#pragma unroll
-              for (int i = 0; i < kBatch; ++i) {
-                const int r = r0 + i * kAtOnce + lane / kLanes;
-                raw[i] = make_uint4(0, 0, 0, 0);
-                if (r < rows && d < p.D)
-                  raw[i] = *reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(job.q0 + job.first + t * tile_tokens + r / p.pack) * p.q_stride +
-                                                           (job.head0 + r % p.pack) * p.D + d);
-              }
-#pragma unroll
-              for (int i = 0; i < kBatch; ++i) {
-                const int r = r0 + i * kAtOnce + lane / kLanes;
-                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-                float x[8];
-                float top = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  x[2 * e] = __uint_as_float(w[e] << 16);
-                  x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-                  top = fmaxf(top, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
-                }
-#pragma unroll
-                for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                // the row's largest value to [2^7, 2^8)
-                const int field = min(261 - static_cast<int>(__float_as_uint(top) >> 23), 253);
-                const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
-                uint32_t hi[2], lo[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  hi[e] = lo[e] = 0;
-#pragma unroll
-                  for (int k = 0; k < 2; ++k) {
-                    const float a = x[4 * e + 2 * k] * up, b = x[4 * e + 2 * k + 1] * up;
-                    const uint32_t code = to_e4m3x2(a, b);
-                    float ha, hb;
-                    half2_floats(from_e4m3x2(code), ha, hb);
-                    hi[e] |= code << (16 * k);
-                    lo[e] |= to_e5m2x2(a - ha, b - hb) << (16 * k);
-                  }
-                }
-                if (r < rows) {
-                  const uint32_t at = r * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 8);
-                  st_shared_v2(hi_tile + at, hi[0], hi[1]);
-                  st_shared_v2(lo_tile + at, lo[0], lo[1]);
-                  if (d == 0)  // 1 / up; a row with an infinity is NaN
-                    st_shared(factors + r * 4, top == INFINITY ? 0x7FC00000u : static_cast<uint32_t>(254 - field) << 23);
-                }
-              }
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q_full);
-        }
         for (int j = 0; j < blocks; ++j) {
           ok = __all_sync(0xffffffffu, mbar_wait(v_full(v_stage), v_phase, wd, kWhereConvert) &&
                                            mbar_wait(h_empty(h_stage), h_phase ^ 1, wd, kWhereConvert));
@@ -569,31 +509,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t from = base + L::kOffRaw + v_stage * L::kRaw, to = base + L::kOffHalf + h_stage * L::kHalf;
           const uint32_t nan = ld_shared(base + L::kOffMask + (count++ & (L::kInfo - 1)) * 4) >> 8;
           const int past = job.lk - (job.t0 + j) * kRows;  // rows from here on are not this sequence's
-          constexpr int kChunks = HD / 16;                 // 16-byte runs of a row of codes
-          const int chunk = lane % kChunks;
-#pragma unroll 4
-          for (int r0 = 0; r0 < kRows / 2; r0 += 32 / kChunks) {
-            const int r = me * (kRows / 2) + r0 + lane / kChunks;
-            uint4 x = ld_shared_v4(from + r * HD + chunk * 16);
-            if (past < kRows && r >= past) x = make_uint4(0, 0, 0, 0);
-            if (nan && ((nan >> (r >> 4)) & 1) && r < past) x = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            uint32_t y[8];
+          // A lane takes a run of 16 codes to two runs of 16 bytes of fp16.  Eight lanes take four runs of two rows, 5 apart
+          // (1, where a row has four runs), so that they meet in no bank: neither reading, with the codes' swizzle, nor writing.
+          const int q = lane >> 3, sub = (lane >> 2) & 1;
+          const int r8 = HD == 128 ? (sub ? (2 * q + 5) & 7 : 2 * q) : lane >> 2;
+          auto convert = [&](auto plain) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              y[2 * e] = from_e4m3x2(w[e]);
-              y[2 * e + 1] = from_e4m3x2(w[e] >> 16);
-            }
-            // runs 2 c and 2 c + 1 of the fp16 row; a row's upper half of lanes writes them the other way round, so that
-            // the eight lanes of a row meet in no bank
-            const uint32_t box = to + chunk / 4 * L::kBox + r * 128;
-            const int run = 2 * (chunk % 4), flip = HD == 128 ? chunk >> 2 : 0;
+            for (int h = 0; h < HD / 64; ++h) {
+              const int run = 4 * h + (lane & 3);
+              const uint32_t src = from + (me * (kRows / 2) + r8) * HD + (HD == 128 ? (run ^ r8) << 4 : run << 4);
+              const uint32_t dst = to + h * L::kBox + (me * (kRows / 2) + r8) * 128;
+              const uint32_t to0 = dst + (((2 * (lane & 3)) ^ r8) << 4), to1 = dst + (((2 * (lane & 3) + 1) ^ r8) << 4);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int h = k ^ flip;
-              st_shared_v4(box + (((run + h) ^ (r & 7)) << 4), h ? y[4] : y[0], h ? y[5] : y[1], h ? y[6] : y[2], h ? y[7] : y[3]);
+              for (int i = 0; i < kRows / 16; ++i) {
+                uint4 x = ld_shared_v4(src + i * 8 * HD);
+                if constexpr (!decltype(plain)::value) {
+                  const int r = me * (kRows / 2) + 8 * i + r8;
+                  if ((nan >> (r >> 4)) & 1) x = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                  if (r >= past) x = make_uint4(0, 0, 0, 0);
+                }
+                st_shared_v4(to0 + i * 1024, from_e4m3x2(x.x), from_e4m3x2(x.x >> 16), from_e4m3x2(x.y), from_e4m3x2(x.y >> 16));
+                st_shared_v4(to1 + i * 1024, from_e4m3x2(x.z), from_e4m3x2(x.z >> 16), from_e4m3x2(x.w), from_e4m3x2(x.w >> 16));
+              }
             }
-          }
+          };
+          if (past >= kRows && nan == 0)
+            convert(Flag<true>{});
+          else
+            convert(Flag<false>{});
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -752,7 +695,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quarter * 32 + lane;
     uint32_t turn = 0, outputs = 0, merges = 0;  // parities of the next scores, the next output, the next meeting of the halves
     int count = 0;                               // key blocks of the jobs before
+    int q_fills = 0;
+    // The query rows of a job that has key blocks, as two terms: a share of them a warp.  Past the job's scores that
+    // came before; false: the CTA gives up.
+    auto queries = [&](int i, const Job& job) {
+      if (q_fills > 0 && !__all_sync(0xffffffffu, mbar_wait(q_empty, (q_fills - 1) & 1, wd, kWhereConvert))) return false;
+      ++q_fills;
+      // HD / 8 lanes a row, 8 dimensions each
+      constexpr int kLanes = HD / 8, kAtOnce = 32 / kLanes, kBatch = 4;
+      const int d = 8 * (lane % kLanes), share = job.tiles == 2 ? 32 : 16, tile = job.tiles == 2 ? t : 0;
+      const int rows = min(job.lq - job.first - tile * tile_tokens, tile_tokens) * p.pack;  // those that have a query
+      const uint32_t hi_tile = q_tile(tile, 0), lo_tile = q_tile(tile, 1), factors = base + L::kOffRow + (((i & 1) * 2 + tile) * kRows) * 4;
+      const int begin = (job.tiles == 2 ? quarter : warp) * share;
+      const uint16_t* const from = p.q + static_cast<int64_t>(job.q0 + job.first + tile * tile_tokens) * p.q_stride + job.head0 * p.D + d;
+#pragma unroll 1
+      for (int r0 = begin; r0 < begin + share; r0 += kAtOnce * kBatch) {
+        uint4 raw[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int r = r0 + k * kAtOnce + lane / kLanes, token = r * p.pack_inverse >> 16;
+          raw[k] = make_uint4(0, 0, 0, 0);  // rows without a query are zeros, so that what their threads find does not vary
+          if (r < rows && d < p.D) raw[k] = *reinterpret_cast<const uint4*>(from + token * p.q_stride + (r - token * p.pack) * p.D);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int r = r0 + k * kAtOnce + lane / kLanes;
+          const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+          float x[8];
+          float top = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[2 * e] = __uint_as_float(w[e] << 16);
+            x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+            top = fmaxf(top, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
+          }
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // the row's largest value to [2^7, 2^8)
+          const int field = min(261 - static_cast<int>(__float_as_uint(top) >> 23), 253);
+          const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            hi[e] = lo[e] = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float a = x[4 * e + 2 * h] * up, b = x[4 * e + 2 * h + 1] * up;
+              const uint32_t code = to_e4m3x2(a, b);
+              float ha, hb;
+              half2_floats(from_e4m3x2(code), ha, hb);
+              hi[e] |= code << (16 * h);
+              lo[e] |= to_e5m2x2(a - ha, b - hb) << (16 * h);
+            }
+          }
+          const uint32_t at = r * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 8);
+          st_shared_v2(hi_tile + at, hi[0], hi[1]);
+          st_shared_v2(lo_tile + at, lo[0], lo[1]);
+          if (d == 0)  // 1 / up; a row with an infinity is NaN
+            st_shared(factors + r * 4, top == INFINITY ? 0x7FC00000u : static_cast<uint32_t>(254 - field) << 23);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+      return true;
+    };
     bool ok = true;
+    {
+      Job job;
+      if (peek(0, job) && job.t1 > job.t0) ok = queries(0, job);
+    }
 #pragma unroll 1
     for (int it = 0; ok; ++it) {
       int n, lim, t0, each, blocks;  // key blocks of this tile; keys that this row sees; the job's first block; blocks from one to the next
@@ -817,16 +829,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           top[c] = fmaxf(x, y) * g[c];
         }
         const float mx = fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]), max3(top[5], top[6], top[7]));
-        auto v_top = [&](float ref) {
-          float x[8];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float4 y = ld_shared_f4(info + slot * 64 + c * 16);
-            x[2 * c] = (top[2 * c] - ref) + y.y, x[2 * c + 1] = (top[2 * c + 1] - ref) + y.w;
-          }
-          return fmaxf(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(x[5], x[6], x[7]));
-        };
-        if (__any_sync(0xffffffffu, mx > m + kSlack || v_top(m) > nn + (kLift + kSlack))) {
+        const uint2 range = ld_shared_v2(base + L::kOffRange + slot * 8);
+        const float least = __uint_as_float(range.x), most = __uint_as_float(range.y);
+        // may a reference have to move?  (the largest exponent stands for those of the largest scores)
+        if (__any_sync(0xffffffffu, mx > m + kSlack || (mx - m) + most > nn + (kLift + kSlack))) {
           const float up = ceilf(mx);
           if (up > m) {
             const float by = ex2(m - up);
@@ -834,11 +840,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             nn += m - up;
             m = up;
           }
-          const float vx = ceilf(v_top(m)) - kLift;
+          float x[8];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float4 y = ld_shared_f4(info + slot * 64 + c * 16);
+            x[2 * c] = (top[2 * c] - m) + y.y, x[2 * c + 1] = (top[2 * c + 1] - m) + y.w;
+          }
+          const float vx = ceilf(fmaxf(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(x[5], x[6], x[7]))) - kLift;
           const bool lift = vx > nn;
           const float by = lift ? ex2(nn - vx) : 1.f;
           if (lift) nn = vx;
-          if (j > 0) {
+          if (j > 0 && __any_sync(0xffffffffu, lift)) {
 #pragma unroll 1
             for (int c = 0; c < HD / 16; ++c) {  // S fills the registers: a little of O at a time
               uint32_t o[16];
@@ -852,55 +864,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // before a row has seen a key its references are unset: any do
         const float ref = m == kUnset ? 0.f : m, vref = m == kUnset ? 0.f : nn;
-        const float least = __uint_as_float(ld_shared(base + L::kOffLeast + slot * 4));
-        const bool slow = __any_sync(0xffffffffu, fabsf(ref) > kExact || least - vref < kSpread);
-        if (slow) {
-          float more = 0.f;
+        if (!__any_sync(0xffffffffu, fabsf(ref) > kExact || least - vref < kSpread)) {
+          uint32_t w[16];  // two blocks' weights
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
+          for (int c = 0; c < 8; ++c) {
+            const float b = __uint_as_float(ld_shared(info + slot * 64 + c * 8 + 4));
+            const float up = b - vref, off = up - ref, out = ex2(-up);
+            const uint64_t g2 = pack_f32x2(g[c], g[c]), off2 = pack_f32x2(off, off);
+            uint64_t part = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float x, y;
+              unpack_f32x2(fma_f32x2(pack_f32x2(s[c / 2][c % 2 * 16 + 2 * i], s[c / 2][c % 2 * 16 + 2 * i + 1]), g2, off2), x, y);
+              x = ex2(x);
+              y = ex2(y);
+              part = i ? add_f32x2(part, pack_f32x2(x, y)) : pack_f32x2(x, y);
+              w[c % 2 * 8 + i] = pack_f16x2(x, y);
+            }
+            sum2 = fma_f32x2(part, pack_f32x2(out, out), sum2);  // the weights without the values' scale
+            if (c & 1) {
+              if (c / 2 == kEarly / 2) {  // by now what was stored before is there
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_half(t));
+              }
+              tmem_st_32x32b_x16(s_addr + 16 * (c / 2), w);
+            }
+          }
+        } else {
+          // Score, difference and sum one by one, 16 keys at a time; scores are still in tensor memory, and
+          // weights (half as wide) do not reach those that are yet to be read.
+          const bool edge = __any_sync(0xffffffffu, room < kRows) || gone;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t x[16], w[8];
+            tmem_ld_32x32b_x16(s_addr + 16 * c, x);
+            const float2 about = make_float2(__uint_as_float(ld_shared(info + slot * 64 + c * 8)), __uint_as_float(ld_shared(info + slot * 64 + c * 8 + 4)));
+            const int left = !edge ? 16 : (gone >> c) & 1 ? 0 : room - 16 * c;
+            const float by = about.x * factor;
+            tmem_wait_ld();
+            float more = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              uint32_t& x = s[c / 2][c % 2 * 16 + i];
-              const float y = __fsub_rn(__fmul_rn(__uint_as_float(x), g[c]), ref);
+              const float y = i < left ? __fsub_rn(__fmul_rn(__uint_as_float(x[i]), by), ref) : -INFINITY;
               more += ex2(y);
-              x = __float_as_uint(y);
+              x[i] = __float_as_uint(ex2(y + (about.y - vref)));
             }
-          sum2 = add_f32x2(sum2, pack_f32x2(more, 0.f));
-        }
-        uint32_t w[16];  // two blocks' weights
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float b = __uint_as_float(ld_shared(info + slot * 64 + c * 8 + 4));
-          const float by = slow ? 1.f : g[c], off = slow ? b - vref : (b - vref) - ref;
-          const uint64_t g2 = pack_f32x2(by, by), off2 = pack_f32x2(off, off);
-          uint64_t part = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float x, y;
-            unpack_f32x2(fma_f32x2(pack_f32x2(s[c / 2][c % 2 * 16 + 2 * i], s[c / 2][c % 2 * 16 + 2 * i + 1]), g2, off2), x, y);
-            x = ex2(x);
-            y = ex2(y);
-            part = i ? add_f32x2(part, pack_f32x2(x, y)) : pack_f32x2(x, y);
-            w[c % 2 * 8 + i] = pack_f16x2(x, y);
+            for (int i = 0; i < 8; ++i) w[i] = pack_f16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            sum2 = add_f32x2(sum2, pack_f32x2(more, 0.f));
+            tmem_st_32x32b_x8(s_addr + 8 * c, w);
           }
-          if (!slow) {  // the weights without the values' scale
-            const float out = ex2(vref - b);
-            sum2 = fma_f32x2(part, pack_f32x2(out, out), sum2);
-          }
-          if (c & 1) {
-            if (c / 2 == kEarly / 2) {  // by now what was stored before is there
-              tmem_wait_st();
-              tc_fence_before();
-              mbar_arrive(p_half(t));
-            }
-            tmem_st_32x32b_x16(s_addr + 16 * (c / 2), w);
-          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(p_half(t));
         }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(p_full(t));
       }
       count += blocks;
+      if (ok) {  // the next job's queries, while the last product runs
+        Job job;
+        if (peek(it + 1, job) && job.t1 > job.t0) ok = queries(it + 1, job);
+      }
       if (n > 0 && ok) {
         ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), outputs, wd, kWhereEpiTmemFull));
         outputs ^= 1;
@@ -1132,7 +1159,8 @@ sg_status_t launch(const AttnShape& s, const AttnArgs& a, const ChunkParams& p) 
   const uint32_t bk[3] = {128, static_cast<uint32_t>(s.page), 1}, bv[3] = {HD, static_cast<uint32_t>(s.page), 1};
   CUtensorMap tmK, tmV;
   if (!encode_3d(&tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.cache.k, dims, sk, bk, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_3d(&tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.cache.v, dims, sv, bv, CU_TENSOR_MAP_SWIZZLE_NONE))
+      !encode_3d(&tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.cache.v, dims, sv, bv,
+                 HD == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE))
     return SG_ERR_CUDA;
   GemmLaunch l(dim3(s.num_sms), dim3(kThreads), ChunkLayout<HD>::kDynSmem, a.stream, 1);
   const sg_status_t r = launch_error(cudaLaunchKernelEx(&l.cfg, chunk_kernel<HD>, tmK, tmV, p));
@@ -1177,6 +1205,7 @@ sg_status_t chunk_launch(const AttnShape& s, const AttnArgs& a) {
   while ((1 << p.page_shift) < s.page) ++p.page_shift;
   p.group = s.Hq / s.Hk;
   p.pack = heads_packed(p.group);
+  p.pack_inverse = 65536 / p.pack + 1;
   p.head_groups = s.Hq / p.pack;
   p.skip = s.skip_tile;
   p.scale_log2 = a.scale * 1.4426950408889634f;
