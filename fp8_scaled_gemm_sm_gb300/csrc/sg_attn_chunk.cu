@@ -38,11 +38,13 @@ namespace sg {
 namespace {
 
 constexpr int kRows = 128;  // rows of a tile, keys of a block
-constexpr int kThreads = 640;
-constexpr int kSoftmaxWarps = 16;
-constexpr int kSoftmaxRegs = 104, kIssueRegs = 64;  // 4 x 104 + 64 = 5 x 96, what the block is launched with
+constexpr int kThreads = 384;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxRegs = 208, kIssueRegs = 88;  // 2 x 208 + 88 = 3 x 168, what the block is launched with
 constexpr int kWhereJob = 0x41, kWhereMerge = 0x42, kWhereConvert = 0x43;  // waits beside those of sg_ptx.cuh
 constexpr int kJobReaders = kSoftmaxWarps + 3;  // warps that take jobs
+constexpr int kEarly = 4;        // 16-key steps of a block whose weights are handed over first
+constexpr int kAsks = 2000;      // of a wait that is due soon
 constexpr int kUnitCost = 512;   // what a unit costs beside its keys, in keys of one row tile
 constexpr int kUncut = 8;        // units of up to 1 / kUncut of a range are not cut
 constexpr int kLeast = 1024;     // of a range; at least 256, so that every range of a cut unit has a block of it
@@ -92,22 +94,20 @@ struct ChunkLayout {
   static constexpr int kOffK = 4 * kTile;            // after two terms of two query tiles
   static constexpr int kOffHalf = kOffK + kKStages * kTile;
   static constexpr int kOffRaw = kOffHalf + kHalfStages * kHalf;
-  static constexpr int kOffStats = kOffRaw + kVStages * kRaw;  // a row's references and sum, by row tile and half of the keys
-  static constexpr int kOffSwap = kOffStats + 4 * kRows * 16;  // its largest score and value weight
+  static constexpr int kOffStats = kOffRaw + kVStages * kRaw;  // a row's references and sum, by row tile
   static constexpr int kInfo = 8;                    // key blocks whose scales are held
-  static constexpr int kOffInfo = kOffSwap + 4 * kRows * 8;        // for each 16 keys: the scores' factor, the values' exponent, twice each
-  static constexpr int kOffInverse = kOffInfo + kInfo * 128; // 2^-exponent
+  static constexpr int kOffInfo = kOffStats + 2 * kRows * 16;        // of its 16-key blocks: the scores' factors, the values' exponents
+  static constexpr int kOffInverse = kOffInfo + kInfo * 64;  // 2^-exponent
   static constexpr int kOffMask = kOffInverse + kInfo * 32;  // a word a block: pages that are not there, value scales that are NaN, odd ones
-  static constexpr int kOffRange = kOffMask + kInfo * 4;     // the least exponent of a block's values
-  static constexpr int kOffRow = kOffRange + kInfo * 4;      // a query row's factor, by job and row
+  static constexpr int kOffRow = kOffMask + kInfo * 4;      // a query row's factor, by job and row
   static constexpr int kOffBar = kOffRow + 2 * 2 * kRows * 4;
-  static constexpr int kNumBars = 2 * (kKStages + kVStages + kHalfStages) + 10 + 6 + 8;
+  static constexpr int kNumBars = 2 * (kKStages + kVStages + kHalfStages) + 10 + 8 + kInfo;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffJobs = kOffMisc + 16;
   static constexpr int kOffSums = kOffStats;         // while work is planned: int64 per thread
   static constexpr int kBytes = kOffJobs + 2 * 48;
   static constexpr int kDynSmem = kBytes + 1024;
-  static_assert(kThreads * 8 <= 4 * kRows * 16 && kOffInfo % 16 == 0 && kOffBar % 8 == 0 && kOffJobs % 16 == 0 && kDynSmem <= 232448, "shared memory");
+  static_assert(kThreads * 8 <= 2 * kRows * 16 && kOffInfo % 16 == 0 && kOffBar % 8 == 0 && kOffJobs % 16 == 0 && kDynSmem <= 232448, "shared memory");
 };
 
 // Key blocks; sizes reach 2^31.
@@ -241,9 +241,6 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
   const uint4 v = ld_shared_v4(a);
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
-__device__ __forceinline__ void ld_shared_pairs(uint32_t a, uint64_t& x, uint64_t& y) {
-  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a) : "memory");
-}
 __device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
@@ -257,6 +254,15 @@ __device__ __forceinline__ uint32_t ld_shared(uint32_t a) {
 __device__ __forceinline__ void st_shared(uint32_t a, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
 __device__ __forceinline__ void st_shared_v2(uint32_t a, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+
+// Waits for a phase that is due within microseconds: asks again and again before it waits as mbar_wait does, which wakes
+// later (4 chunks behind contexts @@@).  For few warps: asking takes issue slots.
+__device__ __forceinline__ bool mbar_wait_soon(uint32_t bar, uint32_t parity, const Watchdog& wd, int where) {
+#pragma unroll 1
+  for (int i = 0; i < kAsks; ++i)
+    if (mbar_probe(bar, parity)) return true;
+  return mbar_wait(bar, parity, wd, where);
 }
 
 template <int HD>
@@ -281,9 +287,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto o_full = [&](int t) { return bar0 + 8 * (kMore + 4 + t); };
   auto job_full = [&](int s) { return bar0 + 8 * (kMore + 6 + s); };
   auto job_empty = [&](int s) { return bar0 + 8 * (kMore + 8 + s); };
-  auto drain_bar = [&](int t) { return bar0 + 8 * (kMore + 10 + t); };
+  const uint32_t drain_bar = bar0 + 8 * (kMore + 10);
   const uint32_t q_full = bar0 + 8 * (kMore + 12), q_empty = bar0 + 8 * (kMore + 13), merge_bar = bar0 + 8 * (kMore + 14);
-  auto swap_bar = [&](int i) { return bar0 + 8 * (kMore + 15 + i); };
+  auto p_half = [&](int t) { return bar0 + 8 * (kMore + 15 + t); };
+  auto info_full = [&](uint32_t slot) { return bar0 + 8 * (kMore + 17 + slot); };
   int* misc = reinterpret_cast<int*>(smem + L::kOffMisc);  // [0] TMEM base, [1] abort
   Job* jobs = reinterpret_cast<Job*>(smem + L::kOffJobs);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -296,16 +303,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 32) {
     for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar0 + 8 * i, 1);
-    for (int s = 0; s < KS; ++s) mbar_init(k_empty(s), 2);
-    for (int s = 0; s < HS; ++s) mbar_init(h_empty(s), 2);
+    for (int s = 0; s < VS; ++s) mbar_init(v_empty(s), 2);
+    for (int s = 0; s < HS; ++s) mbar_init(h_full(s), 2);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(p_full(t), 2 * kRows);
+      mbar_init(p_full(t), kRows);
+      mbar_init(p_half(t), kRows);
       mbar_init(job_empty(t), kJobReaders);
     }
     mbar_init(q_full, kSoftmaxWarps);
-    mbar_init(q_empty, 2);
-    mbar_init(merge_bar, 4 * kRows);
-    for (int i = 0; i < 8; ++i) mbar_init(swap_bar(i), 64);
+    mbar_init(merge_bar, 2 * kRows);
     misc[1] = 0;
     fence_mbarrier_init();
   }
@@ -456,17 +462,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t slot = count++ & (L::kInfo - 1);
           if ((lane >> 3) == in) {
             const uint32_t x = __float_as_uint(about.x), y = __float_as_uint(about.y);
-            st_shared_v4(base + L::kOffInfo + slot * 128 + c8 * 16, x, x, y, y);
+            st_shared(base + L::kOffInfo + slot * 64 + c8 * 4, x);
+            st_shared(base + L::kOffInfo + slot * 64 + 32 + c8 * 4, y);
             st_shared(base + L::kOffInverse + slot * 32 + c8 * 4, __float_as_uint(ex2(-about.y)));
           }
-          float least = about.y;
-#pragma unroll
-          for (int o = 1; o < 8; o <<= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
-          if (lane == 8 * in) st_shared(base + L::kOffRange + slot * 4, __float_as_uint(least));
           if (lane == 0) st_shared(base + L::kOffMask + slot * 4, ((gone >> (8 * in)) & 255) | ((nan >> (8 * in)) & 255) << 8 | ((odd >> (8 * in)) & 255) << 16);
           const bool mine = (lane >> 3) == in && c8 % (8 / boxes) == 0;
           const int y = (head << p.page_shift) + ((t * kRows + 16 * c8) & (p.page - 1)), part = c8 / (8 / boxes);
           __syncwarp();
+          if (lane == 0) mbar_arrive(info_full(slot));
           if (t != p.skip) {
             if (lane == 0) mbar_arrive_expect_tx(k_full(k_stage), L::kTile);
             __syncwarp();
@@ -502,8 +506,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < VS; ++s)
           if ((v_issued >> s) & 1) mbar_wait_drain(v_full(s), (v_par >> s) & 1, 200000000ull);
       }
-    } else if (warp == kSoftmaxWarps + 3) {
+    } else if (warp >= kSoftmaxWarps + 2) {
       // ---------------- values to fp16 ----------------
+      const int me = warp - kSoftmaxWarps - 2;
       int v_stage = 0, h_stage = 0, count = 0;
       uint32_t v_phase = 0, h_phase = 0;
       Job job;
@@ -511,8 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = 0; ok && peek(it, job); ++it) {
         const int blocks = job.t1 - job.t0;
         for (int j = 0; j < blocks; ++j) {
-          ok = __all_sync(0xffffffffu, mbar_wait(v_full(v_stage), v_phase, wd, kWhereConvert) &&
-                                           mbar_wait(h_empty(h_stage), h_phase ^ 1, wd, kWhereConvert));
+          ok = __all_sync(0xffffffffu, mbar_wait_soon(v_full(v_stage), v_phase, wd, kWhereConvert) &&
+                                           mbar_wait_soon(h_empty(h_stage), h_phase ^ 1, wd, kWhereConvert));
           if (!ok) break;
           const uint32_t from = base + L::kOffRaw + v_stage * L::kRaw, to = base + L::kOffHalf + h_stage * L::kHalf;
           const uint32_t nan = (ld_shared(base + L::kOffMask + (count++ & (L::kInfo - 1)) * 4) >> 8) & 255;
@@ -523,10 +528,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int r8 = HD == 128 ? (sub ? (2 * q + 5) & 7 : 2 * q) : lane >> 2;
           auto convert = [&](auto plain) {
 #pragma unroll 1
-            for (int h = 0; h < HD / 32; ++h) {  // half of the rows, four of a row's runs
-              const int r0 = (h & 1) * (kRows / 2) + r8, run = 4 * (h >> 1) + (lane & 3);
+            for (int h = 0; h < HD / 64; ++h) {  // four of a row's runs
+              const int r0 = me * (kRows / 2) + r8, run = 4 * h + (lane & 3);
               const uint32_t src = from + r0 * HD + (HD == 128 ? (run ^ r8) << 4 : run << 4);
-              const uint32_t dst = to + (h >> 1) * L::kBox + r0 * 128;
+              const uint32_t dst = to + h * L::kBox + r0 * 128;
               const uint32_t to0 = dst + (((2 * (lane & 3)) ^ r8) << 4), to1 = dst + (((2 * (lane & 3) + 1) ^ r8) << 4);
               uint4 all[kRows / 16];  // on their way together
 #pragma unroll
@@ -567,134 +572,166 @@ __global__ void __launch_bounds__(kThreads, 1)
         done(it);
       }
     } else if (elect_one()) {
-      // ---------------- MMA issuers: one thread a row tile, which goes through all key blocks ----------------
-      const int t = warp - kSoftmaxWarps - 1;
-      const uint32_t s_col = tmem + t * 128, o_col = tmem + 256 + t * 128;
+      // ---------------- MMA issuer: one thread for all of it ----------------
       int k_stage = 0, h_stage = 0, q_uses = 0;
-      uint32_t k_phase = 0, h_phase = 0, turn = 0;  // turn: parity of the next weights
+      uint32_t k_phase = 0, h_phase = 0, turn = 0;  // turn: parities of the tiles' next weights, a bit each
       auto wait = [&](uint32_t bar, uint32_t parity, int where) {
-        const bool got = mbar_wait<true>(bar, parity, wd, where);
+        const bool got = mbar_wait_soon(bar, parity, wd, where);
         tc_fence_after();
         return got;
       };
       bool ok = true;
+      Job job;
       for (int it = 0; ok; ++it) {
-        int blocks, keys, mine, q_of;
-        bool pair;
-        {
-          ok = wait(job_full(it & 1), (it >> 1) & 1, kWhereJob);
-          if (!ok) break;
-          const Job job = jobs[it & 1];
-          mbar_arrive(job_empty(it & 1));
-          if (job.b == -2) break;
-          blocks = job.t1 - job.t0;
-          pair = job.tiles == 2;
-          q_of = pair ? t : 0;
-          keys = tile_keys(job, q_of) - job.t0 * kRows;
-          mine = tile_blocks(job, t);
-        }
+        ok = wait(job_full(it & 1), (it >> 1) & 1, kWhereJob);
+        if (!ok) break;
+        job = jobs[it & 1];
+        mbar_arrive(job_empty(it & 1));
+        if (job.b == -2) break;
+        const int blocks = job.t1 - job.t0;
         if (blocks == 0) continue;
-        auto own = [&](int j) { return pair ? j < mine : (j & 1) == t; };
-        // S = Q K_j^T in two terms, where block j is this tile's
-        auto scores = [&](int j) {
-          ok = wait(k_full(k_stage), k_phase, kWhereMmaFull);
-          if (!ok) return;
-          if (own(j)) {
-            const int n = (min(kRows, keys - j * kRows) + 15) & ~15;
-            const uint64_t k = kmajor_sw128_desc(base + L::kOffK + k_stage * L::kTile), a = kmajor_sw128_desc(q_tile(q_of, 0));
+        const bool pair = job.tiles == 2;
+        const int keys0 = tile_keys(job, 0) - job.t0 * kRows, keys1 = pair ? tile_keys(job, 1) - job.t0 * kRows : keys0;
+        const int mine0 = tile_blocks(job, 0), mine1 = tile_blocks(job, 1);
+        auto scores = [&](int t, int j) {  // S_t = Q K_j^T, in two terms
+          const int n = (min(kRows, (t ? keys1 : keys0) - j * kRows) + 15) & ~15;
+          const uint64_t k = kmajor_sw128_desc(base + L::kOffK + k_stage * L::kTile);
 #pragma unroll
-            for (int term = 0; term < 2; ++term) {
-              const uint32_t idesc = instr_desc(term, 0, kRows, n);  // e4m3, then e5m2
+          for (int term = 0; term < 2; ++term) {
+            const uint64_t a = kmajor_sw128_desc(q_tile(pair ? t : 0, term));
+            const uint32_t idesc = instr_desc(term, 0, kRows, n);  // e4m3, then e5m2
 #pragma unroll
-              for (int i = 0; i < HD / 32; ++i)
-                mma_f8f6f4(s_col, desc_advance(a, term * L::kTile + i * 32), desc_advance(k, i * 32), idesc, (term | i) != 0);
-            }
-            mma_commit(s_full(t));
-            mma_commit(k_empty(k_stage));
-          } else {
-            mbar_arrive(k_empty(k_stage));
+            for (int i = 0; i < HD / 32; ++i) mma_f8f6f4(tmem + t * 128, desc_advance(a, i * 32), desc_advance(k, i * 32), idesc, (term | i) != 0);
           }
-          if (j + 1 == blocks) mma_commit(q_empty);
+          mma_commit(s_full(t));
+        };
+        auto next_k = [&]() {
+          mma_commit(k_empty(k_stage));
           if (++k_stage == KS) {
             k_stage = 0;
             k_phase ^= 1;
           }
         };
-        ok = wait(q_full, q_uses & 1, kWhereMmaFull);
-        ++q_uses;
-        if (ok) scores(0);
-        if (ok && !pair && blocks > 1) scores(1);
-        for (int j = 0; j < blocks && ok; ++j) {
-          ok = wait(h_full(h_stage), h_phase, kWhereMmaFull);
-          if (!ok) break;
-          if (own(j)) {
-            ok = wait(p_full(t), turn, kWhereMmaTmemEmpty);
-            turn ^= 1;
-            if (!ok) break;
-            // O += P V_j
-            const uint64_t v = smem_desc(base + L::kOffHalf + h_stage * L::kHalf, L::kBox, 1024, 2);
-            constexpr uint32_t idesc = instr_desc(0, 0, kRows, HD) | kIdescBMajorN;
-            const int steps = (min(kRows, keys - j * kRows) + 15) / 16;
-            const bool first = pair ? j == 0 : j < 2;
+        auto output = [&](int t, int j, bool last) {  // O_t += P_t V_j: what is stored first, then the rest
+          const uint64_t v = smem_desc(base + L::kOffHalf + h_stage * L::kHalf, L::kBox, 1024, 2);
+          constexpr uint32_t idesc = instr_desc(0, 0, kRows, HD) | kIdescBMajorN;
+          const int steps = (min(kRows, (t ? keys1 : keys0) - j * kRows) + 15) / 16;
+          const bool first = pair ? j == 0 : j < 2;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i < steps) mma_f16_ts(o_col, s_col + i * 8, desc_advance(v, i * 2048), idesc, !(first && i == 0));
-            if (pair ? j + 1 == mine : j + 2 >= blocks) mma_commit(o_full(t));
-            mma_commit(h_empty(h_stage));
-          } else {
-            mbar_arrive(h_empty(h_stage));
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && wait(h ? p_full(t) : p_half(t), (turn >> t) & 1, kWhereMmaTmemEmpty);
+            if (ok) {
+#pragma unroll
+              for (int i = h ? kEarly : 0; i < (h ? 8 : kEarly); ++i)
+                if (i < steps) mma_f16_ts(tmem + 256 + t * 128, tmem + t * 128 + i * 8, desc_advance(v, i * 2048), idesc, !(first && i == 0));
+              if (h && last) mma_commit(o_full(t));
+            }
           }
+          turn ^= 1u << t;
+        };
+        auto next_v = [&]() {
+          mma_commit(h_empty(h_stage));
           if (++h_stage == HS) {
             h_stage = 0;
             h_phase ^= 1;
           }
-          const int next = j + (pair ? 1 : 2);
-          if (next < blocks) scores(next);
+        };
+        auto k_ready = [&]() { return wait(k_full(k_stage), k_phase, kWhereMmaFull); };
+        auto v_ready = [&]() { return wait(h_full(h_stage), h_phase, kWhereMmaFull); };
+        // A wait takes 300 cycles where its phase has long passed (the tensor cores have shared memory to themselves), so
+        // what is due early is waited for before the weights are.
+        ok = wait(q_full, q_uses & 1, kWhereMmaFull) && k_ready();
+        ++q_uses;
+        if (pair) {
+          if (ok) {
+            if (mine0 > 0) scores(0, 0);
+            if (mine1 > 0) scores(1, 0);
+            next_k();
+            if (blocks == 1) mma_commit(q_empty);
+          }
+          for (int j = 0; j < blocks && ok; ++j) {
+            ok = v_ready() && (j + 1 == blocks || k_ready());
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int mine = t ? mine1 : mine0;
+              if (ok && j < mine) {
+                output(t, j, j + 1 == mine);
+                if (ok && j + 1 < mine) scores(t, j + 1);
+              }
+            }
+            next_v();
+            if (j + 1 < blocks) {
+              next_k();
+              if (j + 2 == blocks) mma_commit(q_empty);  // the job's last scores
+            }
+          }
+        } else {
+          if (ok) {
+            scores(0, 0);
+            next_k();
+          }
+          if (ok && blocks > 1) {
+            ok = k_ready();
+            if (ok) {
+              scores(1, 1);
+              next_k();
+            }
+          }
+          if (blocks <= 2) mma_commit(q_empty);
+          for (int j = 0; j < blocks && ok; ++j) {
+            ok = v_ready() && (j + 2 >= blocks || k_ready());
+            if (!ok) break;
+            if (j & 1) {
+              output(1, j, j + 2 >= blocks);
+              if (ok && j + 2 < blocks) scores(1, j + 2);
+            } else {
+              output(0, j, j + 2 >= blocks);
+              if (ok && j + 2 < blocks) scores(0, j + 2);
+            }
+            next_v();
+            if (j + 2 < blocks) {
+              next_k();
+              if (j + 3 == blocks) mma_commit(q_empty);
+            }
+          }
         }
       }
       // every MMA has finished and every commit has landed before the CTA exits
-      mma_commit(drain_bar(t));
-      mbar_wait_drain(drain_bar(t), 0, 200000000ull);
+      mma_commit(drain_bar);
+      mbar_wait_drain(drain_bar, 0, 200000000ull);
     }
   } else {
     reg_inc<kSoftmaxRegs>();
     // ---------------- softmax and output ----------------
-    // A row has two threads, for the keys and dimensions of half a block each; they meet once a block to agree on the references.
-    const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+    const int t = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_addr = tmem + lanes + t * 128, o_addr = tmem + lanes + 256;
     const int row = quarter * 32 + lane;
-    const uint32_t swap_mine = base + L::kOffSwap + ((2 * t + half) * kRows + row) * 8;
-    const uint32_t swap_other = base + L::kOffSwap + ((2 * t + (half ^ 1)) * kRows + row) * 8;
-    const uint32_t stats_mine = base + L::kOffStats + ((2 * t + half) * kRows + row) * 16;
-    const uint32_t stats_other = base + L::kOffStats + ((2 * t + (half ^ 1)) * kRows + row) * 16;
-    const uint32_t meet = swap_bar(t * 4 + quarter);
-    uint32_t turn = 0, outputs = 0, merges = 0, meets = 0;  // parities of the next scores, output, meetings
-    int count = 0;                                          // key blocks of the jobs before
-    // Larger of the row's two threads' x and y; false: the CTA gives up.
-    auto agree = [&](uint32_t mine, uint32_t theirs, float& x, float& y) {
-      st_shared_v2(mine, __float_as_uint(x), __float_as_uint(y));
-      mbar_arrive(meet);
-      if (!__all_sync(0xffffffffu, mbar_wait(meet, meets & 1, wd, kWhereMerge))) return false;
-      ++meets;
-      const uint2 other = ld_shared_v2(theirs);
-      x = fmaxf(x, __uint_as_float(other.x));
-      y = fmaxf(y, __uint_as_float(other.y));
-      return true;
+    uint32_t turn = 0, outputs = 0, merges = 0;  // parities of the next scores, output, meeting of the halves
+    int count = 0;                               // key blocks of the jobs before
+    auto tile_wait = [&](uint32_t bar, uint32_t parity, int where) {
+      const bool got = __all_sync(0xffffffffu, mbar_wait(bar, parity, wd, where));
+      tc_fence_after();
+      return got;
+    };
+    auto take_job = [&](int i, Job& job) {  // false: no more, or the CTA gives up
+      if (!tile_wait(job_full(i & 1), (i >> 1) & 1, kWhereJob)) return false;
+      read(i, job);
+      return job.b != -2;
     };
     int q_fills = 0;
     // The query rows of a job that has key blocks, as two terms: a share of them a warp.  Past the job's scores that
     // came before; false: the CTA gives up.
     auto queries = [&](int i, const Job& job) {
-      if (q_fills > 0 && !__all_sync(0xffffffffu, mbar_wait(q_empty, (q_fills - 1) & 1, wd, kWhereConvert))) return false;
+      if (q_fills > 0 && !tile_wait(q_empty, (q_fills - 1) & 1, kWhereConvert)) return false;
       ++q_fills;
       // HD / 8 lanes a row, 8 dimensions each
       constexpr int kLanes = HD / 8, kAtOnce = 32 / kLanes;
-      const int d = 8 * (lane % kLanes), share = job.tiles == 2 ? 16 : 8, tile = job.tiles == 2 ? t : 0;
+      const int d = 8 * (lane % kLanes), share = job.tiles == 2 ? 32 : 16, tile = job.tiles == 2 ? t : 0;
       const int rows = min(job.lq - job.first - tile * tile_tokens, tile_tokens) * p.pack;  // those that have a query
       const uint32_t hi_tile = q_tile(tile, 0), lo_tile = q_tile(tile, 1), factors = base + L::kOffRow + (((i & 1) * 2 + tile) * kRows) * 4;
-      const int begin = (job.tiles == 2 ? warp & 7 : warp) * share;
-      constexpr int kBatch = 8 / kAtOnce;
+      const int begin = (job.tiles == 2 ? quarter : warp) * share;
+      constexpr int kBatch = 16 / kAtOnce;
       const uint16_t* const from = p.q + static_cast<int64_t>(job.q0 + job.first + tile * tile_tokens) * p.q_stride + job.head0 * p.D + d;
 #pragma unroll 1
       for (int r0 = begin; r0 < begin + share; r0 += kAtOnce * kBatch) {
@@ -751,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     {
       Job job;
-      if (peek(0, job) && job.t1 > job.t0) ok = queries(0, job);
+      if (take_job(0, job) && job.t1 > job.t0) ok = queries(0, job);
     }
 #pragma unroll 1
     for (int it = 0; ok; ++it) {
@@ -759,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool halves, idle;
       {
         Job job;
-        if (!peek(it, job)) break;
+        if (!take_job(it, job)) break;
         halves = job.tiles == 1;
         n = tile_blocks(job, t);
         blocks = job.t1 - job.t0;
@@ -771,39 +808,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float factor = 0.f;                 // of the query row's codes
       float m = kUnset, nn = kUnset;      // references, in log2 units: of scores, of the output's weights (relative to m)
-      float sum = 0.f;                    // of this thread's keys
+      float sum = 0.f;
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
-        ok = __all_sync(0xffffffffu, mbar_wait(s_full(t), turn, wd, kWhereEpiTmemFull));
+        // What shared memory holds is read before the scores are there: operands that the tensor cores take from it
+        // keep a load waiting for hundreds of cycles.
+        const uint32_t block = count + (halves ? 2 * j + t : j), slot = block & (L::kInfo - 1);
+        ok = tile_wait(info_full(slot), (block / L::kInfo) & 1, kWhereEpiTmemFull);
+        if (!ok) break;
+        // of the 16-key blocks: factors of their scores, exponents of their values and the inverses of those
+        float g[8], b[8], inverse[8];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float4 x = ld_shared_f4(base + L::kOffInfo + slot * 64 + c * 16), y = ld_shared_f4(base + L::kOffInfo + slot * 64 + 32 + c * 16);
+          const float4 z = ld_shared_f4(base + L::kOffInverse + slot * 32 + c * 16);
+          g[4 * c] = x.x, g[4 * c + 1] = x.y, g[4 * c + 2] = x.z, g[4 * c + 3] = x.w;
+          b[4 * c] = y.x, b[4 * c + 1] = y.y, b[4 * c + 2] = y.z, b[4 * c + 3] = y.w;
+          inverse[4 * c] = z.x, inverse[4 * c + 1] = z.y, inverse[4 * c + 2] = z.z, inverse[4 * c + 3] = z.w;
+        }
+        const uint32_t about = ld_shared(base + L::kOffMask + slot * 4), gone = about & 255;
+        ok = tile_wait(s_full(t), turn, kWhereEpiTmemFull);
         turn ^= 1;
         if (!ok) break;
-        tc_fence_after();
-        uint32_t s[2][32];
-        tmem_ld_32x32b_x32(s_addr + 64 * half, s[0]);  // past the last key: hidden below
-        tmem_ld_32x32b_x32(s_addr + 64 * half + 32, s[1]);
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_addr + 32 * c, s[c]);  // past the last key: hidden below
         if (j == 0) factor = idle ? 1.f : __uint_as_float(ld_shared(base + L::kOffRow + (((it & 1) * 2 + (halves ? 0 : t)) * kRows + row) * 4));
-        const uint32_t slot = (count + (halves ? 2 * j + t : j)) & (L::kInfo - 1);
-        const uint32_t about = ld_shared(base + L::kOffMask + slot * 4), gone = about >> (4 * half) & 15;
-        const uint32_t at = base + L::kOffInfo + slot * 128 + half * 64;
-        const int room = lim - (t0 + each * j) * kRows - 64 * half;
-        const bool edge = __any_sync(0xffffffffu, room < 64) || gone;
+        float least = b[0], most = b[0];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          g[c] *= factor;
+          least = fminf(least, b[c]);
+          most = fmaxf(most, b[c]);
+        }
+        const int room = lim - (t0 + each * j) * kRows;
+        const bool edge = __any_sync(0xffffffffu, room < kRows) || gone;
         tmem_wait_ld();
         bool slow = (about >> 16) != 0;
         if (edge) {
           slow |= __any_sync(0xffffffffu, factor < kLight);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 8; ++c) {
             const int left = (gone >> c) & 1 ? 0 : room - 16 * c;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               if (i >= left) s[c / 2][c % 2 * 16 + i] = 0xFF800000u;
           }
         }
-        // the largest score, and the largest of the sums with the exponents of their values, relative to m
-        const float before = m == kUnset ? 0.f : m;
-        float mx = -INFINITY, vx = -INFINITY, top[4];
+        float top[8];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 8; ++c) {
           float x = -INFINITY, y = -INFINITY;
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
@@ -811,61 +865,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             y = max3(y, __uint_as_float(s[c / 2][c % 2 * 16 + i + 2]), __uint_as_float(s[c / 2][c % 2 * 16 + i + 3]));
           }
           x = fmaxf(x, y);
-          const float4 scales = ld_shared_f4(at + 16 * c);
           // rounded, as m will be; a row that sees none of a block does not take its scale, which may be NaN
-          top[c] = x == -INFINITY ? x : __fmul_rn(x, scales.x * factor);
-          mx = fmaxf(mx, top[c]);
-          vx = fmaxf(vx, (top[c] - before) + scales.z);
+          top[c] = x == -INFINITY ? x : __fmul_rn(x, g[c]);
         }
-        ok = agree(swap_mine, swap_other, mx, vx);
-        if (!ok) break;
-        if (__any_sync(0xffffffffu, mx > m + kSlack || vx > nn + (kLift + kSlack))) {
+        const float mx = fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]), max3(top[5], top[6], top[7]));
+        // may a reference have to move?  (the largest exponent stands for those of the largest scores)
+        if (__any_sync(0xffffffffu, mx > m + kSlack || (mx - m) + most > nn + (kLift + kSlack))) {
           const float up = ceilf(mx);
           if (up > m) {
             sum *= ex2(m - up);
             nn += m - up;
             m = up;
           }
-          if (__any_sync(0xffffffffu, (fabsf(mx) > kExact && mx > -INFINITY) || fabsf(before) > kExact)) {
-            vx = -INFINITY;  // beside such scores the exponents may have been lost
+          float vx = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) vx = fmaxf(vx, (top[c] - m) + __uint_as_float(ld_shared(at + 16 * c + 8)));
-            // in a place of its own: the other thread may still be reading what was found first
-            ok = agree(stats_mine, stats_other, mx, vx);
-            if (!ok) break;
-          } else if (m != kUnset) {
-            vx += before - m;
-          }
+          for (int c = 0; c < 8; ++c) vx = fmaxf(vx, (top[c] - m) + b[c]);
           vx = ceilf(vx) - kLift;
           const bool lift = vx > nn;
           const float by = lift ? ex2(nn - vx) : 1.f;
           if (lift) nn = vx;
           if (j > 0 && __any_sync(0xffffffffu, lift)) {
 #pragma unroll 1
-            for (int c = 0; c < HD / 32; ++c) {
-              const uint32_t from = o_addr + t * 128 + half * (HD / 2) + 16 * c;
+            for (int c = 0; c < HD / 16; ++c) {  // S fills the registers: a little of O at a time
               uint32_t o[16];
-              tmem_ld_32x32b_x16(from, o);
+              tmem_ld_32x32b_x16(o_addr + t * 128 + 16 * c, o);
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
-              tmem_st_32x32b_x16(from, o);
+              tmem_st_32x32b_x16(o_addr + t * 128 + 16 * c, o);
             }
           }
         }
         // before a row has seen a key its references are unset: any do
         const float ref = m == kUnset ? 0.f : m, vref = m == kUnset ? 0.f : nn;
-        const float least = __uint_as_float(ld_shared(base + L::kOffRange + slot * 4));
         slow |= __any_sync(0xffffffffu, fabsf(ref) > kExact || least - vref < kSpread);
         if (!slow) {
-          const uint64_t factor2 = pack_f32x2(factor, factor), off2 = pack_f32x2(-vref - ref, -vref - ref);
+          const float off = -vref - ref;
           float sums[2] = {0.f, 0.f};  // of the weights without the values' scales, by 2^vref
+          uint32_t w[16];              // two blocks' weights
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint64_t g2, b2;
-            ld_shared_pairs(at + 16 * c, g2, b2);
-            g2 = mul_f32x2(g2, factor2);
-            b2 = add_f32x2(b2, off2);
+          for (int c = 0; c < 8; ++c) {
+            const uint64_t g2 = pack_f32x2(g[c], g[c]), b2 = pack_f32x2(b[c] + off, b[c] + off);
             uint64_t part = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -874,32 +914,45 @@ __global__ void __launch_bounds__(kThreads, 1)
               x = ex2(x);
               y = ex2(y);
               part = i ? add_f32x2(part, pack_f32x2(x, y)) : pack_f32x2(x, y);
-              s[c / 2][c % 2 * 8 + i] = pack_f16x2(x, y);  // over scores that have been taken
+              w[c % 2 * 8 + i] = pack_f16x2(x, y);
             }
             float lo, hi;
             unpack_f32x2(part, lo, hi);
-            sums[c & 1] = fmaf(lo + hi, __uint_as_float(ld_shared(base + L::kOffInverse + slot * 32 + half * 16 + c * 4)), sums[c & 1]);
-            if (c & 1) tmem_st_32x32b_x16(s_addr + 32 * half + 16 * (c / 2), *reinterpret_cast<uint32_t (*)[16]>(&s[c / 2][0]));
+            sums[c & 1] = fmaf(lo + hi, inverse[c], sums[c & 1]);
+            if (c & 1) {
+              if (c / 2 == kEarly / 2) {  // by now what was stored before is there
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_half(t));
+              }
+              tmem_st_32x32b_x16(s_addr + 16 * (c / 2), w);
+            }
           }
           sum = fmaf(sums[0] + sums[1], ex2(vref), sum);
         } else {
-          // score, difference and sum one by one
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float4 scales = ld_shared_f4(at + 16 * c);
-            const float by = scales.x * factor, lift = scales.z - vref;
+          // Score, difference and sum one by one, 16 keys at a time; scores are still in tensor memory, and
+          // weights (half as wide) do not reach those that are yet to be read.
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t x[16], w[8];
+            tmem_ld_32x32b_x16(s_addr + 16 * c, x);
+            const float by = __uint_as_float(ld_shared(base + L::kOffInfo + slot * 64 + c * 4)) * factor;
+            const float lift = __uint_as_float(ld_shared(base + L::kOffInfo + slot * 64 + 32 + c * 4)) - vref;
             const int left = !edge ? 16 : (gone >> c) & 1 ? 0 : room - 16 * c;
-            float more = 0.f;
+            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float x = 2 * i < left ? __fsub_rn(__fmul_rn(__uint_as_float(s[c / 2][c % 2 * 16 + 2 * i]), by), ref) : -INFINITY;
-              const float y = 2 * i + 1 < left ? __fsub_rn(__fmul_rn(__uint_as_float(s[c / 2][c % 2 * 16 + 2 * i + 1]), by), ref) : -INFINITY;
-              more += ex2(x) + ex2(y);
-              s[c / 2][c % 2 * 8 + i] = pack_f16x2(ex2(x + lift), ex2(y + lift));
+            for (int i = 0; i < 16; ++i) {
+              const float y = i < left ? __fsub_rn(__fmul_rn(__uint_as_float(x[i]), by), ref) : -INFINITY;
+              sum += ex2(y);
+              x[i] = __float_as_uint(ex2(y + lift));
             }
-            sum += more;
-            if (c & 1) tmem_st_32x32b_x16(s_addr + 32 * half + 16 * (c / 2), *reinterpret_cast<uint32_t (*)[16]>(&s[c / 2][0]));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = pack_f16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            tmem_st_32x32b_x8(s_addr + 8 * c, w);
           }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(p_half(t));
         }
         tmem_wait_st();
         tc_fence_before();
@@ -909,40 +962,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       count += blocks;
       {  // the next job's queries, while the last product runs
         Job job;
-        if (peek(it + 1, job) && job.t1 > job.t0) ok = queries(it + 1, job);
+        if (take_job(it + 1, job) && job.t1 > job.t0) ok = queries(it + 1, job);
       }
       if (n > 0 && ok) {
-        ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), outputs, wd, kWhereEpiTmemFull));
+        ok = tile_wait(o_full(t), outputs, kWhereEpiTmemFull);
         outputs ^= 1;
-        tc_fence_after();
       }
       if (!ok) break;
-      // A row's threads meet: the two of a tile of its own, or the four of a unit that has one tile, whose even and odd blocks
-      // have outputs of their own.  Each then writes its share of the dimensions.
+      // A tile's output is what its thread has; the even and odd blocks of a unit that has one tile have outputs of their own,
+      // whose threads meet here: each then writes half of the dimensions of both.
       const uint32_t stats = base + L::kOffStats;
-      const uint32_t all_meet = halves ? merge_bar : meet;
-      uint32_t& parity = halves ? merges : meets;
-      auto gather = [&]() {
-        mbar_arrive(all_meet);
-        const bool got = __all_sync(0xffffffffu, mbar_wait(all_meet, parity & 1, wd, kWhereMerge));
-        ++parity;
-        return got;
+      auto meet = [&]() {
+        mbar_arrive(merge_bar);
+        return tile_wait(merge_bar, merges++ & 1, kWhereMerge);
       };
-      st_shared_v4(stats_mine, __float_as_uint(m), __float_as_uint(nn), __float_as_uint(sum), n > 0);
-      ok = gather();
-      if (!ok) break;
-      auto half_sum = [&](int tile, int h) { return __uint_as_float(ld_shared(stats + ((2 * tile + h) * kRows + row) * 16 + 8)); };
-      sum = half_sum(t, 0) + half_sum(t, 1);  // in their order, so that both form the same
-      float part0 = 1.f, part1 = 0.f;         // what the halves' outputs are multiplied by
-      bool has0 = n > 0, has1 = false;        // of a tile of its own: has0
+      float part0 = 1.f, part1 = 0.f;   // what the halves' outputs are multiplied by
+      bool has0 = n > 0, has1 = false;  // of a tile of its own: has0
       if (halves) {
-        const uint4 x = ld_shared_v4(stats + 2 * (t ^ 1) * kRows * 16 + row * 16);
-        const float m1 = __uint_as_float(x.x), n1 = __uint_as_float(x.y), sum1 = half_sum(t ^ 1, 0) + half_sum(t ^ 1, 1);
+        st_shared_v4(stats + (t * kRows + row) * 16, __float_as_uint(m), __float_as_uint(nn), __float_as_uint(sum), n > 0);
+        ok = meet();
+        if (!ok) break;
+        const uint4 x = ld_shared_v4(stats + ((t ^ 1) * kRows + row) * 16);
+        const float m1 = __uint_as_float(x.x), n1 = __uint_as_float(x.y), sum1 = __uint_as_float(x.z);
         const float both = fmaxf(m, m1);
         const float d0 = m == kUnset ? kUnset : (m - both) + nn, d1 = m1 == kUnset ? kUnset : (m1 - both) + n1;
         const float most = fmaxf(d0, d1);
         const float a0 = sum * ex2(m - both), a1 = sum1 * ex2(m1 - both);
-        sum = t == 0 ? a0 + a1 : a1 + a0;
+        sum = t == 0 ? a0 + a1 : a1 + a0;  // in the order of the halves, so that both form the same
         const float mine = ex2(d0 - most), other = ex2(d1 - most);
         part0 = t ? other : mine;
         part1 = t ? mine : other;
@@ -956,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int token = row * p.pack_inverse >> 16, tok = job.first + (halves ? 0 : t * tile_tokens) + token;
       const bool mine = row < tile_tokens * p.pack && tok < job.lq;
       // dimensions [from, from + width) of this row, 16 at a time
-      const int width = halves ? HD / 4 : HD / 2, from = halves ? (2 * t + half) * (HD / 4) : half * (HD / 2);
+      const int width = halves ? HD / 2 : HD, from = halves ? t * (HD / 2) : 0;
       const uint32_t first_o = o_addr + (halves ? 0 : t * 128);
       auto load = [&](int c, float (&o)[16]) {
         uint32_t x[16];
@@ -975,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 16; ++i) o[i] = fmaf(__uint_as_float(x[i]), part1, o[i]);
         }
       };
-      const bool writes_row = half == 0 && (t == 0 || !halves);  // what a row has once
+      const bool writes_row = t == 0 || !halves;  // what a row has once
       if (job.whole) {
         const bool none = sum == 0.f;
         const float root = ex2(0.5f * nn), by = root / sum;  // 2^n in two steps: by itself it may leave fp32's range
@@ -1009,8 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();  // the next job's weights are handed over after these loads
-      ok = gather();      // and by none of a row's threads while another reads its output or its numbers
-      if (!ok) break;
+      if (halves && !(ok = meet())) break;  // and by neither half while the other reads its output or its numbers
       done(it);
     }
   }
