@@ -203,11 +203,6 @@ struct Walk {
   }
 };
 
-template <bool V>
-struct Flag {
-  static constexpr bool value = V;
-};
-
 // Two fp32 values to two e4m3 (e5m2) codes, to nearest even; two e4m3 codes to fp16.
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   uint16_t r;
@@ -526,33 +521,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (1, where a row has four runs), so that they meet in no bank: neither reading, with the codes' swizzle, nor writing.
           const int q = lane >> 3, sub = (lane >> 2) & 1;
           const int r8 = HD == 128 ? (sub ? (2 * q + 5) & 7 : 2 * q) : lane >> 2;
-          auto convert = [&](auto plain) {
+          const bool odd = past < kRows || nan != 0;
 #pragma unroll 1
-            for (int h = 0; h < HD / 64; ++h) {  // four of a row's runs
-              const int r0 = me * (kRows / 2) + r8, run = 4 * h + (lane & 3);
-              const uint32_t src = from + r0 * HD + (HD == 128 ? (run ^ r8) << 4 : run << 4);
-              const uint32_t dst = to + h * L::kBox + r0 * 128;
-              const uint32_t to0 = dst + (((2 * (lane & 3)) ^ r8) << 4), to1 = dst + (((2 * (lane & 3) + 1) ^ r8) << 4);
-              uint4 all[kRows / 16];  // on their way together
+          for (int h = 0; h < HD / 64; ++h) {  // four of a row's runs
+            const int r0 = me * (kRows / 2) + r8, run = 4 * h + (lane & 3);
+            const uint32_t src = from + r0 * HD + (HD == 128 ? (run ^ r8) << 4 : run << 4);
+            const uint32_t dst = to + h * L::kBox + r0 * 128;
+            const uint32_t to0 = dst + (((2 * (lane & 3)) ^ r8) << 4), to1 = dst + (((2 * (lane & 3) + 1) ^ r8) << 4);
+            uint4 all[kRows / 16];  // on their way together
 #pragma unroll
-              for (int i = 0; i < kRows / 16; ++i) all[i] = ld_shared_v4(src + i * 8 * HD);
+            for (int i = 0; i < kRows / 16; ++i) all[i] = ld_shared_v4(src + i * 8 * HD);
+            if (odd) {
 #pragma unroll
               for (int i = 0; i < kRows / 16; ++i) {
-                uint4 x = all[i];
-                if constexpr (!decltype(plain)::value) {
-                  const int r = 8 * i + r0;
-                  if ((nan >> (r >> 4)) & 1) x = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                  if (r >= past) x = make_uint4(0, 0, 0, 0);
-                }
-                st_shared_v4(to0 + i * 1024, from_e4m3x2(x.x), from_e4m3x2(x.x >> 16), from_e4m3x2(x.y), from_e4m3x2(x.y >> 16));
-                st_shared_v4(to1 + i * 1024, from_e4m3x2(x.z), from_e4m3x2(x.z >> 16), from_e4m3x2(x.w), from_e4m3x2(x.w >> 16));
+                const int r = 8 * i + r0;
+                if ((nan >> (r >> 4)) & 1) all[i] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                if (r >= past) all[i] = make_uint4(0, 0, 0, 0);
               }
             }
-          };
-          if (past >= kRows && nan == 0)
-            convert(Flag<true>{});
-          else
-            convert(Flag<false>{});
+#pragma unroll
+            for (int i = 0; i < kRows / 16; ++i) {
+              const uint4& x = all[i];
+              st_shared_v4(to0 + i * 1024, from_e4m3x2(x.x), from_e4m3x2(x.x >> 16), from_e4m3x2(x.y), from_e4m3x2(x.y >> 16));
+              st_shared_v4(to1 + i * 1024, from_e4m3x2(x.z), from_e4m3x2(x.z >> 16), from_e4m3x2(x.w), from_e4m3x2(x.w >> 16));
+            }
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -592,106 +585,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (blocks == 0) continue;
         const bool pair = job.tiles == 2;
         const int keys0 = tile_keys(job, 0) - job.t0 * kRows, keys1 = pair ? tile_keys(job, 1) - job.t0 * kRows : keys0;
-        const int mine0 = tile_blocks(job, 0), mine1 = tile_blocks(job, 1);
-        auto scores = [&](int t, int j) {  // S_t = Q K_j^T, in two terms
-          const int n = (min(kRows, (t ? keys1 : keys0) - j * kRows) + 15) & ~15;
-          const uint64_t k = kmajor_sw128_desc(base + L::kOffK + k_stage * L::kTile);
-#pragma unroll
-          for (int term = 0; term < 2; ++term) {
-            const uint64_t a = kmajor_sw128_desc(q_tile(pair ? t : 0, term));
-            const uint32_t idesc = instr_desc(term, 0, kRows, n);  // e4m3, then e5m2
-#pragma unroll
-            for (int i = 0; i < HD / 32; ++i) mma_f8f6f4(tmem + t * 128, desc_advance(a, i * 32), desc_advance(k, i * 32), idesc, (term | i) != 0);
-          }
-          mma_commit(s_full(t));
-        };
-        auto next_k = [&]() {
-          mma_commit(k_empty(k_stage));
-          if (++k_stage == KS) {
-            k_stage = 0;
-            k_phase ^= 1;
-          }
-        };
-        auto output = [&](int t, int j, bool last) {  // O_t += P_t V_j: what is stored first, then the rest
-          const uint64_t v = smem_desc(base + L::kOffHalf + h_stage * L::kHalf, L::kBox, 1024, 2);
-          constexpr uint32_t idesc = instr_desc(0, 0, kRows, HD) | kIdescBMajorN;
-          const int steps = (min(kRows, (t ? keys1 : keys0) - j * kRows) + 15) / 16;
-          const bool first = pair ? j == 0 : j < 2;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            ok = ok && wait(h ? p_full(t) : p_half(t), (turn >> t) & 1, kWhereMmaTmemEmpty);
-            if (ok) {
-#pragma unroll
-              for (int i = h ? kEarly : 0; i < (h ? 8 : kEarly); ++i)
-                if (i < steps) mma_f16_ts(tmem + 256 + t * 128, tmem + t * 128 + i * 8, desc_advance(v, i * 2048), idesc, !(first && i == 0));
-              if (h && last) mma_commit(o_full(t));
-            }
-          }
-          turn ^= 1u << t;
-        };
-        auto next_v = [&]() {
-          mma_commit(h_empty(h_stage));
-          if (++h_stage == HS) {
-            h_stage = 0;
-            h_phase ^= 1;
-          }
-        };
-        auto k_ready = [&]() { return wait(k_full(k_stage), k_phase, kWhereMmaFull); };
-        auto v_ready = [&]() { return wait(h_full(h_stage), h_phase, kWhereMmaFull); };
-        // A wait takes 300 cycles where its phase has long passed (the tensor cores have shared memory to themselves), so
-        // what is due early is waited for before the weights are.
-        ok = wait(q_full, q_uses & 1, kWhereMmaFull) && k_ready();
+        const int mine0 = tile_blocks(job, 0);
+        ok = wait(q_full, q_uses & 1, kWhereMmaFull);
         ++q_uses;
-        if (pair) {
-          if (ok) {
-            if (mine0 > 0) scores(0, 0);
-            if (mine1 > 0) scores(1, 0);
-            next_k();
-            if (blocks == 1) mma_commit(q_empty);
+        // Step s: O_t += P_t V_j, then the scores of the block that tile t has next; t = s & 1, and j goes up every
+        // other step (two row tiles) or every step (one, whose even and odd blocks are two).  Steps -2 and -1 have scores alone.
+        // One copy of the code: instructions that it takes twice as many of are not there when they are wanted, and this
+        // thread's time is in every tile's way.
+        const int steps = pair ? 2 * blocks : blocks;
+#pragma unroll 1
+        for (int step = -2; step < steps && ok; ++step) {
+          const int t = step & 1, j = pair ? step >> 1 : step, next = j + (pair ? 1 : 2);
+          const bool first_of = !pair || t == 0, last_of = !pair || t == 1;  // of the steps that share K and V
+          // What is due early is waited for before the weights are: a wait takes 300 cycles where its phase has long passed (the
+          // tensor cores have shared memory to themselves).
+          if (first_of) {
+            if (j >= 0) ok = wait(h_full(h_stage), h_phase, kWhereMmaFull);
+            if (ok && next < blocks) ok = wait(k_full(k_stage), k_phase, kWhereMmaFull);
+            if (!ok) break;
           }
-          for (int j = 0; j < blocks && ok; ++j) {
-            ok = v_ready() && (j + 1 == blocks || k_ready());
+          const int keys = t ? keys1 : keys0, mine = pair ? (t ? blocks : mine0) : blocks;
+          const uint32_t s_col = tmem + t * 128, o_col = s_col + 256;
+          if (j >= 0 && j < mine) {  // what is stored first, then the rest
+            const uint64_t v = smem_desc(base + L::kOffHalf + h_stage * L::kHalf, L::kBox, 1024, 2);
+            constexpr uint32_t idesc = instr_desc(0, 0, kRows, HD) | kIdescBMajorN;
+            const int parts = (min(kRows, keys - j * kRows) + 15) / 16;
+            const bool first = pair ? j == 0 : j < 2;
+            ok = wait(p_half(t), (turn >> t) & 1, kWhereMmaTmemEmpty);
+            if (!ok) break;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const int mine = t ? mine1 : mine0;
-              if (ok && j < mine) {
-                output(t, j, j + 1 == mine);
-                if (ok && j + 1 < mine) scores(t, j + 1);
+            for (int i = 0; i < kEarly; ++i)
+              if (i < parts) mma_f16_ts(o_col, s_col + i * 8, desc_advance(v, i * 2048), idesc, !(first && i == 0));
+            ok = wait(p_full(t), (turn >> t) & 1, kWhereMmaTmemEmpty);
+            if (!ok) break;
+#pragma unroll
+            for (int i = kEarly; i < 8; ++i)
+              if (i < parts) mma_f16_ts(o_col, s_col + i * 8, desc_advance(v, i * 2048), idesc, 1);
+            turn ^= 1u << t;
+            if (pair ? next == mine : next >= blocks) mma_commit(o_full(t));
+          }
+          if (next < mine) {  // S_t = Q K^T, in two terms
+            const int n = (min(kRows, keys - next * kRows) + 15) & ~15;
+            const uint64_t k = kmajor_sw128_desc(base + L::kOffK + k_stage * L::kTile), a = kmajor_sw128_desc(q_tile(pair ? t : 0, 0));
+#pragma unroll
+            for (int term = 0; term < 2; ++term) {
+              const uint32_t idesc = instr_desc(term, 0, kRows, n);  // e4m3, then e5m2
+#pragma unroll
+              for (int i = 0; i < HD / 32; ++i)
+                mma_f8f6f4(s_col, desc_advance(a, term * L::kTile + i * 32), desc_advance(k, i * 32), idesc, (term | i) != 0);
+            }
+            mma_commit(s_full(t));
+          }
+          if (last_of) {
+            if (j >= 0) {
+              mma_commit(h_empty(h_stage));
+              if (++h_stage == HS) {
+                h_stage = 0;
+                h_phase ^= 1;
               }
             }
-            next_v();
-            if (j + 1 < blocks) {
-              next_k();
-              if (j + 2 == blocks) mma_commit(q_empty);  // the job's last scores
-            }
-          }
-        } else {
-          if (ok) {
-            scores(0, 0);
-            next_k();
-          }
-          if (ok && blocks > 1) {
-            ok = k_ready();
-            if (ok) {
-              scores(1, 1);
-              next_k();
-            }
-          }
-          if (blocks <= 2) mma_commit(q_empty);
-          for (int j = 0; j < blocks && ok; ++j) {
-            ok = v_ready() && (j + 2 >= blocks || k_ready());
-            if (!ok) break;
-            if (j & 1) {
-              output(1, j, j + 2 >= blocks);
-              if (ok && j + 2 < blocks) scores(1, j + 2);
-            } else {
-              output(0, j, j + 2 >= blocks);
-              if (ok && j + 2 < blocks) scores(0, j + 2);
-            }
-            next_v();
-            if (j + 2 < blocks) {
-              next_k();
-              if (j + 3 == blocks) mma_commit(q_empty);
+            if (next < blocks) {
+              mma_commit(k_empty(k_stage));
+              if (++k_stage == KS) {
+                k_stage = 0;
+                k_phase ^= 1;
+              }
+              if (next + 1 == blocks) mma_commit(q_empty);  // the job's last scores
             }
           }
         }
