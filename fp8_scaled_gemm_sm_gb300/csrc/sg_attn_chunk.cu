@@ -98,8 +98,8 @@ struct ChunkLayout {
   static constexpr int kInfo = 8;                    // key blocks whose scales are held
   static constexpr int kOffInfo = kOffStats + 2 * kRows * 16;        // of its 16-key blocks: the scores' factors, the values' exponents
   static constexpr int kOffInverse = kOffInfo + kInfo * 64;  // 2^-exponent
-  static constexpr int kOffMask = kOffInverse + kInfo * 32;  // a word a block: pages that are not there, value scales that are NaN, odd ones
-  static constexpr int kOffRow = kOffMask + kInfo * 4;      // a query row's factor, by job and row
+  static constexpr int kOffMask = kOffInverse + kInfo * 32;  // pages that are not there, value scales that are NaN, odd ones; least and largest exponent
+  static constexpr int kOffRow = kOffMask + kInfo * 16;      // a query row's factor, by job and row
   static constexpr int kOffBar = kOffRow + 2 * 2 * kRows * 4;
   static constexpr int kNumBars = 2 * (kKStages + kVStages + kHalfStages) + 10 + 8 + kInfo;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
@@ -235,11 +235,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
   const uint4 v = ld_shared_v4(a);
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
-}
-__device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
 }
 __device__ __forceinline__ uint32_t ld_shared(uint32_t a) {
   uint32_t v;
@@ -461,7 +456,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             st_shared(base + L::kOffInfo + slot * 64 + 32 + c8 * 4, y);
             st_shared(base + L::kOffInverse + slot * 32 + c8 * 4, __float_as_uint(ex2(-about.y)));
           }
-          if (lane == 0) st_shared(base + L::kOffMask + slot * 4, ((gone >> (8 * in)) & 255) | ((nan >> (8 * in)) & 255) << 8 | ((odd >> (8 * in)) & 255) << 16);
+          float least = about.y, most = about.y;
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) {
+            least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          }
+          if (lane == 8 * in)
+            st_shared_v4(base + L::kOffMask + slot * 16, ((gone >> (8 * in)) & 255) | ((nan >> (8 * in)) & 255) << 8 | ((odd >> (8 * in)) & 255) << 16,
+                         __float_as_uint(least), __float_as_uint(most), 0);
           const bool mine = (lane >> 3) == in && c8 % (8 / boxes) == 0;
           const int y = (head << p.page_shift) + ((t * kRows + 16 * c8) & (p.page - 1)), part = c8 / (8 / boxes);
           __syncwarp();
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            mbar_wait_soon(h_empty(h_stage), h_phase ^ 1, wd, kWhereConvert));
           if (!ok) break;
           const uint32_t from = base + L::kOffRaw + v_stage * L::kRaw, to = base + L::kOffHalf + h_stage * L::kHalf;
-          const uint32_t nan = (ld_shared(base + L::kOffMask + (count++ & (L::kInfo - 1)) * 4) >> 8) & 255;
+          const uint32_t nan = (ld_shared(base + L::kOffMask + (count++ & (L::kInfo - 1)) * 16) >> 8) & 255;
           const int past = job.lk - (job.t0 + j) * kRows;  // rows from here on are not this sequence's
           // A lane takes a run of 16 codes to two runs of 16 bytes of fp16.  Eight lanes take four runs of two rows, 5 apart
           // (1, where a row has four runs), so that they meet in no bank: neither reading, with the codes' swizzle, nor writing.
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4 all[kRows / 16];  // on their way together
 #pragma unroll
             for (int i = 0; i < kRows / 16; ++i) all[i] = ld_shared_v4(src + i * 8 * HD);
-            if (odd) {
+            if (__builtin_expect(odd, 0)) {
 #pragma unroll
               for (int i = 0; i < kRows / 16; ++i) {
                 const int r = 8 * i + r0;
@@ -785,7 +788,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           b[4 * c] = y.x, b[4 * c + 1] = y.y, b[4 * c + 2] = y.z, b[4 * c + 3] = y.w;
           inverse[4 * c] = z.x, inverse[4 * c + 1] = z.y, inverse[4 * c + 2] = z.z, inverse[4 * c + 3] = z.w;
         }
-        const uint32_t about = ld_shared(base + L::kOffMask + slot * 4), gone = about & 255;
+        const float4 more = ld_shared_f4(base + L::kOffMask + slot * 16);
+        const uint32_t about = __float_as_uint(more.x), gone = about & 255;
+        const float least = more.y, most = more.z;
         ok = tile_wait(s_full(t), turn, kWhereEpiTmemFull);
         turn ^= 1;
         if (!ok) break;
@@ -793,18 +798,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_addr + 32 * c, s[c]);  // past the last key: hidden below
         if (j == 0) factor = idle ? 1.f : __uint_as_float(ld_shared(base + L::kOffRow + (((it & 1) * 2 + (halves ? 0 : t)) * kRows + row) * 4));
-        float least = b[0], most = b[0];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          g[c] *= factor;
-          least = fminf(least, b[c]);
-          most = fmaxf(most, b[c]);
-        }
+        for (int c = 0; c < 8; ++c) g[c] *= factor;
         const int room = lim - (t0 + each * j) * kRows;
         const bool edge = __any_sync(0xffffffffu, room < kRows) || gone;
         tmem_wait_ld();
         bool slow = (about >> 16) != 0;
-        if (edge) {
+        if (__builtin_expect(edge, 0)) {
           slow |= __any_sync(0xffffffffu, factor < kLight);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
@@ -824,12 +824,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             y = max3(y, __uint_as_float(s[c / 2][c % 2 * 16 + i + 2]), __uint_as_float(s[c / 2][c % 2 * 16 + i + 3]));
           }
           x = fmaxf(x, y);
-          // rounded, as m will be; a row that sees none of a block does not take its scale, which may be NaN
-          top[c] = x == -INFINITY ? x : __fmul_rn(x, g[c]);
+          top[c] = __fmul_rn(x, g[c]);  // rounded, as m will be; a scale that is NaN leaves the maximum alone
         }
         const float mx = fmaxf(max3(max3(top[0], top[1], top[2]), top[3], top[4]), max3(top[5], top[6], top[7]));
         // may a reference have to move?  (the largest exponent stands for those of the largest scores)
-        if (__any_sync(0xffffffffu, mx > m + kSlack || (mx - m) + most > nn + (kLift + kSlack))) {
+        if (__builtin_expect(__any_sync(0xffffffffu, mx > m + kSlack || (mx - m) + most > nn + (kLift + kSlack)), 0)) {
           const float up = ceilf(mx);
           if (up > m) {
             sum *= ex2(m - up);
@@ -844,13 +843,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float by = lift ? ex2(nn - vx) : 1.f;
           if (lift) nn = vx;
           if (j > 0 && __any_sync(0xffffffffu, lift)) {
+            const uint64_t by2 = pack_f32x2(by, by);
 #pragma unroll 1
             for (int c = 0; c < HD / 16; ++c) {  // S fills the registers: a little of O at a time
               uint32_t o[16];
               tmem_ld_32x32b_x16(o_addr + t * 128 + 16 * c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+              for (int i = 0; i < 16; i += 2) {
+                float x, y;
+                unpack_f32x2(mul_f32x2(pack_f32x2(o[i], o[i + 1]), by2), x, y);
+                o[i] = __float_as_uint(x), o[i + 1] = __float_as_uint(y);
+              }
               tmem_st_32x32b_x16(o_addr + t * 128 + 16 * c, o);
             }
           }
@@ -858,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // before a row has seen a key its references are unset: any do
         const float ref = m == kUnset ? 0.f : m, vref = m == kUnset ? 0.f : nn;
         slow |= __any_sync(0xffffffffu, fabsf(ref) > kExact || least - vref < kSpread);
-        if (!slow) {
+        if (__builtin_expect(!slow, 1)) {
           const float off = -vref - ref;
           float sums[2] = {0.f, 0.f};  // of the weights without the values' scales, by 2^vref
           uint32_t w[16];              // two blocks' weights
