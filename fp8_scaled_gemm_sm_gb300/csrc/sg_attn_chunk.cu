@@ -44,10 +44,9 @@ constexpr int kSoftmaxRegs = 208, kIssueRegs = 88;  // 2 x 208 + 88 = 3 x 168, w
 constexpr int kWhereJob = 0x41, kWhereMerge = 0x42, kWhereConvert = 0x43;  // waits beside those of sg_ptx.cuh
 constexpr int kJobReaders = kSoftmaxWarps + 3;  // warps that take jobs
 constexpr int kEarly = 4;        // 16-key steps of a block whose weights are handed over first
-constexpr int kAsks = 2000;      // of a wait that is due soon
-constexpr int kUnitCost = 512;   // what a unit costs beside its keys, in keys of one row tile
-constexpr int kUncut = 8;        // units of up to 1 / kUncut of a range are not cut
-constexpr int kLeast = 1024;     // of a range; at least 256, so that every range of a cut unit has a block of it
+constexpr int kUnitCost = 1536;   // what a unit costs beside its keys, in keys of one row tile
+constexpr int kUncut = 32;        // units of up to 1 / kUncut of a range are not cut
+constexpr int kLeast = 256;     // of a range; at least 256, so that every range of a cut unit has a block of it
 constexpr float kSlack = 8.f;    // log2 of how far a maximum may pass its reference
 constexpr float kLift = 7.f;     // the output's weights at its reference are 2^kLift, the largest 2^15
 constexpr float kUnset = -FLT_MAX;
@@ -246,15 +245,6 @@ __device__ __forceinline__ void st_shared_v2(uint32_t a, uint32_t x, uint32_t y)
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 
-// Waits for a phase that is due within microseconds: asks again and again before it waits as mbar_wait does, which wakes
-// later (4 chunks behind contexts @@@).  For few warps: asking takes issue slots.
-__device__ __forceinline__ bool mbar_wait_soon(uint32_t bar, uint32_t parity, const Watchdog& wd, int where) {
-#pragma unroll 1
-  for (int i = 0; i < kAsks; ++i)
-    if (mbar_probe(bar, parity)) return true;
-  return mbar_wait(bar, parity, wd, where);
-}
-
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const ChunkParams p) {
@@ -402,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       Cut cut{};
       cut.last = -1;
-      const uint64_t policy = l2_policy_evict_last();
+      const uint64_t policy = l2_policy_evict_first();
       int k_stage = 0, v_stage = 0, count = 0;
       uint32_t k_phase = 0, v_phase = 0, k_issued = 0, v_issued = 0, k_par = 0, v_par = 0;
       const int block_shift = p.page_shift - 4, boxes = min(kRows / p.page, 8);
@@ -514,8 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = 0; ok && peek(it, job); ++it) {
         const int blocks = job.t1 - job.t0;
         for (int j = 0; j < blocks; ++j) {
-          ok = __all_sync(0xffffffffu, mbar_wait_soon(v_full(v_stage), v_phase, wd, kWhereConvert) &&
-                                           mbar_wait_soon(h_empty(h_stage), h_phase ^ 1, wd, kWhereConvert));
+          ok = __all_sync(0xffffffffu, mbar_wait(v_full(v_stage), v_phase, wd, kWhereConvert) &&
+                                           mbar_wait(h_empty(h_stage), h_phase ^ 1, wd, kWhereConvert));
           if (!ok) break;
           const uint32_t from = base + L::kOffRaw + v_stage * L::kRaw, to = base + L::kOffHalf + h_stage * L::kHalf;
           const uint32_t nan = (ld_shared(base + L::kOffMask + (count++ & (L::kInfo - 1)) * 16) >> 8) & 255;
@@ -572,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int k_stage = 0, h_stage = 0, q_uses = 0;
       uint32_t k_phase = 0, h_phase = 0, turn = 0;  // turn: parities of the tiles' next weights, a bit each
       auto wait = [&](uint32_t bar, uint32_t parity, int where) {
-        const bool got = mbar_wait_soon(bar, parity, wd, where);
+        const bool got = mbar_wait<true>(bar, parity, wd, where);
         tc_fence_after();
         return got;
       };
@@ -688,59 +678,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (q_fills > 0 && !tile_wait(q_empty, (q_fills - 1) & 1, kWhereConvert)) return false;
       ++q_fills;
       // HD / 8 lanes a row, 8 dimensions each
-      constexpr int kLanes = HD / 8, kAtOnce = 32 / kLanes;
+      constexpr int kLanes = HD / 8, kAtOnce = 32 / kLanes, kFlight = 4;
       const int d = 8 * (lane % kLanes), share = job.tiles == 2 ? 32 : 16, tile = job.tiles == 2 ? t : 0;
       const int rows = min(job.lq - job.first - tile * tile_tokens, tile_tokens) * p.pack;  // those that have a query
-      const uint32_t hi_tile = q_tile(tile, 0), lo_tile = q_tile(tile, 1), factors = base + L::kOffRow + (((i & 1) * 2 + tile) * kRows) * 4;
-      const int begin = (job.tiles == 2 ? quarter : warp) * share;
-      constexpr int kBatch = 16 / kAtOnce;
+      const uint32_t hi_tile = q_tile(tile, 0), factors = base + L::kOffRow + (((i & 1) * 2 + tile) * kRows) * 4;
+      const int begin = (job.tiles == 2 ? quarter : warp) * share + lane / kLanes;
       const uint16_t* const from = p.q + static_cast<int64_t>(job.q0 + job.first + tile * tile_tokens) * p.q_stride + job.head0 * p.D + d;
+      auto fetch = [&](int r) {  // rows without a query are zeros, so that what their threads find does not vary
+        const int token = r * p.pack_inverse >> 16;
+        return r < rows && d < p.D ? *reinterpret_cast<const uint4*>(from + token * p.q_stride + (r - token * p.pack) * p.D) : make_uint4(0, 0, 0, 0);
+      };
+      uint4 flight[kFlight];
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k) flight[k] = fetch(begin + k * kAtOnce);
 #pragma unroll 1
-      for (int r0 = begin; r0 < begin + share; r0 += kAtOnce * kBatch) {
-        uint4 raw[kBatch];
+      for (int r = begin; r < begin + share; r += kAtOnce) {
+        const uint32_t w[4] = {flight[0].x, flight[0].y, flight[0].z, flight[0].w};
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int r = r0 + k * kAtOnce + lane / kLanes, token = r * p.pack_inverse >> 16;
-          raw[k] = make_uint4(0, 0, 0, 0);  // rows without a query are zeros, so that what their threads find does not vary
-          if (r < rows && d < p.D) raw[k] = *reinterpret_cast<const uint4*>(from + token * p.q_stride + (r - token * p.pack) * p.D);
+        for (int k = 1; k < kFlight; ++k) flight[k - 1] = flight[k];
+        flight[kFlight - 1] = fetch(r + kFlight * kAtOnce < begin + share ? r + kFlight * kAtOnce : kRows);
+        float x[8];
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[2 * e] = __uint_as_float(w[e] << 16);
+          x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+          top = max3(top, fabsf(x[2 * e]), fabsf(x[2 * e + 1]));
         }
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int r = r0 + k * kAtOnce + lane / kLanes;
-          const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-          float x[8];
-          float top = 0.f;
+        for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // the row's largest value to [2^7, 2^8)
+        const int field = min(261 - static_cast<int>(__float_as_uint(top) >> 23), 253);
+        const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
+        uint32_t hi[2], lo[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[2 * e] = __uint_as_float(w[e] << 16);
-            x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-            top = fmaxf(top, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
+        for (int e = 0; e < 2; ++e) {
+          hi[e] = lo[e] = 0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float a = x[4 * e + 2 * h] * up, b = x[4 * e + 2 * h + 1] * up;
+            const uint32_t code = to_e4m3x2(a, b);
+            float ha, hb;
+            half2_floats(from_e4m3x2(code), ha, hb);
+            hi[e] |= code << (16 * h);
+            lo[e] |= to_e5m2x2(a - ha, b - hb) << (16 * h);
           }
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          // the row's largest value to [2^7, 2^8)
-          const int field = min(261 - static_cast<int>(__float_as_uint(top) >> 23), 253);
-          const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
-          uint32_t hi[2], lo[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            hi[e] = lo[e] = 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float a = x[4 * e + 2 * h] * up, b = x[4 * e + 2 * h + 1] * up;
-              const uint32_t code = to_e4m3x2(a, b);
-              float ha, hb;
-              half2_floats(from_e4m3x2(code), ha, hb);
-              hi[e] |= code << (16 * h);
-              lo[e] |= to_e5m2x2(a - ha, b - hb) << (16 * h);
-            }
-          }
-          const uint32_t at = r * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 8);
-          st_shared_v2(hi_tile + at, hi[0], hi[1]);
-          st_shared_v2(lo_tile + at, lo[0], lo[1]);
-          if (d == 0)  // 1 / up; a row with an infinity is NaN
-            st_shared(factors + r * 4, top == INFINITY ? 0x7FC00000u : static_cast<uint32_t>(254 - field) << 23);
         }
+        const uint32_t at = hi_tile + r * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 8);
+        st_shared_v2(at, hi[0], hi[1]);
+        st_shared_v2(at + L::kTile, lo[0], lo[1]);
+        if (d == 0)  // 1 / up; a row with an infinity is NaN
+          st_shared(factors + r * 4, top == INFINITY ? 0x7FC00000u : static_cast<uint32_t>(254 - field) << 23);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -964,24 +952,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       read(it, job);  // again: scores left no room to keep it
       const int token = row * p.pack_inverse >> 16, tok = job.first + (halves ? 0 : t * tile_tokens) + token;
       const bool mine = row < tile_tokens * p.pack && tok < job.lq;
-      // dimensions [from, from + width) of this row, 16 at a time
+      // dimensions [from, from + width) of this row, 32 at a time
       const int width = halves ? HD / 2 : HD, from = halves ? t * (HD / 2) : 0;
       const uint32_t first_o = o_addr + (halves ? 0 : t * 128);
-      auto load = [&](int c, float (&o)[16]) {
-        uint32_t x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = 0.f;
+      auto load = [&](int c, uint32_t (&x)[32]) {
         if (has0) {
-          tmem_ld_32x32b_x16(first_o + c, x);
+          tmem_ld_32x32b_x32(first_o + c, x);
           tmem_wait_ld();
+        } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(x[i]) * part0;
+          for (int i = 0; i < 32; ++i) x[i] = 0;
         }
-        if (has1) {
-          tmem_ld_32x32b_x16(o_addr + 128 + c, x);
-          tmem_wait_ld();
+        if (halves) {
+          uint32_t y[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = fmaf(__uint_as_float(x[i]), part1, o[i]);
+          for (int i = 0; i < 32; ++i) y[i] = 0;
+          if (has1) {
+            tmem_ld_32x32b_x32(o_addr + 128 + c, y);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), part1, __uint_as_float(x[i]) * part0));
         }
       };
       const bool writes_row = t == 0 || !halves;  // what a row has once
@@ -989,17 +980,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool none = sum == 0.f;
         const float root = ex2(0.5f * nn), by = root / sum;  // 2^n in two steps: by itself it may leave fp32's range
         const int64_t at = static_cast<int64_t>(job.q0 + tok) * p.Hq + job.head0 + row - token * p.pack;
+        const uint64_t root2 = pack_f32x2(root, root), by2 = pack_f32x2(by, by);
 #pragma unroll 1
-        for (int c = from; c < from + width; c += 16) {
-          float o[16];
-          load(c, o);
-          if (!mine || c >= p.D) continue;
-          uint32_t w[8];
+        for (int c = from; c < from + width; c += 32) {
+          uint32_t x[32];
+          load(c, x);
+          if (!mine) continue;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = none ? 0u : pack_bf16x2(o[2 * i] * root * by, o[2 * i + 1] * root * by);
-          uint4* const to = reinterpret_cast<uint4*>(p.out + at * p.D + c);
-          to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          for (int i = 0; i < 4; ++i) {
+            if (c + 8 * i >= p.D) break;
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float a, b;
+              unpack_f32x2(mul_f32x2(mul_f32x2(pack_f32x2(x[8 * i + 2 * e], x[8 * i + 2 * e + 1]), root2), by2), a, b);
+              w[e] = none ? 0u : pack_bf16x2(a, b);
+            }
+            *reinterpret_cast<uint4*>(p.out + at * p.D + c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
         if (mine && p.lse && writes_row) p.lse[at] = none ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
       } else {
@@ -1008,12 +1006,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* const out = p.part_o + tile * (kRows * HD);
         if (halves || has0) {
 #pragma unroll 1
-          for (int c = from; c < from + width; c += 16) {
-            float o[16];
-            load(c, o);
+          for (int c = from; c < from + width; c += 32) {
+            uint32_t x[32];
+            load(c, x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<float4*>(out + ((c / 4 + i) * kRows + row) * 4) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(out + ((c / 4 + i) * kRows + row) * 4) = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           }
         }
       }
