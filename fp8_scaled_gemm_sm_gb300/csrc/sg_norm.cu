@@ -15,7 +15,7 @@
 // It costs 3.5 instructions an element (5.5 for fp32 rows, whose squares are not exact in 24 bits).
 //
 // The bound is memory: x and the residual are read once, the sum is written once and the
-// codes once; the row stays in registers in between.  A CTA of T threads a row, rows dealt out in turn;
+// codes once; the row stays in registers in between.  A CTA a row, rows dealt out in turn;
 // the next row's vectors are already loading while this one is summed up.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -29,7 +29,7 @@ namespace sg {
 
 namespace {
 
-constexpr int kMaxThreads = 256;
+constexpr int kMaxWarps = 32;
 constexpr float kFar = 0x1p90f;     // row sums of squares past this are formed again from
 constexpr float kDown = 0x1p-80f;   // elements scaled by this
 
@@ -69,6 +69,8 @@ __device__ __forceinline__ float inverse_root(const Pair& sum, float C, float ep
   return __fmaf_rn(0.5f * y, __fsub_rn(__fsub_rn(1.f, p), p_lo), y);
 }
 
+__device__ __forceinline__ uint64_t pair_of(float a, float b) { return pack_f32x2(__float_as_uint(a), __float_as_uint(b)); }
+
 template <bool BF16>
 __device__ __forceinline__ void load_vec(const void* X, int64_t elem, Raw8<BF16>& raw) {
   const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(X) + elem * (BF16 ? 2 : 4));
@@ -76,17 +78,17 @@ __device__ __forceinline__ void load_vec(const void* X, int64_t elem, Raw8<BF16>
   for (int i = 0; i < (BF16 ? 1 : 2); ++i) raw.w[i] = p[i];
 }
 
-template <int MODE, bool BF16, int VPT, int T>
-__global__ void __launch_bounds__(T) norm_kernel(const NormParams p) {
-  __shared__ Pair red_sum[2][T / 32];
-  __shared__ float red_max[2][T / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// VPT: vectors of eight elements a thread; MOST: threads at most.
+template <int MODE, bool BF16, int VPT, int MOST>
+__global__ void __launch_bounds__(MOST) norm_kernel(const NormParams p) {
+  __shared__ Pair red_sum[2][kMaxWarps];
+  __shared__ float red_max[2][kMaxWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x, warps = T >> 5;
   const int nvec = p.C / 8;
-  constexpr bool kScaled = MODE != kModeBf16;
   // Vector i of this thread: as in the quantiser, so that a block's vectors lie in consecutive lanes.
   constexpr int kVB = MODE == kModeBlockscale ? (VPT < 4 ? VPT : 4) : 1;
   auto vidx = [&](int i) { return (i / kVB) * (T * kVB) + tid * kVB + (i % kVB); };
-  constexpr bool kAhead = VPT * (BF16 ? 8 : 16) <= 32;  // the next row's vectors in up to 32 registers
+  constexpr bool kAhead = VPT == 1;  // the next row's vectors load while this one is worked on, where they take few registers
   auto fetch = [&](Raw8<BF16>(&x)[VPT], Raw8<BF16>(&r)[VPT], int row) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -140,14 +142,13 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormParams p) {
 
     // the sum of squares, of elements scaled by `by`
     auto square_sum = [&](float by, int slot) {
-      const uint64_t minus = pack_f32x2(__float_as_uint(-1.f), __float_as_uint(-1.f));
-      const uint64_t by2 = pack_f32x2(__float_as_uint(by), __float_as_uint(by));
+      const uint64_t minus = pair_of(-1.f, -1.f), by2 = pair_of(by, by);
       uint64_t s = 0, e = 0;
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint64_t v = pack_f32x2(__float_as_uint(f[i][2 * k]), __float_as_uint(f[i][2 * k + 1]));
+          uint64_t v = pair_of(f[i][2 * k], f[i][2 * k + 1]);
           if (by != 1.f) v = mul_f32x2(v, by2);
           const uint64_t q = mul_f32x2(v, v);
           if constexpr (!BF16) e = add_f32x2(e, fma_f32x2(v, v, mul_f32x2(q, minus)));
@@ -162,12 +163,13 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormParams p) {
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1)
         sum = add(sum, Pair{__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)});
+      if (warps == 1) return sum;
       if (lane == 0) red_sum[slot][warp] = sum;
       __syncthreads();
-      sum = red_sum[slot][0];
-#pragma unroll
-      for (int w = 1; w < T / 32; ++w) sum = add(sum, red_sum[slot][w]);
-      return sum;
+      sum = lane < warps ? red_sum[slot][lane] : Pair{0.f, 0.f};
+      for (int o = 1; o < warps; o <<= 1)
+        sum = add(sum, Pair{__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)});
+      return Pair{__shfl_sync(0xffffffffu, sum.hi, 0), __shfl_sync(0xffffffffu, sum.lo, 0)};
     };
     Pair sum = square_sum(1.f, turn);
     float g;
@@ -179,6 +181,7 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormParams p) {
       __syncthreads();
       g = inverse_root(sum, static_cast<float>(p.C), 0.f, 0.f) * kDown;
     }
+    const uint64_t g2 = pair_of(g, g);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = vidx(i);
@@ -188,7 +191,8 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormParams p) {
       float w[8];
       unpack8<BF16>(raw, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[i][e] = __fmul_rn(__fmul_rn(f[i][e], g), w[e]);
+      for (int e = 0; e < 8; e += 2)
+        unpack_f32x2(mul_f32x2(mul_f32x2(pair_of(f[i][e], f[i][e + 1]), g2), pair_of(w[e], w[e + 1])), f[i][e], f[i][e + 1]);
     }
 
     if constexpr (MODE == kModeBf16) {
@@ -208,11 +212,13 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormParams p) {
         for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[i][e]));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (lane == 0) red_max[turn][warp] = top;
-      __syncthreads();
-      top = red_max[turn][0];
+      if (warps > 1) {
+        if (lane == 0) red_max[turn][warp] = top;
+        __syncthreads();
+        top = lane < warps ? red_max[turn][lane] : 0.f;
 #pragma unroll
-      for (int w = 1; w < T / 32; ++w) top = fmaxf(top, red_max[turn][w]);
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
       const float s = top > 0.f ? __fdiv_rn(top, 448.0f) : 1.0f;
       if (tid == 0) static_cast<float*>(p.scale)[r] = s;
       const Recip rc = make_recip(s);
@@ -264,11 +270,12 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormParams p) {
   }
 }
 
-template <int MODE, bool BF16, int VPT, int T>
+template <int MODE, bool BF16, int VPT, int MOST>
 sg_status_t launch(const NormParams& p, int num_sms, cudaStream_t stream) {
-  const int most = 8 * num_sms;
-  GemmLaunch l(dim3(p.R < most ? p.R : most), dim3(T), 0, stream, 1);
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, norm_kernel<MODE, BF16, VPT, T>, p);
+  const int threads = ((p.C / 8 + VPT - 1) / VPT + 31) / 32 * 32;
+  const int64_t most = static_cast<int64_t>(num_sms) * (threads >= 256 ? 8 : 2048 / threads < 24 ? 2048 / threads : 24);
+  GemmLaunch l(dim3(static_cast<unsigned>(p.R < most ? p.R : most)), dim3(threads), 0, stream, 1);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, norm_kernel<MODE, BF16, VPT, MOST>, p);
   if (e == cudaSuccess) return SG_OK;
   note_cuda_error(e);
   cudaGetLastError();
@@ -277,12 +284,11 @@ sg_status_t launch(const NormParams& p, int num_sms, cudaStream_t stream) {
 
 template <int MODE, bool BF16>
 sg_status_t launch_width(const NormParams& p, int num_sms, cudaStream_t stream) {
-  const int vecs = (p.C / 8 + kMaxThreads - 1) / kMaxThreads;
-  if (vecs <= 1) return launch<MODE, BF16, 1, kMaxThreads>(p, num_sms, stream);
-  if (vecs <= 2) return launch<MODE, BF16, 2, kMaxThreads>(p, num_sms, stream);
-  if (vecs <= 4) return launch<MODE, BF16, 4, kMaxThreads>(p, num_sms, stream);
-  if (vecs <= 8) return launch<MODE, BF16, 8, kMaxThreads>(p, num_sms, stream);
-  return launch<MODE, BF16, 16, kMaxThreads>(p, num_sms, stream);
+  const int vecs = p.C / 8;  // at most 4096
+  if (vecs <= 1024 && (!BF16 || p.R <= 2 * num_sms)) return launch<MODE, BF16, 1, 1024>(p, num_sms, stream);
+  if (vecs <= (BF16 ? 1024 : 2048)) return launch<MODE, BF16, 2, 1024>(p, num_sms, stream);
+  if (vecs <= 2048) return launch<MODE, BF16, 4, 512>(p, num_sms, stream);
+  return launch<MODE, BF16, 8, 512>(p, num_sms, stream);
 }
 
 template <int MODE>
