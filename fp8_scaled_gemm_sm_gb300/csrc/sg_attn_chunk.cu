@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (q_fills > 0 && !tile_wait(q_empty, (q_fills - 1) & 1, kWhereConvert)) return false;
       ++q_fills;
       // HD / 8 lanes a row, 8 dimensions each
-      constexpr int kLanes = HD / 8, kAtOnce = 32 / kLanes, kFlight = 4;
+      constexpr int kLanes = HD / 8, kAtOnce = 32 / kLanes, kFlight = 8;
       const int d = 8 * (lane % kLanes), share = job.tiles == 2 ? 32 : 16, tile = job.tiles == 2 ? t : 0;
       const int rows = min(job.lq - job.first - tile * tile_tokens, tile_tokens) * p.pack;  // those that have a query
       const uint32_t hi_tile = q_tile(tile, 0), factors = base + L::kOffRow + (((i & 1) * 2 + tile) * kRows) * 4;
@@ -952,27 +952,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       read(it, job);  // again: scores left no room to keep it
       const int token = row * p.pack_inverse >> 16, tok = job.first + (halves ? 0 : t * tile_tokens) + token;
       const bool mine = row < tile_tokens * p.pack && tok < job.lq;
-      // dimensions [from, from + width) of this row, 32 at a time
+      // dimensions [from, from + width) of this row, 16 at a time
       const int width = halves ? HD / 2 : HD, from = halves ? t * (HD / 2) : 0;
       const uint32_t first_o = o_addr + (halves ? 0 : t * 128);
-      auto load = [&](int c, uint32_t (&x)[32]) {
+      auto load = [&](int c, uint32_t (&x)[16]) {
         if (has0) {
-          tmem_ld_32x32b_x32(first_o + c, x);
+          tmem_ld_32x32b_x16(first_o + c, x);
           tmem_wait_ld();
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = 0;
+          for (int i = 0; i < 16; ++i) x[i] = 0;
         }
         if (halves) {
-          uint32_t y[32];
+          uint32_t y[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = 0;
+          for (int i = 0; i < 16; ++i) y[i] = 0;
           if (has1) {
-            tmem_ld_32x32b_x32(o_addr + 128 + c, y);
+            tmem_ld_32x32b_x16(o_addr + 128 + c, y);
             tmem_wait_ld();
           }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), part1, __uint_as_float(x[i]) * part0));
+          for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), part1, __uint_as_float(x[i]) * part0));
         }
       };
       const bool writes_row = t == 0 || !halves;  // what a row has once
@@ -982,12 +982,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t at = static_cast<int64_t>(job.q0 + tok) * p.Hq + job.head0 + row - token * p.pack;
         const uint64_t root2 = pack_f32x2(root, root), by2 = pack_f32x2(by, by);
 #pragma unroll 1
-        for (int c = from; c < from + width; c += 32) {
-          uint32_t x[32];
+        for (int c = from; c < from + width; c += 16) {
+          uint32_t x[16];
           load(c, x);
           if (!mine) continue;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2; ++i) {
             if (c + 8 * i >= p.D) break;
             uint32_t w[4];
 #pragma unroll
@@ -1006,11 +1006,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* const out = p.part_o + tile * (kRows * HD);
         if (halves || has0) {
 #pragma unroll 1
-          for (int c = from; c < from + width; c += 32) {
-            uint32_t x[32];
+          for (int c = from; c < from + width; c += 16) {
+            uint32_t x[16];
             load(c, x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4; ++i)
               *reinterpret_cast<uint4*>(out + ((c / 4 + i) * kRows + row) * 4) = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           }
         }
