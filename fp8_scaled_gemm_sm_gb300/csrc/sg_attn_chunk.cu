@@ -8,7 +8,7 @@
 //   * Scores: K as it lies in the cache, through the fp8 tensor cores.  A query row, scaled by a power of two so that its largest
 //     value lies in [2^7, 2^8), is the sum of two terms: e4m3 (4 significant bits), and what that leaves of bf16's 8 in
 //     e5m2 (3 bits hold every remainder).  Elements down to 2^-13 of the row's largest are exact, smaller ones off by at most
-//     2^-22 of it.  Two products at twice bf16's rate: nothing is converted and nothing is lost, as K has no copy.
+//     2^-21 of it.  Two products at twice bf16's rate, and K needs no conversion and no copy in shared memory.
 //   * K's block scales are part of the factor that every score takes on its way to the exponential.
 //   * Values: codes to fp16, which holds them exactly, by two warps; their block scales go into the weights, 2^(s_j - m + b_j - n)
 //     in fp16 (2^-11 of each), and out of the row sum again, a block's sum at a time.  m follows the maximum of s_j, m + n
@@ -16,14 +16,29 @@
 //     with a single rounding.  Rows whose scores pass 2^22, or whose value scales lie 2^96 apart, take a
 //     slower way that forms score, difference and sum one by one.
 // Rows are packed as in sg_attn_prompt.cu: a tile's 128 rows are tokens times query heads of one key/value head.  A CTA
-// works on two row tiles in opposition, or, where a unit has but one (few tokens), on the even and the odd
-// key blocks of that one, whose halves it joins at the end out of tensor memory.  Warps: 0-3, 4-7 softmax and output, one thread a row;
-// 8 work and TMA; 9 MMA, one thread; 10, 11 queries to their two terms, values to fp16.
+// works on two row tiles, or, where a unit has but one (few tokens), on the even and the odd
+// key blocks of that one, whose halves it joins at the end out of tensor memory:
+//   warps 0-3, 4-7  softmax and output of tile 0 / 1, one thread a row; the next unit's queries to their two terms
+//   warp 8          work, pages and scales, TMA: K_0, V_0, K_1, V_1, ... through two rings
+//   warp 9          MMAs, one thread
+//   warps 10, 11    values to fp16
 //
 // Work: units (two row tiles of a sequence and head) are numbered by what they cost, and every CTA takes
 // an equal range of the numbers, so a few tokens over a long cache fill the GPU as well as many over a short one.
 // Units that are short beside a range are not cut; the parts of a cut one are joined by a second
 // kernel in the order of their ranges, so results do not depend on timing.
+//
+// What bounds it: the chain scores, softmax, weights, product of a tile, 2.1 us a block of both where the tensor cores need
+// 1.1 and take 1.5 without the softmax.  Two things lengthen it.  Shared memory: operands of the MMAs, loads and the
+// conversion take 2200 of a block's cycles, and every load and barrier of the other warps waits in between (hundreds of
+// cycles: so scales are read before the scores are there).  Instructions: five kinds of warps, each in a loop of its own, do not
+// fit the caches nearest to them, and the code's length shows in every time.  And a unit costs 12 us beside its blocks, with its queries,
+// first and last softmax and output.  Measured, with the join: 4 chunks of 1000 to 2048 tokens behind up to 24000,
+// 32 heads of 128 over 8: 1180 us, 1.15 PFLOP/s; 40 sequences of 1 to 300 tokens, 40 heads over 8: 362; 2 of 101 and 256 behind 120000
+// and more, 64 heads over 8: 1415; 24 of 5 to 700, 16 heads of 64: 124; one of 24 behind 900: 25.
+// Measured slower (4 chunks, and the form that each was tried on): the issuing thread's code for both tiles written out 1444 us, one copy 1364; loads of
+// scales after the scores are there, two threads a row or not, 1530 to 1580; two issuing threads, whose tiles then run in step, 1535, or
+// in turn 1530 (1325 with one); a unit's cost taken as 512 keys, a third of what it is, 1335 (1230 with 1536).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -44,9 +59,9 @@ constexpr int kSoftmaxRegs = 208, kIssueRegs = 88;  // 2 x 208 + 88 = 3 x 168, w
 constexpr int kWhereJob = 0x41, kWhereMerge = 0x42, kWhereConvert = 0x43;  // waits beside those of sg_ptx.cuh
 constexpr int kJobReaders = kSoftmaxWarps + 3;  // warps that take jobs
 constexpr int kEarly = 4;        // 16-key steps of a block whose weights are handed over first
-constexpr int kUnitCost = 1536;   // what a unit costs beside its keys, in keys of one row tile
-constexpr int kUncut = 32;        // units of up to 1 / kUncut of a range are not cut
-constexpr int kLeast = 256;     // of a range; at least 256, so that every range of a cut unit has a block of it
+constexpr int kUnitCost = 1536;  // what a unit costs beside its keys, in keys of one row tile (40 mixed: 363 us; 1024: 369, 512: 463)
+constexpr int kUncut = 32;       // units of up to 1 / kUncut of a range are not cut (4 chunks: 1222 us; 8: 1250, 4: 1380)
+constexpr int kLeast = 256;      // of a range, so that every range of a cut unit has a block of it (one question: 24.6 us; 1024: 32.8)
 constexpr float kSlack = 8.f;    // log2 of how far a maximum may pass its reference
 constexpr float kLift = 7.f;     // the output's weights at its reference are 2^kLift, the largest 2^15
 constexpr float kUnset = -FLT_MAX;

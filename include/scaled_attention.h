@@ -3,7 +3,7 @@
  * (libscaledgemm.so, GB300 / sm_103a).
  *
  * A decoder's attention lies between two of the library's GEMMs, the QKV projection
- * and the output projection.  The three operators here are what happens in between
+ * and the output projection.  The operators here are what happens in between
  * when a server keeps keys and values in a paged 8-bit cache:
  *
  *   scaled_attn_append   rotate queries and keys by their positions; append keys and
@@ -42,20 +42,21 @@
  *
  * Precision: scores, softmax statistics and sums are held in fp32; bf16 outputs are rounded once, to nearest even.
  * The weights of the product with v are rounded to what the tensor cores take, each to nearest: in
- * scaled_attn_prompt to bf16 (by at most 2^-8 of itself), in scaled_attn_decode to fp16 (2^-11; with its value block's
+ * scaled_attn_prompt to bf16 (by at most 2^-8 of itself), in scaled_attn_decode and scaled_attn_chunk to fp16 (2^-11; with its value block's
  * scale inside, and to no finer than 2^-32 of the row's largest such weight: where one visible block's value scale is 2^22 or
  * more above the others', their light weights lose bits in every dimension).  The denominator takes them unrounded.
+ * scaled_attn_chunk takes a query row's elements to 2^-21 of its largest; those from 2^-13 of it on are exact.
  *
  * NaN and infinity: what a row does not see does not reach it, with one exception, a non-finite
  * VALUE (v) of the row's own sequence behind the causal edge: its weight is zero, but the matrix
  * product takes it with keys that other rows see, and zero times infinity is NaN.  In
  * scaled_attn_prompt the value of a key up to 142 past the last that a row sees (the rest of its
- * tile of 128 rows, rounded up to 16 keys) may make that dimension of the row NaN; in
- * scaled_attn_decode with several query tokens, one of them may do so to the rows before it.
+ * tile of 128 rows, rounded up to 16 keys) may make that dimension of the row NaN, and so may it in scaled_attn_chunk
+ * (where a value scale that is NaN stands for its 16 keys); in scaled_attn_decode with several query tokens, one of them may do so to the rows before it.
  * Keys (k), bytes of the cache that no token has been written to, and other sequences never do.
  *
  * Errors, streams and programmatic launches: as in scaled_gemm.h.  A handle owns a
- * workspace that scaled_attn_decode uses, so decodes on one handle must be ordered (one
+ * workspace that scaled_attn_decode and scaled_attn_chunk use, so those calls on one handle must be ordered (one
  * stream, ordered streams, or a handle per stream); append and prompt may run
  * concurrently with anything that does not touch their buffers.  No call synchronises,
  * allocates or reads device memory on the host, so all of them can be captured in a CUDA graph.
@@ -184,7 +185,7 @@ sg_status_t scaled_attn_pool_compact(sg_attn_t h, const sg_page_pool_t* pool, co
 sg_status_t scaled_attn_debug_status(sg_attn_t h, sg_stream_t stream, int32_t* code, int32_t* where);
 
 /* Set the time limit of every kernel-side wait of the plan (nanoseconds; 0 = the default, 4 s) and, for tests only,
- * leave out the load of key tile `skip_tile` (-1: none) of every sequence (scaled_attn_decode) or of every few
+ * leave out the load of key tile `skip_tile` (-1: none) of every sequence (scaled_attn_decode, scaled_attn_chunk) or of every few
  * query tokens (scaled_attn_prompt), so that the wait for it runs out.  After a timeout the call's outputs are undefined;
  * nothing else is written.
  * Not to be called while a launch on the plan is being made. */

@@ -3,7 +3,7 @@
 Tolerances.  The output: half a bf16 step, fp16 weights (2^-11 of each, and 2^-31 of the row's largest for light ones), fp32
 scores, exponentials and sums (attn_ref.out_tolerance).  Scores: products and sums in fp32, as
 attn_ref.lse_tolerance has them, and a query's elements below 2^-13 of its row's largest, which are off by
-up to 2^-22 of that: a score moves by at most 2^-22 max|q| sum|k|, and so does the logarithm of the sum; a weight
+up to 2^-21 of that (tests/test_chunk_terms.py): a score moves by at most 2^-21 max|q| sum|k|, and so does the logarithm of the sum; a weight
 moves by that share of itself, and the output by twice that share of sum w |v| (weights and their sum)."""
 import ctypes
 
@@ -106,7 +106,7 @@ class Case:
             # what light weights and a row's smallest elements may add
             kk = np.abs(np.nan_to_num(k)).sum(2).max(0, initial=0).repeat(self.hq // self.hk)
             vv = np.abs(np.nan_to_num(v)).max((0, 2), initial=0).repeat(self.hq // self.hk)
-            small = 2.0 ** -22 * np.abs(np.nan_to_num(qh[t0 + i])).max(2) * kk[None] * self.scale
+            small = 2.0 ** -21 * np.abs(np.nan_to_num(qh[t0 + i])).max(2) * kk[None] * self.scale
             tol = ref.out_tolerance(o, mag, 11) + 2 * small[..., None] * mag + (m * 2.0 ** -31 * vv)[None, :, None]
             err = np.abs(go[t0 + i] - o)
             assert (err <= tol).all(), (b, n, m, np.argwhere(~(err <= tol))[:4].tolist(), float(np.nanmax(err / tol)))
