@@ -9,6 +9,10 @@
 ``AttentionLayer`` keeps the plans, the quantised weights and the cache; ``prompt`` and
 ``decode`` are what a server calls.  The decode step is captured in a CUDA graph,
 with the lengths and the block table in fixed buffers.
+
+``step`` is a layer of a server that mixes them: the residual's addition, norm and quantisation in
+one, and attention over the cache for as many new tokens as each sequence has, whose pages a ``PagePool`` hands out
+(``--answers N`` forks the first prompt N times and lets each fork go on by itself).
 """
 import argparse
 import os
@@ -18,7 +22,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 import torch
 
-from fp8_scaled_gemm_sm_gb300 import PagedAttention, ScaledGemm, binding, rotary_table
+from fp8_scaled_gemm_sm_gb300 import PagedAttention, PagePool, ScaledGemm, binding, norm_quantize, rotary_table
 
 
 class AttentionLayer:
@@ -32,7 +36,9 @@ class AttentionLayer:
         self.w_qkv, self.w_out = binding.quantize("ptpc", w_qkv), binding.quantize("ptpc", w_out)
 
     def _project(self, x):
-        codes, scale = binding.quantize("ptpc", x)
+        return self._heads(*binding.quantize("ptpc", x), x)
+
+    def _heads(self, codes, scale, x):
         rows = self.qkv(codes, self.w_qkv[0], scale, self.w_qkv[1]).view(x.shape[0], -1, self.dim)
         q, k = self.q_heads, self.kv_heads
         return rows[:, :q], rows[:, q:q + k], rows[:, q + k:]
@@ -56,6 +62,42 @@ class AttentionLayer:
         return self._output(o)
 
 
+    def step(self, x, residual, weight, pool, rows, tokens, cu_seqlens):
+        """x and residual [tokens, hidden], packed by cu_seqlens: `tokens` new ones of each of the pool's `rows`, whose pages it
+        hands out here.  Returns the output, the residual stream, and whether each row got its pages."""
+        codes, scale, residual = norm_quantize("ptpc", x, weight, residual=residual)
+        q, k, v = self._heads(codes, scale, x)
+        at = rows.long()
+        before = pool.lens[at]
+        ok = pool.grow(rows, tokens)
+        table = pool.table[at]
+        q, _ = self.plan.append(q, k, v, self.cache, table, before, cu_seqlens)
+        o, _ = self.plan.chunk(q, self.cache, table, pool.lens[at], cu_seqlens)
+        return self._output(o), residual, ok
+
+
+def answers(layer, count, tokens, prompt, weight, page):
+    """`count` answers to one prompt [tokens, hidden]: a row holds the prompt, forks share its pages."""
+    dev, n = prompt.device, prompt.shape[0]
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+    pool = PagePool.new(layer.plan, layer.cache, count + 1, -(-(n + tokens) // page) + 1)
+    y, r, ok = layer.step(prompt, torch.zeros_like(prompt), weight, pool, ints(0), ints(n), ints(0, n))
+    forks = torch.arange(1, count + 1, dtype=torch.int32, device=dev)
+    forked = pool.fork(torch.zeros_like(forks), forks)
+    x, res = y[-1:].repeat(count, 1), r[-1:].repeat(count, 1)
+    each, one = torch.arange(count + 1, dtype=torch.int32, device=dev), torch.ones_like(forks)
+    for _ in range(tokens):
+        x, res, grown = layer.step(x, res, weight, pool, forks, one, each)
+        ok = torch.cat([ok, grown])
+    used = int((pool.refs > 0).sum())
+    if not bool(ok.all()) or not bool(forked.all()):
+        raise SystemExit("no pages left")
+    print("answers: %d forks of %d tokens, %d more each, on %d pages" % (count, n, tokens, used))
+    pool.release(forks)
+    pool.compact()
+    return x
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--hidden", type=int, default=2048)
@@ -63,6 +105,7 @@ def main(argv=None):
     ap.add_argument("--dim", type=int, default=128)
     ap.add_argument("--prompts", type=int, nargs="+", default=[700, 33, 1])
     ap.add_argument("--steps", type=int, default=16)
+    ap.add_argument("--answers", type=int, default=0, metavar="N", help="forks of the first prompt, each answered by itself")
     a = ap.parse_args(argv)
     dev, page = "cuda", 64
     g = torch.Generator(dev).manual_seed(0)
@@ -71,7 +114,11 @@ def main(argv=None):
     width = (hq + 2 * hk) * a.dim
     w_qkv = (torch.randn(width, a.hidden, generator=g, device=dev) * a.hidden ** -0.5).bfloat16()
     w_out = (torch.randn(a.hidden, hq * a.dim, generator=g, device=dev) * (hq * a.dim) ** -0.5).bfloat16()
-    layer = AttentionLayer(a.hidden, hq, hk, a.dim, w_qkv, w_out, max(sum(a.prompts), n), sum(need), page)
+    spare = need[0] + 2 * a.answers if a.answers else 0
+    layer = AttentionLayer(a.hidden, hq, hk, a.dim, w_qkv, w_out, max(sum(a.prompts), n, a.answers), sum(need) + spare, page)
+    if a.answers:
+        x = torch.randn(a.prompts[0], a.hidden, generator=torch.Generator(dev).manual_seed(1), device=dev).bfloat16()
+        answers(layer, a.answers, a.steps, x, torch.ones(a.hidden, dtype=torch.bfloat16, device=dev), page)
     table = torch.full((n, max(need)), -1, dtype=torch.int32, device=dev)
     ids = iter(torch.randperm(sum(need), generator=torch.Generator().manual_seed(1)).tolist())
     for b, pages in enumerate(need):
