@@ -417,7 +417,9 @@ sg_status_t scaled_gemm_norm_quantize(int mode, int x_dtype, const void* X, cons
   if (x_dtype != SG_DTYPE_BF16 && x_dtype != SG_DTYPE_F32) return fail(SG_ERR_INVALID_ARG, "norm_quantize: bad x_dtype");
   if (R < 0 || C < 0) return fail(SG_ERR_INVALID_ARG, "norm_quantize: negative size");
   if (!(eps >= 0x1p-60 && eps <= 0x1p60)) return fail(SG_ERR_INVALID_ARG, "norm_quantize: eps outside [2^-60, 2^60]");
-  if (R > kMaxDim || C > sg::quantize_max_cols()) return fail(SG_ERR_UNSUPPORTED_SHAPE, "norm_quantize: R >= 2^31 or C > 32768");
+  // rows are counted in 32 bits, in strides of the grid
+  if (R > kMaxDim - 65536 || C > sg::quantize_max_cols())
+    return fail(SG_ERR_UNSUPPORTED_SHAPE, "norm_quantize: R >= 2^31 - 65536 or C > 32768");
   if (C % k_multiple(mode) != 0) return fail(SG_ERR_UNSUPPORTED_SHAPE, "norm_quantize: C not a multiple of the mode's block");
   if (R == 0 || C == 0) return SG_OK;
   if (!X || !weight || !Q || (mode != SG_MODE_BF16 && !scale) || (residual && !residual_out))

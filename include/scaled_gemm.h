@@ -224,7 +224,7 @@ sg_status_t scaled_gemm_quantize(int mode, int x_dtype, const void* X, int64_t R
  * residual, residual_out and weight [C] are of x_dtype.  Sums and products are in fp32: g is the fp32
  * number nearest to its value but for about one row in 2^16, where it is the next, and the two products of y
  * are rounded one after the other.  Finite values; 2^-60 <= eps <= 2^60.  Shape rules of scaled_gemm_quantize
- * (SG_MODE_BF16: C % 8 == 0); pointers 16-byte aligned, device memory, caller-owned.  residual_out may be X or
+ * (SG_MODE_BF16: C % 8 == 0), R < 2^31 - 65536; pointers 16-byte aligned, device memory, caller-owned.  residual_out may be X or
  * residual, and Q may be X where both are bf16; no other output may overlap an input or
  * another output (checked: SG_ERR_INVALID_ARG).  Asynchronous on `stream`, which is of the current device. */
 sg_status_t scaled_gemm_norm_quantize(int mode, int x_dtype, const void* X, const void* residual, void* residual_out,

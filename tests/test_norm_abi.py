@@ -31,3 +31,8 @@ def test_refusals(call, bad, status):
 
 def test_nothing_to_do(call):
     assert call(R=0) == 0 and call(C=0) == 0
+
+
+def test_rows_counted_in_32_bits(call):
+    far = 1 << 50  # buffers of that many rows do not overlap
+    assert call(mode=0, R=(1 << 31) - 1, C=8, x=far, res=None, kept=None, w=2 * far, q=3 * far, scale=None) == 2
