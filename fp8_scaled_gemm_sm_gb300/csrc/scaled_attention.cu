@@ -19,6 +19,7 @@ using sg::refuse;
 
 constexpr uint64_t kTimeoutNs = 4000000000ull;
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxCount = kMaxDim - 65536;  // of what a kernel counts in 32 bits, in strides of its threads
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
@@ -69,8 +70,8 @@ sg_status_t check_device(const sg_attn* h) {
 sg_status_t check_pool(const sg_page_pool_t* p) {
   if (!p) return refuse(SG_ERR_INVALID_ARG, "pool: NULL pool");
   if (p->rows < 0 || p->table_stride < 0 || p->num_pages < 0) return refuse(SG_ERR_INVALID_ARG, "pool: negative size");
-  if (p->rows > kMaxDim || p->num_pages > kMaxDim || p->table_stride > kMaxDim || p->rows * p->table_stride > kMaxDim)
-    return refuse(SG_ERR_UNSUPPORTED_SHAPE, "pool: size >= 2^31");
+  if (p->rows > kMaxCount || p->num_pages > kMaxCount) return refuse(SG_ERR_UNSUPPORTED_SHAPE, "pool: rows or pages >= 2^31 - 65536");
+  if (p->table_stride > kMaxDim || p->rows * p->table_stride > kMaxDim) return refuse(SG_ERR_UNSUPPORTED_SHAPE, "pool: table entries >= 2^31");
   if (!p->table || !p->lens || !p->refs || !p->scratch) return refuse(SG_ERR_INVALID_ARG, "pool: NULL pointer");
   if (!aligned(p->table, 4) || !aligned(p->lens, 4) || !aligned(p->refs, 16) || !aligned(p->scratch, 16))
     return refuse(SG_ERR_MISALIGNED, "pool: pointer");
@@ -382,7 +383,7 @@ sg_status_t scaled_attn_prompt(sg_attn_t h, const void* q, int64_t q_stride, con
 }
 
 int64_t scaled_attn_pool_scratch_bytes(int64_t rows, int64_t num_pages) {
-  if (rows < 0 || num_pages < 0 || rows > kMaxDim || num_pages > kMaxDim) return 0;
+  if (rows < 0 || num_pages < 0 || rows > kMaxCount || num_pages > kMaxCount) return 0;
   return sg::pool_scratch_bytes(rows, num_pages);
 }
 
@@ -391,7 +392,7 @@ sg_status_t scaled_attn_pool_release(sg_attn_t h, const sg_page_pool_t* pool, co
   if (!h) return refuse(SG_ERR_INVALID_ARG, "pool release: NULL handle");
   SG_TRY(check_pool(pool));
   if (n < 0) return refuse(SG_ERR_INVALID_ARG, "pool release: negative n");
-  if (n > kMaxDim) return refuse(SG_ERR_UNSUPPORTED_SHAPE, "pool release: n >= 2^31");
+  if (n > kMaxCount) return refuse(SG_ERR_UNSUPPORTED_SHAPE, "pool release: n >= 2^31 - 65536");
   if (n == 0) return SG_OK;
   SG_TRY(check_ints(which, "pool release: which"));
   SG_TRY(check_device(h));

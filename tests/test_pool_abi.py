@@ -27,3 +27,10 @@ def test_scratch(lib):
     for rows, pages in ((0, 0), (1, 1), (7, 1000), (1000, 7)):
         # counters, two words a row, one a page, and a move of two words for each row or page
         assert size(rows, pages) >= 16 + 8 * rows + 4 * pages + 8 * max(rows, pages)
+
+
+def test_rows_and_pages_counted_in_32_bits(lib):
+    most = (1 << 31) - 1 - 65536
+    size = binding.scaled_attn_pool_scratch_bytes
+    assert size(most, 1) > 0 and size(1, most) > 0
+    assert size(most + 1, 1) == 0 and size(1, most + 1) == 0
