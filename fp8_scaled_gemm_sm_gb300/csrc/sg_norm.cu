@@ -175,11 +175,11 @@ __global__ void __launch_bounds__(MOST) norm_kernel(const NormParams p) {
     float g;
     if (sum.hi <= kFar) {
       g = inverse_root(sum, static_cast<float>(p.C), p.eps_hi, p.eps_lo);
-    } else {  // squares near fp32's largest, beside which eps is nothing
+    } else {  // squares near fp32's largest
       __syncthreads();
       sum = square_sum(kDown, turn);
       __syncthreads();
-      g = inverse_root(sum, static_cast<float>(p.C), 0.f, 0.f) * kDown;
+      g = inverse_root(sum, static_cast<float>(p.C), p.eps_hi * kDown * kDown, p.eps_lo * kDown * kDown) * kDown;
     }
     const uint64_t g2 = pair_of(g, g);
 #pragma unroll

@@ -113,6 +113,16 @@ def test_bf16_over_its_input(norm):
     assert torch.equal(x, want)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_large_eps_beside_large_rows(norm, dtype):
+    """Row sums past 2^90, where squares are formed of scaled elements, and an eps of 2^-20 and 2^-25 of their means."""
+    g = torch.Generator("cpu").manual_seed(8)
+    x = ((1 + torch.rand(6, 32768, generator=g)) * torch.tensor([2.0 ** 40, 2.0 ** 42, 2.0 ** 38, 2.0 ** 37.5, 2.0 ** 30, 2.0 ** 60])[:, None]).to(dtype)
+    w = torch.ones(32768, dtype=dtype)
+    for eps in (2.0 ** 60, 3e17):
+        _check("ptpc", x, None, w, eps, norm("ptpc", x.cuda(), w.cuda(), eps))
+
+
 def test_the_quantiser_gives_the_same_codes(norm):
     """What the norm quantises is what binding.quantize makes of the same y in fp32."""
     from fp8_scaled_gemm_sm_gb300 import binding
