@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(kThreads) compact_plan_kernel(const PoolParams
   each_page(p, [&](int page, int refs) {
     if (page < used && refs <= 0) p.scratch.moves[hole++].y = page;
     if (page >= used && refs > 0) p.scratch.moves[tail++].x = page;
+    if (page >= used && refs <= 0) p.scratch.pages[page] = page;  // an entry may name it all the same
   });
   __syncthreads();
   for (int i = threadIdx.x; i < moves; i += kThreads) {

@@ -53,8 +53,8 @@ class PagePool:
         return self._grow(self.plan._p, self._p, rows, tokens, ok, stream)
 
     def fork(self, src, dst, ok=None, stream=None):
-        """Row dst[i], which is empty, becomes a copy of row src[i]: full pages are shared, a last page that is not full
-        is copied in every cache.  Returns the answer."""
+        """Row dst[i], which is empty, becomes a copy of row src[i] as it was before the call: full pages are shared, a last
+        page that is not full is copied in every cache.  Returns the answer."""
         return self._fork(self.plan._p, self._p, src, dst, ok, stream)
 
     def compact(self, in_use=None, stream=None):

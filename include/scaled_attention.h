@@ -176,7 +176,7 @@ sg_status_t scaled_attn_pool_fork(sg_attn_t h, const sg_page_pool_t* pool, const
                                   const int32_t* src, const int32_t* dst, int64_t n, int32_t* ok, sg_stream_t stream);
 
 /* The pages in use move to the numbers [0, *in_use), each by the table and in all caches: those past it, in order, to
- * the free ones below it, in order.  in_use: int32, device memory. */
+ * the free ones below it, in order.  Entries that name a free page stay.  in_use: int32, device memory. */
 sg_status_t scaled_attn_pool_compact(sg_attn_t h, const sg_page_pool_t* pool, const sg_kv_cache_t* caches, int64_t layers,
                                      int32_t* in_use, sg_stream_t stream);
 

@@ -202,6 +202,17 @@ def test_names_outside_the_pool(pkg):
     _same(pool, model, arrays)
 
 
+def test_compaction_leaves_entries_of_free_pages(pkg):
+    pool, model, arrays, _ = _setup(pkg, 3, 3, 12)
+    model.table[:] = [[9, 11, -1], [2, 10, 7], [6, 99, -5]]
+    model.refs[[9, 2]] = 1  # 11, 10, 7 and 6 are free
+    pool.table.copy_(torch.from_numpy(model.table))
+    pool.refs.copy_(torch.from_numpy(model.refs))
+    pool.scratch.fill_(0x55)
+    assert pool.compact().tolist() == [model.compact()]
+    _same(pool, model, arrays)
+
+
 def test_captured(pkg):
     """Grow, fork, release and compact as one graph, replayed from other states."""
     pool, model, arrays, _ = _setup(pkg, 6, 6, 40)
