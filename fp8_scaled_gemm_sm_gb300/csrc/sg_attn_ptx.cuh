@@ -37,12 +37,6 @@ __device__ __forceinline__ bool elect_one() {
   return yes != 0;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
   return pack_f32x2(__float_as_uint(lo), __float_as_uint(hi));
 }
@@ -111,12 +105,6 @@ __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t
 }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {  // for all but the last N groups
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // Asks to run a CTA of this grid that has not been launched yet in this one: 16 bytes at `answer`,
 // counted by the mbarrier.  Not to be asked again once there was none.

@@ -82,14 +82,15 @@ struct Recip {
   bool fast;      // s in [2^-60, 2^60]
 };
 
-__device__ __forceinline__ Recip make_recip(float s) {
-  const float r = __frcp_rn(s);
+__device__ __forceinline__ Recip make_recip(float s, float r) {  // r = RN(1/s)
   Recip q;
   q.r2 = pack_f32x2(__float_as_uint(r), __float_as_uint(r));
   q.ns2 = pack_f32x2(__float_as_uint(-s), __float_as_uint(-s));
   q.fast = s >= 0x1p-60f && s <= 0x1p+60f;
   return q;
 }
+
+__device__ __forceinline__ Recip make_recip(float s) { return make_recip(s, __frcp_rn(s)); }
 
 // Eight codes of x / s: the quotient correctly rounded in fp32 (the IEEE division
 // where the scale is outside Markstein's range), then e4m3.

@@ -102,6 +102,33 @@ def test_in_place(norm):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("R,C", [(700, 7168), (1250, 2048), (611, 2304), (613, 4992), (610, 8192), (612, 16384)])
+def test_many_rows(norm, mode, R, C):
+    """More rows than the CTAs have in their first turns, in place; every thread's vectors there, or some past the row."""
+    x, r, w = _make(R, C, R + C, torch.bfloat16)
+    x[R - 1] *= 2.0 ** 80  # the last row of a CTA
+    dx = x.cuda()
+    got = norm(mode, dx, w.cuda(), 1e-6, residual=r.cuda(), residual_out=dx)
+    assert got[2].data_ptr() == dx.data_ptr()
+    _check(mode, x, r, w, 1e-6, got)
+
+
+def test_many_rows_without_residual(norm):
+    x, _, w = _make(700, 4096, 9, torch.bfloat16)
+    _check("ptpc", x, None, w, 1e-6, norm("ptpc", x.cuda(), w.cuda(), 1e-6))
+
+
+def test_many_rows_of_bf16_over_the_residual(norm):
+    from fp8_scaled_gemm_sm_gb300 import binding
+
+    x, r, w = (t.cuda() for t in _make(900, 4096, 10, torch.bfloat16))
+    want, _, kept = norm("bf16", x, w, residual=r)
+    binding.scaled_gemm_norm_quantize("bf16", "bf16", x.data_ptr(), r.data_ptr(), x.data_ptr(), w.data_ptr(), 1e-6, 900, 4096, r.data_ptr(), 0,
+                                      torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(r, want) and torch.equal(x, kept)
+
+
 def test_bf16_over_its_input(norm):
     from fp8_scaled_gemm_sm_gb300 import binding
 
