@@ -32,13 +32,14 @@
 // 1.1 and take 1.5 without the softmax.  Two things lengthen it.  Shared memory: operands of the MMAs, loads and the
 // conversion take 2200 of a block's cycles, and every load and barrier of the other warps waits in between (hundreds of
 // cycles: so scales are read before the scores are there).  Instructions: five kinds of warps, each in a loop of its own, do not
-// fit the caches nearest to them, and the code's length shows in every time.  And a unit costs 12 us beside its blocks, with its queries,
+// fit the caches nearest to them, and the code's length shows in every time.  And a unit costs 8 to 15 us beside its blocks, with its queries,
 // first and last softmax and output.  Measured, with the join: 4 chunks of 1000 to 2048 tokens behind up to 24000,
-// 32 heads of 128 over 8: 1180 us, 1.15 PFLOP/s; 40 sequences of 1 to 300 tokens, 40 heads over 8: 362; 2 of 101 and 256 behind 120000
-// and more, 64 heads over 8: 1415; 24 of 5 to 700, 16 heads of 64: 124; one of 24 behind 900: 25.
+// 32 heads of 128 over 8: 1180 us, 1.15 PFLOP/s; 40 sequences of 1 to 300 tokens, 40 heads over 8: 308; 2 of 101 and 256 behind 120000
+// and more, 64 heads over 8: 1163; 24 of 5 to 700, 16 heads of 64: 111; one of 24 behind 900: 25.
 // Measured slower (4 chunks, and the form that each was tried on): the issuing thread's code for both tiles written out 1444 us, one copy 1364; loads of
 // scales after the scores are there, two threads a row or not, 1530 to 1580; two issuing threads, whose tiles then run in step, 1535, or
-// in turn 1530 (1325 with one); a unit's cost taken as 512 keys, a third of what it is, 1335 (1230 with 1536).
+// in turn 1530 (1325 with one); a unit's cost taken as a third of what it is, 1335 (1230); pages and scales loaded a group ahead of their
+// blocks, in one loop over jobs and groups, 1268 (1222), with a second copy of that code 1364.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -59,9 +60,13 @@ constexpr int kSoftmaxRegs = 208, kIssueRegs = 88;  // 2 x 208 + 88 = 3 x 168, w
 constexpr int kWhereJob = 0x41, kWhereMerge = 0x42, kWhereConvert = 0x43;  // waits beside those of sg_ptx.cuh
 constexpr int kJobReaders = kSoftmaxWarps + 3;  // warps that take jobs
 constexpr int kEarly = 4;        // 16-key steps of a block whose weights are handed over first
-constexpr int kUnitCost = 1536;  // what a unit costs beside its keys, in keys of one row tile (40 mixed: 363 us; 1024: 369, 512: 463)
-constexpr int kUncut = 32;       // units of up to 1 / kUncut of a range are not cut (4 chunks: 1222 us; 8: 1250, 4: 1380)
-constexpr int kLeast = 256;      // of a range, so that every range of a cut unit has a block of it (one question: 24.6 us; 1024: 32.8)
+// What work costs, in quarters of what a key costs a unit of two row tiles: a key of a unit with one tile, whose blocks are loaded and
+// converted for half as many scores (1.2 to 1.6 us a block, 1.9 for both tiles; as half of a pair's 40 mixed take 364 us and
+// 2 long documents 1420, as three quarters 308 and 1163, as five sixths 317 and 1163), and what a unit costs beside its keys
+// (40 mixed and 4 chunks with 3072: 308 and 1190 us; 2304: 354 and 1243).
+constexpr int kPairKey = 4, kSingleKey = 3, kUnitCost = 3072;
+constexpr int kUncut = 32;       // units of up to 1 / kUncut of a range are not cut (4 chunks: 1190 us; 16: 1206)
+constexpr int kLeast = 768;      // of a range, so that every range of a cut unit has a block of it (one question: 24.6 us; 512: 26.6)
 constexpr float kSlack = 8.f;    // log2 of how far a maximum may pass its reference
 constexpr float kLift = 7.f;     // the output's weights at its reference are 2^kLift, the largest 2^15
 constexpr float kUnset = -FLT_MAX;
@@ -148,15 +153,19 @@ __device__ __forceinline__ int unit_keys(const Sequence& s, int i, int span) {
 }
 __device__ __forceinline__ int unit_tiles(const Sequence& s, int i, int span) { return s.lq - i * span > span / 2 ? 2 : 1; }
 
+// What a key costs a unit: an expression without a choice, since this kernel feels every instruction (4 chunks: 1190 us, 1222 with one).
+static_assert(kPairKey == kSingleKey + 1, "");
+__device__ __forceinline__ int key_cost(int tiles) { return tiles + kSingleKey - 1; }
+
 // What the units before unit i (at most the last) cost; all but the last have two tiles and see lk - lq + span (x + 1) keys.
 __device__ __forceinline__ int64_t cost_before(const Sequence& s, int i, int span) {
   const int64_t a = static_cast<int64_t>(s.lk) - s.lq, n = i;
   const int64_t none = a >= 0 ? 0 : min(n, -a / span);
-  return n * kUnitCost + 2 * ((n - none) * a + span * (n * (n + 1) / 2 - none * (none + 1) / 2));
+  return n * kUnitCost + kPairKey * ((n - none) * a + span * (n * (n + 1) / 2 - none * (none + 1) / 2));
 }
 __device__ __forceinline__ int64_t cost(const Sequence& s, int span) {  // of one head group
   if (s.units == 0) return 0;
-  return cost_before(s, s.units - 1, span) + kUnitCost + static_cast<int64_t>(unit_tiles(s, s.units - 1, span)) * s.lk;
+  return cost_before(s, s.units - 1, span) + kUnitCost + static_cast<int64_t>(key_cost(unit_tiles(s, s.units - 1, span))) * s.lk;
 }
 
 // What a CTA works on: blocks [t0, t1) of a unit.  b: -2 no more.
@@ -180,10 +189,10 @@ struct Walk {
     for (;;) {
       if (start >= end) return false;
       const int keys = unit_keys(s, unit, span), tiles = unit_tiles(s, unit, span), blocks = blocks_of(keys);
-      const int64_t each = kRows * tiles, first = start + kUnitCost;
+      const int64_t each = kRows * key_cost(tiles), first = start + kUnitCost;
       int t0 = 0, t1 = blocks;
       bool mine;
-      if (static_cast<int64_t>(tiles) * keys * kUncut <= quota) {
+      if (static_cast<int64_t>(key_cost(tiles)) * keys * kUncut <= quota) {
         mine = start >= begin;
       } else {
         if (begin > first) t0 = static_cast<int>(min((begin - first + each - 1) / each, static_cast<int64_t>(blocks)));
@@ -198,7 +207,7 @@ struct Walk {
           cut = Cut{s.q0, s.lq, unit * span, hg * p.pack, tiles, range, static_cast<int>((first + each * (blocks - 1)) / quota), 0};
       }
       // the next unit
-      start += kUnitCost + static_cast<int64_t>(tiles) * keys;
+      start += kUnitCost + static_cast<int64_t>(key_cost(tiles)) * keys;
       if (++unit == s.units) {
         unit = 0;
         if (++hg == p.head_groups) {
