@@ -1062,7 +1062,8 @@ template <int HD>
 __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const ChunkParams p) {
   constexpr int kGroups = HD / 4 / kJoinWarps;
   __shared__ uint2 staged[32][HD / 4 + 1];
-  grid_dep_launch();
+  // The next kernel starts when this one ends: started early, the next chunk call's CTAs go to SMs in the order in which they get free, and
+  // neighbours in work, which read the same keys, lie on two dies (24 ungrouped in a row: 106 us, early 122; 40 mixed 296, 303; 4 chunks 1178, 1162).
   grid_dep_wait();
   const Cut cut = p.cuts[blockIdx.x];
   if (cut.last < 0) return;
