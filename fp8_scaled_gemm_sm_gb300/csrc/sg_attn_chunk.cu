@@ -63,8 +63,8 @@ constexpr int kEarly = 4;        // 16-key steps of a block whose weights are ha
 // What work costs, in quarters of what a key costs a unit of two row tiles: a key of a unit with one tile, whose blocks are loaded and
 // converted for half as many scores (1.2 to 1.6 us a block, 1.9 for both tiles; as half of a pair's 40 mixed take 364 us and
 // 2 long documents 1420, as three quarters 308 and 1163, as five sixths 317 and 1163), and what a unit costs beside its keys
-// (40 mixed and 4 chunks with 3072: 308 and 1190 us; 2304: 354 and 1243).
-constexpr int kPairKey = 4, kSingleKey = 3, kUnitCost = 3072;
+// (40 mixed and 4 chunks with 3200: 308 and 1182 us; 2304: 354 and 1243).
+constexpr int kPairKey = 4, kSingleKey = 3, kUnitCost = 3200;
 constexpr int kUncut = 32;       // units of up to 1 / kUncut of a range are not cut (4 chunks: 1190 us; 16: 1206)
 constexpr int kLeast = 768;      // of a range, so that every range of a cut unit has a block of it (one question: 24.6 us; 512: 26.6)
 constexpr float kSlack = 8.f;    // log2 of how far a maximum may pass its reference

@@ -404,6 +404,27 @@ def test_between_decodes_on_one_plan():
     assert torch.equal(o1[0], out) and torch.equal(d1[0], dec[0])
 
 
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 128), (6, 6, 64)])
+def test_other_batches_in_a_row_on_one_plan(hq, hk, d):
+    """Parts and cut units of one call are not those of the next: the whole batch, its first sequence, the others, in turn."""
+    c = Case(hq, hk, d, 32, [70, 300, 3, 129], [6000, 40, 9000, 1300], seed=21)
+    table, lens, cu = c.args
+    parts = []
+    for first, last in ((0, 4), (0, 1), (1, 4), (2, 3)):
+        lo, hi = (int(cu[i]) for i in (first, last))
+        parts.append((c.q[lo:hi], table[first:last], lens[first:last], cu[first:last + 1] - cu[first]))
+    call = lambda q, *rest: c.plan.chunk(q, c.cache, *rest, scale=c.scale)  # noqa: E731
+    want = []
+    for x in parts:
+        want.append(call(*x))
+        torch.cuda.synchronize()
+    c.check(*want[0])
+    got = [call(*x) for _ in range(4) for x in parts]
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert torch.equal(g[0], want[i % 4][0]) and torch.equal(g[1], want[i % 4][1])
+
+
 @pytest.mark.parametrize("hq,hk,d,new,ctx,tile", [(8, 2, 128, [30, 100], [500, 900], 0), (4, 4, 64, [5, 9], [3000, 100], 3), (4, 1, 128, [2], [9000], 40)])
 def test_gives_up(hq, hk, d, new, ctx, tile):
     """A load that never comes: the call ends, says so, and the next one is right."""
