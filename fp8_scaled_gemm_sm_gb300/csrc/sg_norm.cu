@@ -18,7 +18,7 @@
 // codes once; the row stays in registers in between.  A CTA a row, rows dealt out in turn.  Where there are many rows, what is close to that
 // bound is instructions and the wait for a row's sum: so rows are on their way two ahead, a warp of its own forms the root
 // while the others take the next row, and a block's scale is divided once.  32768 x 7168 bf16 with a residual: blockscale
-// 297 us (81 % of the copy rate), mxfp8 281, ptpc 279, bf16 309.
+// 295 us (82 % of the copy rate), mxfp8 281, ptpc 279, bf16 309.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -374,10 +374,13 @@ __global__ void __launch_bounds__(MOST, CTAS) norm_rows_kernel(const NormParams 
   };
 #pragma unroll
   for (int s = 0; s < kAhead; ++s) ahead(blockIdx.x + s * step, s);
+  // Weights stay in registers where there are 128 a thread (32768 x 7168 ptpc 278 us, read again for each row 310), not where there are
+  // 96, which would spill (8192 x 16384 195 and 201, 16384 x 8192 183 and 184).
+  constexpr bool kKept = MOST == 256;
   Raw8<true> weight[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
-    if (there(i)) load_vec<true>(p.weight, 8 * static_cast<int64_t>(i * T + tid), weight[i]);
+    if (kKept && there(i)) load_vec<true>(p.weight, 8 * static_cast<int64_t>(i * T + tid), weight[i]);
   int stage = 0;
   // Row r as it is kept, and its squares.
   auto take = [&](int r, int turn, uint4(&kept)[VPT]) {
@@ -421,6 +424,7 @@ __global__ void __launch_bounds__(MOST, CTAS) norm_rows_kernel(const NormParams 
     const uint64_t g2 = pair_of(g, g);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
+      if (!kKept && there(i)) load_vec<true>(p.weight, 8 * static_cast<int64_t>(i * T + tid), weight[i]);
       float w[8];
       unpack8<true>(weight[i], w);
       weigh(f[i], g2, w);
@@ -474,9 +478,10 @@ template <int MODE, bool BF16>
 sg_status_t launch_width(const NormParams& p, int num_sms, cudaStream_t stream) {
   const int vecs = p.C / 8;  // at most 4096
   // From four rows an SM and 2048 columns on, bf16 rows with a residual come through shared memory: 32768 x 7168 for blockscale
-  // 297 us, straight to registers 400; 16384 x 4096 for mxfp8 86 and 100; 20000 x 2048 57 and 60; but 20000 x 1024 for ptpc 42 and 34, where a
-  // CTA's last warp is one of two.  Up to 7168 columns two CTAs have 8 warps each and 128 registers a thread (8192 columns, 9 warps: 96, and some
-  // of them in memory; 16384 x 8192 for ptpc 186 and 214 us), above 8192 one CTA has an SM (8192 x 16384 204 and 225; 16384 x 8192 264).
+  // 295 us, straight to registers 400; 16384 x 4096 for mxfp8 86 and 100; 20000 x 2048 57 and 60; but 20000 x 1024 for ptpc 42 and 34, where a
+  // CTA's last warp is one of two.  Up to 7168 columns two CTAs have 8 warps each and 128 registers a thread, at 8192 9 warps
+  // and 96 (16384 x 8192 for ptpc 183 and 214 us), above 8192 one CTA has an SM (8192 x 16384 195 and 225; 16384 x 8192 264).
+  // More CTAs with fewer registers for narrower rows: 30000 x 4096 blockscale 155 (four), 197 (three), two 147.
   if constexpr (BF16) {
     if (p.R >= 4 * num_sms && p.residual && vecs >= 256) {
       const bool all = vecs % 128 == 0;  // every thread has four

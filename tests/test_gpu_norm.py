@@ -182,6 +182,26 @@ def test_graph_and_stream(norm):
         assert torch.equal(a, b)
 
 
+def test_many_rows_captured_in_place(norm):
+    """The graph adds the residual again with each replay, and rows that are not finite stay alone."""
+    x, r, w = (t.cuda() for t in _make(1000, 4096, 11, torch.bfloat16))
+    x[7, 5], x[650, 9] = float("inf"), float("nan")
+    add, kept = r.clone(), x.clone()
+    norm("mxfp8", kept.clone(), w, residual=add)  # loaded before the capture
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        codes, scale, _ = norm("mxfp8", kept, w, residual=add, residual_out=kept)
+    want = x
+    for _ in range(3):
+        graph.replay()
+        wc, ws, want = norm("mxfp8", want, w, residual=add)
+        assert torch.equal(codes, wc) and torch.equal(scale, ws) and torch.equal(kept.view(torch.int16), want.view(torch.int16))
+    rest = [i for i in range(1000) if i not in (7, 650)]
+    clean, _, _ = norm("mxfp8", torch.where(torch.isfinite(x), x, 0), w, residual=add)
+    first, _, _ = norm("mxfp8", x, w, residual=add)
+    assert torch.equal(first[rest], clean[rest])
+
+
 def test_tensor_refusals(norm):
     from fp8_scaled_gemm_sm_gb300 import ScaledGemmError
 
