@@ -61,7 +61,6 @@ class AttentionLayer:
         o, _ = self.plan.decode(q, self.cache, block_table, ctx_lens + 1)
         return self._output(o)
 
-
     def step(self, x, residual, weight, pool, rows, tokens, cu_seqlens):
         """x and residual [tokens, hidden], packed by cu_seqlens: `tokens` new ones of each of the pool's `rows`, whose pages it
         hands out here.  Returns the output, the residual stream, and whether each row got its pages."""
