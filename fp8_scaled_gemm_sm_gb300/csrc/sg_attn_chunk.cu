@@ -731,9 +731,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // the row's largest value to [2^7, 2^8)
+        // The row's largest value to [2^7, 2^8).  A row with an infinity has NaN for all of its codes, as a row with NaN has for one: every
+        // score is NaN then, and those of keys that the row does not see are put out like any other's, which a factor that is NaN would undo.
         const int field = min(261 - static_cast<int>(__float_as_uint(top) >> 23), 253);
-        const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
+        const float up = __uint_as_float(top == INFINITY ? 0x7FC00000u : static_cast<uint32_t>(field) << 23);
         uint32_t hi[2], lo[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -751,8 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t at = hi_tile + r * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 8);
         st_shared_v2(at, hi[0], hi[1]);
         st_shared_v2(at + L::kTile, lo[0], lo[1]);
-        if (d == 0)  // 1 / up; a row with an infinity is NaN
-          st_shared(factors + r * 4, top == INFINITY ? 0x7FC00000u : static_cast<uint32_t>(254 - field) << 23);
+        if (d == 0) st_shared(factors + r * 4, static_cast<uint32_t>(254 - field) << 23);  // 1 / up
       }
       fence_proxy_async_smem();
       __syncwarp();

@@ -486,3 +486,28 @@ def test_refusals():
         assert L.scaled_attn_chunk(*a) == status, (i, v)
     assert L.scaled_attn_chunk(*good) == 0
     torch.cuda.synchronize()
+
+
+def test_infinite_queries_that_see_no_key():
+    """Zero and -infinity as for any row that sees nothing, where the rows of its tile after it do: ahead of the sequence's first token, and
+    over pages that are not there."""
+    def edit(table, codes, scales):
+        table[1, :2] = -1
+
+    c = Case(4, 2, 64, 16, [50, 20], [0, 20], seed=23, edit=edit)
+    lens = [20, 40]
+    c.args[1] = _ints(lens)
+    clean = c.run()
+    c.check(*clean, lens=lens)
+    assert bool((clean[0][:30] == 0).all()) and bool((clean[0][50:62] == 0).all())  # 12 rows see up to 32 keys, none of which is there
+    c.q = c.q.clone()
+    for r, value in ((7, float("inf")), (29, -float("inf")), (51, float("inf")), (61, float("nan"))):
+        c.q[r, 1, 3] = value
+    out, lse = c.run()
+    assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+    c.q[30, 1, 3] = c.q[62, 1, 3] = float("inf")  # the first rows that see a key
+    out, lse = c.run()
+    for r in (30, 62):
+        assert bool(torch.isnan(out[r, 1].float()).all()) and bool(torch.isnan(lse[r, 1]))
+        out[r, 1], lse[r, 1] = clean[0][r, 1], clean[1][r, 1]
+    assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
