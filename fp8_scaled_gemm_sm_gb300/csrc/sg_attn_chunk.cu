@@ -906,7 +906,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           sum = fmaf(sums[0] + sums[1], ex2(vref), sum);
         } else {
           // Score, difference and sum one by one, 16 keys at a time; scores are still in tensor memory, and
-          // weights (half as wide) do not reach those that are yet to be read.
+          // weights (half as wide) do not reach those that are yet to be read.  A row's sum takes a block's, and that 16 keys', as above: of
+          // 130000 equal weights added one by one it is off by up to 2^-9.
+          float total = 0.f;
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
             uint32_t x[16], w[8];
@@ -915,16 +917,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float lift = __uint_as_float(ld_shared(base + L::kOffInfo + slot * 64 + 32 + c * 4)) - vref;
             const int left = !edge ? 16 : (gone >> c) & 1 ? 0 : room - 16 * c;
             tmem_wait_ld();
+            float part = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float y = i < left ? __fsub_rn(__fmul_rn(__uint_as_float(x[i]), by), ref) : -INFINITY;
-              sum += ex2(y);
+              part += ex2(y);
               x[i] = __float_as_uint(ex2(y + lift));
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = pack_f16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
             tmem_st_32x32b_x8(s_addr + 8 * c, w);
+            total += part;
           }
+          sum += total;
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(p_half(t));

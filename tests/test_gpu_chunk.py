@@ -511,3 +511,27 @@ def test_infinite_queries_that_see_no_key():
         assert bool(torch.isnan(out[r, 1].float()).all()) and bool(torch.isnan(lse[r, 1]))
         out[r, 1], lse[r, 1] = clean[0][r, 1], clean[1][r, 1]
     assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+
+
+@pytest.mark.parametrize("k_code,v_code", [(127, 127), (127, 20), (127, 230), (57, 127)])
+def test_sum_of_many_equal_weights(k_code, v_code):
+    """Sums of up to 130000 weights of 2^-0.95, with scales that take the slower way too.  A CTA adds up to every second block of a row:
+    the sum of a block is off by at most (15 + 7) 2^-24, each of 508 additions by 2^-24 of what they give, the exponential by 2^-22; the
+    logarithm's two roundings and the last product's are of numbers below 32, 2^-20 each."""
+    pkg = _pkg()
+    plan = pkg.PagedAttention(1, 1, 64, 128)
+    codes = [torch.zeros(1, 1, 128, 64, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    codes[0][..., 0] = 0x38  # 1
+    codes[1][:] = 0x38
+    scales = [torch.full((1, 1, 8), x, dtype=torch.uint8, device="cuda") for x in (k_code, v_code)]
+    B, most = 160, 130000  # more sequences than CTAs: a range of the work is nearly a sequence
+    table = torch.zeros(B, 1016, dtype=torch.int32, device="cuda")
+    lens = np.array([most - 37 * b for b in range(B)])
+    q = torch.zeros(B, 1, 64, dtype=torch.bfloat16, device="cuda")
+    q[:, 0, 0] = 2.0 ** (127 - k_code)
+    out, lse = plan.chunk(q, pkg.KVCache(*codes, *scales), table, _ints(lens), _ints(list(range(B + 1))), scale=0.05 * np.log(2))
+    torch.cuda.synchronize()
+    want = 0.05 * np.log(2) + np.log(lens)
+    assert float(np.abs(_f64(lse)[:, 0] - want).max()) <= (15 + 7 + 508) * 2.0 ** -24 + 2.0 ** -22 + 3 * 2.0 ** -20
+    value = 2.0 ** (v_code - 127)
+    assert bool(((out.double() - value).abs() <= value * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -13)).all())
