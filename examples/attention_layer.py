@@ -63,13 +63,15 @@ class AttentionLayer:
 
     def step(self, x, residual, weight, pool, rows, tokens, cu_seqlens):
         """x and residual [tokens, hidden], packed by cu_seqlens: `tokens` new ones of each of the pool's `rows`, whose pages it
-        hands out here.  Returns the output, the residual stream, and whether each row got its pages."""
+        hands out here.  Returns the output, the residual stream, and whether each row got its pages; a row that did not is left as
+        it was, and its tokens attend to nothing."""
         codes, scale, residual = norm_quantize("ptpc", x, weight, residual=residual)
         q, k, v = self._heads(codes, scale, x)
         at = rows.long()
         before = pool.lens[at]
         ok = pool.grow(rows, tokens)
-        table = pool.table[at]
+        # without pages for its new tokens a row has none in this step: behind its last token they would go into a page that it holds
+        table = torch.where(ok[:, None] > 0, pool.table[at], -1)
         q, _ = self.plan.append(q, k, v, self.cache, table, before, cu_seqlens)
         o, _ = self.plan.chunk(q, self.cache, table, pool.lens[at], cu_seqlens)
         return self._output(o), residual, ok

@@ -115,3 +115,27 @@ def test_a_captured_step(example):
 def test_command(example, capsys):
     example.main(["--hidden", "512", "--heads", "8", "2", "--dim", "64", "--prompts", "130", "7", "--steps", "3", "--answers", "5"])
     assert "answers: 5 forks of 130 tokens, 3 more each" in capsys.readouterr().out
+
+
+def test_a_row_that_gets_no_pages_is_left_alone(example):
+    """Its cache and length stay as they were, its tokens see nothing, and the other rows are as in a step without it."""
+    layer, weight, g = _layer(example, pages=4)
+    pool = example.PagePool.new(layer.plan, layer.cache, 2, 4)
+    x = torch.randn(90, 512, generator=g, device="cuda").bfloat16()
+    layer.step(x[:60], torch.zeros_like(x[:60]), weight, pool, ints(0, 1), ints(40, 20), ints(0, 40, 60))  # 2 pages and 1
+    cache = (layer.cache.k, layer.cache.v, layer.cache.k_scale, layer.cache.v_scale)
+    before = [t.clone() for t in cache + (pool.table, pool.lens, pool.refs)]
+    # row 0 gets the last page for its 70 tokens, and there is none for row 1, which has room for 12 of its 15 in the page that it holds
+    lone, _, _ = layer.step(x[60:], torch.zeros_like(x[60:]), weight, pool, ints(0), ints(30), ints(0, 30))
+    for t, b in zip(cache + (pool.table, pool.lens, pool.refs), before):
+        t.copy_(b)
+    both = torch.cat([x[60:], x[60:75]])
+    y, r, ok = layer.step(both, torch.zeros_like(both), weight, pool, ints(0, 1), ints(30, 15), ints(0, 30, 45))
+    assert ok.tolist() == [1, 0] and pool.lens.tolist() == [70, 20]
+    page = int(before[4][1, 0])
+    for t, b in zip(cache, before):
+        assert torch.equal(t[page], b[page])
+    assert torch.equal(pool.table[1], before[4][1]) and torch.equal(r, both)
+    assert bool((y[30:] == 0).all())
+    got, want = y[:30].float(), lone.float()
+    assert float((got - want).norm() / want.norm()) < 2.0 ** -5
