@@ -1,6 +1,7 @@
 // scaled_attention.cu -- the C ABI of the attention operators: plans, argument
 // checks and dispatch (include/scaled_attention.h).
 #include <cmath>
+#include <initializer_list>
 #include <new>
 
 #include <cuda.h>
@@ -75,6 +76,24 @@ sg_status_t check_pool(const sg_page_pool_t* p) {
   if (!p->table || !p->lens || !p->refs || !p->scratch) return refuse(SG_ERR_INVALID_ARG, "pool: NULL pointer");
   if (!aligned(p->table, 4) || !aligned(p->lens, 4) || !aligned(p->refs, 16) || !aligned(p->scratch, 16))
     return refuse(SG_ERR_MISALIGNED, "pool: pointer");
+  return SG_OK;
+}
+
+// A pool call reads its requests while it changes the pool and writes its answer: each lies in memory of its own.
+sg_status_t check_apart(const sg_page_pool_t* p, std::initializer_list<const int32_t*> requests, int64_t n, const int32_t* answer,
+                        int64_t answers) {
+  const struct { const void* p; int64_t bytes; } changed[] = {{p->table, 4 * p->rows * p->table_stride},
+                                                              {p->lens, 4 * p->rows},
+                                                              {p->refs, 4 * p->num_pages},
+                                                              {p->scratch, sg::pool_scratch_bytes(p->rows, p->num_pages)},
+                                                              {answer, 4 * answers}};
+  for (int i = 0; i < 5; ++i) {
+    if (i < 4 && sg::ranges_overlap(changed[i].p, changed[i].bytes, answer, 4 * answers))
+      return refuse(SG_ERR_INVALID_ARG, "pool: the answer overlaps the pool");
+    for (const int32_t* r : requests)
+      if (sg::ranges_overlap(changed[i].p, changed[i].bytes, r, 4 * n))
+        return refuse(SG_ERR_INVALID_ARG, "pool: requests overlap the pool or the answer");
+  }
   return SG_OK;
 }
 
@@ -395,6 +414,7 @@ sg_status_t scaled_attn_pool_release(sg_attn_t h, const sg_page_pool_t* pool, co
   if (n > kMaxCount) return refuse(SG_ERR_UNSUPPORTED_SHAPE, "pool release: n >= 2^31 - 65536");
   if (n == 0) return SG_OK;
   SG_TRY(check_ints(which, "pool release: which"));
+  SG_TRY(check_apart(pool, {which}, n, nullptr, 0));
   SG_TRY(check_device(h));
   const sg_status_t r = sg::pool_release(h->shape, *pool, which, n, reinterpret_cast<cudaStream_t>(stream));
   return r == SG_OK ? SG_OK : refuse(r, "pool release: kernel launch");
@@ -409,6 +429,7 @@ sg_status_t scaled_attn_pool_grow(sg_attn_t h, const sg_page_pool_t* pool, const
   SG_TRY(check_ints(which, "pool grow: which"));
   SG_TRY(check_ints(add, "pool grow: add"));
   SG_TRY(check_ints(ok, "pool grow: ok"));
+  SG_TRY(check_apart(pool, {which, add}, n, ok, n));
   SG_TRY(check_device(h));
   const sg_status_t r = sg::pool_grow(h->shape, *pool, which, add, n, ok, reinterpret_cast<cudaStream_t>(stream));
   return r == SG_OK ? SG_OK : refuse(r, "pool grow: kernel launch");
@@ -424,6 +445,7 @@ sg_status_t scaled_attn_pool_fork(sg_attn_t h, const sg_page_pool_t* pool, const
   SG_TRY(check_ints(src, "pool fork: src"));
   SG_TRY(check_ints(dst, "pool fork: dst"));
   SG_TRY(check_ints(ok, "pool fork: ok"));
+  SG_TRY(check_apart(pool, {src, dst}, n, ok, n));
   SG_TRY(check_device(h));
   const sg_status_t r = sg::pool_fork(h->shape, *pool, caches, layers, src, dst, n, ok, reinterpret_cast<cudaStream_t>(stream));
   return r == SG_OK ? SG_OK : refuse(r, "pool fork: kernel launch");
@@ -435,6 +457,7 @@ sg_status_t scaled_attn_pool_compact(sg_attn_t h, const sg_page_pool_t* pool, co
   SG_TRY(check_pool(pool));
   SG_TRY(check_layers(h, pool, caches, layers));
   SG_TRY(check_ints(in_use, "pool compact: in_use"));
+  SG_TRY(check_apart(pool, {}, 0, in_use, 1));
   SG_TRY(check_device(h));
   const sg_status_t r = sg::pool_compact(h->shape, *pool, caches, layers, in_use, reinterpret_cast<cudaStream_t>(stream));
   return r == SG_OK ? SG_OK : refuse(r, "pool compact: kernel launch");

@@ -16,6 +16,7 @@ class PagePool:
     a CUDA graph.  Calls on one pool have to be ordered, with one another and with attention over the rows that they
     change.  Requests are int32 tensors on the pool's device, carried out in their order, the lowest free pages
     first; an answer is an int32 tensor, 1 where a request was carried out and 0 where it was refused.
+    None of them may share memory with what a call changes (the pool's tensors, the answer).
     """
 
     def __init__(self, plan, caches, table, lens, refs):

@@ -154,7 +154,8 @@ typedef struct sg_page_pool {
  * row twice to be changed, the first request has it and the others are refused (release: it is released).  ok[i] (int32) is 1
  * where request i was carried out, 0 where it was refused, which leaves its row as it was.  Once the free
  * pages do not suffice for a request, later ones that need any are refused too.  rows, num_pages < 2^31 - 65536; rows * table_stride < 2^31;
- * n <= rows, or < 2^31 - 65536 for release. */
+ * n <= rows, or < 2^31 - 65536 for release.  Requests overlap neither the pool's memory nor the answer, nor the answer the pool's (checked:
+ * SG_ERR_INVALID_ARG; two requests of a call may be the same). */
 
 /* Bytes of a pool's scratch; 0 for sizes that no pool has. */
 int64_t scaled_attn_pool_scratch_bytes(int64_t rows, int64_t num_pages);

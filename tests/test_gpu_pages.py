@@ -328,3 +328,23 @@ def test_one_sequence_after_a_fork(pkg):
     pool.compact()
     got, _ = plan.decode(q[2:], cache, pool.table[2:], pool.lens[2:])
     assert torch.equal(got, want)
+
+
+def test_requests_and_answers_that_the_call_changes_are_refused(pkg):
+    """Requests are read while the pool and the answer are written."""
+    pool, model, arrays, _ = _setup(pkg, 6, 6, 40)
+    a, b = ints([0, 1, 2]), ints([20, 7, 33])
+    assert pool.grow(a, b).tolist() == model.grow([0, 1, 2], [20, 7, 33])
+    words = pool.scratch.view(torch.int32)
+    for bad in (lambda: pool.grow(a, b, ok=b), lambda: pool.grow(a, b, ok=a), lambda: pool.grow(a, pool.lens[:3]), lambda: pool.grow(pool.table[0, :3], b),
+                lambda: pool.grow(a, b, ok=pool.lens[3:]), lambda: pool.grow(a, b, ok=pool.refs[-3:]), lambda: pool.grow(words[-3:], b),
+                lambda: pool.fork(a, a + 3, ok=a), lambda: pool.fork(pool.lens[3:], a), lambda: pool.fork(a, pool.refs[:3]),
+                lambda: pool.release(pool.lens), lambda: pool.release(pool.table[1]), lambda: pool.compact(in_use=pool.table[5, 5:]),
+                lambda: pool.compact(in_use=words[:1]), lambda: pool.compact(in_use=pool.refs[39:])):
+        with pytest.raises(pkg.ScaledGemmError):
+            bad()
+    _same(pool, model, arrays)
+    both = ints([0, 1, 2, 3, 4, 5])  # of one tensor, side by side
+    assert pool.fork(both[:3], both[3:]).tolist() == model.fork([0, 1, 2], [3, 4, 5])
+    assert pool.grow(both[:3], both[:3]).tolist() == model.grow([0, 1, 2], [0, 1, 2])
+    _same(pool, model, arrays)
