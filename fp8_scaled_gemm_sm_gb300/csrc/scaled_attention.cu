@@ -73,7 +73,9 @@ sg_status_t check_pool(const sg_page_pool_t* p) {
   if (p->rows < 0 || p->table_stride < 0 || p->num_pages < 0) return refuse(SG_ERR_INVALID_ARG, "pool: negative size");
   if (p->rows > kMaxCount || p->num_pages > kMaxCount) return refuse(SG_ERR_UNSUPPORTED_SHAPE, "pool: rows or pages >= 2^31 - 65536");
   if (p->table_stride > kMaxDim || p->rows * p->table_stride > kMaxDim) return refuse(SG_ERR_UNSUPPORTED_SHAPE, "pool: table entries >= 2^31");
-  if (!p->table || !p->lens || !p->refs || !p->scratch) return refuse(SG_ERR_INVALID_ARG, "pool: NULL pointer");
+  // nothing looks at an array without elements
+  if ((!p->table && p->rows * p->table_stride > 0) || (!p->lens && p->rows > 0) || (!p->refs && p->num_pages > 0) || !p->scratch)
+    return refuse(SG_ERR_INVALID_ARG, "pool: NULL pointer");
   if (!aligned(p->table, 4) || !aligned(p->lens, 4) || !aligned(p->refs, 16) || !aligned(p->scratch, 16))
     return refuse(SG_ERR_MISALIGNED, "pool: pointer");
   return SG_OK;

@@ -138,7 +138,7 @@ sg_status_t scaled_attn_prompt(sg_attn_t h, const void* q, int64_t q_stride, con
                                int64_t Tq, int64_t Tk, int64_t B, int causal, float scale, void* out,
                                float* lse, sg_stream_t stream);
 
-/* The pages of a cache and the sequences that hold them, all in device memory.  The caches of a
+/* The pages of a cache and the sequences that hold them, all in device memory.  An array without elements may be NULL.  The caches of a
  * model's layers share one pool: a page number means that page of each. */
 typedef struct sg_page_pool {
   int32_t* table;  /* [rows][table_stride]: the pages of each row's tokens in order, -1 past the last (4-byte aligned) */

@@ -348,3 +348,18 @@ def test_requests_and_answers_that_the_call_changes_are_refused(pkg):
     assert pool.fork(both[:3], both[3:]).tolist() == model.fork([0, 1, 2], [3, 4, 5])
     assert pool.grow(both[:3], both[:3]).tolist() == model.grow([0, 1, 2], [0, 1, 2])
     _same(pool, model, arrays)
+
+
+@pytest.mark.parametrize("rows,entries,pages", [(0, 4, 5), (3, 0, 5), (3, 4, 0), (0, 0, 0)])
+def test_pools_without_rows_entries_or_pages(pkg, rows, entries, pages):
+    """Torch's empty tensors have no address.  What needs none of what is missing is carried out."""
+    plan = pkg.PagedAttention(4, 2, 64, 16)
+    pool = pkg.PagePool.new(plan, plan.new_cache(pages), rows, entries)
+    pool.release(ints([0, 2, 7]))
+    assert pool.compact().tolist() == [0]
+    if rows:
+        assert pool.grow(ints([0, 1, 2]), ints([0, 1, 0])).tolist() == [1, int(entries > 0 and pages > 0), 1]
+        assert pool.fork(ints([0, 2]), ints([2, 0])).tolist() == [1, 1]
+        assert pool.lens.tolist() == [0, 0, 0]
+    none = ints([])
+    assert pool.grow(none, none).tolist() == [] and pool.fork(none, none).tolist() == []
