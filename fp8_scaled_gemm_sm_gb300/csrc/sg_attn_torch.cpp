@@ -353,6 +353,8 @@ PyObject* make_pool(PyObject*, PyObject* const* a, Py_ssize_t n) {
 const Pool& pool(PyObject* o, const Plan& p) {
   auto* x = static_cast<Pool*>(PyCapsule_GetPointer(o, kPool));
   if (!x) throw BadArgument{"not a pool"};
+  if (x->heads != p.kv_heads || x->page != p.page || x->dim != p.dim || x->device != p.device)
+    throw BadArgument{"the pool's layout differs from the plan's"};
   return *x;
 }
 

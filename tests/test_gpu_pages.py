@@ -363,3 +363,20 @@ def test_pools_without_rows_entries_or_pages(pkg, rows, entries, pages):
         assert pool.lens.tolist() == [0, 0, 0]
     none = ints([])
     assert pool.grow(none, none).tolist() == [] and pool.fork(none, none).tolist() == []
+
+
+def test_plans_of_another_layout_are_refused(pkg):
+    """Pages of another size would be counted and moved with the plan's; one of the same layout serves."""
+    pool, model, arrays, _ = _setup(pkg, 4, 3, 9)
+    a, b = ints([0, 1]), ints([20, 30])
+    own = pool.plan
+    for other in (pkg.PagedAttention(4, 2, 64, 32), pkg.PagedAttention(4, 4, 64, 16), pkg.PagedAttention(4, 2, 128, 16)):
+        pool.plan = other
+        for call in (lambda: pool.grow(a, b), lambda: pool.fork(a, a + 2), lambda: pool.release(a), lambda: pool.compact()):
+            with pytest.raises(ValueError):
+                call()
+    pool.plan = pkg.PagedAttention(8, 2, 64, 16)
+    assert pool.grow(a, b).tolist() == model.grow([0, 1], [20, 30])
+    pool.plan = own
+    assert pool.fork(a, a + 2).tolist() == model.fork([0, 1], [2, 3])
+    _same(pool, model, arrays)
