@@ -3,6 +3,7 @@
 #include <cmath>
 #include <initializer_list>
 #include <new>
+#include <utility>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -115,6 +116,16 @@ sg_status_t check_layers(const sg_attn* h, const sg_page_pool_t* pool, const sg_
 // The bytes that rows of a strided operand cover.
 int64_t row_bytes(int64_t rows, int64_t stride, int64_t width) {
   return rows > 0 ? 2 * ((rows - 1) * stride + width) : 0;
+}
+
+// Of the attention calls: neither out nor lse over q (or k, v: {p, bytes}), nor one over the other.
+sg_status_t check_outputs(const void* out, const float* lse, int64_t rows, const sg::AttnShape& s,
+                          std::initializer_list<std::pair<const void*, int64_t>> inputs, const char* what) {
+  const int64_t out_bytes = 2 * rows * s.Hq * s.D, lse_bytes = 4 * rows * s.Hq;
+  for (const auto& i : inputs)
+    if (sg::ranges_overlap(out, out_bytes, i.first, i.second) || sg::ranges_overlap(lse, lse_bytes, i.first, i.second))
+      return refuse(SG_ERR_INVALID_ARG, what);
+  return sg::ranges_overlap(out, out_bytes, lse, lse_bytes) ? refuse(SG_ERR_INVALID_ARG, what) : SG_OK;
 }
 
 #define SG_TRY(expr)                        \
@@ -297,9 +308,7 @@ sg_status_t scaled_attn_decode(sg_attn_t h, const sg_kv_cache_t* cache, const vo
   SG_TRY(check_ints(kv_lens, "decode: kv_lens"));
   if (!out) return refuse(SG_ERR_INVALID_ARG, "decode: out is NULL");
   if (!aligned(out, 16) || !aligned(lse, 4)) return refuse(SG_ERR_MISALIGNED, "decode: outputs");
-  const int64_t ob = 2 * B * qn * s.Hq * s.D;
-  if (sg::ranges_overlap(out, ob, q, row_bytes(B * qn, q_stride, int64_t(s.Hq) * s.D)))
-    return refuse(SG_ERR_INVALID_ARG, "decode: out overlaps q");
+  SG_TRY(check_outputs(out, lse, B * qn, s, {{q, row_bytes(B * qn, q_stride, int64_t(s.Hq) * s.D)}}, "decode: an output overlaps q or the other"));
   SG_TRY(check_device(h));
   sg::AttnArgs a{};
   a.cache = *cache;
@@ -336,8 +345,7 @@ sg_status_t scaled_attn_chunk(sg_attn_t h, const sg_kv_cache_t* cache, const voi
   SG_TRY(check_ints(cu_q, "chunk: cu_q"));
   if (!out) return refuse(SG_ERR_INVALID_ARG, "chunk: out is NULL");
   if (!aligned(out, 16) || !aligned(lse, 4)) return refuse(SG_ERR_MISALIGNED, "chunk: outputs");
-  if (sg::ranges_overlap(out, 2 * T * s.Hq * s.D, q, row_bytes(T, q_stride, int64_t(s.Hq) * s.D)))
-    return refuse(SG_ERR_INVALID_ARG, "chunk: out overlaps q");
+  SG_TRY(check_outputs(out, lse, T, s, {{q, row_bytes(T, q_stride, int64_t(s.Hq) * s.D)}}, "chunk: an output overlaps q or the other"));
   SG_TRY(check_device(h));
   sg::AttnArgs a{};
   a.cache = *cache;
@@ -376,11 +384,11 @@ sg_status_t scaled_attn_prompt(sg_attn_t h, const void* q, int64_t q_stride, con
   SG_TRY(check_ints(cu_k, "prompt: cu_k"));
   if (!out) return refuse(SG_ERR_INVALID_ARG, "prompt: out is NULL");
   if (!aligned(out, 16) || !aligned(lse, 4)) return refuse(SG_ERR_MISALIGNED, "prompt: outputs");
-  const int64_t ob = 2 * Tq * s.Hq * s.D;
-  if (sg::ranges_overlap(out, ob, q, row_bytes(Tq, q_stride, int64_t(s.Hq) * s.D)) ||
-      sg::ranges_overlap(out, ob, k, row_bytes(Tk, k_stride, int64_t(s.Hk) * s.D)) ||
-      sg::ranges_overlap(out, ob, v, row_bytes(Tk, v_stride, int64_t(s.Hk) * s.D)))
-    return refuse(SG_ERR_INVALID_ARG, "prompt: out overlaps an input");
+  SG_TRY(check_outputs(out, lse, Tq, s,
+                       {{q, row_bytes(Tq, q_stride, int64_t(s.Hq) * s.D)},
+                        {k, row_bytes(Tk, k_stride, int64_t(s.Hk) * s.D)},
+                        {v, row_bytes(Tk, v_stride, int64_t(s.Hk) * s.D)}},
+                       "prompt: an output overlaps an input or the other"));
   SG_TRY(check_device(h));
   sg::AttnArgs a{};
   a.q = q;

@@ -35,6 +35,7 @@
  *                the table uses its last row.
  *   lse          float [rows][Hq] (4-byte aligned): natural logarithm of the softmax's denominator; -infinity
  *                for a row that sees no key, whose output is zero.  NULL: not written.
+ * Outputs of the attention calls overlap neither q, k, v nor each other (checked: SG_ERR_INVALID_ARG), nor anything else that a call reads.
  *
  * Rules: 1 <= Hq, Hk <= 1024, Hq a multiple of Hk; D a multiple of 16, 16 <= D <= 128; page 16, 32, 64
  * or 128; rot a multiple of 16, 0 <= rot <= D; scale positive and finite; in scaled_attn_prompt scores scale q.k of up to 2^29

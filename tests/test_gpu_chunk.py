@@ -535,3 +535,26 @@ def test_sum_of_many_equal_weights(k_code, v_code):
     assert float(np.abs(_f64(lse)[:, 0] - want).max()) <= (15 + 7 + 508) * 2.0 ** -24 + 2.0 ** -22 + 3 * 2.0 ** -20
     value = 2.0 ** (v_code - 127)
     assert bool(((out.double() - value).abs() <= value * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -13)).all())
+
+
+def test_outputs_that_overlap_are_refused():
+    """lse over the queries or the output, in each of the attention calls."""
+    from fp8_scaled_gemm_sm_gb300 import ScaledGemmError
+
+    c = Case(4, 2, 64, 16, [1, 1, 1], [5, 30, 0], seed=24)
+    q = c.q.contiguous()
+    n = q.shape[0]
+    room = torch.empty(n * 4 * 64, dtype=torch.bfloat16, device="cuda")
+    whole = room.view(n, 4, 64)
+    kv = torch.randn(n, 2, 64, generator=torch.Generator("cpu").manual_seed(1)).bfloat16().cuda()
+    calls = {"chunk": lambda **kw: c.plan.chunk(q, c.cache, *c.args, **kw), "decode": lambda **kw: c.plan.decode(q, c.cache, *c.args[:2], **kw),
+             "prompt": lambda **kw: c.plan.prompt(q, kv, kv, c.args[2], **kw)}
+    over = lambda t: t.view(-1)[-2 * n * 4:].view(torch.float32).view(n, 4)  # noqa: E731
+    for name, call in calls.items():
+        for kw in (dict(out=whole, lse=over(room)), dict(lse=over(q)), dict(out=q)) + ((dict(lse=over(kv)),) if name == "prompt" else ()):
+            with pytest.raises(ScaledGemmError):
+                call(**kw)
+        both = torch.empty(n * 4 * 66, dtype=torch.bfloat16, device="cuda")  # side by side
+        out, lse = call(out=both[:n * 4 * 64].view(n, 4, 64), lse=both[n * 4 * 64:].view(torch.float32).view(n, 4))
+        want = call()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
