@@ -217,3 +217,76 @@ def test_tensor_refusals(norm):
     with pytest.raises(ScaledGemmError):
         norm("blockscale", x[:, :144].contiguous(), w[:144].contiguous())
     assert norm("ptpc", x[:0], w)[0].shape == (0, 256)
+
+
+def _pieces(norm, mode, x, r, w, each):
+    """The same rows in calls of `each` and the rest: a row or less for every CTA."""
+    codes, scale = [], []
+    for i in range(0, x.shape[0], each):
+        c, s, _ = norm(mode, x[i:i + each], w, 1e-6, residual=None if r is None else r[i:i + each])
+        codes.append(c), scale.append(s)
+    return torch.cat(codes), None if scale[0] is None else torch.cat(scale, 0 if mode == "ptpc" else 1)
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("R,C,dtype,residual", [
+    (9000, 256, torch.bfloat16, True),     # a warp a row
+    (9000, 384, torch.float32, False),     # two, with the next row on its way
+    (8000, 896, torch.bfloat16, True),     # two, some lanes past the row
+    (3000, 2048, torch.float32, True),
+    (2600, 8192, torch.float32, True),     # a vector a thread, 1024 threads
+    (2700, 4096, torch.bfloat16, False),
+    (2500, 7680, torch.bfloat16, True),    # wide rows whose threads have no whole vectors
+    (2500, 12288, torch.float32, True),
+    (2600, 16384, torch.bfloat16, False),
+    (2490, 10752, torch.bfloat16, True),
+    (2500, 20480, torch.bfloat16, True),   # eight vectors a thread
+    (2450, 20608, torch.float32, False),
+])
+def test_rows_in_their_ctas_later_turns(norm, mode, R, C, dtype, residual):
+    """The loop over rows without shared memory, in place: as in calls whose CTAs have a row each, bit for bit."""
+    g = torch.Generator("cuda").manual_seed(R + C)
+    x = torch.randn(R, C, generator=g, device="cuda") * torch.exp2(torch.randint(-12, 12, (R, 1), generator=g, device="cuda").float())
+    r = torch.randn(R, C, generator=g, device="cuda") if residual else None
+    for i in (1215, 1216, 1217, 2432, 2433, 3647, 3648, R - 1):  # the last row of a turn, the first ones of the next
+        if i < R:
+            x[i] *= 2.0 ** 80
+    x[1300, 5], x[2440, C - 1] = float("inf"), float("nan")
+    w = 1 + 0.5 * torch.randn(C, generator=g, device="cuda")
+    x, w = x.to(dtype), w.to(dtype)
+    r = None if r is None else r.to(dtype)
+    want = _pieces(norm, mode, x, r, w, 1000)
+    total = x if r is None else (x.float() + r.float()).to(dtype)
+    kept = x.clone() if residual else None
+    codes, scale, got = norm(mode, x if kept is None else kept, w, 1e-6, residual=r, residual_out=kept)
+    rows = torch.tensor([i for i in range(R) if i not in (1300, 2440)], device="cuda")
+    assert torch.equal(codes[rows].view(torch.uint8), want[0][rows].view(torch.uint8))
+    if scale is not None:
+        dim = 0 if mode == "ptpc" else 1
+        assert torch.equal(scale.index_select(dim, rows).view(torch.uint8), want[1].index_select(dim, rows).view(torch.uint8))
+    assert torch.equal(got[rows], total[rows])
+
+
+@pytest.mark.parametrize("mode", ["blockscale", "mxfp8"])
+@pytest.mark.parametrize("R,C,dtype,residual", [(8000, 256, torch.bfloat16, True), (3000, 2048, torch.float32, True), (2600, 1152, torch.bfloat16, False)])
+def test_later_turns_against_the_oracle(norm, mode, R, C, dtype, residual):
+    x, r, w = _make(R, C, R + C, dtype)
+    x[R - 1] *= 2.0 ** 80
+    dx = x.cuda()
+    got = norm(mode, dx, w.cuda(), 1e-6, residual=r.cuda() if residual else None, residual_out=dx if residual else None)
+    _check(mode, x, r if residual else None, w, 1e-6, got)
+
+
+@pytest.mark.parametrize("R,C,residual", [(140000, 16384, True), (66000, 32768, False)])
+def test_offsets_past_31_bits(norm, R, C, residual):
+    """More than 2^31 elements: the last rows as in a call of their own."""
+    g = torch.Generator("cuda").manual_seed(R)
+    some = torch.randn(1000, C, generator=g, device="cuda").bfloat16()
+    x = some.repeat(R // 1000, 1)
+    x[-700:] = torch.randn(700, C, generator=g, device="cuda").bfloat16()
+    w = (1 + 0.3 * torch.randn(C, generator=g, device="cuda")).bfloat16()
+    r = x.flip(0) if residual else None
+    part = x[-700:].clone()
+    want = norm("mxfp8", part, w, residual=r[-700:].clone() if residual else None)
+    codes, scale, kept = norm("mxfp8", x, w, residual=r, residual_out=x if residual else None)
+    assert torch.equal(codes[-700:], want[0]) and torch.equal(scale[:, -700:], want[1]) and torch.equal(kept[-700:], want[2])
