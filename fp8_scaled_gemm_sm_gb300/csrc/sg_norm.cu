@@ -492,7 +492,9 @@ sg_status_t launch_width(const NormParams& p, int num_sms, cudaStream_t stream) 
   }
   if (vecs <= 1024 && (!BF16 || p.R <= 2 * num_sms)) return launch<MODE, BF16, 1, 1024>(p, num_sms, stream);
   if (vecs <= (BF16 ? 1024 : 2048)) return launch<MODE, BF16, 2, 1024>(p, num_sms, stream);
-  if (vecs <= 2048) return launch<MODE, BF16, 4, 512>(p, num_sms, stream);
+  if constexpr (BF16) {
+    if (vecs <= 2048) return launch<MODE, BF16, 4, 512>(p, num_sms, stream);
+  }
   return launch<MODE, BF16, 8, 512>(p, num_sms, stream);
 }
 
