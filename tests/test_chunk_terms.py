@@ -19,3 +19,16 @@ def test_terms_of_every_value():
         off = (v.double() - first.double() - second.double()).abs()
         assert bool((off[v.abs() >= 2.0 ** -6] == 0).all())
         assert float(off.max()) <= 2.0 ** -14
+
+
+def test_rows_too_small_to_be_scaled_to_2_to_the_7th():
+    """A row whose largest is below 2^-119 is scaled by 2^126, the most that there is: its elements are multiples of 2^-133, so of 2^-7 then, and the terms keep
+    each of them whole."""
+    bits = torch.arange(1 << 15, dtype=torch.int32)
+    x = (bits << 16).view(torch.float32).double()
+    x = x[x < 2.0 ** -119]
+    assert float(x[1]) == 2.0 ** -133
+    v = (x * 2.0 ** 126).float()
+    first = v.to(torch.float8_e4m3fn).float()
+    second = (v - first).to(torch.float8_e5m2).float()
+    assert bool((v.double() == first.double() + second.double()).all()) and bool((v.double() * 2.0 ** -126 == x).all())

@@ -558,3 +558,76 @@ def test_outputs_that_overlap_are_refused():
         out, lse = call(out=both[:n * 4 * 64].view(n, 4, 64), lse=both[n * 4 * 64:].view(torch.float32).view(n, 4))
         want = call()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("hq,hk,d,ctx", [(4, 2, 64, 100), (8, 1, 128, 100), (4, 2, 128, 700), (2, 2, 96, 260)])
+@pytest.mark.parametrize("what", ["key code", "value code", "key scale", "value scale"])
+@pytest.mark.parametrize("row", [0, 12, 29])
+def test_what_is_not_finite_leaves_the_rest_right(hq, hk, d, ctx, what, row):
+    """One key or value, or one scale, of the new token `row` and head 0 is NaN.  Rows that see it give NaN (a value's code: in its dimension); rows before it may
+    where it is a value's; all else of the head is the formula's, and of other heads and sequences the same bits."""
+    new, seq = 30, ctx + 30
+    c = Case(hq, hk, d, 16, [new, 25], [ctx, 60], seed=25)
+    out0, lse0 = c.run()
+    table, codes, scales = c.host
+    group, which, key, dim = hq // hk, what.startswith("value"), ctx + row, 3
+    pg, slot = int(table[0, key // 16]), key % 16
+    tensors = [[t.clone() for t in (c.cache.k, c.cache.v)], [t.clone() for t in (c.cache.k_scale, c.cache.v_scale)]]
+    if what.endswith("code"):
+        tensors[0][which][pg, 0, slot, dim] = 0x7F
+        first = key
+    else:
+        tensors[1][which][pg, 0, slot // 16] = 255
+        first = key // 16 * 16
+    out, lse = c.plan.chunk(c.q, _pkg().KVCache(*tensors[0], *tensors[1]), *c.args, scale=c.scale)
+    torch.cuda.synchronize()
+    assert torch.equal(out[new:], out0[new:]) and torch.equal(lse[new:], lse0[new:])
+    assert torch.equal(out[:new, group:], out0[:new, group:]) and torch.equal(lse[:new, group:], lse0[:new, group:])
+    # head 0's queries, over what was there before
+    k, _ = ref.cached(codes[0], scales[0], table[0], hk, 16, seq)
+    v, _ = ref.cached(codes[1], scales[1], table[0], hk, 16, seq)
+    q = _f64(c.q[:new, :group])
+    see = ctx + 1 + np.arange(new)
+    o, ls, mag, big = ref.attend(q, k[:, :1], v[:, :1], see, c.scale)
+    small = 2.0 ** -21 * np.abs(q).max(2) * np.abs(k[:, 0]).sum(1).max() * c.scale
+    tol = ref.out_tolerance(o, mag, 11) + 2 * small[..., None] * mag + seq * 2.0 ** -31 * np.abs(v[:, 0]).max()
+    sees = np.broadcast_to((see > first)[:, None, None], o.shape)
+    dims = np.zeros(d, bool)
+    dims[dim if what == "value code" else slice(None)] = True
+    hit = np.broadcast_to(dims, o.shape)
+    go, gl = _f64(out[:new, :group]), _f64(lse[:new, :group])
+    assert np.isnan(go[sees & hit]).all() and (sees & hit).any()
+    right = np.abs(go - o) <= tol
+    may = ~sees & hit & np.isnan(go) if which else np.zeros_like(sees)
+    assert (right | (sees & hit) | may).all(), (float(np.nanmax(np.abs(go - o) / tol)), np.argwhere(~(right | (sees & hit) | may))[:4].tolist())
+    if which:
+        assert (np.abs(gl - ls) <= ref.lse_tolerance(ls, big) + small).all()
+    else:
+        assert np.isnan(gl[sees[..., 0]]).all()
+        assert (np.abs(gl - ls) <= ref.lse_tolerance(ls, big) + small)[~sees[..., 0]].all()
+
+
+def test_terms_of_every_query_value():
+    """The kernel's own two terms of each finite bf16 value below 2^8, beside one of 255 in its row: a sequence of one key, which is 1 in the value's dimension and
+    zero in the other's, so that lse is the value.  Rounding: of the score by 2^-24 of itself, of the reference and its logarithm added up by as much, of the exponential, the
+    sum and the logarithm by 2^-22 each; below 2^-6 the terms leave up to 2^-14."""
+    pkg = _pkg()
+    bits = np.arange(1 << 16, dtype=np.uint32) << 16
+    x = bits.view(np.float32)
+    x = x[np.isfinite(x) & (np.abs(x) < 256)]
+    heads = 64
+    x = np.resize(x, -(-len(x) // heads) * heads).reshape(-1, heads)
+    n = len(x)
+    plan = pkg.PagedAttention(heads, 1, 64, 16)
+    codes = [torch.zeros(1, 1, 16, 64, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    codes[0][..., 1] = 0x38  # 1
+    scales = [torch.full((1, 1, 1), 127, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    q = torch.zeros(n, heads, 64, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 255
+    q[..., 1] = torch.from_numpy(x).bfloat16().cuda()
+    ones = torch.ones(n, dtype=torch.int32, device="cuda")
+    _, lse = plan.chunk(q, pkg.KVCache(*codes, *scales), torch.zeros(n, 1, dtype=torch.int32, device="cuda"), ones, _ints(list(range(n + 1))), scale=1.0)
+    v = x.astype(np.float64)
+    off = np.abs(_f64(lse) - v)
+    tol = np.abs(v) * 2.0 ** -21 + 2.0 ** -20 + np.where(np.abs(v) < 2.0 ** -6, 2.0 ** -14, 0)
+    assert (off <= tol).all(), (float((off / tol).max()), v.flat[np.argmax(off / tol)])
