@@ -168,6 +168,18 @@ __device__ __forceinline__ int64_t cost(const Sequence& s, int span) {  // of on
   return cost_before(s, s.units - 1, span) + kUnitCost + static_cast<int64_t>(key_cost(unit_tiles(s, s.units - 1, span))) * s.lk;
 }
 
+// The first sequence after b that has tokens; B: none.  By a whole warp, 32 at a time: between two that have some there may be
+// millions that are idle, and every other warp of the CTA waits meanwhile, for 4 seconds at most.
+__device__ __forceinline__ int next_sequence(const ChunkParams& p, int b) {
+  for (++b; b < p.B; b += 32) {
+    const int at = b + static_cast<int>(threadIdx.x & 31);
+    auto upto = [&](int i) { return min(max(__ldg(p.cu + i), 0), p.T); };
+    const unsigned there = __ballot_sync(0xffffffffu, at < p.B && upto(at + 1) > upto(at));
+    if (there) return b + __ffs(there) - 1;
+  }
+  return p.B;
+}
+
 // What a CTA works on: blocks [t0, t1) of a unit.  b: -2 no more.
 struct Job {
   int b, q0, lq, lk;     // sequence, its first row, tokens, keys
@@ -184,7 +196,7 @@ struct Walk {
   Sequence s;
   int b, hg, unit;
   int64_t start;  // the unit's number
-  // The first job at or after the unit; false: none.
+  // The first job at or after the unit; false: none.  By a whole warp.
   __device__ __forceinline__ bool find(Job& job, Cut& cut) {
     for (;;) {
       if (start >= end) return false;
@@ -212,13 +224,11 @@ struct Walk {
         unit = 0;
         if (++hg == p.head_groups) {
           hg = 0;
-          do {
-            if (++b >= p.B) {
-              start = end;
-              break;
-            }
+          b = next_sequence(p, b);
+          if (b >= p.B)
+            start = end;
+          else
             s = sequence(p, b, span);
-          } while (s.units == 0);
         }
       }
       if (mine) return true;

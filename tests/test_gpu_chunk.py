@@ -631,3 +631,23 @@ def test_terms_of_every_query_value():
     off = np.abs(_f64(lse) - v)
     tol = np.abs(v) * 2.0 ** -21 + 2.0 ** -20 + np.where(np.abs(v) < 2.0 ** -6, 2.0 ** -14, 0)
     assert (off <= tol).all(), (float((off / tol).max()), v.flat[np.argmax(off / tol)])
+
+
+@pytest.mark.parametrize("B", [1 << 24, (1 << 24) - 33, 40, 33])
+def test_idle_sequences_between(B):
+    """Up to as many sequences as a call may have, all but the first, one in the middle and the last idle, most of those with keys."""
+    from fp8_scaled_gemm_sm_gb300 import binding
+
+    c = Case(4, 2, 64, 16, [3, 1, 40], [60, 20, 11], seed=26)
+    want = c.run()
+    c.check(*want)
+    at = torch.tensor([0, B // 2 + 1, B - 1], device="cuda")
+    table = torch.zeros(B, c.args[0].shape[1], dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), 30, dtype=torch.int32, device="cuda")
+    new = torch.zeros(B, dtype=torch.int32, device="cuda")
+    table[at], lens[at], new[at] = c.args[0], c.args[1], _ints(c.new)
+    cu = torch.cat([_ints([0]), new.cumsum(0, dtype=torch.int32)])
+    out, lse = c.plan.chunk(c.q, c.cache, table, lens, cu, scale=c.scale)
+    torch.cuda.synchronize()
+    assert binding.scaled_attn_debug_status(c.plan.handle)[0] == 0
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
