@@ -100,7 +100,7 @@ sg_status_t check_apart(const sg_page_pool_t* p, std::initializer_list<const int
   return SG_OK;
 }
 
-// The caches of a pool's layers: each of the pool's pages, none of them twice.
+// The caches of a pool's layers, each with all of the pool's pages.  One that is given twice is moved twice, the same bytes to the same place.
 sg_status_t check_layers(const sg_attn* h, const sg_page_pool_t* pool, const sg_kv_cache_t* caches, int64_t layers) {
   if (layers < 0) return refuse(SG_ERR_INVALID_ARG, "pool: negative number of layers");
   if (layers > 65536) return refuse(SG_ERR_UNSUPPORTED_SHAPE, "pool: layers > 65536");

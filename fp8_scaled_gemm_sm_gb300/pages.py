@@ -10,8 +10,8 @@ class PagePool:
     """The pages of `caches` (a ``KVCache``, or one for each layer of a model: a page number means that page of
     each) and the rows that hold them.
 
-    `table` int32 [rows, entries] lists each row's pages in order, -1 past the last; `lens` int32 [rows] is
-    the number of tokens that it has room for in use; `refs` int32 [num_pages] counts the entries that name a page.  The calls change them in
+    `table` int32 [rows, entries] lists each row's pages in order, -1 past the last; `lens` int32 [rows] counts
+    the tokens that each row holds (these calls alone change it; a sequence of which fewer are to be seen takes kv_lens of its own); `refs` int32 [num_pages] counts the entries that name a page.  The calls change them in
     place on torch's current stream, or on `stream` (a CUDA stream's number); nothing synchronises, so all can be captured in
     a CUDA graph.  Calls on one pool have to be ordered, with one another and with attention over the rows that they
     change.  Requests are int32 tensors on the pool's device, carried out in their order, the lowest free pages

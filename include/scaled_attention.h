@@ -143,7 +143,8 @@ sg_status_t scaled_attn_prompt(sg_attn_t h, const void* q, int64_t q_stride, con
  * model's layers share one pool: a page number means that page of each. */
 typedef struct sg_page_pool {
   int32_t* table;  /* [rows][table_stride]: the pages of each row's tokens in order, -1 past the last (4-byte aligned) */
-  int32_t* lens;   /* [rows]: tokens of each row; a negative one counts as 0 (4-byte aligned) */
+  int32_t* lens;   /* [rows]: tokens of each row; a negative one counts as 0 (4-byte aligned).  These calls alone change it: the pages behind a
+                      length that is lowered by hand stay in the table, and grow would write others over them. */
   int32_t* refs;   /* [num_pages]: table entries that name the page; free at 0 (16-byte aligned) */
   int64_t rows, table_stride, num_pages;
   void* scratch;   /* scaled_attn_pool_scratch_bytes(rows, num_pages) bytes, 16-byte aligned */

@@ -380,3 +380,16 @@ def test_plans_of_another_layout_are_refused(pkg):
     pool.plan = own
     assert pool.fork(a, a + 2).tolist() == model.fork([0, 1], [2, 3])
     _same(pool, model, arrays)
+
+
+def test_a_cache_given_twice(pkg):
+    """As given once."""
+    pool, model, arrays, _ = _setup(pkg, 6, 6, 40, layers=1)
+    pool = pkg.PagePool.new(pool.plan, pool.caches * 34, 6, 6)
+    assert pool.grow(ints([0, 1, 2]), ints([20, 7, 33])).tolist() == model.grow([0, 1, 2], [20, 7, 33])
+    assert pool.fork(ints([0, 2, 1]), ints([3, 4, 5])).tolist() == model.fork([0, 2, 1], [3, 4, 5])
+    _same(pool, model, arrays)
+    pool.release(ints([0, 4]))
+    model.release([0, 4])
+    assert pool.compact().tolist() == [model.compact()]
+    _same(pool, model, arrays)
