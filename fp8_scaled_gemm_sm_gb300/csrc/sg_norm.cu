@@ -12,7 +12,7 @@
 // step of Newton's iteration on such pairs.  So g, every y (two fp32 products) and every
 // scale and code after it do not depend on the order of the sum: an e8m0 scale goes
 // by which side of a power of two a block's largest value lies, where any difference would show.
-// It costs 3.5 instructions an element (5.5 for fp32 rows, whose squares are not exact in 24 bits).
+// It costs 4 instructions an element (5.5 for fp32 rows, whose squares are not exact in 24 bits).
 //
 // The bound is memory: x and the residual are read once, the sum is written once and the
 // codes once; the row stays in registers in between.  A CTA a row, rows dealt out in turn.  Where there are many rows, what is close to that
@@ -482,14 +482,21 @@ sg_status_t launch_width(const NormParams& p, int num_sms, cudaStream_t stream) 
   // CTA's last warp is one of two.  Up to 7168 columns two CTAs have 8 warps each and 128 registers a thread, at 8192 9 warps
   // and 96 (16384 x 8192 for ptpc 183 and 214 us), above 8192 one CTA has an SM (8192 x 16384 195 and 225; 16384 x 8192 264).
   // More CTAs with fewer registers for narrower rows: 30000 x 4096 blockscale 155 (four), 197 (three), two 147.
+  // Past 7168 columns rows come that way where every thread has four vectors, at multiples of 1024 columns.  With 96 registers the check of each vector
+  // that other widths need spills 8 to 40 bytes: it gains there (16384 x 7680 for ptpc 184 us, straight to registers 211, mxfp8 203 and 203;
+  // 8192 x 10752 151 and 186, 175 and 187), loses where no check is needed (16384 x 8192 for ptpc 193 and 185, bf16 221 and 178),
+  // and would be eight kernels more; those widths go straight to registers.
   if constexpr (BF16) {
     if (p.R >= 4 * num_sms && p.residual && vecs >= 256) {
       const bool all = vecs % 128 == 0;  // every thread has four
       if (vecs <= 896) return all ? launch_rows<MODE, 256, 2, true>(p, num_sms, stream) : launch_rows<MODE, 256, 2, false>(p, num_sms, stream);
-      if (all && vecs <= 1024) return launch_rows<MODE, 288, 2, true>(p, num_sms, stream);
+      if (vecs == 1024) return launch_rows<MODE, 288, 2, true>(p, num_sms, stream);
       if (all && vecs <= 2048) return launch_rows<MODE, 544, 1, true>(p, num_sms, stream);
     }
   }
+  // Straight to registers: the fewest vectors a thread that 1024 threads allow, for bf16 rows two or four where there are several a CTA.  Rows past
+  // 16384 columns, and fp32 rows past 8192, do not fit the registers: up to 16384 fp32 spills 36 to 64 bytes a thread (8192 x 12288 for ptpc 283 us, floor 193),
+  // past that bf16 248 to 280 (8192 x 20480 585, floor 174) and fp32 448 to 544 (4096 x 32768 for mxfp8 594, floor 258).
   if (vecs <= 1024 && (!BF16 || p.R <= 2 * num_sms)) return launch<MODE, BF16, 1, 1024>(p, num_sms, stream);
   if (vecs <= (BF16 ? 1024 : 2048)) return launch<MODE, BF16, 2, 1024>(p, num_sms, stream);
   if constexpr (BF16) {
