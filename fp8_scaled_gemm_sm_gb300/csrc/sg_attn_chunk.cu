@@ -28,7 +28,7 @@
 // Units that are short beside a range are not cut; the parts of a cut one are joined by a second
 // kernel in the order of their ranges, so results do not depend on timing.
 //
-// What bounds it: the chain scores, softmax, weights, product of a tile, 2.1 us a block of both where the tensor cores need
+// What bounds it: the chain scores, softmax, weights, product of a tile, 1.9 us (2 long documents) to 2.1 (4 chunks) a block of both where the tensor cores need
 // 1.1 and take 1.5 without the softmax.  Two things lengthen it.  Shared memory: operands of the MMAs, loads and the
 // conversion take 2200 of a block's cycles, and every load and barrier of the other warps waits in between (hundreds of
 // cycles: so scales are read before the scores are there).  Instructions: five kinds of warps, each in a loop of its own, do not

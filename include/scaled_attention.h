@@ -44,7 +44,7 @@
  * Precision: scores, softmax statistics and sums are held in fp32; bf16 outputs are rounded once, to nearest even.
  * The weights of the product with v are rounded to what the tensor cores take, each to nearest: in
  * scaled_attn_prompt to bf16 (by at most 2^-8 of itself), in scaled_attn_decode and scaled_attn_chunk to fp16 (2^-11; with its value block's
- * scale inside, and to no finer than 2^-32 of the row's largest such weight: where one visible block's value scale is 2^22 or
+ * scale inside, and light ones by up to 2^-32, in scaled_attn_chunk 2^-31, of the row's largest such weight: where one visible block's value scale is 2^22 or
  * more above the others', their light weights lose bits in every dimension).  The denominator takes them unrounded.
  * scaled_attn_chunk takes a query row's elements to 2^-21 of its largest; those from 2^-13 of it on are exact.
  *
