@@ -28,12 +28,19 @@ class PagePool:
             raise ValueError("table and lens must have as many rows")
         if any(c.k.shape[0] < refs.shape[0] for c in caches):
             raise ValueError("every cache must have the pool's pages")
-        self.plan, self.caches, self.table, self.lens, self.refs = plan, caches, table, lens, refs
-        self.scratch = torch.empty(binding.scaled_attn_pool_scratch_bytes(table.shape[0], refs.shape[0]), dtype=torch.uint8,
-                                   device=plan.device)
+        self.plan, self._caches, self._table, self._lens, self._refs = plan, tuple(caches), table, lens, refs
+        self._scratch = torch.empty(binding.scaled_attn_pool_scratch_bytes(table.shape[0], refs.shape[0]), dtype=torch.uint8,
+                                    device=plan.device)
         ext = _ext()
-        self._p = ext.pool(plan._p, table, lens, refs, self.scratch, [c._c for c in caches])
+        self._p = ext.pool(plan._p, table, lens, refs, self._scratch, [c._c for c in caches])
         self._release, self._grow, self._fork, self._compact = ext.pool_release, ext.pool_grow, ext.pool_fork, ext.pool_compact
+
+    # The calls have the tensors' addresses: others cannot take their places.
+    caches = property(lambda self: list(self._caches))
+    table = property(lambda self: self._table)
+    lens = property(lambda self: self._lens)
+    refs = property(lambda self: self._refs)
+    scratch = property(lambda self: self._scratch)
 
     @classmethod
     def new(cls, plan, caches, rows, entries):

@@ -393,3 +393,14 @@ def test_a_cache_given_twice(pkg):
     model.release([0, 4])
     assert pool.compact().tolist() == [model.compact()]
     _same(pool, model, arrays)
+
+
+def test_tensors_of_a_pool_cannot_be_exchanged(pkg):
+    """The calls go by their addresses: another tensor in one's place would leave them memory that has been given away."""
+    pool, model, arrays, _ = _setup(pkg, 4, 3, 9)
+    for name in ("table", "lens", "refs", "scratch", "caches"):
+        with pytest.raises(AttributeError):
+            setattr(pool, name, getattr(pool, name))
+    pool.caches.clear()
+    assert pool.grow(ints([0, 3]), ints([20, 7])).tolist() == model.grow([0, 3], [20, 7])
+    _same(pool, model, arrays)
