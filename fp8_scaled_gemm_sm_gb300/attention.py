@@ -54,6 +54,7 @@ class KVCache:
             if t.dtype != torch.uint8 or t.shape != (pages, hk, page // BLOCK) or not t.is_contiguous():
                 raise ValueError("cache scales must be contiguous uint8 [num_pages, Hk, page / %d]" % BLOCK)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._held = (k, v, k_scale, v_scale)  # the calls have their addresses, whatever becomes of the names
         self.heads, self.page, self.dim, self.device = hk, page, d, k.device
         least = hk * page * d
         self._c = _ext().cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages,
@@ -120,7 +121,7 @@ class PagedAttention:
         self.q_heads, self.kv_heads, self.dim, self.page_size = int(q_heads), int(kv_heads), int(dim), int(page_size)
         dev = torch.cuda.current_device() if device is None else torch.device("cuda", device).index
         self.device = torch.device("cuda", dev)
-        self.rotary = rotary
+        self.rotary = self._held = rotary  # the calls have its address, whatever becomes of the name
         rot = (0, 0, 0, 0)
         if rotary is not None:
             if rotary.dtype != torch.float32 or rotary.dim() != 3 or rotary.shape[1] != 2 or not rotary.is_contiguous():

@@ -404,3 +404,17 @@ def test_tensors_of_a_pool_cannot_be_exchanged(pkg):
     pool.caches.clear()
     assert pool.grow(ints([0, 3]), ints([20, 7])).tolist() == model.grow([0, 3], [20, 7])
     _same(pool, model, arrays)
+
+
+def test_memory_that_the_calls_have_is_kept(pkg):
+    """Another tensor under a cache's or a plan's name does not give the first one's memory away."""
+    from fp8_scaled_gemm_sm_gb300 import rotary_table
+
+    plan = pkg.PagedAttention(4, 2, 64, 16, rotary=rotary_table(5000, 64))
+    cache = plan.new_cache(500)
+    for owner, name in ((cache, "k"), (cache, "v"), (cache, "k_scale"), (cache, "v_scale"), (plan, "rotary")):
+        t = getattr(owner, name)
+        at, shape, dtype = t.data_ptr(), t.shape, t.dtype
+        del t
+        setattr(owner, name, None)
+        assert all(torch.empty(shape, dtype=dtype, device="cuda").data_ptr() != at for _ in range(3))
