@@ -494,7 +494,7 @@ sg_status_t launch_width(const NormParams& p, int num_sms, cudaStream_t stream) 
       if (all && vecs <= 2048) return launch_rows<MODE, 544, 1, true>(p, num_sms, stream);
     }
   }
-  // Straight to registers: the fewest vectors a thread that 1024 threads allow, for bf16 rows two or four where there are several a CTA.  Rows past
+  // Straight to registers: a vector a thread, two for bf16 rows of which a CTA has several and for wide fp32 rows, and four or eight in 512 threads past that.  Rows past
   // 16384 columns, and fp32 rows past 8192, do not fit the registers: up to 16384 fp32 spills 36 to 64 bytes a thread (8192 x 12288 for ptpc 283 us, floor 193),
   // past that bf16 248 to 280 (8192 x 20480 585, floor 174) and fp32 448 to 544 (4096 x 32768 for mxfp8 594, floor 258).
   if (vecs <= 1024 && (!BF16 || p.R <= 2 * num_sms)) return launch<MODE, BF16, 1, 1024>(p, num_sms, stream);
